@@ -13,7 +13,7 @@ _BINDING_NAMES = None
 
 def __getattr__(name):
     if name.startswith("mxs_") or name in ("MxsError", "QMat", "qmat_alloc", "library_path",
-                                          "STATUS", "NOALLOC_SCRATCH_BYTES"):
+                                          "STATUS", "NOALLOC_SCRATCH_BYTES", "KV4Cache", "kv4_cache_alloc"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, c_char_p, c_double, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
 from dataclasses import dataclass
 
 import torch
@@ -34,6 +34,11 @@ class _QMat(Structure):
                 ("n4", c_int32), ("reserved", c_int32),
                 ("q8", c_void_p), ("ld8", c_int64), ("q6", c_void_p), ("ld6", c_int64),
                 ("q4", c_void_p), ("ld4", c_int64), ("sc", c_void_p), ("lds", c_int64)]
+
+
+class _Kv4Cache(Structure):
+    _fields_ = [("pages", c_int64), ("page_size", c_int32), ("H", c_int32), ("D", c_int32), ("reserved", c_int32),
+                ("kc", c_void_p), ("ks", c_void_p), ("vc", c_void_p), ("vs", c_void_p)]
 
 
 def library_path() -> str:
@@ -79,6 +84,15 @@ def _load():
         "mxs_mixed_gemm_fused_prepared_workspace": (c_size_t, [c_int64, c_int32, POINTER(_QMat)]),
         "mxs_mixed_gemm_fused_prepared": (S, [P, c_int32, c_int64, c_int64, P, POINTER(_QMat), P, c_size_t, P,
                                               c_int64, P, c_size_t, P]),
+        "mxs_rope_frequencies": (S, [c_int32, c_double, c_int32, c_double, c_double, c_double, c_double, P]),
+        "mxs_rope": (S, [P, c_int32, c_int64, c_int64, c_int64, c_int64, c_int64, P, P, c_int32, c_int32, c_float, P,
+                         c_int64, c_int64, P]),
+        "mxs_kv4_append": (S, [P, P, P, c_int32, c_int64, c_int64, c_int64, c_int64, c_int64, P, P, P, c_int32, c_int32,
+                               c_float, P]),
+        "mxs_kv4_read": (S, [P, P, c_int64, c_int32, P, c_int64, c_int64, P, c_int64, c_int64, P]),
+        "mxs_attend_kv4_tree_workspace": (c_size_t, [c_int32] + [c_int64] * 7),
+        "mxs_attend_kv4_tree": (S, [P, c_int32, c_int64, P, P, c_int64, P, P, P, c_int64, c_int64, c_int64, c_int64,
+                                    c_int64, c_int64, c_float, P, c_int64, P, c_size_t, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -94,7 +108,9 @@ EXPORTED = ("mxs_status_string", "mxs_last_error", "mxs_version", "mxs_budget_bl
             "mxs_output_error_workspace", "mxs_output_error", "mxs_layer_budget", "mxs_attend_kv4_workspace",
             "mxs_attend_kv4", "mxs_mixed_gemm_fused_workspace", "mxs_mixed_gemm_fused",
             "mxs_prepare_weights_size", "mxs_prepare_weights", "mxs_mixed_gemm_prepared_workspace",
-            "mxs_mixed_gemm_prepared", "mxs_mixed_gemm_fused_prepared_workspace", "mxs_mixed_gemm_fused_prepared")
+            "mxs_mixed_gemm_prepared", "mxs_mixed_gemm_fused_prepared_workspace", "mxs_mixed_gemm_fused_prepared",
+            "mxs_rope_frequencies", "mxs_rope", "mxs_kv4_append", "mxs_kv4_read", "mxs_attend_kv4_tree_workspace",
+            "mxs_attend_kv4_tree")
 
 
 def _check(status: int, where: str):
@@ -509,4 +525,231 @@ def mxs_attend_kv4(q: torch.Tensor, k_cache, v_cache, scale: float, out=None, ws
     p, n = _workspace(mxs_attend_kv4_workspace(T, Hq, Hkv, D), q.device, ws)
     _check(_lib.mxs_attend_kv4(q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), T, Hq,
                                Hkv, D, float(scale), out.data_ptr(), p, n, _stream(q.device)), "mxs_attend_kv4")
+    return out
+
+
+# ------------------------------------- serving on the 4-bit cache: rotary positions
+ROPE_LAYOUTS = {"half": 0, "pairs": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+def mxs_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                         low: float = 1.0, high: float = 4.0, original_length: float = 8192.0,
+                         device="cuda") -> torch.Tensor:
+    """Radians per position of the rot / 2 rotated pairs, fp64, copied to `device`.
+
+    scaling stretches them for long contexts: "linear" divides by factor, "ntk"
+    raises the base, "parts" divides only the pairs that turn few times within
+    original_length tokens (none above `high` turns, all below `low`)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
+    _check(_lib.mxs_rope_frequencies(rot, base, ROPE_SCALINGS[scaling], factor, low, high, original_length,
+                                     out.data_ptr()), "mxs_rope_frequencies")
+    return out.to(device)
+
+
+def _rows(t: torch.Tensor, name: str, dev):
+    """(pointer, token stride, head stride) of a [T, H, D] GPU tensor with adjacent dims."""
+    if t.dim() != 3 or t.device != dev or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a [T, H, D] tensor on {dev} with unit stride in the last dimension")
+    s = t.stride()
+    return t.data_ptr(), s[0], s[1]
+
+
+def _vector(t: torch.Tensor, name: str, dtype, n: int, dev) -> int:
+    """Pointer of a contiguous [n] tensor of `dtype` on `dev`."""
+    if t.dtype != dtype or t.dim() != 1 or t.numel() != n or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {dev}")
+    return t.data_ptr()
+
+
+def _gpu(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+def _call(dev, fn, name: str, *args):
+    """The C call on the current stream of `dev`, with `dev` current (HIP launches there)."""
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, _stream(dev)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)), name)
+
+
+def _layout(layout: str) -> int:
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    return ROPE_LAYOUTS[layout]
+
+
+def mxs_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, layout: str = "half", mscale: float = 1.0,
+             out: torch.Tensor | None = None) -> torch.Tensor:
+    """x [T, H, D] (bf16 or fp32, any token and head strides) with the first
+    2 * len(freq) dims of every head turned by positions [T] (int64) times freq
+    (fp64, from mxs_rope_frequencies). out may be x. The gradient with respect
+    to x is the same call on the output's gradient at -positions."""
+    dev = _gpu(x, "x")
+    px, xt, xh = _rows(x, "x", dev)
+    T, H, D = x.shape
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and type")
+    py, yt, yh = _rows(out, "out", dev)
+    n = freq.numel()
+    _call(dev, _lib.mxs_rope, "mxs_rope", px, _dtype(x), T, H, D, xt, xh,
+          _vector(positions, "positions", torch.int64, T, dev), _vector(freq, "freq", torch.float64, n, dev), 2 * n,
+          _layout(layout), mscale, py, yt, yh)
+    return out
+
+
+# ------------------------------------------------------- paged 4-bit K/V cache
+@dataclass(frozen=True)
+class KV4Cache:
+    """A pool of pages of 4-bit keys and values (see mxs_kv4_cache): codes kc,
+    vc uint8 [pages, page_size, H, D / 2], E8M0 bytes ks, vs uint8 [pages,
+    page_size, H, D / 32], contiguous. Slot = page * page_size + offset.
+    Frozen: the C struct is built once, on first use, and reused."""
+    kc: torch.Tensor
+    ks: torch.Tensor
+    vc: torch.Tensor
+    vs: torch.Tensor
+
+    def __post_init__(self):
+        if self.kc.dim() != 4 or not self.kc.is_cuda:
+            raise ValueError("kc must be a [pages, page_size, H, D / 2] GPU tensor")
+        P, S, H, h = self.kc.shape
+        for t, w in ((self.kc, h), (self.ks, h // 16), (self.vc, h), (self.vs, h // 16)):
+            if t.dtype != torch.uint8 or tuple(t.shape) != (P, S, H, w) or not t.is_contiguous() \
+                    or t.device != self.kc.device:
+                raise ValueError("cache planes must be contiguous uint8 [pages, page_size, H, D / 2] codes and "
+                                 "[pages, page_size, H, D / 32] scales on one GPU")
+
+    def c_struct(self):
+        c = self.__dict__.get("_c")
+        if c is None:
+            P, S, H, h = self.kc.shape
+            c = _Kv4Cache(P, S, H, 2 * h, 0, self.kc.data_ptr(), self.ks.data_ptr(), self.vc.data_ptr(),
+                          self.vs.data_ptr())
+            object.__setattr__(self, "_c", c)
+        return c
+
+
+def kv4_cache_alloc(pages: int, page_size: int, H: int, D: int, device="cuda") -> KV4Cache:
+    """An empty pool (contents undefined until written)."""
+    if D < 32 or D % 32:
+        raise ValueError("D must be a positive multiple of 32")
+    kw = dict(dtype=torch.uint8, device=device)
+    return KV4Cache(*(torch.empty((pages, page_size, H, D // w), **kw) for w in (2, 32, 2, 32)))
+
+
+def _kv_rows(cache: KV4Cache, t: torch.Tensor, name: str, T: int, dtype, dev):
+    H, h = cache.kc.shape[2:]
+    if t.dtype != dtype or tuple(t.shape) != (T, H, 2 * h):
+        raise ValueError(f"{name} must be a {dtype} [{T}, {H}, {2 * h}] tensor")
+    return _rows(t, name, dev)
+
+
+def mxs_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                   positions: torch.Tensor | None = None, freq: torch.Tensor | None = None, layout: str = "half",
+                   mscale: float = 1.0) -> None:
+    """Quantises k, v [T, H, D] into the cache at slots [T] (int64, distinct;
+    negative or past the pool: skipped). With positions and freq, the keys are
+    rotated first, as by mxs_rope but without rounding in between."""
+    dev = _gpu(cache.kc, "cache")
+    T = slots.numel()
+    pk, kt, kh = _kv_rows(cache, k, "k", T, k.dtype, dev)
+    pv, vt, vh = _kv_rows(cache, v, "v", T, k.dtype, dev)
+    if (positions is None) != (freq is None):
+        raise ValueError("positions and freq go together")
+    n, pp, pf = 0, None, None
+    if positions is not None:
+        n = freq.numel()
+        pp, pf = _vector(positions, "positions", torch.int64, T, dev), _vector(freq, "freq", torch.float64, n, dev)
+    _call(dev, _lib.mxs_kv4_append, "mxs_kv4_append", ctypes.byref(cache.c_struct()), pk, pv, _dtype(k), T, kt, kh, vt,
+          vh, _vector(slots, "slots", torch.int64, T, dev), pp, pf, 2 * n, _layout(layout), mscale)
+
+
+def mxs_kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                 k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None):
+    """(k, v), each [T, H, D]: the values of slots [T] (int64), exact. Rows of
+    slots that are negative or past the pool are left as they were (zero in
+    outputs that the call allocates). dtype is that of outputs not given."""
+    dev = _gpu(cache.kc, "cache")
+    T = slots.numel()
+    if k_out is not None or v_out is not None:
+        dtype = (k_out if k_out is not None else v_out).dtype
+    H, h = cache.kc.shape[2:]
+    if k_out is None:
+        k_out = torch.zeros((T, H, 2 * h), dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.zeros((T, H, 2 * h), dtype=dtype, device=dev)
+    pk, kt, kh = _kv_rows(cache, k_out, "k_out", T, dtype, dev)
+    pv, vt, vh = _kv_rows(cache, v_out, "v_out", T, dtype, dev)
+    _call(dev, _lib.mxs_kv4_read, "mxs_kv4_read", ctypes.byref(cache.c_struct()),
+          _vector(slots, "slots", torch.int64, T, dev), T, _dtype(k_out), pk, kt, kh, pv, vt, vh)
+    return k_out, v_out
+
+
+# ------------------------------------------- attention of drafted tokens over it
+def mxs_attend_kv4_tree_workspace(dtype: torch.dtype, B: int, total_q: int, max_q: int, max_len: int, Hq: int,
+                                  Hkv: int, D: int) -> int:
+    dt = MXS_BF16 if dtype == torch.bfloat16 else MXS_F32
+    return int(_lib.mxs_attend_kv4_tree_workspace(dt, B, total_q, max_q, max_len, Hq, Hkv, D))
+
+
+def mxs_attend_kv4_tree(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
+                        scale: float, mask: torch.Tensor | None = None, max_q: int | None = None,
+                        max_len: int | None = None, out: torch.Tensor | None = None, ws=None) -> torch.Tensor:
+    """out [total_q, Hq, D]: attention of the query tokens q (bf16 or fp32) of B
+    sequences over the cache. Sequence b has lens[b] cached tokens in the pages
+    table[b]; its query rows cu[b] .. cu[b + 1] - 1 are the last of them. mask
+    [total_q, words] int64 holds, for every row, the bits of the drafted tokens
+    it sees (None: those up to itself). table [B, pages], lens [B] and cu
+    [B + 1] are int32. max_q and max_len bound the query and cached tokens of a
+    sequence (default: total_q and what the table can hold); tight bounds give
+    a better split. Rows of no sequence are left as they were in `out` (zero in
+    an output that the call allocates)."""
+    dev = _gpu(q, "q")
+    pq, qt, qh = _rows(q, "q", dev)
+    total, Hq, D = q.shape
+    if qh != D and Hq > 1:
+        raise ValueError("q's heads must be adjacent")
+    if out is None:
+        out = torch.zeros((total, Hq, D), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and type")
+    po, ot, oh = _rows(out, "out", dev)
+    if oh != D and Hq > 1:
+        raise ValueError("out's heads must be adjacent")
+    P, S, H, h = cache.kc.shape
+    if 2 * h != D or cache.kc.device != dev:
+        raise ValueError("q and the cache must have one head dimension and one device")
+    if table.dtype != torch.int32 or table.dim() != 2 or table.device != dev or not table.is_contiguous():
+        raise ValueError(f"table must be a contiguous int32 [B, pages] tensor on {dev}")
+    B, width = table.shape
+    words = 0
+    if mask is not None:
+        if mask.dtype != torch.int64 or mask.dim() != 2 or mask.shape[0] != total or mask.device != dev \
+                or not mask.is_contiguous():
+            raise ValueError(f"mask must be a contiguous int64 [total_q, words] tensor on {dev}")
+        words = mask.shape[1]
+    if max_q is None:
+        max_q = total
+    if max_len is None:
+        max_len = width * S
+    dt = _dtype(q)
+    if ws is None:
+        p, n = _workspace(int(_lib.mxs_attend_kv4_tree_workspace(dt, B, total, max_q, max_len, Hq, H, D)), dev, None)
+    else:
+        if ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on {dev}")
+        p, n = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call(dev, _lib.mxs_attend_kv4_tree, "mxs_attend_kv4_tree", pq, dt, qt, ctypes.byref(cache.c_struct()),
+          table.data_ptr(), width, _vector(lens, "lens", torch.int32, B, dev),
+          _vector(cu, "cu", torch.int32, B + 1, dev), None if mask is None else mask.data_ptr(), words, B, total,
+          max_q, max_len, Hq, scale, po, ot, p, n)
     return out

@@ -100,6 +100,41 @@ mxs_status check_qmat(const mxs_qmat *q, const char *name) {
     return MXS_OK;
 }
 
+mxs_status check_cache(const mxs_kv4_cache *c, const char *where) {
+    if (!c) return fail(MXS_ERR_ARG, "%s: cache is NULL", where);
+    if (c->reserved != 0) return fail(MXS_ERR_ARG, "%s: cache reserved field must be 0", where);
+    if (c->pages < 1 || c->page_size < 1 || c->H < 1 || c->D < 32 || c->D % 32)
+        return fail(MXS_ERR_SHAPE, "%s: cache pages=%lld page_size=%d H=%d D=%d", where, (long long)c->pages,
+                    c->page_size, c->H, c->D);
+    if (c->pages > 0x7FFFFFFF / c->page_size || (int64_t)c->H * c->D > 8 * 65535)
+        return fail(MXS_ERR_UNSUPPORTED, "%s: cache of %lld pages of %d tokens of %d x %d values", where,
+                    (long long)c->pages, c->page_size, c->H, c->D);
+    if (!c->kc || !c->ks || !c->vc || !c->vs) return fail(MXS_ERR_ARG, "%s: cache pointer is NULL", where);
+    if (!aligned(c->kc, 16) || !aligned(c->vc, 16))
+        return fail(MXS_ERR_UNSUPPORTED, "%s: cache codes not 16-byte aligned", where);
+    return MXS_OK;
+}
+
+// rows of [T, H, D] with these strides are at least D apart and, when they
+// are written, do not overlap
+bool strides_ok(int64_t T, int64_t H, int64_t D, int64_t ldt, int64_t ldh, bool written) {
+    if (ldt < 0 || ldh < 0 || ldt > ((int64_t)1 << 40) || ldh > ((int64_t)1 << 40)) return false;
+    if ((T > 1 && ldt < D) || (H > 1 && ldh < D)) return false;
+    if (!written || T <= 1 || H <= 1) return true;
+    return ldt >= (H - 1) * ldh + D || ldh >= (T - 1) * ldt + D;
+}
+
+mxs_status check_rotation(const char *where, const double *freq, int64_t rot, int64_t D, int32_t layout) {
+    if (!freq) return fail(MXS_ERR_ARG, "%s: freq is NULL", where);
+    if (layout != MXS_ROPE_HALF && layout != MXS_ROPE_PAIRS)
+        return fail(MXS_ERR_ARG, "%s: unknown rotary layout %d", where, (int)layout);
+    if (rot < 2 || rot % 2 || rot > D)
+        return fail(MXS_ERR_SHAPE, "%s: rot=%lld of D=%lld", where, (long long)rot, (long long)D);
+    return MXS_OK;
+}
+
+constexpr int64_t kMaxTokens = 0x7FFFFFFF;
+
 }  // namespace
 
 extern "C" {
@@ -428,6 +463,137 @@ mxs_status mxs_quantize_kv(const void *kv, mxs_dtype dtype, int64_t T, int64_t H
     o.sc = scales;
     o.lds = D / 32;
     return device_status(mxs::launch_quantize(kv, dtype, D, nullptr, o, stream), "quantize_kv");
+}
+
+mxs_status mxs_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double low, double high,
+                                double original_length, double *freq) {
+    if (!freq) return fail(MXS_ERR_ARG, "rope_frequencies: freq is NULL");
+    if (scaling < MXS_ROPE_UNSCALED || scaling > MXS_ROPE_PARTS)
+        return fail(MXS_ERR_ARG, "rope_frequencies: unknown scaling %d", (int)scaling);
+    if (rot < 2 || rot % 2 || (scaling == MXS_ROPE_NTK && rot < 4))
+        return fail(MXS_ERR_SHAPE, "rope_frequencies: rot=%d", (int)rot);
+    if (!(base > 0) || !isfinite(base) || !(factor > 0) || !isfinite(factor))
+        return fail(MXS_ERR_ARG, "rope_frequencies: base=%g factor=%g", base, factor);
+    if (scaling == MXS_ROPE_PARTS && (!(original_length > 0) || !isfinite(original_length) || !(high > low) ||
+                                      !isfinite(low) || !isfinite(high)))
+        return fail(MXS_ERR_ARG, "rope_frequencies: low=%g high=%g original_length=%g", low, high, original_length);
+    mxs::rope_frequencies(rot, base, scaling, factor, low, high, original_length, freq);
+    return ok();
+}
+
+mxs_status mxs_rope(const void *x, mxs_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t ldt, int64_t ldh,
+                    const int64_t *positions, const double *freq, int32_t rot, int32_t layout, float mscale,
+                    void *y, int64_t ldyt, int64_t ldyh, hipStream_t stream) {
+    if (!dtype_ok(dtype)) return fail(MXS_ERR_ARG, "rope: unknown dtype %d", (int)dtype);
+    if (T < 0 || H < 0 || D < 1)
+        return fail(MXS_ERR_SHAPE, "rope: T=%lld H=%lld D=%lld", (long long)T, (long long)H, (long long)D);
+    if (T > kMaxTokens || H > 65535 || D > 4096)
+        return fail(MXS_ERR_UNSUPPORTED, "rope: T=%lld H=%lld D=%lld", (long long)T, (long long)H, (long long)D);
+    const mxs_status r = check_rotation("rope", freq, rot, D, layout);
+    if (r != MXS_OK) return r;
+    if (!strides_ok(T, H, D, ldt, ldh, false) || !strides_ok(T, H, D, ldyt, ldyh, true) ||
+        (x == y && ((T > 1 && ldt != ldyt) || (H > 1 && ldh != ldyh))))
+        return fail(MXS_ERR_SHAPE, "rope: strides %lld, %lld -> %lld, %lld", (long long)ldt, (long long)ldh,
+                    (long long)ldyt, (long long)ldyh);
+    if (T == 0 || H == 0) return ok();
+    if (!x || !y || !positions) return fail(MXS_ERR_ARG, "rope: NULL pointer");
+    const size_t es = dtype == MXS_BF16 ? 2 : 4;
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(positions, 8) || !aligned(freq, 8))
+        return fail(MXS_ERR_UNSUPPORTED, "rope: misaligned pointer");
+    return device_status(mxs::launch_rope(x, dtype, T, H, D, ldt, ldh, positions, freq, rot, layout, mscale, y, ldyt,
+                                          ldyh, stream), "rope");
+}
+
+mxs_status mxs_kv4_append(const mxs_kv4_cache *cache, const void *k, const void *v, mxs_dtype dtype, int64_t T,
+                          int64_t ldkt, int64_t ldkh, int64_t ldvt, int64_t ldvh, const int64_t *slots,
+                          const int64_t *positions, const double *freq, int32_t rot, int32_t layout, float mscale,
+                          hipStream_t stream) {
+    mxs_status r = check_cache(cache, "kv4_append");
+    if (r != MXS_OK) return r;
+    if (!dtype_ok(dtype)) return fail(MXS_ERR_ARG, "kv4_append: unknown dtype %d", (int)dtype);
+    if (positions && (r = check_rotation("kv4_append", freq, rot, cache->D, layout)) != MXS_OK) return r;
+    if (T < 0 || !strides_ok(T, cache->H, cache->D, ldkt, ldkh, false) ||
+        !strides_ok(T, cache->H, cache->D, ldvt, ldvh, false))
+        return fail(MXS_ERR_SHAPE, "kv4_append: T=%lld strides %lld, %lld and %lld, %lld", (long long)T,
+                    (long long)ldkt, (long long)ldkh, (long long)ldvt, (long long)ldvh);
+    if (T > kMaxTokens) return fail(MXS_ERR_UNSUPPORTED, "kv4_append: T=%lld", (long long)T);
+    if (positions && rot > 4096) return fail(MXS_ERR_UNSUPPORTED, "kv4_append: rot=%d", (int)rot);
+    if (T == 0) return ok();
+    if (!k || !v || !slots) return fail(MXS_ERR_ARG, "kv4_append: NULL pointer");
+    const size_t es = dtype == MXS_BF16 ? 2 : 4;
+    if (!aligned(k, es) || !aligned(v, es) || !aligned(slots, 8) || !aligned(positions, 8) ||
+        (positions && !aligned(freq, 8)))
+        return fail(MXS_ERR_UNSUPPORTED, "kv4_append: misaligned pointer");
+    return device_status(mxs::launch_kv4_append(*cache, k, v, dtype, T, ldkt, ldkh, ldvt, ldvh, slots, positions, freq,
+                                                rot, layout, mscale, stream), "kv4_append");
+}
+
+mxs_status mxs_kv4_read(const mxs_kv4_cache *cache, const int64_t *slots, int64_t T, mxs_dtype dtype, void *k,
+                        int64_t ldkt, int64_t ldkh, void *v, int64_t ldvt, int64_t ldvh, hipStream_t stream) {
+    const mxs_status r = check_cache(cache, "kv4_read");
+    if (r != MXS_OK) return r;
+    if (!dtype_ok(dtype)) return fail(MXS_ERR_ARG, "kv4_read: unknown dtype %d", (int)dtype);
+    if (T < 0 || (k && !strides_ok(T, cache->H, cache->D, ldkt, ldkh, true)) ||
+        (v && !strides_ok(T, cache->H, cache->D, ldvt, ldvh, true)))
+        return fail(MXS_ERR_SHAPE, "kv4_read: T=%lld strides %lld, %lld and %lld, %lld", (long long)T,
+                    (long long)ldkt, (long long)ldkh, (long long)ldvt, (long long)ldvh);
+    if (T > kMaxTokens) return fail(MXS_ERR_UNSUPPORTED, "kv4_read: T=%lld", (long long)T);
+    if (T == 0) return ok();
+    if ((!k && !v) || !slots) return fail(MXS_ERR_ARG, "kv4_read: NULL pointer");
+    const size_t es = dtype == MXS_BF16 ? 2 : 4;
+    if (!aligned(k, es) || !aligned(v, es) || !aligned(slots, 8))
+        return fail(MXS_ERR_UNSUPPORTED, "kv4_read: misaligned pointer");
+    return device_status(mxs::launch_kv4_read(*cache, slots, T, dtype, k, ldkt, ldkh, v, ldvt, ldvh, stream),
+                         "kv4_read");
+}
+
+size_t mxs_attend_kv4_tree_workspace(mxs_dtype dtype, int64_t B, int64_t total_q, int64_t max_q, int64_t max_len,
+                                     int64_t Hq, int64_t Hkv, int64_t D) {
+    if (!dtype_ok(dtype) || B <= 0 || total_q <= 0 || max_q <= 0 || max_len < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv ||
+        D < 32 || D % 32 || D > 256)
+        return 0;
+    return mxs::attend_kv4_tree_workspace(dtype, B, total_q, max_q, max_len, Hq, Hkv, D);
+}
+
+mxs_status mxs_attend_kv4_tree(const void *q, mxs_dtype dtype, int64_t ldq, const mxs_kv4_cache *cache,
+                               const int32_t *table, int64_t ldt, const int32_t *lens, const int32_t *cu,
+                               const uint64_t *mask, int64_t mask_words, int64_t B, int64_t total_q, int64_t max_q,
+                               int64_t max_len, int64_t Hq, float scale, void *out, int64_t ldo, void *ws,
+                               size_t ws_bytes, hipStream_t stream) {
+    const mxs_status r = check_cache(cache, "attend_kv4_tree");
+    if (r != MXS_OK) return r;
+    if (!dtype_ok(dtype) || !isfinite(scale))
+        return fail(MXS_ERR_ARG, "attend_kv4_tree: dtype %d scale %g", (int)dtype, (double)scale);
+    const int64_t H = cache->H, D = cache->D;
+    if (B < 0 || total_q < 0 || max_q < 0 || max_len < 0 || Hq < H || Hq % H || ldt < 0 || mask_words < 0 ||
+        (mask && mask_words < 1))
+        return fail(MXS_ERR_SHAPE, "attend_kv4_tree: B=%lld total_q=%lld max_q=%lld max_len=%lld Hq=%lld H=%lld",
+                    (long long)B, (long long)total_q, (long long)max_q, (long long)max_len, (long long)Hq,
+                    (long long)H);
+    if (D > 256 || B > 65535 || Hq > 65535 || max_len > (1 << 30) || max_q > (1 << 20) || total_q > (1 << 24) ||
+        mask_words > (1 << 20) || ldt > (1 << 30))
+        return fail(MXS_ERR_UNSUPPORTED, "attend_kv4_tree: D=%lld B=%lld Hq=%lld max_len=%lld max_q=%lld total_q=%lld",
+                    (long long)D, (long long)B, (long long)Hq, (long long)max_len, (long long)max_q,
+                    (long long)total_q);
+    if (ldt * cache->page_size < max_len || (total_q > 1 && (ldq < Hq * D || ldo < Hq * D)) ||
+        ldq > ((int64_t)1 << 40) || ldo > ((int64_t)1 << 40))
+        return fail(MXS_ERR_SHAPE, "attend_kv4_tree: ldt=%lld page_size=%d max_len=%lld ldq=%lld ldo=%lld",
+                    (long long)ldt, cache->page_size, (long long)max_len, (long long)ldq, (long long)ldo);
+    if (B == 0 || total_q == 0 || max_q == 0) return ok();
+    if (!q || !out || !lens || !cu || (max_len > 0 && !table)) return fail(MXS_ERR_ARG, "attend_kv4_tree: NULL pointer");
+    const size_t es = dtype == MXS_BF16 ? 2 : 4;
+    if (!aligned(q, es) || !aligned(out, es) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(cu, 4) ||
+        !aligned(mask, 8))
+        return fail(MXS_ERR_UNSUPPORTED, "attend_kv4_tree: misaligned pointer");
+    if (mxs::attend_kv4_tree_grid(dtype, B, max_q, max_len, Hq, H, D) > 0x7FFFFFFF)
+        return fail(MXS_ERR_UNSUPPORTED, "attend_kv4_tree: too many workgroups");
+    const size_t need = mxs::attend_kv4_tree_workspace(dtype, B, total_q, max_q, max_len, Hq, H, D);
+    if (need && (!ws || ws_bytes < need || !aligned(ws, 16)))
+        return fail(MXS_ERR_WORKSPACE, "attend_kv4_tree: workspace of %zu bytes, needs %zu, 16-byte aligned", ws_bytes,
+                    need);
+    return device_status(mxs::launch_attend_kv4_tree(q, dtype, ldq, *cache, table, ldt, lens, cu, mask, mask_words, B,
+                                                     total_q, max_q, max_len, Hq, scale, out, ldo, ws, stream),
+                         "attend_kv4_tree");
 }
 
 }  // extern "C"

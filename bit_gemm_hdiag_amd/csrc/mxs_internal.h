@@ -63,4 +63,28 @@ hipError_t launch_attend_kv4(const float *q, const uint8_t *kc, const uint8_t *k
                              const uint8_t *vs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float scale,
                              float *out, void *ws, hipStream_t st);
 
+// rotary positions and the paged 4-bit cache (mxs_kvcache.hip)
+void rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double low, double high,
+                      double original_length, double *freq);
+hipError_t launch_rope(const void *x, mxs_dtype dt, int64_t T, int64_t H, int64_t D, int64_t ldt, int64_t ldh,
+                       const int64_t *positions, const double *freq, int32_t rot, int32_t layout, float mscale,
+                       void *y, int64_t ldyt, int64_t ldyh, hipStream_t st);
+hipError_t launch_kv4_append(const mxs_kv4_cache &c, const void *k, const void *v, mxs_dtype dt, int64_t T,
+                             int64_t ldkt, int64_t ldkh, int64_t ldvt, int64_t ldvh, const int64_t *slots,
+                             const int64_t *positions, const double *freq, int32_t rot, int32_t layout,
+                             float mscale, hipStream_t st);
+hipError_t launch_kv4_read(const mxs_kv4_cache &c, const int64_t *slots, int64_t T, mxs_dtype dt, void *k,
+                           int64_t ldkt, int64_t ldkh, void *v, int64_t ldvt, int64_t ldvh, hipStream_t st);
+
+// attention of drafted tokens over the paged cache (mxs_tree_attention.hip)
+size_t attend_kv4_tree_workspace(mxs_dtype dt, int64_t B, int64_t total_q, int64_t max_q, int64_t max_len, int64_t Hq,
+                                 int64_t Hkv, int64_t D);
+int64_t attend_kv4_tree_grid(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
+                             int64_t D);
+hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, const mxs_kv4_cache &c,
+                                  const int32_t *table, int64_t ldt, const int32_t *lens, const int32_t *cu,
+                                  const uint64_t *mask, int64_t words, int64_t B, int64_t total_q, int64_t max_q,
+                                  int64_t max_len, int64_t Hq, float scale, void *out, int64_t ldo, void *ws,
+                                  hipStream_t st);
+
 }  // namespace mxs

@@ -1,0 +1,748 @@
+// mxs_tree_attention.hip -- attention of the drafted tokens of a batch of
+// sequences over the paged 4-bit K/V cache.
+//
+// Sequence b has len cached tokens, found through its row of the page table;
+// its n = cu[b + 1] - cu[b] query tokens are the last n of them (the drafted
+// tokens, written to the cache before the call). Query token i sees every
+// token of the context (the first len - n) and those drafted tokens whose bit
+// is set in row i of the mask (without a mask: drafted tokens j <= i):
+//   s_t = scale q[i, h] . K[t, g],   p = softmax over the seen t,
+//   out[i, h] = sum_t p_t V[t, g],   g = h / G,  G = Hq / Hkv,
+// and 0 where nothing is seen. One query token and no mask is plain decode;
+// n in the hundreds is a chunk of a prompt.
+//
+// Rows. The n G query rows that share a KV head (row i G + h % G) are cut
+// into tiles of 16 columns of the bf16 matrix instruction
+// v_mfma_f32_16x16x32_bf16, in transposed form:
+//   scores  S^T[t, r] = sum_d K[t, d] q[r, d]: A = K, lane (i, c) = token i of
+//           a 16-token tile, words c NDP .. c NDP + NDP - 1 of its row (a word
+//           is 8 dims, one 32-bit load), one word a step; B = the queries;
+//   output  O^T[d, r] += sum_t V[t, d] p[t, r]: A = V, lane (i, c) = dims i DL ..
+//           i DL + DL - 1 of tokens 4 c + r of two tiles; B = p, which the
+//           score step leaves in exactly this lane layout.
+// D is padded to 32 NDP = 64, 128 or 256 dims with zero query dims.
+//
+// Values. A 4-bit code in sign-magnitude form is the bit pattern of the
+// subnormal e4m3 number code 2^-9, so v_cvt_scalef32_pk_bf16_fp8 turns two
+// codes and the block's E8M0 scale into two exact bf16 values code 2^(s - 9)
+// (scale bytes 0 to 2, values below 2^-122, round to multiples of 2^-124);
+// the factors 2^9 go into the score scale and the final normalisation.
+// A block with byte 0xFF is NaN. bf16 queries enter as they are; fp32 queries
+// as the exact sum of three bf16 parts. The softmax weights p enter as bf16
+// parts too: three for fp32 (exact), two for bf16 (an error of 2^-17 of each
+// p; one part, 2^-9, would be as large as the rounding of the bf16 output).
+// Maxima, sums and outputs are fp32.
+#include <cmath>
+
+#include "mxs_device.h"
+#include "mxs_internal.h"
+
+namespace mxs {
+
+namespace {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4;            // waves of a workgroup; they share its tokens
+constexpr int kNTL = 4;              // 16-token tiles of a wave's step
+constexpr int kStep = 16 * kNTL;     // tokens of a wave's step (one bit each in a 64-bit mask)
+
+struct TreeArgs {
+    const void *q;
+    int64_t ldq;                     // elements between query tokens (heads D apart)
+    const uint8_t *kc, *ks, *vc, *vs;
+    int64_t pages;
+    const int32_t *table;
+    int64_t ldt;
+    const int32_t *lens, *cu;
+    const uint64_t *mask;
+    int words;
+    int B, Hq, Hkv, G, D;
+    int total_q, max_q, max_len, ps;
+    uint32_t pmul, pshift;           // t / ps
+    float scale2;                    // |scale| log2(e) 2^9
+    bool negate;                     // scale < 0: queries enter negated
+    int nrt, splits, chunk;
+    void *out;
+    int64_t ldo;
+    float *po, *pml;                 // [row, split, D], [row, split, (m, l)]
+};
+
+// t / ps for 0 <= t < 2^31: pmul = ceil(2^(31 + l) / ps), l = ceil(log2 ps)
+__device__ __forceinline__ int page_of(const TreeArgs &a, int t) {
+    return a.ps == 1 ? t : (int)(__umulhi((uint32_t)t, a.pmul) >> a.pshift);
+}
+
+// four codes, one in the low nibble of each byte -> their e4m3 bytes
+__device__ __forceinline__ uint32_t e4m3_codes(uint32_t x) {
+    const uint32_t s = x & 0x08080808u, m = s >> 3;
+    return (((x & 0x07070707u) ^ (s - m)) + m) | (s << 4);
+}
+
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+template <bool HI>
+__device__ __forceinline__ uint32_t cvt2(uint32_t bytes, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, scale, HI));
+}
+
+// A word's 8 values, in the dim order 0 2 4 6 1 3 5 7
+__device__ __forceinline__ bf8 word_values(uint32_t w, float scale) {
+    const uint32_t e = e4m3_codes(w & 0x0F0F0F0Fu), o = e4m3_codes((w >> 4) & 0x0F0F0F0Fu);
+    const u4 r = {cvt2<false>(e, scale), cvt2<true>(e, scale), cvt2<false>(o, scale), cvt2<true>(o, scale)};
+    return __builtin_bit_cast(bf8, r);
+}
+__device__ __forceinline__ constexpr int word_dim(int s) { return s < 4 ? 2 * s : 2 * (s - 4) + 1; }
+
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// x as the sum of N bf16 parts, each the nearest to what the earlier ones leave
+template <int N>
+__device__ __forceinline__ void split_bf16(float x, __bf16 p[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        p[i] = (__bf16)x;
+        x -= (float)p[i];
+    }
+}
+
+// max over the four lanes c = 0..3 of a column
+__device__ __forceinline__ float col_max(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const float y = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const uint32_t v = __float_as_uint(y);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float col_sum(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const float y = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const uint32_t v = __float_as_uint(y);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// One workgroup's place in the batch
+struct Place {
+    int b, g, rt, split;             // sequence, KV head, row tile, token range
+    int len, ctx, n, q0;             // cached tokens, context, query tokens, first query token
+    int t0, t1;                      // tokens of the workgroup
+};
+
+// Workgroups are dealt to the 8 XCDs in turn. The heads and row tiles of one
+// (token range, sequence) go to one XCD: its row tiles read the same cache
+// rows, and neighbouring heads share 128-byte lines of them.
+__device__ __forceinline__ bool find_place(const TreeArgs &a, Place &p) {
+    const uint32_t units = (uint32_t)a.Hkv * a.nrt, id = blockIdx.x;
+    const uint32_t k = id >> 3, grp = (k / units) * 8 + (id & 7), unit = k % units;
+    if (grp >= (uint32_t)a.B * (uint32_t)a.splits) return false;
+    p.b = (int)(grp / (uint32_t)a.splits);
+    p.split = (int)(grp % (uint32_t)a.splits);
+    p.g = (int)(unit / (uint32_t)a.nrt);
+    p.rt = (int)(unit % (uint32_t)a.nrt);
+    int64_t len = a.lens[p.b];
+    len = len < 0 ? 0 : (len > a.max_len ? a.max_len : len);
+    int q0 = a.cu[p.b], q1 = a.cu[p.b + 1];
+    q0 = q0 < 0 ? 0 : (q0 > a.total_q ? a.total_q : q0);
+    q1 = q1 < q0 ? q0 : (q1 > a.total_q ? a.total_q : q1);
+    p.len = (int)len;
+    p.q0 = q0;
+    p.n = q1 - q0 > a.max_q ? a.max_q : q1 - q0;
+    p.ctx = p.len > p.n ? p.len - p.n : 0;
+    p.t0 = p.split * a.chunk;
+    p.t1 = p.len - p.t0 > a.chunk ? p.t0 + a.chunk : p.len;
+    return p.split == 0 || p.t0 < p.len;
+}
+
+// Bits of drafted tokens 64 k .. 64 k + 63 that query token i sees
+__device__ __forceinline__ uint64_t mask_word(const TreeArgs &a, const Place &p, int i, int k) {
+    if (a.mask) return k < a.words ? a.mask[(int64_t)(p.q0 + i) * a.words + k] : 0ull;
+    const int d = i - 64 * k;
+    return d >= 63 ? ~0ull : (d < 0 ? 0ull : (2ull << d) - 1);
+}
+
+// Bits of tokens lt .. lt + 63 that query token i sees
+__device__ __forceinline__ uint64_t mask_window(const TreeArgs &a, const Place &p, int i, int lt) {
+    const int j = lt - p.ctx;
+    if (j <= -64) return ~0ull;
+    if (j < 0) return (mask_word(a, p, i, 0) << -j) | ((1ull << -j) - 1);
+    const int k = j >> 6, s = j & 63;
+    uint64_t w = mask_word(a, p, i, k) >> s;
+    if (s) w |= mask_word(a, p, i, k + 1) << (64 - s);
+    return w;
+}
+
+// Query rows of a wave as B operands: lane (r, c), step b holds the dims of
+// word c NDP + b of row r (zero past the rows and past D)
+template <int NDP, int CT, int PARTS>
+__device__ __forceinline__ void load_queries(const TreeArgs &a, const Place &p, int row0, int lane,
+                                             bf8 qf[CT][NDP][PARTS]) {
+    const int r = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        const int row = row0 + 16 * t + r;
+        const bool on = row < p.n * a.G;
+        const int i = on ? row / a.G : 0, h = on ? p.g * a.G + row - i * a.G : 0;
+        const int64_t at = (int64_t)(on ? p.q0 + i : 0) * a.ldq + (int64_t)h * a.D;
+#pragma unroll
+        for (int b = 0; b < NDP; ++b) {
+            const int d0 = 8 * (c * NDP + b);
+            const bool in = on && d0 < a.D;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int64_t e = at + (in ? d0 + word_dim(s) : 0);
+                float x = 0.f;
+                if (in) x = PARTS == 1 ? bf16_bits_to_f32(static_cast<const uint16_t *>(a.q)[e])
+                                       : static_cast<const float *>(a.q)[e];
+                if (a.negate) x = -x;
+                __bf16 part[PARTS];
+                split_bf16<PARTS>(x, part);
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k) qf[t][b][k][s] = part[k];
+            }
+        }
+    }
+}
+
+// Raw codes and scale bytes of a wave's step, as one lane loads them
+template <int NDP>
+struct Raw {
+    static constexpr int KB = NDP == 8 ? 2 : 1;      // blocks a lane's K words touch
+    static constexpr int VW = NDP == 8 ? 2 : 1;      // words a lane's V dims touch
+    uint32_t k[kNTL][NDP], kb[kNTL][KB];
+    uint32_t v[kNTL][4][VW], vb[kNTL][4];
+};
+
+// Byte offsets of a lane inside a cache row; dims past D fall back to the
+// row's first block (their query dims are zero, their outputs not stored)
+template <int NDP>
+struct LaneAt {
+    uint32_t k[Raw<NDP>::KB], kb[Raw<NDP>::KB], v, vb;
+    __device__ __forceinline__ LaneAt(int lane, int D) {
+        const int i = lane & 15, c = lane >> 4;
+#pragma unroll
+        for (int b = 0; b < Raw<NDP>::KB; ++b) {
+            const int w = c * NDP + 4 * b;                           // first word
+            k[b] = 8 * w < D ? 4 * w : 0;
+            kb[b] = 8 * w < D ? w >> 2 : 0;
+        }
+        const int d = i * 2 * NDP;                                   // first V dim
+        v = d < D ? d / 2 : 0;
+        vb = d < D ? d >> 5 : 0;
+    }
+};
+
+template <int NDP>
+__device__ __forceinline__ void load_k(Raw<NDP> &x, const TreeArgs &a, const LaneAt<NDP> &at, const uint8_t *kc,
+                                       const uint8_t *ks, const int *rows, int lane) {
+    const int i = lane & 15;
+    const uint32_t cs = (uint32_t)a.Hkv * (a.D / 2), ss = (uint32_t)a.Hkv * (a.D / 32);
+#pragma unroll
+    for (int u = 0; u < kNTL; ++u) {
+        const uint64_t r = (uint32_t)max(rows[16 * u + i], 0);
+        const uint8_t *p = kc + r * cs;
+        if constexpr (NDP == 2) {
+            const u2 w = *reinterpret_cast<const u2 *>(p + at.k[0]);
+            x.k[u][0] = w[0];
+            x.k[u][1] = w[1];
+        } else {
+#pragma unroll
+            for (int b = 0; b < Raw<NDP>::KB; ++b) {
+                const u4 w = *reinterpret_cast<const u4 *>(p + at.k[b]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x.k[u][4 * b + k] = w[k];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < Raw<NDP>::KB; ++b) x.kb[u][b] = ks[r * ss + at.kb[b]];
+    }
+}
+
+template <int NDP>
+__device__ __forceinline__ void load_v(Raw<NDP> &x, const TreeArgs &a, const LaneAt<NDP> &at, const uint8_t *vc,
+                                       const uint8_t *vs, const int *rows, int lane) {
+    const int c = lane >> 4;
+    const uint32_t cs = (uint32_t)a.Hkv * (a.D / 2), ss = (uint32_t)a.Hkv * (a.D / 32);
+#pragma unroll
+    for (int u = 0; u < kNTL; ++u)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint64_t r = (uint32_t)max(rows[16 * u + 4 * c + s], 0);
+            const uint8_t *p = vc + r * cs + at.v;
+            if constexpr (NDP == 2) {
+                x.v[u][s][0] = *reinterpret_cast<const uint16_t *>(p);
+            } else if constexpr (NDP == 4) {
+                x.v[u][s][0] = *reinterpret_cast<const uint32_t *>(p);
+            } else {
+                const u2 w = *reinterpret_cast<const u2 *>(p);
+                x.v[u][s][0] = w[0];
+                x.v[u][s][1] = w[1];
+            }
+            x.vb[u][s] = vs[r * ss + at.vb];
+        }
+}
+
+// Running state of a wave: columns r of its CT tiles. m is the reference the
+// exponents are taken from (raw score units), l this lane's share of the sum.
+template <int NDP, int CT>
+struct State {
+    f4 acc[CT][2 * NDP];
+    float m[CT], l[CT];
+};
+
+// p of one column's scores: with `seen` bits, else all seen. The reference m
+// moves only when a score exceeds it by more than 2^6 (in the exponent), so
+// most steps leave the accumulators alone; p stays below 2^6.
+template <int NDP, int CT, bool PART, bool EXACT>
+__device__ __forceinline__ void soften(State<NDP, CT> &st, f4 sc[CT][kNTL], const uint64_t seen[CT], float scale2,
+                                       int c) {
+    float top[CT];
+    bool grow = false;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kNTL; ++u)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (PART && !((seen[t] >> (16 * u + 4 * c + s)) & 1)) sc[t][u][s] = -INFINITY;
+                x = fmaxf(x, sc[t][u][s]);
+            }
+        top[t] = col_max(x);
+        grow |= (top[t] - st.m[t]) * scale2 > 6.f || (st.m[t] == -INFINITY && top[t] > -INFINITY);
+    }
+    if (__ballot(grow)) {
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            const float m = fmaxf(st.m[t], top[t]);
+            const float f = st.m[t] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.m[t] - m) * scale2);
+            st.m[t] = m;
+            st.l[t] *= f;
+#pragma unroll
+            for (int n = 0; n < 2 * NDP; ++n) st.acc[t][n] *= f;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        // fp32: the difference first, so that the product's rounding scales with
+        // the exponent and not with the score; bf16: one operation instead of two
+        const float mr = st.m[t] == -INFINITY ? 0.f : st.m[t], ms = mr * scale2;
+        float l = 0.f;
+#pragma unroll
+        for (int u = 0; u < kNTL; ++u)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float p = __builtin_amdgcn_exp2f(EXACT ? (sc[t][u][s] - mr) * scale2
+                                                       : __builtin_fmaf(sc[t][u][s], scale2, -ms));
+                if (PART && !((seen[t] >> (16 * u + 4 * c + s)) & 1)) p = 0.f;
+                sc[t][u][s] = p;
+                l += p;
+            }
+        st.l[t] += l;
+    }
+}
+
+// The 2 NDP V operands of tokens 4 c + s of tiles u0, u0 + 1 (tile n = dim
+// i DL + n of lane (i, c))
+template <int NDP>
+__device__ __forceinline__ void v_operands(const uint32_t v[2][4][Raw<NDP>::VW], const uint32_t vb[2][4],
+                                           bf8 out[2 * NDP]) {
+    uint32_t o[2 * NDP][4];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+#pragma unroll
+        for (int w = 0; w < Raw<NDP>::VW; ++w) {
+            uint32_t x[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t word = v[j >> 2][(j & 3) + h][w];
+                const float s = scale_of(vb[j >> 2][(j & 3) + h]);
+                const uint32_t e = e4m3_codes(word & 0x0F0F0F0Fu), d = e4m3_codes((word >> 4) & 0x0F0F0F0Fu);
+                x[h][0] = cvt2<false>(e, s);                          // dims 0, 2
+                x[h][1] = cvt2<false>(d, s);                          // dims 1, 3
+                if constexpr (NDP != 2) {
+                    x[h][2] = cvt2<true>(e, s);                       // dims 4, 6
+                    x[h][3] = cvt2<true>(d, s);                       // dims 5, 7
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < (NDP == 2 ? 2 : 4); ++k) {
+                const int dim = 8 * w + (k >> 1) * 4 + (k & 1);
+                o[dim][j >> 1] = __builtin_amdgcn_perm(x[1][k], x[0][k], 0x05040100u);
+                o[dim + 2][j >> 1] = __builtin_amdgcn_perm(x[1][k], x[0][k], 0x07060302u);
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 2 * NDP; ++n) out[n] = __builtin_bit_cast(bf8, u4{o[n][0], o[n][1], o[n][2], o[n][3]});
+}
+
+// B operands of p for tiles u0, u0 + 1
+template <int PP>
+__device__ __forceinline__ void p_operands(const f4 &p0, const f4 &p1, bf8 out[PP]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        __bf16 part[PP];
+        split_bf16<PP>(j < 4 ? p0[j & 3] : p1[j & 3], part);
+#pragma unroll
+        for (int k = 0; k < PP; ++k) out[k][j] = part[k];
+    }
+}
+
+// Takes the part of V whose blocks are NaN (byte 0xFF) out of the matrix
+// product of a step that some rows do not see whole, where 0 times NaN would
+// reach rows that do not see the token, and gives the NaN to the rows that do.
+template <int NDP, int CT>
+__device__ __forceinline__ void take_out_nan(State<NDP, CT> &st, uint32_t vb[kNTL][4], const uint64_t seen[CT],
+                                             int c) {
+#pragma unroll
+    for (int u = 0; u < kNTL; ++u)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint64_t bad = __ballot(vb[u][s] == 0xFFu);
+            if (!bad) continue;
+            if (vb[u][s] == 0xFFu) vb[u][s] = 0;
+            for (int k = 0; k < 4; ++k) {                             // token 16 u + 4 k + s
+                const uint32_t lanes = (uint32_t)(bad >> (16 * k)) & 0xFFFFu;
+#pragma unroll
+                for (int t = 0; t < CT; ++t) {
+                    if (!((seen[t] >> (16 * u + 4 * k + s)) & 1)) continue;
+#pragma unroll
+                    for (int rr = 0; rr < 4; ++rr)
+                        if ((lanes >> (4 * c + rr)) & 1) {
+#pragma unroll
+                            for (int n = 0; n < 2 * NDP; ++n) st.acc[t][n][rr] = NAN;
+                        }
+                }
+            }
+        }
+}
+
+// Outputs of one column: lane (r, c) holds dims (4 c + rr) DL + n of row r.
+// One token range: normalised, rounded once, to `out` (0 where nothing was
+// seen); several: (m, l) and the unnormalised sums for k_tree_join.
+template <int NDP, int CT, int PARTS>
+__device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, const State<NDP, CT> &st, int row0,
+                                           int lane, bool whole) {
+    constexpr int DL = 2 * NDP;
+    const int r = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        const int row = row0 + 16 * t + r;
+        if (row >= p.n * a.G) continue;
+        const int i = row / a.G, h = p.g * a.G + row - i * a.G;
+        if (whole) {
+            const float f = st.m[t] == -INFINITY ? 0.f : 512.f / st.l[t];
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr) {
+                const int d0 = (4 * c + rr) * DL;
+                if (d0 >= a.D) continue;
+                const int64_t e = (int64_t)(p.q0 + i) * a.ldo + (int64_t)h * a.D + d0;
+#pragma unroll
+                for (int n = 0; n < DL; ++n) {
+                    const float x = st.acc[t][n][rr] * f;
+                    if constexpr (PARTS == 1) static_cast<__bf16 *>(a.out)[e + n] = (__bf16)x;
+                    else static_cast<float *>(a.out)[e + n] = x;
+                }
+            }
+        } else {
+            const int64_t at = ((int64_t)(p.q0 + i) * a.Hq + h) * a.splits + p.split;
+            if (c == 0) {
+                a.pml[2 * at] = st.m[t] == -INFINITY ? -INFINITY : st.m[t] * a.scale2;
+                a.pml[2 * at + 1] = st.l[t];
+            }
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr) {
+                const int d0 = (4 * c + rr) * DL;
+                if (d0 >= a.D) continue;
+                float *o = a.po + at * a.D + d0;
+#pragma unroll
+                for (int n = 0; n < DL; ++n) o[n] = st.acc[t][n][rr];
+            }
+        }
+    }
+}
+
+// Few rows: the waves of a workgroup take its row tile's 16 CT rows and turns
+// of 64 tokens, each dequantising its own tokens in registers; their states
+// are merged in LDS in wave order (2 and 3 into 0 and 1, then 1 into 0).
+template <int NDP, int CT, int PARTS>
+__global__ __launch_bounds__(64 * kWaves) void k_tree_rows(TreeArgs a) {
+    constexpr int PP = PARTS == 1 ? 2 : 3, NT = 2 * NDP;
+    __shared__ __attribute__((aligned(16))) float ex[2][CT * (NT + 1)][64][4];
+    __shared__ __attribute__((aligned(16))) int rowbuf[kWaves][2][kStep];
+    Place p;
+    if (!find_place(a, p)) return;
+    const int lane = threadIdx.x & 63, c = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row0 = p.rt * 16 * CT;
+    if (row0 >= p.n * a.G) return;
+
+    State<NDP, CT> st;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        st.m[t] = -INFINITY;
+        st.l[t] = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
+    }
+    const LaneAt<NDP> at(lane, a.D);
+    const uint8_t *kc = a.kc + p.g * (a.D / 2), *vc = a.vc + p.g * (a.D / 2);
+    const uint8_t *ks = a.ks + p.g * (a.D / 32), *vs = a.vs + p.g * (a.D / 32);
+    const int32_t *table = a.table + (int64_t)p.b * a.ldt;
+
+    // pool row of token lt + lane (-1: past the range, or no valid page)
+    auto page_at = [&](int lt) {
+        const int t = lt + lane;
+        return t < p.t1 ? table[page_of(a, t)] : -1;
+    };
+    auto row_at = [&](int lt, int page) {
+        const int t = lt + lane;
+        return (uint32_t)page < (uint64_t)a.pages ? page * a.ps + (t - page_of(a, t) * a.ps) : -1;
+    };
+
+    int lt = p.t0 + w * kStep;
+    if (lt < p.t1) {
+        Raw<NDP> x;
+        int row = row_at(lt, page_at(lt));
+        uint64_t valid = __ballot(row >= 0);
+        rowbuf[w][0][lane] = row;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        load_k<NDP>(x, a, at, kc, ks, rowbuf[w][0], lane);
+        load_v<NDP>(x, a, at, vc, vs, rowbuf[w][0], lane);
+        int page = page_at(lt + kWaves * kStep);
+        bf8 qf[CT][NDP][PARTS];
+        load_queries<NDP, CT, PARTS>(a, p, row0, lane, qf);
+        int iq[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            const int rw = row0 + 16 * t + (lane & 15);
+            iq[t] = rw < p.n * a.G ? rw / a.G : 0;
+        }
+
+        int buf = 1;
+        for (; lt < p.t1; lt += kWaves * kStep, buf ^= 1) {
+            const int next = lt + kWaves * kStep;
+            row = row_at(next, page);
+            rowbuf[w][buf][lane] = row;
+            page = page_at(next + kWaves * kStep);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+
+            f4 sc[CT][kNTL];
+#pragma unroll
+            for (int u = 0; u < kNTL; ++u) {
+#pragma unroll
+                for (int t = 0; t < CT; ++t) sc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int b = 0; b < NDP; ++b) {
+                    const bf8 kv = word_values(x.k[u][b], scale_of(x.kb[u][Raw<NDP>::KB == 2 ? b >> 2 : 0]));
+#pragma unroll
+                    for (int t = 0; t < CT; ++t)
+#pragma unroll
+                        for (int k = 0; k < PARTS; ++k)
+                            sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][k], sc[t][u], 0, 0, 0);
+                }
+            }
+            load_k<NDP>(x, a, at, kc, ks, rowbuf[w][buf], lane);
+            __builtin_amdgcn_sched_barrier(0);
+
+            uint64_t seen[CT];
+            const bool part = valid != ~0ull || lt + kStep > p.ctx;
+            if (part) {
+#pragma unroll
+                for (int t = 0; t < CT; ++t) seen[t] = valid & mask_window(a, p, iq[t], lt);
+                soften<NDP, CT, true, PARTS == 3>(st, sc, seen, a.scale2, c);
+#pragma unroll
+                for (int u = 0; u < kNTL; ++u)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) x.vb[u][s] = (valid >> (16 * u + 4 * c + s)) & 1 ? x.vb[u][s] : 0u;
+                take_out_nan<NDP, CT>(st, x.vb, seen, c);
+            } else {
+                soften<NDP, CT, false, PARTS == 3>(st, sc, seen, a.scale2, c);
+            }
+#pragma unroll
+            for (int u = 0; u < kNTL; u += 2) {
+                bf8 vf[NT];
+                v_operands<NDP>(&x.v[u], &x.vb[u], vf);
+#pragma unroll
+                for (int t = 0; t < CT; ++t) {
+                    bf8 pf[PP];
+                    p_operands<PP>(sc[t][u], sc[t][u + 1], pf);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < PP; ++k)
+                            st.acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[n], pf[k], st.acc[t][n], 0, 0, 0);
+                }
+            }
+            load_v<NDP>(x, a, at, vc, vs, rowbuf[w][buf], lane);
+            valid = __ballot(row >= 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < CT; ++t) st.l[t] = col_sum(st.l[t]);
+
+    // merge: M = max m, sums and outputs scaled by 2^((m - M) scale2)
+    auto give = [&](int slot) {
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) *reinterpret_cast<f4 *>(ex[slot][t * (NT + 1) + n][lane]) = st.acc[t][n];
+            ex[slot][t * (NT + 1) + NT][lane][0] = st.m[t];
+            ex[slot][t * (NT + 1) + NT][lane][1] = st.l[t];
+        }
+    };
+    auto take = [&](int slot) {
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            const float m = ex[slot][t * (NT + 1) + NT][lane][0], l = ex[slot][t * (NT + 1) + NT][lane][1];
+            const float M = fmaxf(st.m[t], m);
+            const float f0 = st.m[t] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.m[t] - M) * a.scale2);
+            const float f1 = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - M) * a.scale2);
+            st.m[t] = M;
+            st.l[t] = st.l[t] * f0 + l * f1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const f4 o = *reinterpret_cast<const f4 *>(ex[slot][t * (NT + 1) + n][lane]);
+                st.acc[t][n] = st.acc[t][n] * f0 + o * f1;
+            }
+        }
+    };
+    if (w >= 2) give(w - 2);
+    __syncthreads();
+    if (w < 2) take(w);
+    __syncthreads();
+    if (w == 1) give(0);
+    __syncthreads();
+    if (w == 0) {
+        take(0);
+        store_rows<NDP, CT, PARTS>(a, p, st, row0, lane, p.len <= a.chunk);
+    }
+}
+
+// Rows of sequences of several token ranges: out = sum_s O_s 2^(m_s - M) 2^9 /
+// sum_s l_s 2^(m_s - M), ranges in order. One wave a row, at most 64 ranges.
+template <typename T>
+__global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
+    const int b = blockIdx.y, lane = threadIdx.x & 63;
+    const int rw = blockIdx.x * 4 + (threadIdx.x >> 6);             // (query token, head)
+    int len = a.lens[b];
+    len = len > a.max_len ? a.max_len : len;
+    if (len <= a.chunk) return;
+    int q0 = a.cu[b], q1 = a.cu[b + 1];
+    q0 = q0 < 0 ? 0 : (q0 > a.total_q ? a.total_q : q0);
+    q1 = q1 < q0 ? q0 : (q1 > a.total_q ? a.total_q : q1);
+    const int n = q1 - q0 > a.max_q ? a.max_q : q1 - q0;
+    if (rw >= n * a.Hq) return;
+    const int ns = (len + a.chunk - 1) / a.chunk;
+    const int64_t at = ((int64_t)q0 * a.Hq + rw) * a.splits;
+    float m = -INFINITY, l = 0.f;
+    if (lane < ns) {
+        m = a.pml[2 * (at + lane)];
+        l = a.pml[2 * (at + lane) + 1];
+    }
+    float M = m, L;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - M);
+    L = l * f;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) L += __shfl_xor(L, o);
+    const float norm = M == -INFINITY ? 0.f : 512.f / L;
+    const int64_t token = (int64_t)q0 + rw / a.Hq;
+    T *out = static_cast<T *>(a.out) + token * a.ldo + (int64_t)(rw % a.Hq) * a.D;
+    for (int d = 4 * lane; d < a.D; d += 256) {
+        f4 o = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < ns; ++s) {
+            const float fs = __shfl(f, s);
+            o += *reinterpret_cast<const f4 *>(a.po + (at + s) * a.D + d) * fs;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[d + k] = (T)(o[k] * norm);
+    }
+}
+
+struct TreePlan {
+    int NDP, CT, nrt, splits, chunk;
+};
+
+// Row tiles of 16 CT rows, and token ranges: as many as give about two
+// workgroups to each of the 256 CUs, at least a step a wave, at most 64.
+TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv, int64_t D) {
+    TreePlan p;
+    p.NDP = D <= 64 ? 2 : (D <= 128 ? 4 : 8);
+    const int64_t rows = max_q * (Hq / Hkv);
+    p.CT = dt == MXS_BF16 && p.NDP <= 4 && rows > 16 ? 2 : 1;
+    p.nrt = (int)ceil_div(rows, (int64_t)16 * p.CT);
+    const int64_t units = B * Hkv * p.nrt, turn = kWaves * kStep;
+    int64_t s = ceil_div((int64_t)512, units);
+    const int64_t most = ceil_div(max_len > 0 ? max_len : 1, turn);
+    s = s > 64 ? 64 : s;
+    s = s > most ? most : s;
+    p.chunk = (int)(ceil_div(ceil_div(max_len > 0 ? max_len : 1, s), turn) * turn);
+    p.splits = (int)ceil_div(max_len > 0 ? max_len : 1, (int64_t)p.chunk);
+    return p;
+}
+
+template <int NDP, int CT, int PARTS>
+hipError_t rows_go(const TreeArgs &a, unsigned grid, hipStream_t st) {
+    hipLaunchKernelGGL((k_tree_rows<NDP, CT, PARTS>), dim3(grid), dim3(64 * kWaves), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attend_kv4_tree_workspace(mxs_dtype dt, int64_t B, int64_t total_q, int64_t max_q, int64_t max_len, int64_t Hq,
+                                 int64_t Hkv, int64_t D) {
+    const TreePlan p = tree_plan(dt, B, max_q, max_len, Hq, Hkv, D);
+    return p.splits > 1 ? (size_t)(total_q * Hq * p.splits * (D + 2)) * sizeof(float) : 0;
+}
+
+int64_t attend_kv4_tree_grid(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
+                             int64_t D) {
+    const TreePlan p = tree_plan(dt, B, max_q, max_len, Hq, Hkv, D);
+    return ceil_div(B * p.splits, (int64_t)8) * 8 * Hkv * p.nrt;
+}
+
+hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, const mxs_kv4_cache &c,
+                                  const int32_t *table, int64_t ldt, const int32_t *lens, const int32_t *cu,
+                                  const uint64_t *mask, int64_t words, int64_t B, int64_t total_q, int64_t max_q,
+                                  int64_t max_len, int64_t Hq, float scale, void *out, int64_t ldo, void *ws,
+                                  hipStream_t st) {
+    const TreePlan p = tree_plan(dt, B, max_q, max_len, Hq, c.H, c.D);
+    TreeArgs a{};
+    a.q = q; a.ldq = ldq; a.kc = c.kc; a.ks = c.ks; a.vc = c.vc; a.vs = c.vs; a.pages = c.pages;
+    a.table = table; a.ldt = ldt; a.lens = lens; a.cu = cu; a.mask = mask; a.words = (int)words;
+    a.B = (int)B; a.Hq = (int)Hq; a.Hkv = c.H; a.G = (int)(Hq / c.H); a.D = c.D;
+    a.total_q = (int)total_q; a.max_q = (int)max_q; a.max_len = (int)max_len; a.ps = c.page_size;
+    int l = 0;
+    while (((int64_t)1 << l) < c.page_size) ++l;
+    if (l > 0) {
+        a.pmul = (uint32_t)((((uint64_t)1 << (31 + l)) + c.page_size - 1) / (uint64_t)c.page_size);
+        a.pshift = l - 1;
+    }
+    a.scale2 = (float)(fabs((double)scale) * 1.4426950408889634074 * 512.0);
+    a.negate = std::signbit(scale);
+    a.nrt = p.nrt; a.splits = p.splits; a.chunk = p.chunk;
+    a.out = out; a.ldo = ldo;
+    a.po = static_cast<float *>(ws);
+    a.pml = a.po + total_q * Hq * p.splits * c.D;
+    const unsigned grid = (unsigned)attend_kv4_tree_grid(dt, B, max_q, max_len, Hq, c.H, c.D);
+    hipError_t e;
+    const bool f32 = dt == MXS_F32;
+    if (p.NDP == 2) e = f32 ? rows_go<2, 1, 3>(a, grid, st) : (p.CT == 2 ? rows_go<2, 2, 1>(a, grid, st) : rows_go<2, 1, 1>(a, grid, st));
+    else if (p.NDP == 4) e = f32 ? rows_go<4, 1, 3>(a, grid, st) : (p.CT == 2 ? rows_go<4, 2, 1>(a, grid, st) : rows_go<4, 1, 1>(a, grid, st));
+    else e = f32 ? rows_go<8, 1, 3>(a, grid, st) : rows_go<8, 1, 1>(a, grid, st);
+    if (e != hipSuccess || p.splits == 1) return e;
+    const dim3 jg((unsigned)ceil_div(max_q * Hq, (int64_t)4), (unsigned)B);
+    if (f32) hipLaunchKernelGGL((k_tree_join<float>), jg, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_tree_join<__bf16>), jg, dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace mxs

@@ -418,6 +418,153 @@ mxs_status mxs_attend_kv4(const float *q, const uint8_t *kc, const uint8_t *ks, 
                           const uint8_t *vs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, float scale,
                           float *out, void *ws, size_t ws_bytes, hipStream_t stream);
 
+/*
+ * Serving on the 4-bit cache: rotary positions, the cache written and read in
+ * place in pages, and the attention of drafted tokens of a batch over it
+ * ([NL] §4, W4A4KV4: the pages name the 4-bit K/V cache; how a server fills
+ * and reads it is this library's reading).
+ */
+
+/*
+ * A pool of `pages` pages of page_size tokens each. Slot s = page * page_size
+ * + offset is one token: codes [slot, H, D/2] and scale bytes [slot, H, D/32]
+ * for keys (kc, ks) and values (vc, vs), the layout of mxs_quantize_kv (whose
+ * output for T tokens is a pool of one page of T tokens, or of any pages that
+ * divide T). Device memory owned by the caller, codes 16-byte aligned, at
+ * most 2^31 - 1 slots, D % 32 == 0, H D <= 524280. Host struct, read during
+ * the call.
+ */
+typedef struct mxs_kv4_cache {
+    int64_t pages;
+    int32_t page_size;
+    int32_t H, D;       /* KV heads, head dimension */
+    int32_t reserved;   /* must be 0 */
+    uint8_t *kc, *ks;
+    uint8_t *vc, *vs;
+} mxs_kv4_cache;
+
+/* Which dims form pair i of the rotated part: (i, i + rot/2), or (2 i, 2 i + 1). */
+#define MXS_ROPE_HALF  0
+#define MXS_ROPE_PAIRS 1
+
+/* How mxs_rope_frequencies stretches the angles for contexts longer than the
+ * trained one. */
+#define MXS_ROPE_UNSCALED 0   /* f_i = base^(-2 i / rot)                               */
+#define MXS_ROPE_LINEAR   1   /* f_i / factor                                          */
+#define MXS_ROPE_NTK      2   /* base replaced by base * factor^(rot / (rot - 2))      */
+#define MXS_ROPE_PARTS    3   /* by wavelength: with r_i = original_length f_i / 2 pi  */
+                              /* turns in the trained context and                      */
+                              /* k = clamp((r_i - low) / (high - low), 0, 1):          */
+                              /* f_i (k + (1 - k) / factor)                            */
+
+/*
+ * Angular frequencies of rotary positions, radians per position, rot/2 values
+ * in fp64. low, high and original_length are read for MXS_ROPE_PARTS only.
+ * Host-only and pure: freq is host memory; the caller copies it to the device
+ * once.
+ * Errors: MXS_ERR_ARG (freq NULL, unknown scaling, base, factor or
+ * original_length not positive and finite, high <= low), MXS_ERR_SHAPE (rot < 2
+ * or odd; rot < 4 with MXS_ROPE_NTK).
+ */
+mxs_status mxs_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double low, double high,
+                                double original_length, double *freq);
+
+/*
+ * Rotary positions: y = x with the first `rot` dims of every head turned,
+ * pair i of token t by the angle positions[t] freq[i], and multiplied by
+ * mscale (the attention factor of some long-context scalings; 1 otherwise);
+ * the other D - rot dims are copied. Angles in fp64, reduced before they are
+ * rounded; products and sums in fp32, one rounding to `dtype`. The transposed
+ * map (the gradient with respect to x, or undoing a turn at mscale 1) is the
+ * same call at the negated positions.
+ * x, y: [T, H, D] device arrays of `dtype` with element strides ldt (tokens)
+ * and ldh (heads) and adjacent dims; y may be x (same strides); they must not
+ * overlap otherwise. positions: [T] int64 device (any sign); freq: [rot/2]
+ * fp64 device. 16-byte aligned rows whose halves are whole 16-byte vectors
+ * are faster. D <= 4096, H <= 65535, T <= 2^31 - 1. T = 0 or H = 0 is a no-op.
+ * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE (sizes negative, rot odd, < 2 or > D,
+ * strides < D, rows of y that overlap, y == x with other strides),
+ * MXS_ERR_UNSUPPORTED, MXS_ERR_DEVICE.
+ */
+mxs_status mxs_rope(const void *x, mxs_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t ldt, int64_t ldh,
+                    const int64_t *positions, const double *freq, int32_t rot, int32_t layout, float mscale,
+                    void *y, int64_t ldyt, int64_t ldyh, hipStream_t stream);
+
+/*
+ * K/V quantised into the cache as they are written: token t's keys and values
+ * go to slot slots[t] (int64; tokens whose slot is negative or past the pool
+ * are skipped, so padding takes -1), by the rule of mxs_quantize_kv. With
+ * positions (and freq, rot, layout, mscale as in mxs_rope) the keys are
+ * rotated first, in fp64 with no rounding before the quantisation; without
+ * (NULL) they are stored as given and freq, rot, layout and mscale are not
+ * read. A call's slots differ from one another; a slot named twice holds an
+ * unspecified mix of the two tokens, other slots are unaffected. Slots not
+ * named keep their contents.
+ * k, v: [T, H, D] device arrays of `dtype` with element strides as in
+ * mxs_rope. T = 0 is a no-op.
+ * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE (T < 0, strides < D, rot, the cache's
+ * sizes), MXS_ERR_UNSUPPORTED (alignment, sizes), MXS_ERR_DEVICE.
+ */
+mxs_status mxs_kv4_append(const mxs_kv4_cache *cache, const void *k, const void *v, mxs_dtype dtype, int64_t T,
+                          int64_t ldkt, int64_t ldkh, int64_t ldvt, int64_t ldvh, const int64_t *slots,
+                          const int64_t *positions, const double *freq, int32_t rot, int32_t layout, float mscale,
+                          hipStream_t stream);
+
+/*
+ * The cache read back: row t of k and v receives the values of slot slots[t],
+ * code * 2^(byte - 127), exact in both types (a block marked 0xFF gives NaN).
+ * Rows whose slot is negative or past the pool are left as they were. Slots
+ * may repeat. k or v may be NULL (not both): that one is not read.
+ * k, v: [T, H, D] device arrays of `dtype`, element strides as in mxs_rope,
+ * rows not overlapping. T = 0 is a no-op.
+ * Errors: as mxs_kv4_append.
+ */
+mxs_status mxs_kv4_read(const mxs_kv4_cache *cache, const int64_t *slots, int64_t T, mxs_dtype dtype, void *k,
+                        int64_t ldkt, int64_t ldkh, void *v, int64_t ldvt, int64_t ldvh, hipStream_t stream);
+
+/*
+ * Attention of drafted tokens over the cache, for a batch of B sequences.
+ * Sequence b has lens[b] cached tokens, token t in slot table[b, t / page_size]
+ * * page_size + t % page_size; its n = cu[b + 1] - cu[b] query tokens, rows
+ * cu[b] .. cu[b + 1] - 1 of q, are the last n of them (written to the cache
+ * before this call). Query token i sees all of the first lens[b] - n tokens
+ * and, of the last n, those j with bit j % 64 of mask[row, j / 64] set (bits
+ * past mask_words count as clear; a token sees itself only if its own bit is
+ * set); with mask NULL the j <= i. Over the tokens it sees, with g = h / (Hq / H),
+ *     out[row, h] = sum_t p_t V[t, g],  p = softmax_t(scale q[row, h] . K[t, g]),
+ * and 0 if it sees none. Plain decode is n = 1 with mask NULL; a chunk of a
+ * prompt is n tokens with mask NULL; a drafted tree gives every token the bits
+ * of its ancestors and itself. Tokens in no valid page (table entry negative or
+ * past the pool) are seen by no row; what an unseen token's K and V hold, NaN
+ * included, does not reach the output.
+ * fp32 queries: exact products, fp32 sums, fp32 output. bf16 queries: softmax
+ * weights to 2^-17, fp32 sums, output rounded once. Every sum has a fixed
+ * order: the result is deterministic and independent of the other sequences'
+ * contents (not of B, max_q and max_len, which choose the split). Scale bytes
+ * 0 to 2 (values below 2^-122) are read to 2^-124.
+ * q: [total_q, Hq, D] of `dtype`, ldq elements between tokens; out the same
+ * with ldo; rows of no sequence are left as they were. table: [B, ldt] int32;
+ * lens: [B] int32; cu: [B + 1] int32, ascending from 0, at most total_q; mask:
+ * [total_q, mask_words] uint64 or NULL. max_q and max_len are upper bounds of
+ * n and lens known to the host (they size the launch, so that a captured graph
+ * serves any lens up to max_len): longer ones are cut off at the bound. All
+ * device memory except the cache struct. ws: >= mxs_attend_kv4_tree_workspace
+ * bytes of device memory, 16-byte aligned, contents scratch (NULL if 0); calls
+ * that may overlap need one each. D <= 256, max_len <= 2^30 and <= ldt *
+ * page_size. total_q = 0, max_q = 0 or B = 0 is a no-op.
+ * Errors: MXS_ERR_ARG (NULL, unknown dtype, scale not finite), MXS_ERR_SHAPE
+ * (sizes, Hq % H, strides, ldt * page_size < max_len), MXS_ERR_UNSUPPORTED
+ * (D > 256, B > 65535, sizes past the grid, alignment), MXS_ERR_WORKSPACE,
+ * MXS_ERR_DEVICE.
+ */
+size_t mxs_attend_kv4_tree_workspace(mxs_dtype dtype, int64_t B, int64_t total_q, int64_t max_q, int64_t max_len,
+                                     int64_t Hq, int64_t Hkv, int64_t D);
+mxs_status mxs_attend_kv4_tree(const void *q, mxs_dtype dtype, int64_t ldq, const mxs_kv4_cache *cache,
+                               const int32_t *table, int64_t ldt, const int32_t *lens, const int32_t *cu,
+                               const uint64_t *mask, int64_t mask_words, int64_t B, int64_t total_q, int64_t max_q,
+                               int64_t max_len, int64_t Hq, float scale, void *out, int64_t ldo, void *ws,
+                               size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
