@@ -292,26 +292,38 @@ template <int NDP, int CT>
 struct State {
     f4 acc[CT][2 * NDP];
     float m[CT], l[CT];
+    uint32_t nan[CT];                // bit rr: the output's dims of register rr are NaN (see give_nan)
 };
 
-// p of one column's scores: with `seen` bits, else all seen. The reference m
-// moves only when a score exceeds it by more than 2^6 (in the exponent), so
-// most steps leave the accumulators alone; p stays below 2^6.
-template <int NDP, int CT, bool PART, bool EXACT>
-__device__ __forceinline__ void soften(State<NDP, CT> &st, f4 sc[CT][kNTL], const uint64_t seen[CT], float scale2,
-                                       int c) {
+// Scores of tokens that a column's row does not see (bit 16 u + 4 c + s clear)
+template <int CT, int NTL>
+__device__ __forceinline__ void hide(f4 sc[CT][NTL], const uint64_t seen[CT], int c) {
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        const uint64_t w = seen[t] >> (4 * c);
+#pragma unroll
+        for (int u = 0; u < NTL; ++u)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) sc[t][u][s] = (w >> (16 * u + s)) & 1 ? sc[t][u][s] : -INFINITY;
+    }
+}
+
+// Scores to weights p = 2^((s - m) scale2) (0 for hidden ones; scale2 > 0).
+// The reference m moves only when a score exceeds it by more than 2^6 (in the
+// exponent), so most steps leave the accumulators alone; p stays below 2^6.
+// EXACT (fp32): the difference first, so that the product's rounding scales
+// with the exponent and not with the score; bf16: one operation instead of two.
+template <int NDP, int CT, int NTL, bool EXACT>
+__device__ __forceinline__ void soften(State<NDP, CT> &st, f4 sc[CT][NTL], float scale2) {
     float top[CT];
     bool grow = false;
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
         float x = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < kNTL; ++u)
+        for (int u = 0; u < NTL; ++u)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (PART && !((seen[t] >> (16 * u + 4 * c + s)) & 1)) sc[t][u][s] = -INFINITY;
-                x = fmaxf(x, sc[t][u][s]);
-            }
+            for (int s = 0; s < 4; ++s) x = fmaxf(x, sc[t][u][s]);
         top[t] = col_max(x);
         grow |= (top[t] - st.m[t]) * scale2 > 6.f || (st.m[t] == -INFINITY && top[t] > -INFINITY);
     }
@@ -328,17 +340,14 @@ __device__ __forceinline__ void soften(State<NDP, CT> &st, f4 sc[CT][kNTL], cons
     }
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
-        // fp32: the difference first, so that the product's rounding scales with
-        // the exponent and not with the score; bf16: one operation instead of two
         const float mr = st.m[t] == -INFINITY ? 0.f : st.m[t], ms = mr * scale2;
         float l = 0.f;
 #pragma unroll
-        for (int u = 0; u < kNTL; ++u)
+        for (int u = 0; u < NTL; ++u)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                float p = __builtin_amdgcn_exp2f(EXACT ? (sc[t][u][s] - mr) * scale2
-                                                       : __builtin_fmaf(sc[t][u][s], scale2, -ms));
-                if (PART && !((seen[t] >> (16 * u + 4 * c + s)) & 1)) p = 0.f;
+                const float p = __builtin_amdgcn_exp2f(EXACT ? (sc[t][u][s] - mr) * scale2
+                                                             : __builtin_fmaf(sc[t][u][s], scale2, -ms));
                 sc[t][u][s] = p;
                 l += p;
             }
@@ -346,21 +355,20 @@ __device__ __forceinline__ void soften(State<NDP, CT> &st, f4 sc[CT][kNTL], cons
     }
 }
 
-// The 2 NDP V operands of tokens 4 c + s of tiles u0, u0 + 1 (tile n = dim
-// i DL + n of lane (i, c))
+// V of tokens 4 c + s of one tile, in token pairs: o[n] = dim i DL + n of
+// tokens (0, 1) and (2, 3)
 template <int NDP>
-__device__ __forceinline__ void v_operands(const uint32_t v[2][4][Raw<NDP>::VW], const uint32_t vb[2][4],
-                                           bf8 out[2 * NDP]) {
-    uint32_t o[2 * NDP][4];
+__device__ __forceinline__ void v_pairs(const uint32_t v[4][Raw<NDP>::VW], const uint32_t vb[4],
+                                        uint32_t o[2 * NDP][2]) {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
+    for (int j = 0; j < 4; j += 2) {
 #pragma unroll
         for (int w = 0; w < Raw<NDP>::VW; ++w) {
             uint32_t x[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t word = v[j >> 2][(j & 3) + h][w];
-                const float s = scale_of(vb[j >> 2][(j & 3) + h]);
+                const uint32_t word = v[j + h][w];
+                const float s = scale_of(vb[j + h]);
                 const uint32_t e = e4m3_codes(word & 0x0F0F0F0Fu), d = e4m3_codes((word >> 4) & 0x0F0F0F0Fu);
                 x[h][0] = cvt2<false>(e, s);                          // dims 0, 2
                 x[h][1] = cvt2<false>(d, s);                          // dims 1, 3
@@ -377,8 +385,16 @@ __device__ __forceinline__ void v_operands(const uint32_t v[2][4][Raw<NDP>::VW],
             }
         }
     }
+}
+// The 2 NDP V operands of two tiles (tile n = dim i DL + n of lane (i, c))
+template <int NDP>
+__device__ __forceinline__ void v_operands(const uint32_t v[2][4][Raw<NDP>::VW], const uint32_t vb[2][4],
+                                           bf8 out[2 * NDP]) {
+    uint32_t a[2 * NDP][2], b[2 * NDP][2];
+    v_pairs<NDP>(v[0], vb[0], a);
+    v_pairs<NDP>(v[1], vb[1], b);
 #pragma unroll
-    for (int n = 0; n < 2 * NDP; ++n) out[n] = __builtin_bit_cast(bf8, u4{o[n][0], o[n][1], o[n][2], o[n][3]});
+    for (int n = 0; n < 2 * NDP; ++n) out[n] = __builtin_bit_cast(bf8, u4{a[n][0], a[n][1], b[n][0], b[n][1]});
 }
 
 // B operands of p for tiles u0, u0 + 1
@@ -393,33 +409,32 @@ __device__ __forceinline__ void p_operands(const f4 &p0, const f4 &p1, bf8 out[P
     }
 }
 
-// Takes the part of V whose blocks are NaN (byte 0xFF) out of the matrix
-// product of a step that some rows do not see whole, where 0 times NaN would
-// reach rows that do not see the token, and gives the NaN to the rows that do.
+// V blocks that are NaN (byte 0xFF) would reach rows that do not see their
+// token, as 0 times NaN, where a step holds tokens that some rows do not see.
+// There such blocks leave the matrix product (their byte becomes 0; the result
+// has a bit for every lane whose byte it was), and the rows that see the token
+// note which of their dims are NaN: lanes = the 16 dim groups of token tk.
+__device__ __forceinline__ uint64_t take_nan(uint32_t &byte) {
+    const uint64_t bad = __ballot(byte == 0xFFu);
+    if (byte == 0xFFu) byte = 0;
+    return bad;
+}
 template <int NDP, int CT>
-__device__ __forceinline__ void take_out_nan(State<NDP, CT> &st, uint32_t vb[kNTL][4], const uint64_t seen[CT],
-                                             int c) {
+__device__ __forceinline__ void note_nan(State<NDP, CT> &st, uint32_t lanes, int tk, const uint64_t seen[CT], int c) {
 #pragma unroll
-    for (int u = 0; u < kNTL; ++u)
+    for (int t = 0; t < CT; ++t)
+        if ((seen[t] >> tk) & 1) st.nan[t] |= (lanes >> (4 * c)) & 15u;
+}
+template <int NDP, int CT>
+__device__ __forceinline__ void give_nan(State<NDP, CT> &st) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint64_t bad = __ballot(vb[u][s] == 0xFFu);
-            if (!bad) continue;
-            if (vb[u][s] == 0xFFu) vb[u][s] = 0;
-            for (int k = 0; k < 4; ++k) {                             // token 16 u + 4 k + s
-                const uint32_t lanes = (uint32_t)(bad >> (16 * k)) & 0xFFFFu;
+    for (int t = 0; t < CT; ++t) {
+        if (!__ballot(st.nan[t] != 0)) continue;
 #pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    if (!((seen[t] >> (16 * u + 4 * k + s)) & 1)) continue;
+        for (int rr = 0; rr < 4; ++rr)
 #pragma unroll
-                    for (int rr = 0; rr < 4; ++rr)
-                        if ((lanes >> (4 * c + rr)) & 1) {
-#pragma unroll
-                            for (int n = 0; n < 2 * NDP; ++n) st.acc[t][n][rr] = NAN;
-                        }
-                }
-            }
-        }
+            for (int n = 0; n < 2 * NDP; ++n) st.acc[t][n][rr] = (st.nan[t] >> rr) & 1 ? NAN : st.acc[t][n][rr];
+    }
 }
 
 // Outputs of one column: lane (r, c) holds dims (4 c + rr) DL + n of row r.
@@ -467,13 +482,41 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, co
     }
 }
 
+// States of two waves over the same rows, through LDS in lane order (CT (2 NDP
+// + 1) KiB): M = max m, sums and outputs scaled by 2^((m - M) scale2)
+template <int NDP, int CT>
+__device__ __forceinline__ void give_state(const State<NDP, CT> &st, float *ex, int lane) {
+    f4 *e = reinterpret_cast<f4 *>(ex) + lane;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+#pragma unroll
+        for (int n = 0; n < 2 * NDP; ++n) e[64 * (t * (2 * NDP + 1) + n)] = st.acc[t][n];
+        e[64 * (t * (2 * NDP + 1) + 2 * NDP)] = f4{st.m[t], st.l[t], 0.f, 0.f};
+    }
+}
+template <int NDP, int CT>
+__device__ __forceinline__ void take_state(State<NDP, CT> &st, const float *ex, int lane, float scale2) {
+    const f4 *e = reinterpret_cast<const f4 *>(ex) + lane;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        const f4 ml = e[64 * (t * (2 * NDP + 1) + 2 * NDP)];
+        const float m = ml[0], M = fmaxf(st.m[t], m);
+        const float f0 = st.m[t] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.m[t] - M) * scale2);
+        const float f1 = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - M) * scale2);
+        st.m[t] = M;
+        st.l[t] = st.l[t] * f0 + ml[1] * f1;
+#pragma unroll
+        for (int n = 0; n < 2 * NDP; ++n) st.acc[t][n] = st.acc[t][n] * f0 + e[64 * (t * (2 * NDP + 1) + n)] * f1;
+    }
+}
+
 // Few rows: the waves of a workgroup take its row tile's 16 CT rows and turns
 // of 64 tokens, each dequantising its own tokens in registers; their states
 // are merged in LDS in wave order (2 and 3 into 0 and 1, then 1 into 0).
 template <int NDP, int CT, int PARTS>
 __global__ __launch_bounds__(64 * kWaves) void k_tree_rows(TreeArgs a) {
     constexpr int PP = PARTS == 1 ? 2 : 3, NT = 2 * NDP;
-    __shared__ __attribute__((aligned(16))) float ex[2][CT * (NT + 1)][64][4];
+    __shared__ __attribute__((aligned(16))) float ex[2][CT * (NT + 1) * 256];
     __shared__ __attribute__((aligned(16))) int rowbuf[kWaves][2][kStep];
     Place p;
     if (!find_place(a, p)) return;
@@ -487,6 +530,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_tree_rows(TreeArgs a) {
     for (int t = 0; t < CT; ++t) {
         st.m[t] = -INFINITY;
         st.l[t] = 0.f;
+        st.nan[t] = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
     }
@@ -550,20 +594,23 @@ __global__ __launch_bounds__(64 * kWaves) void k_tree_rows(TreeArgs a) {
             load_k<NDP>(x, a, at, kc, ks, rowbuf[w][buf], lane);
             __builtin_amdgcn_sched_barrier(0);
 
-            uint64_t seen[CT];
-            const bool part = valid != ~0ull || lt + kStep > p.ctx;
-            if (part) {
+            if (valid != ~0ull || lt + kStep > p.ctx) {
+                uint64_t seen[CT];
 #pragma unroll
                 for (int t = 0; t < CT; ++t) seen[t] = valid & mask_window(a, p, iq[t], lt);
-                soften<NDP, CT, true, PARTS == 3>(st, sc, seen, a.scale2, c);
+                hide<CT, kNTL>(sc, seen, c);
 #pragma unroll
                 for (int u = 0; u < kNTL; ++u)
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) x.vb[u][s] = (valid >> (16 * u + 4 * c + s)) & 1 ? x.vb[u][s] : 0u;
-                take_out_nan<NDP, CT>(st, x.vb, seen, c);
-            } else {
-                soften<NDP, CT, false, PARTS == 3>(st, sc, seen, a.scale2, c);
+                    for (int s = 0; s < 4; ++s) {
+                        if (!((valid >> (16 * u + 4 * c + s)) & 1)) x.vb[u][s] = 0;
+                        const uint64_t bad = take_nan(x.vb[u][s]);
+                        if (bad)
+                            for (int k = 0; k < 4; ++k)
+                                note_nan<NDP, CT>(st, (uint32_t)(bad >> (16 * k)) & 0xFFFFu, 16 * u + 4 * k + s, seen, c);
+                    }
             }
+            soften<NDP, CT, kNTL, PARTS == 3>(st, sc, a.scale2);
 #pragma unroll
             for (int u = 0; u < kNTL; u += 2) {
                 bf8 vf[NT];
@@ -586,43 +633,222 @@ __global__ __launch_bounds__(64 * kWaves) void k_tree_rows(TreeArgs a) {
     }
 #pragma unroll
     for (int t = 0; t < CT; ++t) st.l[t] = col_sum(st.l[t]);
+    give_nan<NDP, CT>(st);
 
-    // merge: M = max m, sums and outputs scaled by 2^((m - M) scale2)
-    auto give = [&](int slot) {
-#pragma unroll
-        for (int t = 0; t < CT; ++t) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) *reinterpret_cast<f4 *>(ex[slot][t * (NT + 1) + n][lane]) = st.acc[t][n];
-            ex[slot][t * (NT + 1) + NT][lane][0] = st.m[t];
-            ex[slot][t * (NT + 1) + NT][lane][1] = st.l[t];
-        }
-    };
-    auto take = [&](int slot) {
-#pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            const float m = ex[slot][t * (NT + 1) + NT][lane][0], l = ex[slot][t * (NT + 1) + NT][lane][1];
-            const float M = fmaxf(st.m[t], m);
-            const float f0 = st.m[t] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.m[t] - M) * a.scale2);
-            const float f1 = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - M) * a.scale2);
-            st.m[t] = M;
-            st.l[t] = st.l[t] * f0 + l * f1;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const f4 o = *reinterpret_cast<const f4 *>(ex[slot][t * (NT + 1) + n][lane]);
-                st.acc[t][n] = st.acc[t][n] * f0 + o * f1;
-            }
-        }
-    };
-    if (w >= 2) give(w - 2);
+    if (w >= 2) give_state<NDP, CT>(st, ex[w - 2], lane);
     __syncthreads();
-    if (w < 2) take(w);
+    if (w < 2) take_state<NDP, CT>(st, ex[w], lane, a.scale2);
     __syncthreads();
-    if (w == 1) give(0);
+    if (w == 1) give_state<NDP, CT>(st, ex[0], lane);
     __syncthreads();
     if (w == 0) {
-        take(0);
+        take_state<NDP, CT>(st, ex[0], lane, a.scale2);
         store_rows<NDP, CT, PARTS>(a, p, st, row0, lane, p.len <= a.chunk);
     }
+}
+
+// Many rows: the four waves of a workgroup share every 64-token stage. Each
+// dequantises one 16-token tile of K and of V into LDS, in the operands' own
+// lane order (64 lanes x 16 bytes an operand: reads and writes without bank
+// conflicts), then multiplies all of the stage (or half of it, WT = 2) with its
+// own 16 CT rows. Two LDS buffers: one barrier a stage, the next stage's codes
+// in flight meanwhile. With WT = 2 the two waves of a row tile are merged at
+// the end.
+template <int NDP, int CT, int WT, int PARTS>
+struct TileLds {
+    static constexpr int NT = 2 * NDP, TILES = kStep / 16;
+    uint32_t k[2][TILES * NDP][64][4];
+    uint32_t v[2][TILES / 2 * NT][64][4];
+    uint64_t nan[2][TILES][4];
+    uint32_t valid[2][TILES];
+};
+
+template <int NDP, int CT, int WT, int PARTS>
+__global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(TreeArgs a) {
+    constexpr int PP = PARTS == 1 ? 2 : 3, NT = 2 * NDP, WR = kWaves / WT, NTW = kNTL / WT;
+    constexpr int KB = Raw<NDP>::KB, VW = Raw<NDP>::VW;
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+    auto &lds = *reinterpret_cast<TileLds<NDP, CT, WT, PARTS> *>(lds_raw);
+    Place p;
+    if (!find_place(a, p)) return;
+    const int lane = threadIdx.x & 63, i = lane & 15, c = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wr = w % WR, wt = w / WR;
+    if (p.rt * WR * 16 * CT >= p.n * a.G) return;
+    const int row0 = (p.rt * WR + wr) * 16 * CT;
+    const bool busy = row0 < p.n * a.G;
+
+    State<NDP, CT> st;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        st.m[t] = -INFINITY;
+        st.l[t] = 0.f;
+        st.nan[t] = 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (p.t0 < p.t1) {
+        const LaneAt<NDP> at(lane, a.D);
+        const uint8_t *kc = a.kc + p.g * (a.D / 2), *vc = a.vc + p.g * (a.D / 2);
+        const uint8_t *ks = a.ks + p.g * (a.D / 32), *vs = a.vs + p.g * (a.D / 32);
+        const int32_t *table = a.table + (int64_t)p.b * a.ldt;
+        const uint32_t cs = (uint32_t)a.Hkv * (a.D / 2), ss = (uint32_t)a.Hkv * (a.D / 32);
+
+        // token 16 w + i of the stage at lt: its page, its pool row
+        auto page_at = [&](int lt) {
+            const int t = lt + 16 * w + i;
+            return t < p.t1 ? table[page_of(a, t)] : -1;
+        };
+        auto row_at = [&](int lt, int page) {
+            const int t = lt + 16 * w + i;
+            return (uint32_t)page < (uint64_t)a.pages ? page * a.ps + (t - page_of(a, t) * a.ps) : -1;
+        };
+        uint32_t k[NDP], kb[KB], v[4][VW], vb[4];
+        auto load = [&](int row) {
+            const uint64_t r = (uint32_t)max(row, 0);
+            const uint8_t *pk = kc + r * cs;
+            if constexpr (NDP == 2) {
+                const u2 x = *reinterpret_cast<const u2 *>(pk + at.k[0]);
+                k[0] = x[0];
+                k[1] = x[1];
+            } else {
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    const u4 x = *reinterpret_cast<const u4 *>(pk + at.k[b]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) k[4 * b + j] = x[j];
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < KB; ++b) kb[b] = ks[r * ss + at.kb[b]];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint64_t rv = (uint32_t)max(__shfl(row, 4 * c + s), 0);
+                const uint8_t *pv = vc + rv * cs + at.v;
+                if constexpr (NDP == 2) {
+                    v[s][0] = *reinterpret_cast<const uint16_t *>(pv);
+                } else if constexpr (NDP == 4) {
+                    v[s][0] = *reinterpret_cast<const uint32_t *>(pv);
+                } else {
+                    const u2 x = *reinterpret_cast<const u2 *>(pv);
+                    v[s][0] = x[0];
+                    v[s][1] = x[1];
+                }
+                vb[s] = vs[rv * ss + at.vb];
+            }
+        };
+
+        int row = row_at(p.t0, page_at(p.t0));
+        load(row);
+        int page = page_at(p.t0 + kStep);
+        bf8 qf[CT][NDP][PARTS];
+        load_queries<NDP, CT, PARTS>(a, p, row0, lane, qf);
+        int iq[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            const int rw = row0 + 16 * t + i;
+            iq[t] = rw < p.n * a.G ? rw / a.G : 0;
+        }
+
+        int buf = 0;
+        for (int lt = p.t0; lt < p.t1; lt += kStep, buf ^= 1) {
+            // this wave's tiles into LDS
+            const uint32_t ok = (uint32_t)__ballot(row >= 0) & 0xFFFFu;
+            const bool edge = lt + kStep > p.ctx || lt + kStep > p.t1;
+            if (lane == 0) lds.valid[buf][w] = ok;
+            if (edge || ok != 0xFFFFu) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    if (!((ok >> (4 * c + s)) & 1)) vb[s] = 0;
+                    if (edge) {
+                        const uint64_t bad = take_nan(vb[s]);
+                        if (lane == 0) lds.nan[buf][w][s] = bad;
+                    }
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < NDP; ++b)
+                *reinterpret_cast<bf8 *>(lds.k[buf][w * NDP + b][lane]) =
+                    word_values(k[b], scale_of(kb[KB == 2 ? b >> 2 : 0]));
+            __builtin_amdgcn_sched_barrier(0);
+            {
+                uint32_t o[NT][2];
+                v_pairs<NDP>(v, vb, o);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    *reinterpret_cast<u2 *>(&lds.v[buf][(w >> 1) * NT + n][lane][2 * (w & 1)]) = u2{o[n][0], o[n][1]};
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            row = row_at(lt + kStep, page);
+            page = page_at(lt + 2 * kStep);
+            load(row);
+            lds_barrier();
+            if (!busy) continue;
+
+            f4 sc[CT][NTW];
+#pragma unroll
+            for (int u = 0; u < NTW; ++u) {
+#pragma unroll
+                for (int t = 0; t < CT; ++t) sc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int b = 0; b < NDP; ++b) {
+                    const bf8 kv = *reinterpret_cast<const bf8 *>(lds.k[buf][(wt * NTW + u) * NDP + b][lane]);
+#pragma unroll
+                    for (int t = 0; t < CT; ++t)
+#pragma unroll
+                        for (int j = 0; j < PARTS; ++j)
+                            sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][j], sc[t][u], 0, 0, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const uint64_t valid = (uint64_t)(lds.valid[buf][0] | lds.valid[buf][1] << 16) |
+                                   (uint64_t)(lds.valid[buf][2] | lds.valid[buf][3] << 16) << 32;
+            if (valid != ~0ull || edge) {
+                uint64_t seen[CT];
+#pragma unroll
+                for (int t = 0; t < CT; ++t) seen[t] = (valid & mask_window(a, p, iq[t], lt)) >> (16 * NTW * wt);
+                hide<CT, NTW>(sc, seen, c);
+                if (edge)
+                    for (int u = 0; u < NTW; ++u)
+                        for (int s = 0; s < 4; ++s) {
+                            const uint64_t bad = lds.nan[buf][wt * NTW + u][s];
+                            if (bad)
+                                for (int j = 0; j < 4; ++j)
+                                    note_nan<NDP, CT>(st, (uint32_t)(bad >> (16 * j)) & 0xFFFFu, 16 * u + 4 * j + s, seen,
+                                                      c);
+                        }
+            }
+            soften<NDP, CT, NTW, PARTS == 3>(st, sc, a.scale2);
+#pragma unroll
+            for (int u = 0; u < NTW; u += 2) {
+                bf8 pf[CT][PP];
+#pragma unroll
+                for (int t = 0; t < CT; ++t) p_operands<PP>(sc[t][u], sc[t][u + 1], pf[t]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const bf8 vv = *reinterpret_cast<const bf8 *>(lds.v[buf][(wt * NTW + u) / 2 * NT + n][lane]);
+#pragma unroll
+                    for (int t = 0; t < CT; ++t)
+#pragma unroll
+                        for (int j = 0; j < PP; ++j)
+                            st.acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[t][j], st.acc[t][n], 0, 0, 0);
+                    if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < CT; ++t) st.l[t] = col_sum(st.l[t]);
+    give_nan<NDP, CT>(st);
+    if constexpr (WT == 2) {
+        __syncthreads();
+        float *ex = reinterpret_cast<float *>(lds_raw) + wr * CT * (NT + 1) * 256;
+        if (wt == 1) give_state<NDP, CT>(st, ex, lane);
+        __syncthreads();
+        if (wt == 1) return;
+        take_state<NDP, CT>(st, ex, lane, a.scale2);
+    }
+    if (busy) store_rows<NDP, CT, PARTS>(a, p, st, row0, lane, p.len <= a.chunk);
 }
 
 // Rows of sequences of several token ranges: out = sum_s O_s 2^(m_s - M) 2^9 /
@@ -656,36 +882,49 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
     const float norm = M == -INFINITY ? 0.f : 512.f / L;
     const int64_t token = (int64_t)q0 + rw / a.Hq;
     T *out = static_cast<T *>(a.out) + token * a.ldo + (int64_t)(rw % a.Hq) * a.D;
-    for (int d = 4 * lane; d < a.D; d += 256) {
-        f4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < ns; ++s) {
-            const float fs = __shfl(f, s);
-            o += *reinterpret_cast<const f4 *>(a.po + (at + s) * a.D + d) * fs;
-        }
+    // D <= 256: a lane's four dims; every lane stays for the weights it holds
+    const int d = 4 * lane < a.D ? 4 * lane : 0;
+    f4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < ns; ++s) {
+        const float fs = __shfl(f, s);
+        o += *reinterpret_cast<const f4 *>(a.po + (at + s) * a.D + d) * fs;
+    }
+    if (4 * lane < a.D) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) out[d + k] = (T)(o[k] * norm);
     }
 }
 
 struct TreePlan {
-    int NDP, CT, nrt, splits, chunk;
+    int NDP, CT, WT;                 // WT 0: k_tree_rows
+    int nrt, splits, chunk;
 };
 
-// Row tiles of 16 CT rows, and token ranges: as many as give about two
-// workgroups to each of the 256 CUs, at least a step a wave, at most 64.
+// Row tiles and token ranges: as many ranges as give about two workgroups to
+// each of the 256 CUs, at least a step a wave, at most 64.
 TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv, int64_t D) {
     TreePlan p;
     p.NDP = D <= 64 ? 2 : (D <= 128 ? 4 : 8);
     const int64_t rows = max_q * (Hq / Hkv);
-    p.CT = dt == MXS_BF16 && p.NDP <= 4 && rows > 16 ? 2 : 1;
-    p.nrt = (int)ceil_div(rows, (int64_t)16 * p.CT);
-    const int64_t units = B * Hkv * p.nrt, turn = kWaves * kStep;
+    const bool bf = dt == MXS_BF16;
+    int64_t tile;
+    if (rows <= (bf && p.NDP <= 4 ? 32 : 16)) {
+        p.WT = 0;
+        p.CT = rows > 16 ? 2 : 1;
+        tile = 16 * p.CT;
+    } else {
+        p.CT = bf ? 2 : 1;
+        p.WT = rows <= 32 * p.CT ? 2 : 1;
+        tile = 16 * p.CT * (kWaves / p.WT);
+    }
+    p.nrt = (int)ceil_div(rows, tile);
+    const int64_t units = B * Hkv * p.nrt, turn = p.WT ? 2 * kStep : kWaves * kStep, L = max_len > 0 ? max_len : 1;
     int64_t s = ceil_div((int64_t)512, units);
-    const int64_t most = ceil_div(max_len > 0 ? max_len : 1, turn);
+    const int64_t most = ceil_div(L, turn);
     s = s > 64 ? 64 : s;
     s = s > most ? most : s;
-    p.chunk = (int)(ceil_div(ceil_div(max_len > 0 ? max_len : 1, s), turn) * turn);
-    p.splits = (int)ceil_div(max_len > 0 ? max_len : 1, (int64_t)p.chunk);
+    p.chunk = (int)(ceil_div(ceil_div(L, s), turn) * turn);
+    p.splits = (int)ceil_div(L, (int64_t)p.chunk);
     return p;
 }
 
@@ -693,6 +932,26 @@ template <int NDP, int CT, int PARTS>
 hipError_t rows_go(const TreeArgs &a, unsigned grid, hipStream_t st) {
     hipLaunchKernelGGL((k_tree_rows<NDP, CT, PARTS>), dim3(grid), dim3(64 * kWaves), 0, st, a);
     return hipGetLastError();
+}
+template <int NDP, int CT, int WT, int PARTS>
+hipError_t tile_go(const TreeArgs &a, unsigned grid, hipStream_t st) {
+    constexpr size_t lds = sizeof(TileLds<NDP, CT, WT, PARTS>);
+    static_assert(WT == 1 || lds >= (size_t)(kWaves / 2) * CT * (2 * NDP + 1) * 1024, "merge space");
+    hipLaunchKernelGGL((k_tree_tile<NDP, CT, WT, PARTS>), dim3(grid), dim3(64 * kWaves), lds, st, a);
+    return hipGetLastError();
+}
+template <int NDP>
+hipError_t tree_go(const TreePlan &p, const TreeArgs &a, unsigned grid, bool f32, hipStream_t st) {
+    if (f32) {
+        if (p.WT == 0) return rows_go<NDP, 1, 3>(a, grid, st);
+        return p.WT == 1 ? tile_go<NDP, 1, 1, 3>(a, grid, st) : tile_go<NDP, 1, 2, 3>(a, grid, st);
+    }
+    if (p.WT == 0) {
+        if constexpr (NDP <= 4)
+            if (p.CT == 2) return rows_go<NDP, 2, 1>(a, grid, st);
+        return rows_go<NDP, 1, 1>(a, grid, st);
+    }
+    return p.WT == 1 ? tile_go<NDP, 2, 1, 1>(a, grid, st) : tile_go<NDP, 2, 2, 1>(a, grid, st);
 }
 
 }  // namespace
@@ -726,7 +985,8 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
         a.pmul = (uint32_t)((((uint64_t)1 << (31 + l)) + c.page_size - 1) / (uint64_t)c.page_size);
         a.pshift = l - 1;
     }
-    a.scale2 = (float)(fabs((double)scale) * 1.4426950408889634074 * 512.0);
+    // at least 2^-126, so that a hidden score stays -inf at scale 0
+    a.scale2 = fmaxf((float)(fabs((double)scale) * 1.4426950408889634074 * 512.0), 1.17549435e-38f);
     a.negate = std::signbit(scale);
     a.nrt = p.nrt; a.splits = p.splits; a.chunk = p.chunk;
     a.out = out; a.ldo = ldo;
@@ -735,9 +995,9 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     const unsigned grid = (unsigned)attend_kv4_tree_grid(dt, B, max_q, max_len, Hq, c.H, c.D);
     hipError_t e;
     const bool f32 = dt == MXS_F32;
-    if (p.NDP == 2) e = f32 ? rows_go<2, 1, 3>(a, grid, st) : (p.CT == 2 ? rows_go<2, 2, 1>(a, grid, st) : rows_go<2, 1, 1>(a, grid, st));
-    else if (p.NDP == 4) e = f32 ? rows_go<4, 1, 3>(a, grid, st) : (p.CT == 2 ? rows_go<4, 2, 1>(a, grid, st) : rows_go<4, 1, 1>(a, grid, st));
-    else e = f32 ? rows_go<8, 1, 3>(a, grid, st) : rows_go<8, 1, 1>(a, grid, st);
+    if (p.NDP == 2) e = tree_go<2>(p, a, grid, f32, st);
+    else if (p.NDP == 4) e = tree_go<4>(p, a, grid, f32, st);
+    else e = tree_go<8>(p, a, grid, f32, st);
     if (e != hipSuccess || p.splits == 1) return e;
     const dim3 jg((unsigned)ceil_div(max_q * Hq, (int64_t)4), (unsigned)B);
     if (f32) hipLaunchKernelGGL((k_tree_join<float>), jg, dim3(256), 0, st, a);

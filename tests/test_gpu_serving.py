@@ -391,6 +391,8 @@ TREES = [
     ([5000, 257, 1], [4, 2, 1], 16, 2, 128, 256, "tree"),
     ([1500] * 3, [40, 7, 21], 32, 4, 128, 64, "tree"),
     ([400, 600], [70, 90], 24, 3, 192, 32, "holes"),
+    ([17000], [1], 2, 1, 32, 64, "causal"),                      # many token ranges, few lanes a row
+    ([9000, 3], [3, 3], 16, 1, 64, 64, "tree"),
 ]
 
 
@@ -461,7 +463,8 @@ def test_tree_attention_huge_scores(mx):
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_tree_attention_padded_rows_and_strides(mx, dtype):
     b = Batch(mx, [90, 40], [6, 5], 8, 2, 64, 16, dtype, "tree", 31)
-    ref = b.run(mx)
+    ref = b.run(mx, max_q=9, max_len=100)                        # the same bounds: the same split
+    b.check(ref)
     rows = torch.full((20, 8 + 4, 64), float("nan"), dtype=dtype, device=DEV)
     rows[:11, :8] = b.q
     out = torch.full((20, 10, 64), 3.0, dtype=dtype, device=DEV)
