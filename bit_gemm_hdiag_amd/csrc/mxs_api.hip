@@ -552,7 +552,7 @@ size_t mxs_attend_kv4_tree_workspace(mxs_dtype dtype, int64_t B, int64_t total_q
     if (!dtype_ok(dtype) || B <= 0 || total_q <= 0 || max_q <= 0 || max_len < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv ||
         D < 32 || D % 32 || D > 256)
         return 0;
-    return mxs::attend_kv4_tree_workspace(dtype, B, total_q, max_q, max_len, Hq, Hkv, D);
+    return mxs::attend_kv4_tree_workspace(dtype, B, max_q, max_len, Hq, Hkv, D);
 }
 
 mxs_status mxs_attend_kv4_tree(const void *q, mxs_dtype dtype, int64_t ldq, const mxs_kv4_cache *cache,
@@ -585,9 +585,10 @@ mxs_status mxs_attend_kv4_tree(const void *q, mxs_dtype dtype, int64_t ldq, cons
     if (!aligned(q, es) || !aligned(out, es) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(cu, 4) ||
         !aligned(mask, 8))
         return fail(MXS_ERR_UNSUPPORTED, "attend_kv4_tree: misaligned pointer");
-    if (mxs::attend_kv4_tree_grid(dtype, B, max_q, max_len, Hq, H, D) > 0x7FFFFFFF)
-        return fail(MXS_ERR_UNSUPPORTED, "attend_kv4_tree: too many workgroups");
-    const size_t need = mxs::attend_kv4_tree_workspace(dtype, B, total_q, max_q, max_len, Hq, H, D);
+    if (!mxs::attend_kv4_tree_supported(dtype, B, max_q, max_len, Hq, H, D))
+        return fail(MXS_ERR_UNSUPPORTED, "attend_kv4_tree: B=%lld max_q=%lld max_len=%lld Hq=%lld is too much work",
+                    (long long)B, (long long)max_q, (long long)max_len, (long long)Hq);
+    const size_t need = mxs::attend_kv4_tree_workspace(dtype, B, max_q, max_len, Hq, H, D);
     if (need && (!ws || ws_bytes < need || !aligned(ws, 16)))
         return fail(MXS_ERR_WORKSPACE, "attend_kv4_tree: workspace of %zu bytes, needs %zu, 16-byte aligned", ws_bytes,
                     need);

@@ -77,10 +77,10 @@ hipError_t launch_kv4_read(const mxs_kv4_cache &c, const int64_t *slots, int64_t
                            int64_t ldkt, int64_t ldkh, void *v, int64_t ldvt, int64_t ldvh, hipStream_t st);
 
 // attention of drafted tokens over the paged cache (mxs_tree_attention.hip)
-size_t attend_kv4_tree_workspace(mxs_dtype dt, int64_t B, int64_t total_q, int64_t max_q, int64_t max_len, int64_t Hq,
-                                 int64_t Hkv, int64_t D);
-int64_t attend_kv4_tree_grid(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
-                             int64_t D);
+size_t attend_kv4_tree_workspace(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
+                                 int64_t D);
+bool attend_kv4_tree_supported(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
+                               int64_t D);
 hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, const mxs_kv4_cache &c,
                                   const int32_t *table, int64_t ldt, const int32_t *lens, const int32_t *cu,
                                   const uint64_t *mask, int64_t words, int64_t B, int64_t total_q, int64_t max_q,

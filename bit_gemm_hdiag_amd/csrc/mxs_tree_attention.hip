@@ -65,10 +65,10 @@ struct TreeArgs {
     uint32_t pmul, pshift;           // t / ps
     float scale2;                    // |scale| log2(e) 2^9
     bool negate;                     // scale < 0: queries enter negated
-    int nrt, splits, chunk;
+    int R, U, P, minu;               // rows of a tile, tokens of a unit, workgroups, units of a share (at least)
     void *out;
     int64_t ldo;
-    float *po, *pml;                 // [row, split, D], [row, split, (m, l)]
+    float *po, *pml;                 // [2 share + k, R, D], [2 share + k, R, (m, l)]
 };
 
 // t / ps for 0 <= t < 2^31: pmul = ceil(2^(31 + l) / ps), l = ceil(log2 ps)
@@ -126,36 +126,130 @@ __device__ __forceinline__ float col_sum(float x) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// One workgroup's place in the batch
-struct Place {
-    int b, g, rt, split;             // sequence, KV head, row tile, token range
-    int len, ctx, n, q0;             // cached tokens, context, query tokens, first query token
-    int t0, t1;                      // tokens of the workgroup
+// ------------------------------------------------------------------ shares
+// The work of a call is a line of units: sequence by sequence, tile (KV head,
+// then R of the head's n G rows) by tile, U tokens by U tokens (a sequence of
+// no tokens has one empty unit a tile, which writes its zeros). It is cut into
+// P' equal shares, one a workgroup, from the lengths that the call finds on the
+// device: ragged batches are balanced, and a captured graph stays so when its
+// lengths change. A tile that lies in one share is written to `out`; the
+// pieces of the others go to the workspace (a share has at most two: the end of
+// a tile, k = 0, and the start of one, k = 1) and k_tree_join adds them.
+struct Seq {
+    int len, n, q0;                  // cached tokens, query tokens, first query token
+    uint32_t nrt, T;                 // row tiles of a head, units of a tile
 };
-
-// Workgroups are dealt to the 8 XCDs in turn. The heads and row tiles of one
-// (token range, sequence) go to one XCD: its row tiles read the same cache
-// rows, and neighbouring heads share 128-byte lines of them.
-__device__ __forceinline__ bool find_place(const TreeArgs &a, Place &p) {
-    const uint32_t units = (uint32_t)a.Hkv * a.nrt, id = blockIdx.x;
-    const uint32_t k = id >> 3, grp = (k / units) * 8 + (id & 7), unit = k % units;
-    if (grp >= (uint32_t)a.B * (uint32_t)a.splits) return false;
-    p.b = (int)(grp / (uint32_t)a.splits);
-    p.split = (int)(grp % (uint32_t)a.splits);
-    p.g = (int)(unit / (uint32_t)a.nrt);
-    p.rt = (int)(unit % (uint32_t)a.nrt);
-    int64_t len = a.lens[p.b];
-    len = len < 0 ? 0 : (len > a.max_len ? a.max_len : len);
-    int q0 = a.cu[p.b], q1 = a.cu[p.b + 1];
+__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int b) {
+    Seq s;
+    const int len = a.lens[b];
+    s.len = len < 0 ? 0 : (len > a.max_len ? a.max_len : len);
+    int q0 = a.cu[b], q1 = a.cu[b + 1];
     q0 = q0 < 0 ? 0 : (q0 > a.total_q ? a.total_q : q0);
     q1 = q1 < q0 ? q0 : (q1 > a.total_q ? a.total_q : q1);
-    p.len = (int)len;
-    p.q0 = q0;
-    p.n = q1 - q0 > a.max_q ? a.max_q : q1 - q0;
-    p.ctx = p.len > p.n ? p.len - p.n : 0;
-    p.t0 = p.split * a.chunk;
-    p.t1 = p.len - p.t0 > a.chunk ? p.t0 + a.chunk : p.len;
-    return p.split == 0 || p.t0 < p.len;
+    s.q0 = q0;
+    s.n = q1 - q0 > a.max_q ? a.max_q : q1 - q0;
+    s.nrt = ((uint32_t)(s.n * a.G) + a.R - 1) / (uint32_t)a.R;
+    s.T = s.len > 0 ? ((uint32_t)s.len + a.U - 1) / (uint32_t)a.U : 1u;
+    return s;
+}
+__device__ __forceinline__ uint32_t units_of(const TreeArgs &a, const Seq &s) { return (uint32_t)a.Hkv * s.nrt * s.T; }
+
+// inclusive sum over the wave's lanes
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xF, 0xF, true);    // lanes 1, 2, 4, 8 to the left
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xF, 0xF, true);    // in rows of 16
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xF, 0xF, true);
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xF, 0xF, true);
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xA, 0xF, false);   // the last lane of the row before
+    x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xC, 0xF, false);   // lane 31
+    return x;
+}
+
+struct Shares {
+    uint32_t W, P, q, r;             // units, shares, W / P, W % P
+    __device__ __forceinline__ uint32_t start(uint32_t p) const { return p * q + p * r / P; }      // floor(p W / P)
+    // the share of unit x: the last p with p W < (x + 1) P
+    __device__ __forceinline__ uint32_t owner(uint32_t x) const {
+        return (uint32_t)(((double)(x + 1) * (double)P - 1.0) / (double)W);
+    }
+};
+__device__ __forceinline__ Shares shares_of(const TreeArgs &a, int lane) {
+    Shares h;
+    h.W = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        uint32_t u = 0;
+        if (b0 + lane < a.B) u = units_of(a, seq_of(a, b0 + lane));
+        h.W += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(u), 63);
+    }
+    const uint32_t most = (h.W + a.minu - 1) / (uint32_t)a.minu;
+    h.P = most < (uint32_t)a.P ? most : (uint32_t)a.P;
+    h.q = h.P ? h.W / h.P : 0;
+    h.r = h.P ? h.W % h.P : 0;
+    return h;
+}
+// The sequence of unit x < W and its first unit
+__device__ __forceinline__ int find_seq(const TreeArgs &a, uint32_t x, int lane, uint32_t &first) {
+    uint32_t sum = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        uint32_t u = 0;
+        if (b0 + lane < a.B) u = units_of(a, seq_of(a, b0 + lane));
+        const uint32_t end = sum + wave_scan(u);
+        const uint64_t past = __ballot(end > x);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            first = (uint32_t)__builtin_amdgcn_readlane((int)(end - u), l);
+            return b0 + l;
+        }
+        sum = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+    }
+    first = 0;
+    return 0;
+}
+
+// A piece of a share: tokens t0 .. t1 - 1 of one tile
+struct Place {
+    int b, g, row;                   // sequence, KV head, first row of the tile
+    int len, ctx, n, q0;             // cached tokens, context, query tokens, first query token
+    int t0, t1;
+    int64_t slot;                    // workspace slot, -1: the whole tile
+};
+
+// f(place) for every piece of this workgroup's share. Consecutive shares (row
+// tiles of one KV head, then its neighbours in the same 128-byte lines of the
+// cache) go to one XCD: workgroups are dealt to the 8 XCDs in turn.
+template <typename F>
+__device__ __forceinline__ void for_each_piece(const TreeArgs &a, int lane, F f) {
+    const Shares h = shares_of(a, lane);
+    const uint32_t per = (h.P + 7) / 8, p = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((blockIdx.x >> 3) >= per || p >= h.P) return;
+    uint32_t x = h.start(p), first;
+    const uint32_t end = h.start(p + 1);
+    int b = find_seq(a, x, lane, first);
+    while (x < end) {
+        const Seq s = seq_of(a, b);
+        const uint32_t units = units_of(a, s);
+        if (x - first >= units) {
+            first += units;
+            if (++b >= a.B) return;
+            continue;
+        }
+        const uint32_t tile = (x - first) / s.T, u0 = (x - first) - tile * s.T;
+        const uint32_t u1 = s.T - u0 < end - x ? s.T : u0 + (end - x);
+        auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        Place pl;
+        pl.b = uni(b);
+        pl.g = uni((int)(tile / s.nrt));
+        pl.row = uni((int)(tile % s.nrt) * a.R);
+        pl.len = uni(s.len);
+        pl.n = uni(s.n);
+        pl.q0 = uni(s.q0);
+        pl.ctx = uni(s.len > s.n ? s.len - s.n : 0);
+        pl.t0 = uni((int)u0 * a.U);
+        pl.t1 = uni(u1 == s.T ? s.len : (int)u1 * a.U);
+        pl.slot = u0 == 0 && u1 == s.T ? -1 : 2 * (int64_t)p + (u0 > 0 ? 0 : 1);
+        f(pl);
+        x += u1 - u0;
+    }
 }
 
 // Bits of drafted tokens 64 k .. 64 k + 63 that query token i sees
@@ -438,11 +532,11 @@ __device__ __forceinline__ void give_nan(State<NDP, CT> &st) {
 }
 
 // Outputs of one column: lane (r, c) holds dims (4 c + rr) DL + n of row r.
-// One token range: normalised, rounded once, to `out` (0 where nothing was
-// seen); several: (m, l) and the unnormalised sums for k_tree_join.
+// A whole tile: normalised, rounded once, to `out` (0 where nothing was seen);
+// a piece: (m, l) and the unnormalised sums for k_tree_join.
 template <int NDP, int CT, int PARTS>
 __device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, const State<NDP, CT> &st, int row0,
-                                           int lane, bool whole) {
+                                           int lane) {
     constexpr int DL = 2 * NDP;
     const int r = lane & 15, c = lane >> 4;
 #pragma unroll
@@ -450,7 +544,7 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, co
         const int row = row0 + 16 * t + r;
         if (row >= p.n * a.G) continue;
         const int i = row / a.G, h = p.g * a.G + row - i * a.G;
-        if (whole) {
+        if (p.slot < 0) {
             const float f = st.m[t] == -INFINITY ? 0.f : 512.f / st.l[t];
 #pragma unroll
             for (int rr = 0; rr < 4; ++rr) {
@@ -465,7 +559,7 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, co
                 }
             }
         } else {
-            const int64_t at = ((int64_t)(p.q0 + i) * a.Hq + h) * a.splits + p.split;
+            const int64_t at = p.slot * a.R + (row - p.row);
             if (c == 0) {
                 a.pml[2 * at] = st.m[t] == -INFINITY ? -INFINITY : st.m[t] * a.scale2;
                 a.pml[2 * at + 1] = st.l[t];
@@ -514,16 +608,14 @@ __device__ __forceinline__ void take_state(State<NDP, CT> &st, const float *ex, 
 // of 64 tokens, each dequantising its own tokens in registers; their states
 // are merged in LDS in wave order (2 and 3 into 0 and 1, then 1 into 0).
 template <int NDP, int CT, int PARTS>
-__global__ __launch_bounds__(64 * kWaves) void k_tree_rows(TreeArgs a) {
+__global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_rows(TreeArgs a) {
     constexpr int PP = PARTS == 1 ? 2 : 3, NT = 2 * NDP;
     __shared__ __attribute__((aligned(16))) float ex[2][CT * (NT + 1) * 256];
     __shared__ __attribute__((aligned(16))) int rowbuf[kWaves][2][kStep];
-    Place p;
-    if (!find_place(a, p)) return;
     const int lane = threadIdx.x & 63, c = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row0 = p.rt * 16 * CT;
-    if (row0 >= p.n * a.G) return;
+    for_each_piece(a, lane, [&](const Place &p) {
+    const int row0 = p.row;
 
     State<NDP, CT> st;
 #pragma unroll
@@ -643,8 +735,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_tree_rows(TreeArgs a) {
     __syncthreads();
     if (w == 0) {
         take_state<NDP, CT>(st, ex[0], lane, a.scale2);
-        store_rows<NDP, CT, PARTS>(a, p, st, row0, lane, p.len <= a.chunk);
+        store_rows<NDP, CT, PARTS>(a, p, st, row0, lane);
     }
+    __syncthreads();                 // the next piece writes the same LDS
+    });
 }
 
 // Many rows: the four waves of a workgroup share every 64-token stage. Each
@@ -669,13 +763,11 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
     constexpr int KB = Raw<NDP>::KB, VW = Raw<NDP>::VW;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
     auto &lds = *reinterpret_cast<TileLds<NDP, CT, WT, PARTS> *>(lds_raw);
-    Place p;
-    if (!find_place(a, p)) return;
     const int lane = threadIdx.x & 63, i = lane & 15, c = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = w % WR, wt = w / WR;
-    if (p.rt * WR * 16 * CT >= p.n * a.G) return;
-    const int row0 = (p.rt * WR + wr) * 16 * CT;
+    for_each_piece(a, lane, [&](const Place &p) {
+    const int row0 = p.row + wr * 16 * CT;
     const bool busy = row0 < p.n * a.G;
 
     State<NDP, CT> st;
@@ -845,86 +937,116 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
         float *ex = reinterpret_cast<float *>(lds_raw) + wr * CT * (NT + 1) * 256;
         if (wt == 1) give_state<NDP, CT>(st, ex, lane);
         __syncthreads();
-        if (wt == 1) return;
-        take_state<NDP, CT>(st, ex, lane, a.scale2);
+        if (wt == 0) take_state<NDP, CT>(st, ex, lane, a.scale2);
     }
-    if (busy) store_rows<NDP, CT, PARTS>(a, p, st, row0, lane, p.len <= a.chunk);
+    if (busy && wt == 0) store_rows<NDP, CT, PARTS>(a, p, st, row0, lane);
+    __syncthreads();                 // the next piece writes the same LDS
+    });
 }
 
-// Rows of sequences of several token ranges: out = sum_s O_s 2^(m_s - M) 2^9 /
-// sum_s l_s 2^(m_s - M), ranges in order. One wave a row, at most 64 ranges.
+// Rows of tiles that lie in several shares: out = sum_s O_s 2^(m_s - M) 2^9 /
+// sum_s l_s 2^(m_s - M), pieces in order. One wave a row; lane s holds the
+// weight of piece s of a run of 64, D <= 256: a lane's four dims.
 template <typename T>
 __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
     const int b = blockIdx.y, lane = threadIdx.x & 63;
-    const int rw = blockIdx.x * 4 + (threadIdx.x >> 6);             // (query token, head)
-    int len = a.lens[b];
-    len = len > a.max_len ? a.max_len : len;
-    if (len <= a.chunk) return;
-    int q0 = a.cu[b], q1 = a.cu[b + 1];
-    q0 = q0 < 0 ? 0 : (q0 > a.total_q ? a.total_q : q0);
-    q1 = q1 < q0 ? q0 : (q1 > a.total_q ? a.total_q : q1);
-    const int n = q1 - q0 > a.max_q ? a.max_q : q1 - q0;
-    if (rw >= n * a.Hq) return;
-    const int ns = (len + a.chunk - 1) / a.chunk;
-    const int64_t at = ((int64_t)q0 * a.Hq + rw) * a.splits;
-    float m = -INFINITY, l = 0.f;
-    if (lane < ns) {
-        m = a.pml[2 * (at + lane)];
-        l = a.pml[2 * (at + lane) + 1];
+    const int rw = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // (query token, head)
+    const Seq s = seq_of(a, b);
+    if (rw >= s.n * a.Hq || s.T < 2) return;
+    const Shares sh = shares_of(a, lane);
+    uint32_t first = 0;
+    for (int b0 = 0; b0 < b; b0 += 64) {
+        uint32_t u = 0;
+        if (b0 + lane < b) u = units_of(a, seq_of(a, b0 + lane));
+        first += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(u), 63);
     }
-    float M = m, L;
-#pragma unroll
-    for (int o = 32; o; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - M);
-    L = l * f;
-#pragma unroll
-    for (int o = 32; o; o >>= 1) L += __shfl_xor(L, o);
-    const float norm = M == -INFINITY ? 0.f : 512.f / L;
-    const int64_t token = (int64_t)q0 + rw / a.Hq;
-    T *out = static_cast<T *>(a.out) + token * a.ldo + (int64_t)(rw % a.Hq) * a.D;
-    // D <= 256: a lane's four dims; every lane stays for the weights it holds
+    const int i = rw / a.Hq, h = rw - i * a.Hq, g = h / a.G, row = i * a.G + h - g * a.G;
+    first += ((uint32_t)g * s.nrt + (uint32_t)(row / a.R)) * s.T;
+    const uint32_t p0 = sh.owner(first), p1 = sh.owner(first + s.T - 1);
+    if (p0 == p1) return;
+    const int in = row % a.R;
     const int d = 4 * lane < a.D ? 4 * lane : 0;
+    float M = -INFINITY, L = 0.f;
     f4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < ns; ++s) {
-        const float fs = __shfl(f, s);
-        o += *reinterpret_cast<const f4 *>(a.po + (at + s) * a.D + d) * fs;
+    for (uint32_t q = p0; q <= p1; q += 64) {
+        const int ns = (int)(p1 - q + 1 < 64 ? p1 - q + 1 : 64);
+        // piece of share q + lane: slot 1 where the share starts at or before the tile, else 0
+        const uint32_t me = q + (lane < ns ? lane : 0);
+        const int64_t at = (2 * (int64_t)me + (sh.start(me) > first ? 0 : 1)) * a.R + in;
+        float m = -INFINITY, l = 0.f;
+        if (lane < ns) {
+            m = a.pml[2 * at];
+            l = a.pml[2 * at + 1];
+        }
+        float Mn = m;
+#pragma unroll
+        for (int k = 32; k; k >>= 1) Mn = fmaxf(Mn, __shfl_xor(Mn, k));
+        Mn = fmaxf(M, Mn);
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - Mn);
+        const float old = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(M - Mn);
+        float ls = l * f;
+#pragma unroll
+        for (int k = 32; k; k >>= 1) ls += __shfl_xor(ls, k);
+        L = L * old + ls;
+        o *= old;
+        M = Mn;
+        const float *po = a.po + d;
+        const int64_t base = ((2 * (int64_t)q) * a.R + in) * a.D, next = 2 * (int64_t)a.R * a.D;
+        const int64_t one = (int64_t)a.R * a.D;
+        for (int k = 0; k < ns; k += 8) {
+            f4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t pk = k + j < ns ? k + j : ns - 1;
+                v[j] = *reinterpret_cast<const f4 *>(po + base + pk * next + (sh.start(q + pk) > first ? 0 : one));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float fk = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(f), k + j < ns ? k + j : 0));
+                if (k + j < ns) o += v[j] * fk;
+            }
+        }
     }
+    const float norm = M == -INFINITY ? 0.f : 512.f / L;
+    T *out = static_cast<T *>(a.out) + ((int64_t)s.q0 + i) * a.ldo + (int64_t)h * a.D + d;
     if (4 * lane < a.D) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) out[d + k] = (T)(o[k] * norm);
+        for (int k = 0; k < 4; ++k) out[k] = (T)(o[k] * norm);
     }
 }
 
 struct TreePlan {
     int NDP, CT, WT;                 // WT 0: k_tree_rows
-    int nrt, splits, chunk;
+    int R, U, P, minu;
+    int64_t bound;                   // units at most
+    int join;                        // some tile may lie in several shares
 };
 
-// Row tiles and token ranges: as many ranges as give about two workgroups to
-// each of the 256 CUs, at least a step a wave, at most 64.
+// Kernel, tile and number of workgroups from what the host knows: two
+// workgroups fit on each of the 256 CUs (one with D > 128 in k_tree_tile).
 TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv, int64_t D) {
     TreePlan p;
     p.NDP = D <= 64 ? 2 : (D <= 128 ? 4 : 8);
     const int64_t rows = max_q * (Hq / Hkv);
     const bool bf = dt == MXS_BF16;
-    int64_t tile;
     if (rows <= (bf && p.NDP <= 4 ? 32 : 16)) {
         p.WT = 0;
         p.CT = rows > 16 ? 2 : 1;
-        tile = 16 * p.CT;
+        p.R = 16 * p.CT;
+        p.U = kWaves * kStep;
+        p.minu = 1;
     } else {
         p.CT = bf ? 2 : 1;
         p.WT = rows <= 32 * p.CT ? 2 : 1;
-        tile = 16 * p.CT * (kWaves / p.WT);
+        p.R = 16 * p.CT * (kWaves / p.WT);
+        p.U = kStep;
+        p.minu = 2;
     }
-    p.nrt = (int)ceil_div(rows, tile);
-    const int64_t units = B * Hkv * p.nrt, turn = p.WT ? 2 * kStep : kWaves * kStep, L = max_len > 0 ? max_len : 1;
-    int64_t s = ceil_div((int64_t)512, units);
-    const int64_t most = ceil_div(L, turn);
-    s = s > 64 ? 64 : s;
-    s = s > most ? most : s;
-    p.chunk = (int)(ceil_div(ceil_div(L, s), turn) * turn);
-    p.splits = (int)ceil_div(L, (int64_t)p.chunk);
+    const int64_t T = max_len > 0 ? ceil_div(max_len, (int64_t)p.U) : 1;
+    p.bound = B * Hkv * ceil_div(rows, (int64_t)p.R) * T;
+    const int64_t slots = p.WT && p.NDP == 8 ? 256 : 512, most = ceil_div(ceil_div(p.bound, (int64_t)p.minu), (int64_t)8) * 8;
+    p.P = (int)(most < slots ? most : slots);
+    p.join = T > 1;
     return p;
 }
 
@@ -956,16 +1078,17 @@ hipError_t tree_go(const TreePlan &p, const TreeArgs &a, unsigned grid, bool f32
 
 }  // namespace
 
-size_t attend_kv4_tree_workspace(mxs_dtype dt, int64_t B, int64_t total_q, int64_t max_q, int64_t max_len, int64_t Hq,
-                                 int64_t Hkv, int64_t D) {
+size_t attend_kv4_tree_workspace(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
+                                 int64_t D) {
     const TreePlan p = tree_plan(dt, B, max_q, max_len, Hq, Hkv, D);
-    return p.splits > 1 ? (size_t)(total_q * Hq * p.splits * (D + 2)) * sizeof(float) : 0;
+    return p.join ? (size_t)(2 * p.P) * p.R * (D + 2) * sizeof(float) : 0;
 }
 
-int64_t attend_kv4_tree_grid(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
-                             int64_t D) {
-    const TreePlan p = tree_plan(dt, B, max_q, max_len, Hq, Hkv, D);
-    return ceil_div(B * p.splits, (int64_t)8) * 8 * Hkv * p.nrt;
+bool attend_kv4_tree_supported(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
+                               int64_t D) {
+    const int64_t rows = max_q * (Hq / Hkv);
+    return rows <= (1 << 30) && max_q * Hq <= ((int64_t)1 << 31) &&
+           tree_plan(dt, B, max_q, max_len, Hq, Hkv, D).bound <= (1 << 30);
 }
 
 hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, const mxs_kv4_cache &c,
@@ -988,17 +1111,17 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     // at least 2^-126, so that a hidden score stays -inf at scale 0
     a.scale2 = fmaxf((float)(fabs((double)scale) * 1.4426950408889634074 * 512.0), 1.17549435e-38f);
     a.negate = std::signbit(scale);
-    a.nrt = p.nrt; a.splits = p.splits; a.chunk = p.chunk;
+    a.R = p.R; a.U = p.U; a.P = p.P; a.minu = p.minu;
     a.out = out; a.ldo = ldo;
     a.po = static_cast<float *>(ws);
-    a.pml = a.po + total_q * Hq * p.splits * c.D;
-    const unsigned grid = (unsigned)attend_kv4_tree_grid(dt, B, max_q, max_len, Hq, c.H, c.D);
+    a.pml = a.po + (int64_t)(2 * p.P) * p.R * c.D;
+    const unsigned grid = (unsigned)p.P;
     hipError_t e;
     const bool f32 = dt == MXS_F32;
     if (p.NDP == 2) e = tree_go<2>(p, a, grid, f32, st);
     else if (p.NDP == 4) e = tree_go<4>(p, a, grid, f32, st);
     else e = tree_go<8>(p, a, grid, f32, st);
-    if (e != hipSuccess || p.splits == 1) return e;
+    if (e != hipSuccess || !p.join) return e;
     const dim3 jg((unsigned)ceil_div(max_q * Hq, (int64_t)4), (unsigned)B);
     if (f32) hipLaunchKernelGGL((k_tree_join<float>), jg, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((k_tree_join<__bf16>), jg, dim3(256), 0, st, a);
