@@ -28,10 +28,11 @@
 // (scale bytes 0 to 2, values below 2^-122, round to multiples of 2^-124);
 // the factors 2^9 go into the score scale and the final normalisation.
 // A block with byte 0xFF is NaN. bf16 queries enter as they are; fp32 queries
-// as the exact sum of three bf16 parts. The softmax weights p enter as bf16
-// parts too: three for fp32 (exact), two for bf16 (an error of 2^-17 of each
-// p; one part, 2^-9, would be as large as the rounding of the bf16 output).
-// Maxima, sums and outputs are fp32.
+// as the exact sum of three bf16 parts, and so do their softmax weights p. For
+// bf16 queries p is rounded to one bf16 (2^-9 of each p, independent from token
+// to token, against the output's own rounding of 2^-9; two parts took PPP),
+// and the sum that normalises is that of the rounded values, so one dominant
+// token gives its V exactly. Maxima, sums and outputs are fp32.
 #include <cmath>
 
 #include "mxs_device.h"
@@ -117,15 +118,6 @@ __device__ __forceinline__ float col_max(float x) {
     const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
-__device__ __forceinline__ float col_sum(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    const float y = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const uint32_t v = __float_as_uint(y);
-    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 // ------------------------------------------------------------------ shares
 // The work of a call is a line of units: sequence by sequence, tile (KV head,
 // then R of the head's n G rows) by tile, U tokens by U tokens (a sequence of
@@ -381,11 +373,14 @@ __device__ __forceinline__ void load_v(Raw<NDP> &x, const TreeArgs &a, const Lan
 }
 
 // Running state of a wave: columns r of its CT tiles. m is the reference the
-// exponents are taken from (raw score units), l this lane's share of the sum.
+// exponents are taken from (raw score units), l the sum of the weights, formed
+// by the matrix product of p with ones (the same in all four registers): it
+// sums the very values that multiply V, and costs the vector ALU nothing.
 template <int NDP, int CT>
 struct State {
     f4 acc[CT][2 * NDP];
-    float m[CT], l[CT];
+    float m[CT];
+    f4 l[CT];
     uint32_t nan[CT];                // bit rr: the output's dims of register rr are NaN (see give_nan)
 };
 
@@ -435,17 +430,12 @@ __device__ __forceinline__ void soften(State<NDP, CT> &st, f4 sc[CT][NTL], float
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
         const float mr = st.m[t] == -INFINITY ? 0.f : st.m[t], ms = mr * scale2;
-        float l = 0.f;
 #pragma unroll
         for (int u = 0; u < NTL; ++u)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const float p = __builtin_amdgcn_exp2f(EXACT ? (sc[t][u][s] - mr) * scale2
+            for (int s = 0; s < 4; ++s)
+                sc[t][u][s] = __builtin_amdgcn_exp2f(EXACT ? (sc[t][u][s] - mr) * scale2
                                                              : __builtin_fmaf(sc[t][u][s], scale2, -ms));
-                sc[t][u][s] = p;
-                l += p;
-            }
-        st.l[t] += l;
     }
 }
 
@@ -491,16 +481,29 @@ __device__ __forceinline__ void v_operands(const uint32_t v[2][4][Raw<NDP>::VW],
     for (int n = 0; n < 2 * NDP; ++n) out[n] = __builtin_bit_cast(bf8, u4{a[n][0], a[n][1], b[n][0], b[n][1]});
 }
 
-// B operands of p for tiles u0, u0 + 1
+// B operands of p for tiles u0, u0 + 1, in PP bf16 parts
 template <int PP>
-__device__ __forceinline__ void p_operands(const f4 &p0, const f4 &p1, bf8 out[PP]) {
+__device__ __forceinline__ void p_operands(f4 p0, f4 p1, bf8 out[PP]) {
+    float x[8] = {p0[0], p0[1], p0[2], p0[3], p1[0], p1[1], p1[2], p1[3]};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        __bf16 part[PP];
-        split_bf16<PP>(j < 4 ? p0[j & 3] : p1[j & 3], part);
+    for (int k = 0; k < PP; ++k) {
+        u4 w;
 #pragma unroll
-        for (int k = 0; k < PP; ++k) out[k][j] = part[k];
+        for (int j = 0; j < 4; ++j) {
+            const bf2 h = {(__bf16)x[2 * j], (__bf16)x[2 * j + 1]};
+            w[j] = __builtin_bit_cast(uint32_t, h);
+            if (k + 1 < PP) {
+                x[2 * j] -= __uint_as_float(w[j] << 16);
+                x[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        }
+        out[k] = __builtin_bit_cast(bf8, w);
     }
+}
+// A operand of ones: its product with p is sum_t p_t in every register
+__device__ __forceinline__ bf8 ones() {
+    const u4 w = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    return __builtin_bit_cast(bf8, w);
 }
 
 // V blocks that are NaN (byte 0xFF) would reach rows that do not see their
@@ -545,7 +548,7 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, co
         if (row >= p.n * a.G) continue;
         const int i = row / a.G, h = p.g * a.G + row - i * a.G;
         if (p.slot < 0) {
-            const float f = st.m[t] == -INFINITY ? 0.f : 512.f / st.l[t];
+            const float f = st.m[t] == -INFINITY ? 0.f : 512.f / st.l[t][0];
 #pragma unroll
             for (int rr = 0; rr < 4; ++rr) {
                 const int d0 = (4 * c + rr) * DL;
@@ -562,7 +565,7 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, co
             const int64_t at = p.slot * a.R + (row - p.row);
             if (c == 0) {
                 a.pml[2 * at] = st.m[t] == -INFINITY ? -INFINITY : st.m[t] * a.scale2;
-                a.pml[2 * at + 1] = st.l[t];
+                a.pml[2 * at + 1] = st.l[t][0];
             }
 #pragma unroll
             for (int rr = 0; rr < 4; ++rr) {
@@ -585,7 +588,7 @@ __device__ __forceinline__ void give_state(const State<NDP, CT> &st, float *ex, 
     for (int t = 0; t < CT; ++t) {
 #pragma unroll
         for (int n = 0; n < 2 * NDP; ++n) e[64 * (t * (2 * NDP + 1) + n)] = st.acc[t][n];
-        e[64 * (t * (2 * NDP + 1) + 2 * NDP)] = f4{st.m[t], st.l[t], 0.f, 0.f};
+        e[64 * (t * (2 * NDP + 1) + 2 * NDP)] = f4{st.m[t], st.l[t][0], 0.f, 0.f};
     }
 }
 template <int NDP, int CT>
@@ -609,7 +612,7 @@ __device__ __forceinline__ void take_state(State<NDP, CT> &st, const float *ex, 
 // are merged in LDS in wave order (2 and 3 into 0 and 1, then 1 into 0).
 template <int NDP, int CT, int PARTS>
 __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_rows(TreeArgs a) {
-    constexpr int PP = PARTS == 1 ? 2 : 3, NT = 2 * NDP;
+    constexpr int PP = PARTS, NT = 2 * NDP;
     __shared__ __attribute__((aligned(16))) float ex[2][CT * (NT + 1) * 256];
     __shared__ __attribute__((aligned(16))) int rowbuf[kWaves][2][kStep];
     const int lane = threadIdx.x & 63, c = lane >> 4;
@@ -621,7 +624,7 @@ __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_row
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
         st.m[t] = -INFINITY;
-        st.l[t] = 0.f;
+        st.l[t] = f4{0.f, 0.f, 0.f, 0.f};
         st.nan[t] = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
@@ -712,6 +715,9 @@ __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_row
                     bf8 pf[PP];
                     p_operands<PP>(sc[t][u], sc[t][u + 1], pf);
 #pragma unroll
+                    for (int k = 0; k < PP; ++k)
+                        st.l[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones(), pf[k], st.l[t], 0, 0, 0);
+#pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int k = 0; k < PP; ++k)
@@ -723,8 +729,6 @@ __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_row
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-#pragma unroll
-    for (int t = 0; t < CT; ++t) st.l[t] = col_sum(st.l[t]);
     give_nan<NDP, CT>(st);
 
     if (w >= 2) give_state<NDP, CT>(st, ex[w - 2], lane);
@@ -759,7 +763,7 @@ struct TileLds {
 
 template <int NDP, int CT, int WT, int PARTS>
 __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(TreeArgs a) {
-    constexpr int PP = PARTS == 1 ? 2 : 3, NT = 2 * NDP, WR = kWaves / WT, NTW = kNTL / WT;
+    constexpr int PP = PARTS, NT = 2 * NDP, WR = kWaves / WT, NTW = kNTL / WT;
     constexpr int KB = Raw<NDP>::KB, VW = Raw<NDP>::VW;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
     auto &lds = *reinterpret_cast<TileLds<NDP, CT, WT, PARTS> *>(lds_raw);
@@ -774,7 +778,7 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
         st.m[t] = -INFINITY;
-        st.l[t] = 0.f;
+        st.l[t] = f4{0.f, 0.f, 0.f, 0.f};
         st.nan[t] = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
@@ -891,7 +895,6 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
                         for (int j = 0; j < PARTS; ++j)
                             sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][j], sc[t][u], 0, 0, 0);
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
             const uint64_t valid = (uint64_t)(lds.valid[buf][0] | lds.valid[buf][1] << 16) |
                                    (uint64_t)(lds.valid[buf][2] | lds.valid[buf][3] << 16) << 32;
@@ -915,7 +918,12 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
             for (int u = 0; u < NTW; u += 2) {
                 bf8 pf[CT][PP];
 #pragma unroll
-                for (int t = 0; t < CT; ++t) p_operands<PP>(sc[t][u], sc[t][u + 1], pf[t]);
+                for (int t = 0; t < CT; ++t) {
+                    p_operands<PP>(sc[t][u], sc[t][u + 1], pf[t]);
+#pragma unroll
+                    for (int j = 0; j < PP; ++j)
+                        st.l[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones(), pf[t][j], st.l[t], 0, 0, 0);
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const bf8 vv = *reinterpret_cast<const bf8 *>(lds.v[buf][(wt * NTW + u) / 2 * NT + n][lane]);
@@ -924,13 +932,10 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
 #pragma unroll
                         for (int j = 0; j < PP; ++j)
                             st.acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[t][j], st.acc[t][n], 0, 0, 0);
-                    if (n % 4 == 3) __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
     }
-#pragma unroll
-    for (int t = 0; t < CT; ++t) st.l[t] = col_sum(st.l[t]);
     give_nan<NDP, CT>(st);
     if constexpr (WT == 2) {
         __syncthreads();

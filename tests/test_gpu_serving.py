@@ -14,8 +14,9 @@ Tolerances, from the number of roundings (u = 2^-24, one fp32 rounding):
   eps_t = |scale| (D + 2) u sum_d |q_d K_td|; the score scale and the reference
   of the exponents are fp32 numbers, so the exponent moves by up to
   4 u max |s|; exponential, T-term sums and merges: 8 (T + D) u, all relative
-  errors of the weights. bf16 queries: the weights enter the product to 2^-17.
-  |o - exact| <= 2 expm1(2 max eps + 8 u max |s| + 8 (T + D) u (+ 2^-16)) sum_t
+  errors of the weights. bf16 queries: a weight is rounded to bf16 (2^-8 at
+  most) in the product and in the sum that normalises, 2^-7 together.
+  |o - exact| <= 2 expm1(2 max eps + 8 u max |s| + 8 (T + D) u (+ 2^-7)) sum_t
   p_t |V_t|, plus the output's rounding (bf16: half of 2^-7 relative).
 """
 import math
@@ -343,7 +344,7 @@ class Batch:
         q = n64(self.q)
         D, G = self.D, self.Hq // self.Hkv
         out, tol = np.zeros(q.shape), np.zeros(q.shape)
-        low = 0.0 if self.q.dtype == F32 else 2.0 ** -16
+        low = 0.0 if self.q.dtype == F32 else 2.0 ** -7
         for b, (L, n) in enumerate(zip(self.lens, self.ns)):
             t = np.arange(L)
             pg = self.table[b, t // self.page]
@@ -556,7 +557,7 @@ class Server:
                     p /= p.sum()
                     want[r + i, h] = p @ V[see, h // G]
                     eps = self.D ** -0.5 * (self.D + 2) * U * np.abs(qk).sum(1).max()
-                    rel = np.expm1(2 * eps + 8 * U * np.abs(s).max() + 8 * (len(K) + self.D) * U + 2.0 ** -16)
+                    rel = np.expm1(2 * eps + 8 * U * np.abs(s).max() + 8 * (len(K) + self.D) * U + 2.0 ** -7)
                     tol[r + i, h] = 2 * rel * (p @ np.abs(V[see, h // G]))
             r += n
         tol += HALF[BF] * (np.abs(want) + tol)
