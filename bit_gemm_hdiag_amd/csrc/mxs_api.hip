@@ -110,8 +110,8 @@ mxs_status check_cache(const mxs_kv4_cache *c, const char *where) {
         return fail(MXS_ERR_UNSUPPORTED, "%s: cache of %lld pages of %d tokens of %d x %d values", where,
                     (long long)c->pages, c->page_size, c->H, c->D);
     if (!c->kc || !c->ks || !c->vc || !c->vs) return fail(MXS_ERR_ARG, "%s: cache pointer is NULL", where);
-    if (!aligned(c->kc, 16) || !aligned(c->vc, 16))
-        return fail(MXS_ERR_UNSUPPORTED, "%s: cache codes not 16-byte aligned", where);
+    if (!aligned(c->kc, 16) || !aligned(c->vc, 16) || !aligned(c->ks, 8) || !aligned(c->vs, 8))
+        return fail(MXS_ERR_UNSUPPORTED, "%s: cache codes not 16-byte or scales not 8-byte aligned", where);
     return MXS_OK;
 }
 

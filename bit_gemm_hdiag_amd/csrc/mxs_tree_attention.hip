@@ -48,8 +48,9 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;            // waves of a workgroup; they share its tokens
-constexpr int kNTL = 4;              // 16-token tiles of a wave's step
-constexpr int kStep = 16 * kNTL;     // tokens of a wave's step (one bit each in a 64-bit mask)
+constexpr int kRowTiles = 4;         // 16-token tiles of a wave's step in k_tree_rows
+constexpr int kNTL = 4;              // 16-token tiles of a stage in k_tree_tile
+constexpr int kStep = 16 * kNTL;     // tokens of a stage
 
 struct TreeArgs {
     const void *q;
@@ -89,9 +90,24 @@ __device__ __forceinline__ uint32_t cvt2(uint32_t bytes, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(bytes, scale, HI));
 }
 
+// e4m3 bytes of a word's even and odd dims: the codes, or (OFF) code + 8, whose
+// pattern is the number itself
+template <bool OFF>
+__device__ __forceinline__ void word_bytes(uint32_t w, uint32_t &even, uint32_t &odd) {
+    if constexpr (OFF) {
+        w ^= 0x88888888u;
+        even = w & 0x0F0F0F0Fu;
+        odd = (w >> 4) & 0x0F0F0F0Fu;
+    } else {
+        even = e4m3_codes(w);
+        odd = e4m3_codes(w >> 4);
+    }
+}
 // A word's 8 values, in the dim order 0 2 4 6 1 3 5 7
+template <bool OFF>
 __device__ __forceinline__ bf8 word_values(uint32_t w, float scale) {
-    const uint32_t e = e4m3_codes(w & 0x0F0F0F0Fu), o = e4m3_codes((w >> 4) & 0x0F0F0F0Fu);
+    uint32_t e, o;
+    word_bytes<OFF>(w, e, o);
     const u4 r = {cvt2<false>(e, scale), cvt2<true>(e, scale), cvt2<false>(o, scale), cvt2<true>(o, scale)};
     return __builtin_bit_cast(bf8, r);
 }
@@ -294,13 +310,44 @@ __device__ __forceinline__ void load_queries(const TreeArgs &a, const Place &p, 
     }
 }
 
-// Raw codes and scale bytes of a wave's step, as one lane loads them
+// Operands that take the offset of 8 codes out of the scores: A = the scales of
+// a lane's K blocks as bf16, three times each (a 0xFF byte gives Inf, and NaN in
+// the sum); B = -8 2^-9 times the sum of the lane's query dims of each block,
+// as three bf16 parts
+template <int NDP>
+__device__ __forceinline__ bf8 query_sums(const bf8 qf[NDP][1]) {
+    constexpr int KB = NDP == 8 ? 2 : 1;
+    bf8 r;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) r[s] = (__bf16)0.f;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+        float x = 0.f;
+#pragma unroll
+        for (int b = k * (NDP / KB); b < (k + 1) * (NDP / KB); ++b)
+#pragma unroll
+            for (int s = 0; s < 8; ++s) x += (float)qf[b][0][s];
+        __bf16 part[3];
+        split_bf16<3>(x * -0.015625f, part);
+#pragma unroll
+        for (int s = 0; s < 3; ++s) r[3 * k + s] = part[s];
+    }
+    return r;
+}
+template <int NDP>
+__device__ __forceinline__ bf8 scale_operand(const uint32_t e[NDP == 8 ? 2 : 1]) {
+    const uint32_t s = e[0] * 0x00800080u;
+    if constexpr (NDP == 8) {
+        const uint32_t x = e[1] << 7;
+        return __builtin_bit_cast(bf8, u4{s, (e[0] << 7) | (x << 16), x | (x << 16), 0u});
+    }
+    return __builtin_bit_cast(bf8, u4{s, e[0] << 7, 0u, 0u});
+}
+
 template <int NDP>
 struct Raw {
     static constexpr int KB = NDP == 8 ? 2 : 1;      // blocks a lane's K words touch
     static constexpr int VW = NDP == 8 ? 2 : 1;      // words a lane's V dims touch
-    uint32_t k[kNTL][NDP], kb[kNTL][KB];
-    uint32_t v[kNTL][4][VW], vb[kNTL][4];
 };
 
 // Byte offsets of a lane inside a cache row; dims past D fall back to the
@@ -322,54 +369,50 @@ struct LaneAt {
     }
 };
 
+// A lane's K words of the cache row at p, V word(s) of the row at p
 template <int NDP>
-__device__ __forceinline__ void load_k(Raw<NDP> &x, const TreeArgs &a, const LaneAt<NDP> &at, const uint8_t *kc,
-                                       const uint8_t *ks, const int *rows, int lane) {
-    const int i = lane & 15;
-    const uint32_t cs = (uint32_t)a.Hkv * (a.D / 2), ss = (uint32_t)a.Hkv * (a.D / 32);
+__device__ __forceinline__ void load_k(uint32_t k[NDP], const uint8_t *p, const LaneAt<NDP> &at) {
+    if constexpr (NDP == 2) {
+        const u2 w = *reinterpret_cast<const u2 *>(p + at.k[0]);
+        k[0] = w[0];
+        k[1] = w[1];
+    } else {
 #pragma unroll
-    for (int u = 0; u < kNTL; ++u) {
-        const uint64_t r = (uint32_t)max(rows[16 * u + i], 0);
-        const uint8_t *p = kc + r * cs;
-        if constexpr (NDP == 2) {
-            const u2 w = *reinterpret_cast<const u2 *>(p + at.k[0]);
-            x.k[u][0] = w[0];
-            x.k[u][1] = w[1];
-        } else {
+        for (int b = 0; b < Raw<NDP>::KB; ++b) {
+            const u4 w = *reinterpret_cast<const u4 *>(p + at.k[b]);
 #pragma unroll
-            for (int b = 0; b < Raw<NDP>::KB; ++b) {
-                const u4 w = *reinterpret_cast<const u4 *>(p + at.k[b]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x.k[u][4 * b + k] = w[k];
-            }
+            for (int j = 0; j < 4; ++j) k[4 * b + j] = w[j];
         }
-#pragma unroll
-        for (int b = 0; b < Raw<NDP>::KB; ++b) x.kb[u][b] = ks[r * ss + at.kb[b]];
     }
 }
-
 template <int NDP>
-__device__ __forceinline__ void load_v(Raw<NDP> &x, const TreeArgs &a, const LaneAt<NDP> &at, const uint8_t *vc,
-                                       const uint8_t *vs, const int *rows, int lane) {
-    const int c = lane >> 4;
-    const uint32_t cs = (uint32_t)a.Hkv * (a.D / 2), ss = (uint32_t)a.Hkv * (a.D / 32);
+__device__ __forceinline__ void load_v(uint32_t v[Raw<NDP>::VW], const uint8_t *p, const LaneAt<NDP> &at) {
+    if constexpr (NDP == 2) {
+        v[0] = *reinterpret_cast<const uint16_t *>(p + at.v);
+    } else if constexpr (NDP == 4) {
+        v[0] = *reinterpret_cast<const uint32_t *>(p + at.v);
+    } else {
+        const u2 w = *reinterpret_cast<const u2 *>(p + at.v);
+        v[0] = w[0];
+        v[1] = w[1];
+    }
+}
+// The D / 32 scale bytes of one row, in one or two words
+template <int NDP>
+__device__ __forceinline__ void load_scales(uint32_t x[Raw<NDP>::KB], const uint8_t *p, int nd) {
+    if (NDP == 8 && nd == 8) {
+        const u2 w = *reinterpret_cast<const u2 *>(p);
+        x[0] = w[0];
+        x[Raw<NDP>::KB - 1] = w[1];
+    } else if (nd == 4) {
+        x[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
 #pragma unroll
-    for (int u = 0; u < kNTL; ++u)
+        for (int i = 0; i < Raw<NDP>::KB; ++i) x[i] = 0;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint64_t r = (uint32_t)max(rows[16 * u + 4 * c + s], 0);
-            const uint8_t *p = vc + r * cs + at.v;
-            if constexpr (NDP == 2) {
-                x.v[u][s][0] = *reinterpret_cast<const uint16_t *>(p);
-            } else if constexpr (NDP == 4) {
-                x.v[u][s][0] = *reinterpret_cast<const uint32_t *>(p);
-            } else {
-                const u2 w = *reinterpret_cast<const u2 *>(p);
-                x.v[u][s][0] = w[0];
-                x.v[u][s][1] = w[1];
-            }
-            x.vb[u][s] = vs[r * ss + at.vb];
-        }
+        for (int i = 0; i < NDP; ++i)
+            if (i < nd) x[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    }
 }
 
 // Running state of a wave: columns r of its CT tiles. m is the reference the
@@ -381,6 +424,7 @@ struct State {
     f4 acc[CT][2 * NDP];
     float m[CT];
     f4 l[CT];
+    f4 w[CT];                        // Offset: sum of p 2^s of the lane's V block
     uint32_t nan[CT];                // bit rr: the output's dims of register rr are NaN (see give_nan)
 };
 
@@ -423,6 +467,7 @@ __device__ __forceinline__ void soften(State<NDP, CT> &st, f4 sc[CT][NTL], float
             const float f = st.m[t] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.m[t] - m) * scale2);
             st.m[t] = m;
             st.l[t] *= f;
+            st.w[t] *= f;
 #pragma unroll
             for (int n = 0; n < 2 * NDP; ++n) st.acc[t][n] *= f;
         }
@@ -441,8 +486,8 @@ __device__ __forceinline__ void soften(State<NDP, CT> &st, f4 sc[CT][NTL], float
 
 // V of tokens 4 c + s of one tile, in token pairs: o[n] = dim i DL + n of
 // tokens (0, 1) and (2, 3)
-template <int NDP>
-__device__ __forceinline__ void v_pairs(const uint32_t v[4][Raw<NDP>::VW], const uint32_t vb[4],
+template <int NDP, bool OFF>
+__device__ __forceinline__ void v_pairs(const uint32_t v[4][Raw<NDP>::VW], const float sc[4],
                                         uint32_t o[2 * NDP][2]) {
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
@@ -451,9 +496,9 @@ __device__ __forceinline__ void v_pairs(const uint32_t v[4][Raw<NDP>::VW], const
             uint32_t x[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t word = v[j + h][w];
-                const float s = scale_of(vb[j + h]);
-                const uint32_t e = e4m3_codes(word & 0x0F0F0F0Fu), d = e4m3_codes((word >> 4) & 0x0F0F0F0Fu);
+                const float s = sc[j + h];
+                uint32_t e, d;
+                word_bytes<OFF>(v[j + h][w], e, d);
                 x[h][0] = cvt2<false>(e, s);                          // dims 0, 2
                 x[h][1] = cvt2<false>(d, s);                          // dims 1, 3
                 if constexpr (NDP != 2) {
@@ -470,15 +515,25 @@ __device__ __forceinline__ void v_pairs(const uint32_t v[4][Raw<NDP>::VW], const
         }
     }
 }
-// The 2 NDP V operands of two tiles (tile n = dim i DL + n of lane (i, c))
-template <int NDP>
+// The 2 NDP V operands of two tiles (tile n = dim i DL + n of lane (i, c)); OFF:
+// `off` is the operand of the lane's scales
+template <int NDP, bool OFF>
 __device__ __forceinline__ void v_operands(const uint32_t v[2][4][Raw<NDP>::VW], const uint32_t vb[2][4],
-                                           bf8 out[2 * NDP]) {
-    uint32_t a[2 * NDP][2], b[2 * NDP][2];
-    v_pairs<NDP>(v[0], vb[0], a);
-    v_pairs<NDP>(v[1], vb[1], b);
+                                           bf8 out[2 * NDP], bf8 &off) {
+    uint32_t o[2][2 * NDP][2], w[2][2];
 #pragma unroll
-    for (int n = 0; n < 2 * NDP; ++n) out[n] = __builtin_bit_cast(bf8, u4{a[n][0], a[n][1], b[n][0], b[n][1]});
+    for (int u = 0; u < 2; ++u) {
+        float sc[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) sc[s] = scale_of(vb[u][s]);
+        v_pairs<NDP, OFF>(v[u], sc, o[u]);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            w[u][s] = __builtin_amdgcn_perm(__float_as_uint(sc[2 * s + 1]), __float_as_uint(sc[2 * s]), 0x07060302u);
+    }
+#pragma unroll
+    for (int n = 0; n < 2 * NDP; ++n) out[n] = __builtin_bit_cast(bf8, u4{o[0][n][0], o[0][n][1], o[1][n][0], o[1][n][1]});
+    off = __builtin_bit_cast(bf8, u4{w[0][0], w[0][1], w[1][0], w[1][1]});
 }
 
 // B operands of p for tiles u0, u0 + 1, in PP bf16 parts
@@ -607,141 +662,206 @@ __device__ __forceinline__ void take_state(State<NDP, CT> &st, const float *ex, 
     }
 }
 
-// Few rows: the waves of a workgroup take its row tile's 16 CT rows and turns
-// of 64 tokens, each dequantising its own tokens in registers; their states
+// Few rows: the waves of a workgroup take its tile's 16 CT rows and turns of
+// 16 NTL tokens, each dequantising its own tokens in registers; their states
 // are merged in LDS in wave order (2 and 3 into 0 and 1, then 1 into 0).
-template <int NDP, int CT, int PARTS>
+// Lane = token finds the pool rows and loads both scale rows, one load each,
+// and passes them to the lanes that need them through LDS.
+// Here the vector ALU counts, and codes cost it least with 8 added, where the
+// e4m3 pattern is the number itself: K enters as (code + 8) 2^(s - 9) and a
+// product of the lane's block scales with -8 times the sum of its query dims
+// (in three bf16 parts) takes the excess out of the scores; V enters likewise,
+// and a product of p with the block scales (State::w) takes it out at the end.
+// fp32 queries keep the exact codes.
+template <int NDP, int CT, int NTL, int PARTS>
 __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_rows(TreeArgs a) {
-    constexpr int PP = PARTS, NT = 2 * NDP;
+    constexpr int PP = PARTS, NT = 2 * NDP, KB = Raw<NDP>::KB, VW = Raw<NDP>::VW, STEP = 16 * NTL;
+    constexpr bool OFF = PARTS == 1;
+    constexpr uint64_t ALL = ~0ull >> (64 - STEP);
     __shared__ __attribute__((aligned(16))) float ex[2][CT * (NT + 1) * 256];
-    __shared__ __attribute__((aligned(16))) int rowbuf[kWaves][2][kStep];
-    const int lane = threadIdx.x & 63, c = lane >> 4;
+    __shared__ __attribute__((aligned(16))) int rowbuf[kWaves][2][STEP];
+    __shared__ __attribute__((aligned(16))) uint32_t scbuf[kWaves][2][STEP][KB];       // scale rows of K, of V
+    const int lane = threadIdx.x & 63, i = lane & 15, c = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nd = a.D / 32;
     for_each_piece(a, lane, [&](const Place &p) {
-    const int row0 = p.row;
-
-    State<NDP, CT> st;
-#pragma unroll
-    for (int t = 0; t < CT; ++t) {
-        st.m[t] = -INFINITY;
-        st.l[t] = f4{0.f, 0.f, 0.f, 0.f};
-        st.nan[t] = 0;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
-    }
-    const LaneAt<NDP> at(lane, a.D);
-    const uint8_t *kc = a.kc + p.g * (a.D / 2), *vc = a.vc + p.g * (a.D / 2);
-    const uint8_t *ks = a.ks + p.g * (a.D / 32), *vs = a.vs + p.g * (a.D / 32);
-    const int32_t *table = a.table + (int64_t)p.b * a.ldt;
-
-    // pool row of token lt + lane (-1: past the range, or no valid page)
-    auto page_at = [&](int lt) {
-        const int t = lt + lane;
-        return t < p.t1 ? table[page_of(a, t)] : -1;
-    };
-    auto row_at = [&](int lt, int page) {
-        const int t = lt + lane;
-        return (uint32_t)page < (uint64_t)a.pages ? page * a.ps + (t - page_of(a, t) * a.ps) : -1;
-    };
-
-    int lt = p.t0 + w * kStep;
-    if (lt < p.t1) {
-        Raw<NDP> x;
-        int row = row_at(lt, page_at(lt));
-        uint64_t valid = __ballot(row >= 0);
-        rowbuf[w][0][lane] = row;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        load_k<NDP>(x, a, at, kc, ks, rowbuf[w][0], lane);
-        load_v<NDP>(x, a, at, vc, vs, rowbuf[w][0], lane);
-        int page = page_at(lt + kWaves * kStep);
-        bf8 qf[CT][NDP][PARTS];
-        load_queries<NDP, CT, PARTS>(a, p, row0, lane, qf);
-        int iq[CT];
+        State<NDP, CT> st;
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
-            const int rw = row0 + 16 * t + (lane & 15);
-            iq[t] = rw < p.n * a.G ? rw / a.G : 0;
+            st.m[t] = -INFINITY;
+            st.l[t] = f4{0.f, 0.f, 0.f, 0.f};
+            st.w[t] = f4{0.f, 0.f, 0.f, 0.f};
+            st.nan[t] = 0;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
         }
+        const LaneAt<NDP> at(lane, a.D);
+        const uint8_t *kc = a.kc + p.g * (a.D / 2), *vc = a.vc + p.g * (a.D / 2);
+        const uint8_t *ks = a.ks + p.g * nd, *vs = a.vs + p.g * nd;
+        const uint32_t cs = (uint32_t)a.Hkv * (a.D / 2), ss = (uint32_t)a.Hkv * nd;
+        const int32_t *table = a.table + (int64_t)p.b * a.ldt;
 
-        int buf = 1;
-        for (; lt < p.t1; lt += kWaves * kStep, buf ^= 1) {
-            const int next = lt + kWaves * kStep;
-            row = row_at(next, page);
-            rowbuf[w][buf][lane] = row;
-            page = page_at(next + kWaves * kStep);
+        // pool row of token lt + lane (-1: past the range, or no valid page)
+        auto page_at = [&](int lt) {
+            const int t = lt + lane;
+            return lane < STEP && t < p.t1 ? table[page_of(a, t)] : -1;
+        };
+        auto row_at = [&](int lt, int page) {
+            const int t = lt + lane;
+            return (uint32_t)page < (uint64_t)a.pages ? page * a.ps + (t - page_of(a, t) * a.ps) : -1;
+        };
+        uint32_t k[NTL][NDP], v[NTL][4][VW], ksc[KB], vsc[KB];
+        auto load_ks = [&](int row, const int *rows) {
+            const uint64_t r = (uint32_t)max(row, 0);
+            load_scales<NDP>(ksc, ks + r * ss, nd);
+            load_scales<NDP>(vsc, vs + r * ss, nd);
+#pragma unroll
+            for (int u = 0; u < NTL; ++u) load_k<NDP>(k[u], kc + (uint64_t)(uint32_t)max(rows[16 * u + i], 0) * cs, at);
+        };
+        auto load_vs = [&](const int *rows) {
+#pragma unroll
+            for (int u = 0; u < NTL; ++u)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    load_v<NDP>(v[u][s], vc + (uint64_t)(uint32_t)max(rows[16 * u + 4 * c + s], 0) * cs, at);
+        };
+
+        int lt = p.t0 + w * STEP;
+        if (lt < p.t1) {
+            int row = row_at(lt, page_at(lt));
+            uint64_t valid = __ballot(row >= 0);
+            if (lane < STEP) rowbuf[w][0][lane] = row;
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-
-            f4 sc[CT][kNTL];
+            load_ks(row, rowbuf[w][0]);
+            load_vs(rowbuf[w][0]);
+            int page = page_at(lt + kWaves * STEP);
+            bf8 qf[CT][NDP][PARTS], qoff[CT];
+            load_queries<NDP, CT, PARTS>(a, p, p.row, lane, qf);
+            int iq[CT];
 #pragma unroll
-            for (int u = 0; u < kNTL; ++u) {
-#pragma unroll
-                for (int t = 0; t < CT; ++t) sc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int b = 0; b < NDP; ++b) {
-                    const bf8 kv = word_values(x.k[u][b], scale_of(x.kb[u][Raw<NDP>::KB == 2 ? b >> 2 : 0]));
-#pragma unroll
-                    for (int t = 0; t < CT; ++t)
-#pragma unroll
-                        for (int k = 0; k < PARTS; ++k)
-                            sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][k], sc[t][u], 0, 0, 0);
-                }
+            for (int t = 0; t < CT; ++t) {
+                const int rw = p.row + 16 * t + i;
+                iq[t] = rw < p.n * a.G ? rw / a.G : 0;
+                if constexpr (OFF) qoff[t] = query_sums<NDP>(qf[t]);
             }
-            load_k<NDP>(x, a, at, kc, ks, rowbuf[w][buf], lane);
-            __builtin_amdgcn_sched_barrier(0);
 
-            if (valid != ~0ull || lt + kStep > p.ctx) {
-                uint64_t seen[CT];
+            int buf = 1;
+            for (; lt < p.t1; lt += kWaves * STEP, buf ^= 1) {
+                const int next = lt + kWaves * STEP;
+                if (lane < STEP) {
 #pragma unroll
-                for (int t = 0; t < CT; ++t) seen[t] = valid & mask_window(a, p, iq[t], lt);
-                hide<CT, kNTL>(sc, seen, c);
-#pragma unroll
-                for (int u = 0; u < kNTL; ++u)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        if (!((valid >> (16 * u + 4 * c + s)) & 1)) x.vb[u][s] = 0;
-                        const uint64_t bad = take_nan(x.vb[u][s]);
-                        if (bad)
-                            for (int k = 0; k < 4; ++k)
-                                note_nan<NDP, CT>(st, (uint32_t)(bad >> (16 * k)) & 0xFFFFu, 16 * u + 4 * k + s, seen, c);
+                    for (int b = 0; b < KB; ++b) {
+                        scbuf[w][0][lane][b] = ksc[b];
+                        scbuf[w][1][lane][b] = vsc[b];
                     }
-            }
-            soften<NDP, CT, kNTL, PARTS == 3>(st, sc, a.scale2);
-#pragma unroll
-            for (int u = 0; u < kNTL; u += 2) {
-                bf8 vf[NT];
-                v_operands<NDP>(&x.v[u], &x.vb[u], vf);
-#pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    bf8 pf[PP];
-                    p_operands<PP>(sc[t][u], sc[t][u + 1], pf);
-#pragma unroll
-                    for (int k = 0; k < PP; ++k)
-                        st.l[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones(), pf[k], st.l[t], 0, 0, 0);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int k = 0; k < PP; ++k)
-                            st.acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[n], pf[k], st.acc[t][n], 0, 0, 0);
                 }
-            }
-            load_v<NDP>(x, a, at, vc, vs, rowbuf[w][buf], lane);
-            valid = __ballot(row >= 0);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-    give_nan<NDP, CT>(st);
+                row = row_at(next, page);
+                if (lane < STEP) rowbuf[w][buf][lane] = row;
+                page = page_at(next + kWaves * STEP);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                const uint8_t *kb = reinterpret_cast<const uint8_t *>(scbuf[w][0]);
+                const uint8_t *vbp = reinterpret_cast<const uint8_t *>(scbuf[w][1]);
 
-    if (w >= 2) give_state<NDP, CT>(st, ex[w - 2], lane);
-    __syncthreads();
-    if (w < 2) take_state<NDP, CT>(st, ex[w], lane, a.scale2);
-    __syncthreads();
-    if (w == 1) give_state<NDP, CT>(st, ex[0], lane);
-    __syncthreads();
-    if (w == 0) {
-        take_state<NDP, CT>(st, ex[0], lane, a.scale2);
-        store_rows<NDP, CT, PARTS>(a, p, st, row0, lane);
-    }
-    __syncthreads();                 // the next piece writes the same LDS
+                f4 sc[CT][NTL];
+#pragma unroll
+                for (int u = 0; u < NTL; ++u) {
+                    uint32_t e[KB];
+#pragma unroll
+                    for (int b = 0; b < KB; ++b) e[b] = kb[4 * KB * (16 * u + i) + at.kb[b]];
+#pragma unroll
+                    for (int t = 0; t < CT; ++t) sc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int b = 0; b < NDP; ++b) {
+                        const bf8 kv = word_values<OFF>(k[u][b], scale_of(e[KB == 2 ? b >> 2 : 0]));
+#pragma unroll
+                        for (int t = 0; t < CT; ++t)
+#pragma unroll
+                            for (int j = 0; j < PARTS; ++j)
+                                sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][j], sc[t][u], 0, 0, 0);
+                    }
+                    if constexpr (OFF) {
+                        const bf8 es = scale_operand<NDP>(e);
+#pragma unroll
+                        for (int t = 0; t < CT; ++t)
+                            sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(es, qoff[t], sc[t][u], 0, 0, 0);
+                    }
+                }
+                uint32_t vb[NTL][4];
+#pragma unroll
+                for (int u = 0; u < NTL; ++u)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) vb[u][s] = vbp[4 * KB * (16 * u + 4 * c + s) + at.vb];
+                load_ks(row, rowbuf[w][buf]);
+                __builtin_amdgcn_sched_barrier(0);
+
+                if (valid != ALL || lt + STEP > p.ctx) {
+                    uint64_t seen[CT];
+#pragma unroll
+                    for (int t = 0; t < CT; ++t) seen[t] = valid & mask_window(a, p, iq[t], lt);
+                    hide<CT, NTL>(sc, seen, c);
+#pragma unroll
+                    for (int u = 0; u < NTL; ++u)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            if (!((valid >> (16 * u + 4 * c + s)) & 1)) vb[u][s] = 0;
+                            const uint64_t bad = take_nan(vb[u][s]);
+                            if (bad)
+                                for (int j = 0; j < 4; ++j)
+                                    note_nan<NDP, CT>(st, (uint32_t)(bad >> (16 * j)) & 0xFFFFu, 16 * u + 4 * j + s,
+                                                      seen, c);
+                        }
+                }
+                soften<NDP, CT, NTL, PARTS == 3>(st, sc, a.scale2);
+#pragma unroll
+                for (int u = 0; u < NTL; u += 2) {
+                    bf8 vf[NT], off;
+                    v_operands<NDP, OFF>(&v[u], &vb[u], vf, off);
+#pragma unroll
+                    for (int t = 0; t < CT; ++t) {
+                        bf8 pf[PP];
+                        p_operands<PP>(sc[t][u], sc[t][u + 1], pf);
+#pragma unroll
+                        for (int j = 0; j < PP; ++j)
+                            st.l[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones(), pf[j], st.l[t], 0, 0, 0);
+                        if constexpr (OFF)
+                            st.w[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(off, pf[0], st.w[t], 0, 0, 0);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int j = 0; j < PP; ++j)
+                                st.acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[n], pf[j], st.acc[t][n], 0, 0, 0);
+                    }
+                }
+                load_vs(rowbuf[w][buf]);
+                valid = __ballot(row >= 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if constexpr (OFF) {
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    st.acc[t][n] -= st.w[t] * 0.015625f;                                // 8 / 2^9
+                    // blocks of byte 0 (zeros) leave up to l 2^-133: outputs of 2^-124 are 0
+#pragma unroll
+                    for (int rr = 0; rr < 4; ++rr)
+                        st.acc[t][n][rr] = fabsf(st.acc[t][n][rr]) <= st.l[t][0] * 0x1p-132f ? 0.f : st.acc[t][n][rr];
+                }
+        }
+        give_nan<NDP, CT>(st);
+
+        if (w >= 2) give_state<NDP, CT>(st, ex[w - 2], lane);
+        __syncthreads();
+        if (w < 2) take_state<NDP, CT>(st, ex[w], lane, a.scale2);
+        __syncthreads();
+        if (w == 1) give_state<NDP, CT>(st, ex[0], lane);
+        __syncthreads();
+        if (w == 0) {
+            take_state<NDP, CT>(st, ex[0], lane, a.scale2);
+            store_rows<NDP, CT, PARTS>(a, p, st, p.row, lane);
+        }
+        __syncthreads();                 // the next piece writes the same LDS
     });
 }
 
@@ -779,6 +899,7 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
     for (int t = 0; t < CT; ++t) {
         st.m[t] = -INFINITY;
         st.l[t] = f4{0.f, 0.f, 0.f, 0.f};
+        st.w[t] = f4{0.f, 0.f, 0.f, 0.f};
         st.nan[t] = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
@@ -802,34 +923,13 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
         uint32_t k[NDP], kb[KB], v[4][VW], vb[4];
         auto load = [&](int row) {
             const uint64_t r = (uint32_t)max(row, 0);
-            const uint8_t *pk = kc + r * cs;
-            if constexpr (NDP == 2) {
-                const u2 x = *reinterpret_cast<const u2 *>(pk + at.k[0]);
-                k[0] = x[0];
-                k[1] = x[1];
-            } else {
-#pragma unroll
-                for (int b = 0; b < KB; ++b) {
-                    const u4 x = *reinterpret_cast<const u4 *>(pk + at.k[b]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) k[4 * b + j] = x[j];
-                }
-            }
+            load_k<NDP>(k, kc + r * cs, at);
 #pragma unroll
             for (int b = 0; b < KB; ++b) kb[b] = ks[r * ss + at.kb[b]];
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const uint64_t rv = (uint32_t)max(__shfl(row, 4 * c + s), 0);
-                const uint8_t *pv = vc + rv * cs + at.v;
-                if constexpr (NDP == 2) {
-                    v[s][0] = *reinterpret_cast<const uint16_t *>(pv);
-                } else if constexpr (NDP == 4) {
-                    v[s][0] = *reinterpret_cast<const uint32_t *>(pv);
-                } else {
-                    const u2 x = *reinterpret_cast<const u2 *>(pv);
-                    v[s][0] = x[0];
-                    v[s][1] = x[1];
-                }
+                load_v<NDP>(v[s], vc + rv * cs, at);
                 vb[s] = vs[rv * ss + at.vb];
             }
         };
@@ -865,11 +965,14 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
 #pragma unroll
             for (int b = 0; b < NDP; ++b)
                 *reinterpret_cast<bf8 *>(lds.k[buf][w * NDP + b][lane]) =
-                    word_values(k[b], scale_of(kb[KB == 2 ? b >> 2 : 0]));
+                    word_values<false>(k[b], scale_of(kb[KB == 2 ? b >> 2 : 0]));
             __builtin_amdgcn_sched_barrier(0);
             {
                 uint32_t o[NT][2];
-                v_pairs<NDP>(v, vb, o);
+                float vsc[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) vsc[s] = scale_of(vb[s]);
+                v_pairs<NDP, false>(v, vsc, o);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     *reinterpret_cast<u2 *>(&lds.v[buf][(w >> 1) * NT + n][lane][2 * (w & 1)]) = u2{o[n][0], o[n][1]};
@@ -1038,7 +1141,7 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
         p.WT = 0;
         p.CT = rows > 16 ? 2 : 1;
         p.R = 16 * p.CT;
-        p.U = kWaves * kStep;
+        p.U = kWaves * 16 * kRowTiles;
         p.minu = 1;
     } else {
         p.CT = bf ? 2 : 1;
@@ -1057,7 +1160,7 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
 
 template <int NDP, int CT, int PARTS>
 hipError_t rows_go(const TreeArgs &a, unsigned grid, hipStream_t st) {
-    hipLaunchKernelGGL((k_tree_rows<NDP, CT, PARTS>), dim3(grid), dim3(64 * kWaves), 0, st, a);
+    hipLaunchKernelGGL((k_tree_rows<NDP, CT, kRowTiles, PARTS>), dim3(grid), dim3(64 * kWaves), 0, st, a);
     return hipGetLastError();
 }
 template <int NDP, int CT, int WT, int PARTS>

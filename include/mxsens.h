@@ -430,9 +430,9 @@ mxs_status mxs_attend_kv4(const float *q, const uint8_t *kc, const uint8_t *ks, 
  * + offset is one token: codes [slot, H, D/2] and scale bytes [slot, H, D/32]
  * for keys (kc, ks) and values (vc, vs), the layout of mxs_quantize_kv (whose
  * output for T tokens is a pool of one page of T tokens, or of any pages that
- * divide T). Device memory owned by the caller, codes 16-byte aligned, at
- * most 2^31 - 1 slots, D % 32 == 0, H D <= 524280. Host struct, read during
- * the call.
+ * divide T). Device memory owned by the caller, codes 16-byte and scales
+ * 8-byte aligned, at most 2^31 - 1 slots, D % 32 == 0, H D <= 524280. Host
+ * struct, read during the call.
  */
 typedef struct mxs_kv4_cache {
     int64_t pages;

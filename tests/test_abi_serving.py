@@ -26,7 +26,7 @@ def cache(**kw):
 
 BAD_CACHES = [(dict(pages=0), SHAPE), (dict(page_size=0), SHAPE), (dict(H=0), SHAPE), (dict(D=48), SHAPE),
               (dict(D=0), SHAPE), (dict(reserved=1), ARG), (dict(kc=None), ARG), (dict(vs=None), ARG),
-              (dict(kc=P(0x10008)), UNSUPPORTED), (dict(vc=P(0x10004)), UNSUPPORTED),
+              (dict(kc=P(0x10008)), UNSUPPORTED), (dict(ks=P(0x10004)), UNSUPPORTED), (dict(vc=P(0x10004)), UNSUPPORTED),
               (dict(pages=1 << 28), UNSUPPORTED), (dict(H=20000), UNSUPPORTED)]
 
 

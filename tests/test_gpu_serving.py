@@ -15,7 +15,9 @@ Tolerances, from the number of roundings (u = 2^-24, one fp32 rounding):
   of the exponents are fp32 numbers, so the exponent moves by up to
   4 u max |s|; exponential, T-term sums and merges: 8 (T + D) u, all relative
   errors of the weights. bf16 queries: a weight is rounded to bf16 (2^-8 at
-  most) in the product and in the sum that normalises, 2^-7 together.
+  most) in the product and in the sum that normalises, 2^-7 together; codes may
+  enter with 8 added, taken out by further products, so the sums' terms are
+  at most |q| (|K| + 16 step) and p (|V| + 16 step), step = 2^s the block's scale.
   |o - exact| <= 2 expm1(2 max eps + 8 u max |s| + 8 (T + D) u (+ 2^-7)) sum_t
   p_t |V_t|, plus the output's rounding (bf16: half of 2^-7 relative).
 """
@@ -351,6 +353,7 @@ class Batch:
             valid = (pg >= 0) & (pg < pages)
             slot = np.where(valid, pg, 0).astype(np.int64) * self.page + t % self.page
             K, V = values64(kc[slot], ks[slot]), values64(vc[slot], vs[slot])
+            sk, sv = (np.repeat(np.exp2(x[slot].astype(np.float64) - 127.0), 32, -1) for x in (ks, vs))
             for i in range(n):
                 row = self.cu[b] + i
                 see = valid.copy()
@@ -365,9 +368,13 @@ class Batch:
                         p = np.exp(s - s.max())
                     p /= p.sum()
                     out[row, h] = p @ V[see, g]
-                    eps = abs(scale) * (D + 2) * U * np.abs(qk).sum(1).max()
-                    rel = np.expm1(2 * eps + 8 * U * np.abs(s).max() + 8 * (L + D) * U + low)
-                    tol[row, h] = 2 * rel * (p @ np.abs(V[see, g]))
+                    mk, mv = np.abs(K[see, g]), np.abs(V[see, g])
+                    if low:
+                        mk, mv = mk + 16 * sk[see, g], mv + 16 * sv[see, g]
+                    eps = abs(scale) * (D + 2) * U * (mk * np.abs(q[row, h])).sum(1).max()
+                    sums = 8 * (L + D) * U
+                    rel = np.expm1(2 * eps + 8 * U * np.abs(s).max() + sums + low)
+                    tol[row, h] = 2 * rel * (p @ np.abs(V[see, g])) + 2 * sums * (p @ mv)
         return out, tol + HALF[self.q.dtype] * (np.abs(out) + tol) + 1e-30
 
     def check(self, got, scale=None):
@@ -690,3 +697,24 @@ def test_slots_past_four_gigabytes(mx):
     far = mx.mxs_attend_kv4_tree(q, c, tokens(pages - 1), i32(page), i32(0, 2), 0.0625, max_q=2, max_len=page)
     near = mx.mxs_attend_kv4_tree(q, small, tokens(0), i32(page), i32(0, 2), 0.0625, max_q=2, max_len=page)
     assert torch.equal(far, near)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [1, 8, 40])
+def test_tree_attention_zero_values_give_zero(mx, dtype, rows):
+    """Blocks of zeros (byte 0) and tiny values: no offset or scale is left over."""
+    b = Batch(mx, [200], [rows], 4, 2, 64, 16, dtype, "tree", 70)
+    b.cache.vc[:] = 0
+    b.cache.vs[:] = 0
+    assert not b.run(mx).any()
+    b.cache.kc[:] = 0
+    b.cache.ks[:] = 0
+    b.cache.vs[:] = 130                                          # zeros at a scale of 8
+    assert not b.run(mx).any()
+    b.cache.vc[..., 0] = 0x21                                    # 1 and 2, times 8, in every token
+    out = n64(b.run(mx))
+    # constant columns: the ratio of two T-term fp32 sums over the same weights (each
+    # within 8 (T + D) u of its exact value), then the output's rounding
+    tol = 2 * 8 * (200 + 64) * U + (1 + 2 ** -8) * HALF[dtype]
+    assert np.all(np.abs(out[..., 0] - 8.0) <= 8.0 * tol)
+    assert np.all(np.abs(out[..., 1] - 16.0) <= 16.0 * tol) and not out[..., 2:].any()
