@@ -68,9 +68,10 @@ struct TreeArgs {
     float scale2;                    // |scale| log2(e) 2^9
     bool negate;                     // scale < 0: queries enter negated
     int R, U, P, minu;               // rows of a tile, tokens of a unit, workgroups, units of a share (at least)
+    int HG;                          // KV heads of a tile
     void *out;
     int64_t ldo;
-    float *po, *pml;                 // [2 share + k, R, D], [2 share + k, R, (m, l)]
+    float *po, *pml;                 // [2 share + k, HG, R, D], [2 share + k, HG, R, (m, l)]
 };
 
 // t / ps for 0 <= t < 2^31: pmul = ceil(2^(31 + l) / ps), l = ceil(log2 ps)
@@ -135,8 +136,8 @@ __device__ __forceinline__ float col_max(float x) {
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 // ------------------------------------------------------------------ shares
-// The work of a call is a line of units: sequence by sequence, tile (KV head,
-// then R of the head's n G rows) by tile, U tokens by U tokens (a sequence of
+// The work of a call is a line of units: sequence by sequence, tile (HG KV
+// heads, R of the n G rows of each) by tile, U tokens by U tokens (a sequence of
 // no tokens has one empty unit a tile, which writes its zeros). It is cut into
 // P' equal shares, one a workgroup, from the lengths that the call finds on the
 // device: ragged batches are balanced, and a captured graph stays so when its
@@ -160,7 +161,9 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs &a, int b) {
     s.T = s.len > 0 ? ((uint32_t)s.len + a.U - 1) / (uint32_t)a.U : 1u;
     return s;
 }
-__device__ __forceinline__ uint32_t units_of(const TreeArgs &a, const Seq &s) { return (uint32_t)a.Hkv * s.nrt * s.T; }
+__device__ __forceinline__ uint32_t units_of(const TreeArgs &a, const Seq &s) {
+    return (uint32_t)(a.Hkv / a.HG) * s.nrt * s.T;
+}
 
 // inclusive sum over the wave's lanes
 __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
@@ -216,7 +219,7 @@ __device__ __forceinline__ int find_seq(const TreeArgs &a, uint32_t x, int lane,
 
 // A piece of a share: tokens t0 .. t1 - 1 of one tile
 struct Place {
-    int b, g, row;                   // sequence, KV head, first row of the tile
+    int b, g, row;                   // sequence, first KV head and first row of the tile
     int len, ctx, n, q0;             // cached tokens, context, query tokens, first query token
     int t0, t1;
     int64_t slot;                    // workspace slot, -1: the whole tile
@@ -246,7 +249,7 @@ __device__ __forceinline__ void for_each_piece(const TreeArgs &a, int lane, F f)
         auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
         Place pl;
         pl.b = uni(b);
-        pl.g = uni((int)(tile / s.nrt));
+        pl.g = uni((int)(tile / s.nrt) * a.HG);
         pl.row = uni((int)(tile % s.nrt) * a.R);
         pl.len = uni(s.len);
         pl.n = uni(s.n);
@@ -281,14 +284,14 @@ __device__ __forceinline__ uint64_t mask_window(const TreeArgs &a, const Place &
 // Query rows of a wave as B operands: lane (r, c), step b holds the dims of
 // word c NDP + b of row r (zero past the rows and past D)
 template <int NDP, int CT, int PARTS>
-__device__ __forceinline__ void load_queries(const TreeArgs &a, const Place &p, int row0, int lane,
+__device__ __forceinline__ void load_queries(const TreeArgs &a, const Place &p, int g, int row0, int lane,
                                              bf8 qf[CT][NDP][PARTS]) {
     const int r = lane & 15, c = lane >> 4;
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
         const int row = row0 + 16 * t + r;
         const bool on = row < p.n * a.G;
-        const int i = on ? row / a.G : 0, h = on ? p.g * a.G + row - i * a.G : 0;
+        const int i = on ? row / a.G : 0, h = on ? g * a.G + row - i * a.G : 0;
         const int64_t at = (int64_t)(on ? p.q0 + i : 0) * a.ldq + (int64_t)h * a.D;
 #pragma unroll
         for (int b = 0; b < NDP; ++b) {
@@ -593,15 +596,15 @@ __device__ __forceinline__ void give_nan(State<NDP, CT> &st) {
 // A whole tile: normalised, rounded once, to `out` (0 where nothing was seen);
 // a piece: (m, l) and the unnormalised sums for k_tree_join.
 template <int NDP, int CT, int PARTS>
-__device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, const State<NDP, CT> &st, int row0,
-                                           int lane) {
+__device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, const State<NDP, CT> &st, int g,
+                                           int row0, int lane) {
     constexpr int DL = 2 * NDP;
     const int r = lane & 15, c = lane >> 4;
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
         const int row = row0 + 16 * t + r;
         if (row >= p.n * a.G) continue;
-        const int i = row / a.G, h = p.g * a.G + row - i * a.G;
+        const int i = row / a.G, h = g * a.G + row - i * a.G;
         if (p.slot < 0) {
             const float f = st.m[t] == -INFINITY ? 0.f : 512.f / st.l[t][0];
 #pragma unroll
@@ -617,7 +620,7 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, co
                 }
             }
         } else {
-            const int64_t at = p.slot * a.R + (row - p.row);
+            const int64_t at = (p.slot * a.HG + (g - p.g)) * a.R + (row - p.row);
             if (c == 0) {
                 a.pml[2 * at] = st.m[t] == -INFINITY ? -INFINITY : st.m[t] * a.scale2;
                 a.pml[2 * at + 1] = st.l[t][0];
@@ -662,9 +665,12 @@ __device__ __forceinline__ void take_state(State<NDP, CT> &st, const float *ex, 
     }
 }
 
-// Few rows: the waves of a workgroup take its tile's 16 CT rows and turns of
-// 16 NTL tokens, each dequantising its own tokens in registers; their states
-// are merged in LDS in wave order (2 and 3 into 0 and 1, then 1 into 0).
+// Few rows: wave (head w % HG, part w / HG) takes the 16 CT rows of one of the
+// tile's HG heads and turns of 16 NTL tokens, which it dequantises in registers.
+// The heads of a token lie side by side in its cache row: read together they
+// use whole 128-byte lines (a head alone has 64 bytes of codes and 4 of scales in
+// a row at D = 128, and its neighbours would fetch the lines again: NNN). The
+// parts of a head are merged in LDS, the upper half into the lower, by halves.
 // Lane = token finds the pool rows and loads both scale rows, one load each,
 // and passes them to the lanes that need them through LDS.
 // Here the vector ALU counts, and codes cost it least with 8 added, where the
@@ -673,17 +679,19 @@ __device__ __forceinline__ void take_state(State<NDP, CT> &st, const float *ex, 
 // (in three bf16 parts) takes the excess out of the scores; V enters likewise,
 // and a product of p with the block scales (State::w) takes it out at the end.
 // fp32 queries keep the exact codes.
+__host__ __device__ constexpr int rows_waves(int NDP, int CT) { return NDP * CT <= 4 ? 8 : 4; }
 template <int NDP, int CT, int NTL, int PARTS>
-__global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_rows(TreeArgs a) {
+__global__ __launch_bounds__(64 * rows_waves(NDP, CT)) void k_tree_rows(TreeArgs a) {
     constexpr int PP = PARTS, NT = 2 * NDP, KB = Raw<NDP>::KB, VW = Raw<NDP>::VW, STEP = 16 * NTL;
     constexpr bool OFF = PARTS == 1;
     constexpr uint64_t ALL = ~0ull >> (64 - STEP);
-    __shared__ __attribute__((aligned(16))) float ex[2][CT * (NT + 1) * 256];
-    __shared__ __attribute__((aligned(16))) int rowbuf[kWaves][2][STEP];
-    __shared__ __attribute__((aligned(16))) uint32_t scbuf[kWaves][2][STEP][KB];       // scale rows of K, of V
+    constexpr int NW = rows_waves(NDP, CT);
+    __shared__ __attribute__((aligned(16))) float ex[NW / 2][CT * (NT + 1) * 256];
+    __shared__ __attribute__((aligned(16))) int rowbuf[NW][2][STEP];
+    __shared__ __attribute__((aligned(16))) uint32_t scbuf[NW][2][STEP][KB];           // scale rows of K, of V
     const int lane = threadIdx.x & 63, i = lane & 15, c = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nd = a.D / 32;
+    const int nd = a.D / 32, parts = NW / a.HG, part = w / a.HG, turn = parts * STEP;
     for_each_piece(a, lane, [&](const Place &p) {
         State<NDP, CT> st;
 #pragma unroll
@@ -696,8 +704,9 @@ __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_row
             for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
         }
         const LaneAt<NDP> at(lane, a.D);
-        const uint8_t *kc = a.kc + p.g * (a.D / 2), *vc = a.vc + p.g * (a.D / 2);
-        const uint8_t *ks = a.ks + p.g * nd, *vs = a.vs + p.g * nd;
+        const int g = p.g + (w - part * a.HG);
+        const uint8_t *kc = a.kc + g * (a.D / 2), *vc = a.vc + g * (a.D / 2);
+        const uint8_t *ks = a.ks + g * nd, *vs = a.vs + g * nd;
         const uint32_t cs = (uint32_t)a.Hkv * (a.D / 2), ss = (uint32_t)a.Hkv * nd;
         const int32_t *table = a.table + (int64_t)p.b * a.ldt;
 
@@ -726,7 +735,7 @@ __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_row
                     load_v<NDP>(v[u][s], vc + (uint64_t)(uint32_t)max(rows[16 * u + 4 * c + s], 0) * cs, at);
         };
 
-        int lt = p.t0 + w * STEP;
+        int lt = p.t0 + part * STEP;
         if (lt < p.t1) {
             int row = row_at(lt, page_at(lt));
             uint64_t valid = __ballot(row >= 0);
@@ -734,9 +743,9 @@ __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_row
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             load_ks(row, rowbuf[w][0]);
             load_vs(rowbuf[w][0]);
-            int page = page_at(lt + kWaves * STEP);
+            int page = page_at(lt + turn);
             bf8 qf[CT][NDP][PARTS], qoff[CT];
-            load_queries<NDP, CT, PARTS>(a, p, p.row, lane, qf);
+            load_queries<NDP, CT, PARTS>(a, p, g, p.row, lane, qf);
             int iq[CT];
 #pragma unroll
             for (int t = 0; t < CT; ++t) {
@@ -746,8 +755,8 @@ __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_row
             }
 
             int buf = 1;
-            for (; lt < p.t1; lt += kWaves * STEP, buf ^= 1) {
-                const int next = lt + kWaves * STEP;
+            for (; lt < p.t1; lt += turn, buf ^= 1) {
+                const int next = lt + turn;
                 if (lane < STEP) {
 #pragma unroll
                     for (int b = 0; b < KB; ++b) {
@@ -757,7 +766,7 @@ __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_row
                 }
                 row = row_at(next, page);
                 if (lane < STEP) rowbuf[w][buf][lane] = row;
-                page = page_at(next + kWaves * STEP);
+                page = page_at(next + turn);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 const uint8_t *kb = reinterpret_cast<const uint8_t *>(scbuf[w][0]);
                 const uint8_t *vbp = reinterpret_cast<const uint8_t *>(scbuf[w][1]);
@@ -851,17 +860,13 @@ __global__ __launch_bounds__(64 * kWaves, NDP * CT <= 4 ? 2 : 1) void k_tree_row
         }
         give_nan<NDP, CT>(st);
 
-        if (w >= 2) give_state<NDP, CT>(st, ex[w - 2], lane);
-        __syncthreads();
-        if (w < 2) take_state<NDP, CT>(st, ex[w], lane, a.scale2);
-        __syncthreads();
-        if (w == 1) give_state<NDP, CT>(st, ex[0], lane);
-        __syncthreads();
-        if (w == 0) {
-            take_state<NDP, CT>(st, ex[0], lane, a.scale2);
-            store_rows<NDP, CT, PARTS>(a, p, st, p.row, lane);
+        for (int half = parts / 2; half; half /= 2) {
+            if (part >= half && part < 2 * half) give_state<NDP, CT>(st, ex[w - half * a.HG], lane);
+            __syncthreads();
+            if (part < half) take_state<NDP, CT>(st, ex[w], lane, a.scale2);
+            __syncthreads();
         }
-        __syncthreads();                 // the next piece writes the same LDS
+        if (part == 0) store_rows<NDP, CT, PARTS>(a, p, st, g, p.row, lane);
     });
 }
 
@@ -938,7 +943,7 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
         load(row);
         int page = page_at(p.t0 + kStep);
         bf8 qf[CT][NDP][PARTS];
-        load_queries<NDP, CT, PARTS>(a, p, row0, lane, qf);
+        load_queries<NDP, CT, PARTS>(a, p, p.g, row0, lane, qf);
         int iq[CT];
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
@@ -1047,7 +1052,7 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
         __syncthreads();
         if (wt == 0) take_state<NDP, CT>(st, ex, lane, a.scale2);
     }
-    if (busy && wt == 0) store_rows<NDP, CT, PARTS>(a, p, st, row0, lane);
+    if (busy && wt == 0) store_rows<NDP, CT, PARTS>(a, p, st, p.g, row0, lane);
     __syncthreads();                 // the next piece writes the same LDS
     });
 }
@@ -1069,10 +1074,10 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
         first += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(u), 63);
     }
     const int i = rw / a.Hq, h = rw - i * a.Hq, g = h / a.G, row = i * a.G + h - g * a.G;
-    first += ((uint32_t)g * s.nrt + (uint32_t)(row / a.R)) * s.T;
+    first += ((uint32_t)(g / a.HG) * s.nrt + (uint32_t)(row / a.R)) * s.T;
     const uint32_t p0 = sh.owner(first), p1 = sh.owner(first + s.T - 1);
     if (p0 == p1) return;
-    const int in = row % a.R;
+    const int in = g % a.HG * a.R + row % a.R, SR = a.HG * a.R;        // row and rows of a slot
     const int d = 4 * lane < a.D ? 4 * lane : 0;
     float M = -INFINITY, L = 0.f;
     f4 o = {0.f, 0.f, 0.f, 0.f};
@@ -1080,7 +1085,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
         const int ns = (int)(p1 - q + 1 < 64 ? p1 - q + 1 : 64);
         // piece of share q + lane: slot 1 where the share starts at or before the tile, else 0
         const uint32_t me = q + (lane < ns ? lane : 0);
-        const int64_t at = (2 * (int64_t)me + (sh.start(me) > first ? 0 : 1)) * a.R + in;
+        const int64_t at = (2 * (int64_t)me + (sh.start(me) > first ? 0 : 1)) * SR + in;
         float m = -INFINITY, l = 0.f;
         if (lane < ns) {
             m = a.pml[2 * at];
@@ -1099,8 +1104,8 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
         o *= old;
         M = Mn;
         const float *po = a.po + d;
-        const int64_t base = ((2 * (int64_t)q) * a.R + in) * a.D, next = 2 * (int64_t)a.R * a.D;
-        const int64_t one = (int64_t)a.R * a.D;
+        const int64_t base = ((2 * (int64_t)q) * SR + in) * a.D, next = 2 * (int64_t)SR * a.D;
+        const int64_t one = (int64_t)SR * a.D;
         for (int k = 0; k < ns; k += 8) {
             f4 v[8];
 #pragma unroll
@@ -1125,34 +1130,41 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
 
 struct TreePlan {
     int NDP, CT, WT;                 // WT 0: k_tree_rows
-    int R, U, P, minu;
+    int R, U, P, minu, HG;
     int64_t bound;                   // units at most
     int join;                        // some tile may lie in several shares
 };
 
-// Kernel, tile and number of workgroups from what the host knows: two
-// workgroups fit on each of the 256 CUs (one with D > 128 in k_tree_tile).
+// Kernel, tile and number of workgroups from what the host knows: eight waves
+// (four where one needs more than 256 registers) fit on each of the 256 CUs.
 TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv, int64_t D) {
     TreePlan p;
     p.NDP = D <= 64 ? 2 : (D <= 128 ? 4 : 8);
     const int64_t rows = max_q * (Hq / Hkv);
     const bool bf = dt == MXS_BF16;
+    int64_t slots;
     if (rows <= (bf && p.NDP <= 4 ? 32 : 16)) {
         p.WT = 0;
         p.CT = rows > 16 ? 2 : 1;
         p.R = 16 * p.CT;
-        p.U = kWaves * 16 * kRowTiles;
+        const int nw = rows_waves(p.NDP, p.CT);
+        p.HG = nw;
+        while (Hkv % p.HG) p.HG /= 2;
+        p.U = nw / p.HG * 16 * kRowTiles;
         p.minu = 1;
+        slots = 256;
     } else {
         p.CT = bf ? 2 : 1;
         p.WT = rows <= 32 * p.CT ? 2 : 1;
         p.R = 16 * p.CT * (kWaves / p.WT);
+        p.HG = 1;
         p.U = kStep;
         p.minu = 2;
+        slots = p.NDP == 8 ? 256 : 512;
     }
     const int64_t T = max_len > 0 ? ceil_div(max_len, (int64_t)p.U) : 1;
-    p.bound = B * Hkv * ceil_div(rows, (int64_t)p.R) * T;
-    const int64_t slots = p.WT && p.NDP == 8 ? 256 : 512, most = ceil_div(ceil_div(p.bound, (int64_t)p.minu), (int64_t)8) * 8;
+    p.bound = B * (Hkv / p.HG) * ceil_div(rows, (int64_t)p.R) * T;
+    const int64_t most = ceil_div(ceil_div(p.bound, (int64_t)p.minu), (int64_t)8) * 8;
     p.P = (int)(most < slots ? most : slots);
     p.join = T > 1;
     return p;
@@ -1160,7 +1172,7 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
 
 template <int NDP, int CT, int PARTS>
 hipError_t rows_go(const TreeArgs &a, unsigned grid, hipStream_t st) {
-    hipLaunchKernelGGL((k_tree_rows<NDP, CT, kRowTiles, PARTS>), dim3(grid), dim3(64 * kWaves), 0, st, a);
+    hipLaunchKernelGGL((k_tree_rows<NDP, CT, kRowTiles, PARTS>), dim3(grid), dim3(64 * rows_waves(NDP, CT)), 0, st, a);
     return hipGetLastError();
 }
 template <int NDP, int CT, int WT, int PARTS>
@@ -1189,7 +1201,7 @@ hipError_t tree_go(const TreePlan &p, const TreeArgs &a, unsigned grid, bool f32
 size_t attend_kv4_tree_workspace(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
                                  int64_t D) {
     const TreePlan p = tree_plan(dt, B, max_q, max_len, Hq, Hkv, D);
-    return p.join ? (size_t)(2 * p.P) * p.R * (D + 2) * sizeof(float) : 0;
+    return p.join ? (size_t)(2 * p.P) * p.HG * p.R * (D + 2) * sizeof(float) : 0;
 }
 
 bool attend_kv4_tree_supported(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
@@ -1219,10 +1231,10 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     // at least 2^-126, so that a hidden score stays -inf at scale 0
     a.scale2 = fmaxf((float)(fabs((double)scale) * 1.4426950408889634074 * 512.0), 1.17549435e-38f);
     a.negate = std::signbit(scale);
-    a.R = p.R; a.U = p.U; a.P = p.P; a.minu = p.minu;
+    a.R = p.R; a.U = p.U; a.P = p.P; a.minu = p.minu; a.HG = p.HG;
     a.out = out; a.ldo = ldo;
     a.po = static_cast<float *>(ws);
-    a.pml = a.po + (int64_t)(2 * p.P) * p.R * c.D;
+    a.pml = a.po + (int64_t)(2 * p.P) * p.HG * p.R * c.D;
     const unsigned grid = (unsigned)p.P;
     hipError_t e;
     const bool f32 = dt == MXS_F32;
