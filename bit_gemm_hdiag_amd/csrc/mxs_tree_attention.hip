@@ -34,6 +34,7 @@
 // and the sum that normalises is that of the rounded values, so one dominant
 // token gives its V exactly. Maxima, sums and outputs are fp32.
 #include <cmath>
+#include <type_traits>
 
 #include "mxs_device.h"
 #include "mxs_internal.h"
@@ -48,7 +49,8 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;            // waves of a workgroup; they share its tokens
-constexpr int kRowTiles = 4;         // 16-token tiles of a wave's step in k_tree_rows
+constexpr int kRowTiles = 2;         // 16-token tiles of a wave's step in k_tree_rows
+constexpr int kRowSets = 3;          // steps whose codes a wave holds or has in flight
 constexpr int kNTL = 4;              // 16-token tiles of a stage in k_tree_tile
 constexpr int kStep = 16 * kNTL;     // tokens of a stage
 
@@ -69,9 +71,12 @@ struct TreeArgs {
     bool negate;                     // scale < 0: queries enter negated
     int R, U, P, minu;               // rows of a tile, tokens of a unit, workgroups, units of a share (at least)
     int HG;                          // KV heads of a tile
+    int join;                        // a k_tree_join follows
+    int JR;                          // its rows of a workgroup
     void *out;
     int64_t ldo;
     float *po, *pml;                 // [2 share + k, HG, R, D], [2 share + k, HG, R, (m, l)]
+    int *todo;                       // [8 share + .]: see JoinOf
 };
 
 // t / ps for 0 <= t < 2^31: pmul = ceil(2^(31 + l) / ps), l = ceil(log2 ps)
@@ -184,37 +189,59 @@ struct Shares {
         return (uint32_t)(((double)(x + 1) * (double)P - 1.0) / (double)W);
     }
 };
-__device__ __forceinline__ Shares shares_of(const TreeArgs &a, int lane) {
+
+// 64 sequences, one a lane, and the line of units up to them
+struct Window {
+    int b0;                          // first sequence, a multiple of 64
+    Seq s;                           // of sequence b0 + lane
+    uint32_t units, end;             // of it; the units of the sequences up to it
+    __device__ __forceinline__ void load(const TreeArgs &a, int b, uint32_t before, int lane) {
+        b0 = b;
+        units = 0;
+        if (b + lane < a.B) {
+            s = seq_of(a, b + lane);
+            units = units_of(a, s);
+        }
+        end = before + wave_scan(units);
+    }
+    __device__ __forceinline__ uint32_t last() const { return (uint32_t)__builtin_amdgcn_readlane((int)end, 63); }
+    __device__ __forceinline__ uint32_t first(int l) const {          // first unit of lane l's sequence
+        return (uint32_t)__builtin_amdgcn_readlane((int)(end - units), l);
+    }
+    __device__ __forceinline__ Seq seq(int l) const {
+        Seq r;
+        r.len = __builtin_amdgcn_readlane(s.len, l);
+        r.n = __builtin_amdgcn_readlane(s.n, l);
+        r.q0 = __builtin_amdgcn_readlane(s.q0, l);
+        r.nrt = (uint32_t)__builtin_amdgcn_readlane((int)s.nrt, l);
+        r.T = (uint32_t)__builtin_amdgcn_readlane((int)s.T, l);
+        return r;
+    }
+    // the lane of the sequence of unit x, which lies in a window from this one on
+    __device__ __forceinline__ int find(const TreeArgs &a, uint32_t x, int lane) {
+        for (;;) {
+            const uint64_t past = __ballot(end > x);
+            if (past) return __builtin_ctzll(past);
+            if (b0 + 64 >= a.B) return -1;
+            load(a, b0 + 64, last(), lane);
+        }
+    }
+};
+// The shares, and the window of the first 64 sequences
+__device__ __forceinline__ Shares shares_of(const TreeArgs &a, Window &w, int lane) {
     Shares h;
-    h.W = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-        uint32_t u = 0;
-        if (b0 + lane < a.B) u = units_of(a, seq_of(a, b0 + lane));
-        h.W += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(u), 63);
+    w.load(a, 0, 0, lane);
+    h.W = w.last();
+    for (int b = 64; b < a.B; b += 64) {
+        Window v;
+        v.load(a, b, h.W, lane);
+        h.W = v.last();
     }
     const uint32_t most = (h.W + a.minu - 1) / (uint32_t)a.minu;
     h.P = most < (uint32_t)a.P ? most : (uint32_t)a.P;
     h.q = h.P ? h.W / h.P : 0;
     h.r = h.P ? h.W % h.P : 0;
     return h;
-}
-// The sequence of unit x < W and its first unit
-__device__ __forceinline__ int find_seq(const TreeArgs &a, uint32_t x, int lane, uint32_t &first) {
-    uint32_t sum = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-        uint32_t u = 0;
-        if (b0 + lane < a.B) u = units_of(a, seq_of(a, b0 + lane));
-        const uint32_t end = sum + wave_scan(u);
-        const uint64_t past = __ballot(end > x);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            first = (uint32_t)__builtin_amdgcn_readlane((int)(end - u), l);
-            return b0 + l;
-        }
-        sum = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
-    }
-    first = 0;
-    return 0;
 }
 
 // A piece of a share: tokens t0 .. t1 - 1 of one tile
@@ -225,25 +252,36 @@ struct Place {
     int64_t slot;                    // workspace slot, -1: the whole tile
 };
 
+// What k_tree_join finds at todo + 8 p: the tile whose first piece is the end of
+// share p, if there is one (last > p)
+struct JoinOf {
+    int last;                        // share of its last piece
+    int q0, n, g, row;               // Place's
+};
+
 // f(place) for every piece of this workgroup's share. Consecutive shares (row
 // tiles of one KV head, then its neighbours in the same 128-byte lines of the
 // cache) go to one XCD: workgroups are dealt to the 8 XCDs in turn.
 template <typename F>
 __device__ __forceinline__ void for_each_piece(const TreeArgs &a, int lane, F f) {
-    const Shares h = shares_of(a, lane);
+    Window win;
+    const Shares h = shares_of(a, win, lane);
     const uint32_t per = (h.P + 7) / 8, p = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || p >= h.P) return;
-    uint32_t x = h.start(p), first;
-    const uint32_t end = h.start(p + 1);
-    int b = find_seq(a, x, lane, first);
-    while (x < end) {
-        const Seq s = seq_of(a, b);
-        const uint32_t units = units_of(a, s);
-        if (x - first >= units) {
-            first += units;
-            if (++b >= a.B) return;
-            continue;
+    if (a.join) {                    // no tile to join yet; todo[8 P] = the number of shares
+        if (threadIdx.x == 0) {
+            if ((blockIdx.x >> 3) < per && p < h.P) a.todo[8 * p] = 0;
+            if (blockIdx.x == 0) a.todo[8 * a.P] = (int)h.P;
         }
+    }
+    if ((blockIdx.x >> 3) >= per || p >= h.P) return;
+    uint32_t x = h.start(p);
+    const uint32_t end = h.start(p + 1);
+    while (x < end) {
+        const int l = win.find(a, x, lane);
+        if (l < 0) return;
+        const Seq s = win.seq(l);
+        const int b = win.b0 + l;
+        const uint32_t first = win.first(l);
         const uint32_t tile = (x - first) / s.T, u0 = (x - first) - tile * s.T;
         const uint32_t u1 = s.T - u0 < end - x ? s.T : u0 + (end - x);
         auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
@@ -258,6 +296,14 @@ __device__ __forceinline__ void for_each_piece(const TreeArgs &a, int lane, F f)
         pl.t0 = uni((int)u0 * a.U);
         pl.t1 = uni(u1 == s.T ? s.len : (int)u1 * a.U);
         pl.slot = u0 == 0 && u1 == s.T ? -1 : 2 * (int64_t)p + (u0 > 0 ? 0 : 1);
+        if (u0 == 0 && u1 < s.T && threadIdx.x == 0) {
+            int *t = a.todo + 8 * p;
+            t[0] = (int)h.owner(x + s.T - 1);
+            t[1] = pl.q0;
+            t[2] = pl.n;
+            t[3] = pl.g;
+            t[4] = pl.row;
+        }
         f(pl);
         x += u1 - u0;
     }
@@ -400,21 +446,30 @@ __device__ __forceinline__ void load_v(uint32_t v[Raw<NDP>::VW], const uint8_t *
         v[1] = w[1];
     }
 }
-// The D / 32 scale bytes of one row, in one or two words
-template <int NDP>
+// The D / 32 scale bytes of one row, in one or two words: one load where D is
+// not padded (FULL), else a byte load each, those past the row repeating its
+// last byte. No load sits behind a branch: at the join of the two paths the
+// compiler would wait for every load in flight.
+template <int NDP, bool FULL>
 __device__ __forceinline__ void load_scales(uint32_t x[Raw<NDP>::KB], const uint8_t *p, int nd) {
-    if (NDP == 8 && nd == 8) {
+    if constexpr (FULL && NDP == 8) {
         const u2 w = *reinterpret_cast<const u2 *>(p);
         x[0] = w[0];
-        x[Raw<NDP>::KB - 1] = w[1];
-    } else if (nd == 4) {
+        x[1] = w[1];
+    } else if constexpr (FULL && NDP == 4) {
         x[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (FULL) {
+        x[0] = *reinterpret_cast<const uint16_t *>(p);
     } else {
+        uint32_t b[NDP];
 #pragma unroll
-        for (int i = 0; i < Raw<NDP>::KB; ++i) x[i] = 0;
+        for (int i = 0; i < NDP; ++i) b[i] = p[i < nd ? i : nd - 1];
 #pragma unroll
-        for (int i = 0; i < NDP; ++i)
-            if (i < nd) x[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+        for (int i = 0; i < Raw<NDP>::KB; ++i) {
+            x[i] = 0;
+#pragma unroll
+            for (int j = 0; j < (NDP < 4 ? NDP : 4); ++j) x[i] |= b[4 * i + j] << (8 * j);
+        }
     }
 }
 
@@ -680,14 +735,22 @@ __device__ __forceinline__ void take_state(State<NDP, CT> &st, const float *ex, 
 // and a product of p with the block scales (State::w) takes it out at the end.
 // fp32 queries keep the exact codes.
 __host__ __device__ constexpr int rows_waves(int NDP, int CT) { return NDP * CT <= 4 ? 8 : 4; }
-template <int NDP, int CT, int NTL, int PARTS>
+// f(0), f(1), ... f(N - 1) with constant arguments
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unroll_sets(F f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unroll_sets<N, I + 1>(f);
+    }
+}
+template <int NDP, int CT, int NTL, int SETS, int PARTS, bool FULL>
 __global__ __launch_bounds__(64 * rows_waves(NDP, CT)) void k_tree_rows(TreeArgs a) {
     constexpr int PP = PARTS, NT = 2 * NDP, KB = Raw<NDP>::KB, VW = Raw<NDP>::VW, STEP = 16 * NTL;
     constexpr bool OFF = PARTS == 1;
     constexpr uint64_t ALL = ~0ull >> (64 - STEP);
     constexpr int NW = rows_waves(NDP, CT);
     __shared__ __attribute__((aligned(16))) float ex[NW / 2][CT * (NT + 1) * 256];
-    __shared__ __attribute__((aligned(16))) int rowbuf[NW][2][STEP];
+    __shared__ __attribute__((aligned(16))) int rowbuf[NW][SETS][STEP];
     __shared__ __attribute__((aligned(16))) uint32_t scbuf[NW][2][STEP][KB];           // scale rows of K, of V
     const int lane = threadIdx.x & 63, i = lane & 15, c = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -711,140 +774,148 @@ __global__ __launch_bounds__(64 * rows_waves(NDP, CT)) void k_tree_rows(TreeArgs
         const int32_t *table = a.table + (int64_t)p.b * a.ldt;
 
         // pool row of token lt + lane (-1: past the range, or no valid page)
-        auto page_at = [&](int lt) {
-            const int t = lt + lane;
-            return lane < STEP && t < p.t1 ? table[page_of(a, t)] : -1;
-        };
+        auto page_at = [&](int lt) { return table[page_of(a, min(lt + lane, p.t1 - 1))]; };
         auto row_at = [&](int lt, int page) {
             const int t = lt + lane;
-            return (uint32_t)page < (uint64_t)a.pages ? page * a.ps + (t - page_of(a, t) * a.ps) : -1;
+            return lane < STEP && t < p.t1 && (uint32_t)page < (uint64_t)a.pages ? page * a.ps + (t - page_of(a, t) * a.ps) : -1;
         };
-        uint32_t k[NTL][NDP], v[NTL][4][VW], ksc[KB], vsc[KB];
-        auto load_ks = [&](int row, const int *rows) {
+        uint32_t k[SETS][NTL][NDP], v[SETS][NTL][4][VW], ksc[SETS][KB], vsc[SETS][KB];
+        uint64_t valid[SETS];
+        auto load_ks = [&](auto J, int row) {
             const uint64_t r = (uint32_t)max(row, 0);
-            load_scales<NDP>(ksc, ks + r * ss, nd);
-            load_scales<NDP>(vsc, vs + r * ss, nd);
+            load_scales<NDP, FULL>(ksc[J], ks + r * ss, nd);
+            load_scales<NDP, FULL>(vsc[J], vs + r * ss, nd);
 #pragma unroll
-            for (int u = 0; u < NTL; ++u) load_k<NDP>(k[u], kc + (uint64_t)(uint32_t)max(rows[16 * u + i], 0) * cs, at);
+            for (int u = 0; u < NTL; ++u)
+                load_k<NDP>(k[J][u], kc + (uint64_t)(uint32_t)max(rowbuf[w][J][16 * u + i], 0) * cs, at);
         };
-        auto load_vs = [&](const int *rows) {
+        auto load_vs = [&](auto J) {
 #pragma unroll
             for (int u = 0; u < NTL; ++u)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    load_v<NDP>(v[u][s], vc + (uint64_t)(uint32_t)max(rows[16 * u + 4 * c + s], 0) * cs, at);
+                    load_v<NDP>(v[J][u][s], vc + (uint64_t)(uint32_t)max(rowbuf[w][J][16 * u + 4 * c + s], 0) * cs, at);
+        };
+        auto rows_of = [&](auto J, int lt, int page) {
+            const int row = row_at(lt, page);
+            if (lane < STEP) rowbuf[w][J][lane] = row;
+            return row;
+        };
+
+        bf8 qf[CT][NDP][PARTS], qoff[CT];
+        int iq[CT], page = -1;
+        // One step: the tokens at lt, whose codes are set J; the codes of the step
+        // SETS turns on are loaded into J as it is used up
+        auto step = [&](auto J, int lt) {
+            const int next = lt + SETS * turn;
+            if (lane < STEP) {
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    scbuf[w][0][lane][b] = ksc[J][b];
+                    scbuf[w][1][lane][b] = vsc[J][b];
+                }
+            }
+            const int row = rows_of(J, next, page);
+            page = page_at(next + turn);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            const uint8_t *kb = reinterpret_cast<const uint8_t *>(scbuf[w][0]);
+            const uint8_t *vbp = reinterpret_cast<const uint8_t *>(scbuf[w][1]);
+
+            f4 sc[CT][NTL];
+#pragma unroll
+            for (int u = 0; u < NTL; ++u) {
+                uint32_t e[KB];
+#pragma unroll
+                for (int b = 0; b < KB; ++b) e[b] = kb[4 * KB * (16 * u + i) + at.kb[b]];
+#pragma unroll
+                for (int t = 0; t < CT; ++t) sc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int b = 0; b < NDP; ++b) {
+                    const bf8 kv = word_values<OFF>(k[J][u][b], scale_of(e[KB == 2 ? b >> 2 : 0]));
+#pragma unroll
+                    for (int t = 0; t < CT; ++t)
+#pragma unroll
+                        for (int j = 0; j < PARTS; ++j)
+                            sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][j], sc[t][u], 0, 0, 0);
+                }
+                if constexpr (OFF) {
+                    const bf8 es = scale_operand<NDP>(e);
+#pragma unroll
+                    for (int t = 0; t < CT; ++t)
+                        sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(es, qoff[t], sc[t][u], 0, 0, 0);
+                }
+            }
+            uint32_t vb[NTL][4];
+#pragma unroll
+            for (int u = 0; u < NTL; ++u)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) vb[u][s] = vbp[4 * KB * (16 * u + 4 * c + s) + at.vb];
+            load_ks(J, row);
+            __builtin_amdgcn_sched_barrier(0);
+
+            if (valid[J] != ALL || lt + STEP > p.ctx) {
+                uint64_t seen[CT];
+#pragma unroll
+                for (int t = 0; t < CT; ++t) seen[t] = valid[J] & mask_window(a, p, iq[t], lt);
+                hide<CT, NTL>(sc, seen, c);
+#pragma unroll
+                for (int u = 0; u < NTL; ++u)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        if (!((valid[J] >> (16 * u + 4 * c + s)) & 1)) vb[u][s] = 0;
+                        const uint64_t bad = take_nan(vb[u][s]);
+                        if (bad)
+                            for (int j = 0; j < 4; ++j)
+                                note_nan<NDP, CT>(st, (uint32_t)(bad >> (16 * j)) & 0xFFFFu, 16 * u + 4 * j + s, seen, c);
+                    }
+            }
+            soften<NDP, CT, NTL, PARTS == 3>(st, sc, a.scale2);
+#pragma unroll
+            for (int u = 0; u < NTL; u += 2) {
+                bf8 vf[NT], off;
+                v_operands<NDP, OFF>(&v[J][u], &vb[u], vf, off);
+#pragma unroll
+                for (int t = 0; t < CT; ++t) {
+                    bf8 pf[PP];
+                    p_operands<PP>(sc[t][u], sc[t][u + 1], pf);
+#pragma unroll
+                    for (int j = 0; j < PP; ++j)
+                        st.l[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones(), pf[j], st.l[t], 0, 0, 0);
+                    if constexpr (OFF)
+                        st.w[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(off, pf[0], st.w[t], 0, 0, 0);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < PP; ++j)
+                            st.acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[n], pf[j], st.acc[t][n], 0, 0, 0);
+                }
+            }
+            load_vs(J);
+            valid[J] = __ballot(row >= 0);
+            __builtin_amdgcn_sched_barrier(0);
         };
 
         int lt = p.t0 + part * STEP;
         if (lt < p.t1) {
-            int row = row_at(lt, page_at(lt));
-            uint64_t valid = __ballot(row >= 0);
-            if (lane < STEP) rowbuf[w][0][lane] = row;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            load_ks(row, rowbuf[w][0]);
-            load_vs(rowbuf[w][0]);
-            int page = page_at(lt + turn);
-            bf8 qf[CT][NDP][PARTS], qoff[CT];
+            unroll_sets<SETS>([&](auto J) {
+                const int row = rows_of(J, lt + J * turn, page_at(lt + J * turn));
+                valid[J] = __ballot(row >= 0);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                load_ks(J, row);
+                load_vs(J);
+            });
+            page = page_at(lt + SETS * turn);
             load_queries<NDP, CT, PARTS>(a, p, g, p.row, lane, qf);
-            int iq[CT];
 #pragma unroll
             for (int t = 0; t < CT; ++t) {
                 const int rw = p.row + 16 * t + i;
                 iq[t] = rw < p.n * a.G ? rw / a.G : 0;
                 if constexpr (OFF) qoff[t] = query_sums<NDP>(qf[t]);
             }
-
-            int buf = 1;
-            for (; lt < p.t1; lt += turn, buf ^= 1) {
-                const int next = lt + turn;
-                if (lane < STEP) {
-#pragma unroll
-                    for (int b = 0; b < KB; ++b) {
-                        scbuf[w][0][lane][b] = ksc[b];
-                        scbuf[w][1][lane][b] = vsc[b];
-                    }
-                }
-                row = row_at(next, page);
-                if (lane < STEP) rowbuf[w][buf][lane] = row;
-                page = page_at(next + turn);
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                const uint8_t *kb = reinterpret_cast<const uint8_t *>(scbuf[w][0]);
-                const uint8_t *vbp = reinterpret_cast<const uint8_t *>(scbuf[w][1]);
-
-                f4 sc[CT][NTL];
-#pragma unroll
-                for (int u = 0; u < NTL; ++u) {
-                    uint32_t e[KB];
-#pragma unroll
-                    for (int b = 0; b < KB; ++b) e[b] = kb[4 * KB * (16 * u + i) + at.kb[b]];
-#pragma unroll
-                    for (int t = 0; t < CT; ++t) sc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int b = 0; b < NDP; ++b) {
-                        const bf8 kv = word_values<OFF>(k[u][b], scale_of(e[KB == 2 ? b >> 2 : 0]));
-#pragma unroll
-                        for (int t = 0; t < CT; ++t)
-#pragma unroll
-                            for (int j = 0; j < PARTS; ++j)
-                                sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][j], sc[t][u], 0, 0, 0);
-                    }
-                    if constexpr (OFF) {
-                        const bf8 es = scale_operand<NDP>(e);
-#pragma unroll
-                        for (int t = 0; t < CT; ++t)
-                            sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(es, qoff[t], sc[t][u], 0, 0, 0);
-                    }
-                }
-                uint32_t vb[NTL][4];
-#pragma unroll
-                for (int u = 0; u < NTL; ++u)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) vb[u][s] = vbp[4 * KB * (16 * u + 4 * c + s) + at.vb];
-                load_ks(row, rowbuf[w][buf]);
-                __builtin_amdgcn_sched_barrier(0);
-
-                if (valid != ALL || lt + STEP > p.ctx) {
-                    uint64_t seen[CT];
-#pragma unroll
-                    for (int t = 0; t < CT; ++t) seen[t] = valid & mask_window(a, p, iq[t], lt);
-                    hide<CT, NTL>(sc, seen, c);
-#pragma unroll
-                    for (int u = 0; u < NTL; ++u)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            if (!((valid >> (16 * u + 4 * c + s)) & 1)) vb[u][s] = 0;
-                            const uint64_t bad = take_nan(vb[u][s]);
-                            if (bad)
-                                for (int j = 0; j < 4; ++j)
-                                    note_nan<NDP, CT>(st, (uint32_t)(bad >> (16 * j)) & 0xFFFFu, 16 * u + 4 * j + s,
-                                                      seen, c);
-                        }
-                }
-                soften<NDP, CT, NTL, PARTS == 3>(st, sc, a.scale2);
-#pragma unroll
-                for (int u = 0; u < NTL; u += 2) {
-                    bf8 vf[NT], off;
-                    v_operands<NDP, OFF>(&v[u], &vb[u], vf, off);
-#pragma unroll
-                    for (int t = 0; t < CT; ++t) {
-                        bf8 pf[PP];
-                        p_operands<PP>(sc[t][u], sc[t][u + 1], pf);
-#pragma unroll
-                        for (int j = 0; j < PP; ++j)
-                            st.l[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones(), pf[j], st.l[t], 0, 0, 0);
-                        if constexpr (OFF)
-                            st.w[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(off, pf[0], st.w[t], 0, 0, 0);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int j = 0; j < PP; ++j)
-                                st.acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[n], pf[j], st.acc[t][n], 0, 0, 0);
-                    }
-                }
-                load_vs(rowbuf[w][buf]);
-                valid = __ballot(row >= 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (; lt < p.t1; lt += SETS * turn)
+                unroll_sets<SETS>([&](auto J) {
+                    if (J == 0 || lt + J * turn < p.t1) step(J, lt + J * turn);
+                });
         }
         if constexpr (OFF) {
 #pragma unroll
@@ -917,13 +988,10 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
         const uint32_t cs = (uint32_t)a.Hkv * (a.D / 2), ss = (uint32_t)a.Hkv * (a.D / 32);
 
         // token 16 w + i of the stage at lt: its page, its pool row
-        auto page_at = [&](int lt) {
-            const int t = lt + 16 * w + i;
-            return t < p.t1 ? table[page_of(a, t)] : -1;
-        };
+        auto page_at = [&](int lt) { return table[page_of(a, min(lt + 16 * w + i, p.t1 - 1))]; };
         auto row_at = [&](int lt, int page) {
             const int t = lt + 16 * w + i;
-            return (uint32_t)page < (uint64_t)a.pages ? page * a.ps + (t - page_of(a, t) * a.ps) : -1;
+            return t < p.t1 && (uint32_t)page < (uint64_t)a.pages ? page * a.ps + (t - page_of(a, t) * a.ps) : -1;
         };
         uint32_t k[NDP], kb[KB], v[4][VW], vb[4];
         auto load = [&](int row) {
@@ -1058,73 +1126,69 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
 }
 
 // Rows of tiles that lie in several shares: out = sum_s O_s 2^(m_s - M) 2^9 /
-// sum_s l_s 2^(m_s - M), pieces in order. One wave a row; lane s holds the
-// weight of piece s of a run of 64, D <= 256: a lane's four dims.
+// sum_s l_s 2^(m_s - M), pieces in order. Workgroup (p, y): the tile that starts
+// in share p, if it ends in another, JR of its rows from y JR on, one wave a row;
+// lane s holds the weight of piece s of a run of 64, and four dims (D <= 256).
 template <typename T>
 __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
-    const int b = blockIdx.y, lane = threadIdx.x & 63;
-    const int rw = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // (query token, head)
-    const Seq s = seq_of(a, b);
-    if (rw >= s.n * a.Hq || s.T < 2) return;
-    const Shares sh = shares_of(a, lane);
-    uint32_t first = 0;
-    for (int b0 = 0; b0 < b; b0 += 64) {
-        uint32_t u = 0;
-        if (b0 + lane < b) u = units_of(a, seq_of(a, b0 + lane));
-        first += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(u), 63);
-    }
-    const int i = rw / a.Hq, h = rw - i * a.Hq, g = h / a.G, row = i * a.G + h - g * a.G;
-    first += ((uint32_t)(g / a.HG) * s.nrt + (uint32_t)(row / a.R)) * s.T;
-    const uint32_t p0 = sh.owner(first), p1 = sh.owner(first + s.T - 1);
-    if (p0 == p1) return;
-    const int in = g % a.HG * a.R + row % a.R, SR = a.HG * a.R;        // row and rows of a slot
+    const int lane = threadIdx.x & 63, p0 = blockIdx.x;
+    const int shares = a.todo[8 * a.P];
+    const JoinOf t = {a.todo[8 * p0], a.todo[8 * p0 + 1], a.todo[8 * p0 + 2], a.todo[8 * p0 + 3], a.todo[8 * p0 + 4]};
+    if (p0 >= shares || t.last <= p0) return;
+    const int SR = a.HG * a.R;
     const int d = 4 * lane < a.D ? 4 * lane : 0;
-    float M = -INFINITY, L = 0.f;
-    f4 o = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t q = p0; q <= p1; q += 64) {
-        const int ns = (int)(p1 - q + 1 < 64 ? p1 - q + 1 : 64);
-        // piece of share q + lane: slot 1 where the share starts at or before the tile, else 0
-        const uint32_t me = q + (lane < ns ? lane : 0);
-        const int64_t at = (2 * (int64_t)me + (sh.start(me) > first ? 0 : 1)) * SR + in;
-        float m = -INFINITY, l = 0.f;
-        if (lane < ns) {
-            m = a.pml[2 * at];
-            l = a.pml[2 * at + 1];
-        }
-        float Mn = m;
-#pragma unroll
-        for (int k = 32; k; k >>= 1) Mn = fmaxf(Mn, __shfl_xor(Mn, k));
-        Mn = fmaxf(M, Mn);
-        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - Mn);
-        const float old = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(M - Mn);
-        float ls = l * f;
-#pragma unroll
-        for (int k = 32; k; k >>= 1) ls += __shfl_xor(ls, k);
-        L = L * old + ls;
-        o *= old;
-        M = Mn;
-        const float *po = a.po + d;
-        const int64_t base = ((2 * (int64_t)q) * SR + in) * a.D, next = 2 * (int64_t)SR * a.D;
-        const int64_t one = (int64_t)SR * a.D;
-        for (int k = 0; k < ns; k += 8) {
-            f4 v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t pk = k + j < ns ? k + j : ns - 1;
-                v[j] = *reinterpret_cast<const f4 *>(po + base + pk * next + (sh.start(q + pk) > first ? 0 : one));
+    const int64_t one = (int64_t)SR * a.D;               // a slot
+    for (int k = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); k < a.JR; k += 4) {
+        const int in = blockIdx.y * a.JR + k;
+        const int gi = in / a.R, row = t.row + in - gi * a.R;
+        if (in >= SR || row >= t.n * a.G) continue;
+        const int i = row / a.G, h = (t.g + gi) * a.G + row - i * a.G;
+        float M = -INFINITY, L = 0.f;
+        f4 o = {0.f, 0.f, 0.f, 0.f};
+        for (int q = p0; q <= t.last; q += 64) {
+            const int ns = t.last - q + 1 < 64 ? t.last - q + 1 : 64;
+            // slot 1 of the tile's first share, slot 0 of the others
+            const int me = q + (lane < ns ? lane : 0);
+            const int64_t at = (2 * (int64_t)me + (me == p0 ? 1 : 0)) * SR + in;
+            float m = -INFINITY, lsum = 0.f;
+            if (lane < ns) {
+                m = a.pml[2 * at];
+                lsum = a.pml[2 * at + 1];
             }
+            float Mn = m;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float fk = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(f), k + j < ns ? k + j : 0));
-                if (k + j < ns) o += v[j] * fk;
+            for (int j = 32; j; j >>= 1) Mn = fmaxf(Mn, __shfl_xor(Mn, j));
+            Mn = fmaxf(M, Mn);
+            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - Mn);
+            const float old = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(M - Mn);
+            float ls = lsum * f;
+#pragma unroll
+            for (int j = 32; j; j >>= 1) ls += __shfl_xor(ls, j);
+            L = L * old + ls;
+            o *= old;
+            M = Mn;
+            const float *po = a.po + d + 2 * (int64_t)q * one + (int64_t)in * a.D;
+            for (int j0 = 0; j0 < ns; j0 += 8) {
+                f4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int pk = j0 + j < ns ? j0 + j : ns - 1;
+                    v[j] = *reinterpret_cast<const f4 *>(po + 2 * pk * one + (q + pk == p0 ? one : 0));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float fk =
+                        __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(f), j0 + j < ns ? j0 + j : 0));
+                    if (j0 + j < ns) o += v[j] * fk;
+                }
             }
         }
-    }
-    const float norm = M == -INFINITY ? 0.f : 512.f / L;
-    T *out = static_cast<T *>(a.out) + ((int64_t)s.q0 + i) * a.ldo + (int64_t)h * a.D + d;
-    if (4 * lane < a.D) {
+        const float norm = M == -INFINITY ? 0.f : 512.f / L;
+        T *out = static_cast<T *>(a.out) + ((int64_t)t.q0 + i) * a.ldo + (int64_t)h * a.D + d;
+        if (4 * lane < a.D) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) out[k] = (T)(o[k] * norm);
+            for (int j = 0; j < 4; ++j) out[j] = (T)(o[j] * norm);
+        }
     }
 }
 
@@ -1172,7 +1236,12 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
 
 template <int NDP, int CT, int PARTS>
 hipError_t rows_go(const TreeArgs &a, unsigned grid, hipStream_t st) {
-    hipLaunchKernelGGL((k_tree_rows<NDP, CT, kRowTiles, PARTS>), dim3(grid), dim3(64 * rows_waves(NDP, CT)), 0, st, a);
+    if (a.D == 32 * NDP)
+        hipLaunchKernelGGL((k_tree_rows<NDP, CT, kRowTiles, kRowSets, PARTS, true>), dim3(grid),
+                           dim3(64 * rows_waves(NDP, CT)), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_tree_rows<NDP, CT, kRowTiles, kRowSets, PARTS, false>), dim3(grid),
+                           dim3(64 * rows_waves(NDP, CT)), 0, st, a);
     return hipGetLastError();
 }
 template <int NDP, int CT, int WT, int PARTS>
@@ -1201,14 +1270,14 @@ hipError_t tree_go(const TreePlan &p, const TreeArgs &a, unsigned grid, bool f32
 size_t attend_kv4_tree_workspace(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
                                  int64_t D) {
     const TreePlan p = tree_plan(dt, B, max_q, max_len, Hq, Hkv, D);
-    return p.join ? (size_t)(2 * p.P) * p.HG * p.R * (D + 2) * sizeof(float) : 0;
+    // pieces (outputs, then maxima and sums), then todo
+    return p.join ? (size_t)(2 * p.P) * p.HG * p.R * (D + 2) * sizeof(float) + (size_t)(p.P + 1) * 32 : 0;
 }
 
 bool attend_kv4_tree_supported(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
                                int64_t D) {
     const int64_t rows = max_q * (Hq / Hkv);
-    return rows <= (1 << 30) && max_q * Hq <= ((int64_t)1 << 31) &&
-           tree_plan(dt, B, max_q, max_len, Hq, Hkv, D).bound <= (1 << 30);
+    return rows <= (1 << 30) && tree_plan(dt, B, max_q, max_len, Hq, Hkv, D).bound <= (1 << 30);
 }
 
 hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, const mxs_kv4_cache &c,
@@ -1235,6 +1304,10 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     a.out = out; a.ldo = ldo;
     a.po = static_cast<float *>(ws);
     a.pml = a.po + (int64_t)(2 * p.P) * p.HG * p.R * c.D;
+    a.todo = reinterpret_cast<int *>(a.pml + (int64_t)(2 * p.P) * p.HG * p.R * 2);
+    a.join = p.join;
+    // one row a wave where that makes few workgroups, else four
+    a.JR = (int64_t)p.P * p.HG * p.R <= 32768 ? 4 : 16;
     const unsigned grid = (unsigned)p.P;
     hipError_t e;
     const bool f32 = dt == MXS_F32;
@@ -1242,7 +1315,7 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     else if (p.NDP == 4) e = tree_go<4>(p, a, grid, f32, st);
     else e = tree_go<8>(p, a, grid, f32, st);
     if (e != hipSuccess || !p.join) return e;
-    const dim3 jg((unsigned)ceil_div(max_q * Hq, (int64_t)4), (unsigned)B);
+    const dim3 jg((unsigned)p.P, (unsigned)ceil_div(p.HG * p.R, a.JR));
     if (f32) hipLaunchKernelGGL((k_tree_join<float>), jg, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((k_tree_join<__bf16>), jg, dim3(256), 0, st, a);
     return hipGetLastError();
