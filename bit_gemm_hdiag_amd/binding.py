@@ -549,34 +549,42 @@ def mxs_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none",
     return out.to(device)
 
 
-def _rows(t: torch.Tensor, name: str, dev):
-    """(pointer, token stride, head stride) of a [T, H, D] GPU tensor with adjacent dims."""
-    if t.dim() != 3 or t.device != dev or t.stride(2) != 1:
-        raise ValueError(f"{name} must be a [T, H, D] tensor on {dev} with unit stride in the last dimension")
+# The calls of a decode step are short, so their checks avoid what is slow in
+# Python: device objects are compared by index, strides read once.
+def _gpu(t: torch.Tensor, name: str) -> int:
+    """Index of the GPU that holds t."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return i
+
+
+def _rows(t: torch.Tensor, name: str, gpu: int):
+    """(pointer, token stride, head stride) of a [T, H, D] tensor on that GPU with adjacent dims."""
+    if t.dim() != 3 or t.get_device() != gpu:
+        raise ValueError(f"{name} must be a [T, H, D] tensor on cuda:{gpu}")
     s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name} must have unit stride in the last dimension")
     return t.data_ptr(), s[0], s[1]
 
 
-def _vector(t: torch.Tensor, name: str, dtype, n: int, dev) -> int:
-    """Pointer of a contiguous [n] tensor of `dtype` on `dev`."""
-    if t.dtype != dtype or t.dim() != 1 or t.numel() != n or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {dev}")
+def _vector(t: torch.Tensor, name: str, dtype, n: int, gpu: int) -> int:
+    """Pointer of a contiguous [n] tensor of `dtype` on that GPU."""
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or t.get_device() != gpu or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{gpu}")
     return t.data_ptr()
 
 
-def _gpu(t: torch.Tensor, name: str):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    return t.device
-
-
-def _call(dev, fn, name: str, *args):
-    """The C call on the current stream of `dev`, with `dev` current (HIP launches there)."""
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, _stream(dev)), name)
+def _call(gpu: int, fn, name: str, *args):
+    """The C call on the current stream of that GPU, with the GPU current (HIP launches there)."""
+    if torch._C._cuda_getDevice() == gpu:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)), name)
+        with torch.cuda.device(gpu):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
+    if status:
+        _check(status, name)
 
 
 def _layout(layout: str) -> int:
@@ -591,17 +599,17 @@ def mxs_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, layou
     2 * len(freq) dims of every head turned by positions [T] (int64) times freq
     (fp64, from mxs_rope_frequencies). out may be x. The gradient with respect
     to x is the same call on the output's gradient at -positions."""
-    dev = _gpu(x, "x")
-    px, xt, xh = _rows(x, "x", dev)
+    gpu = _gpu(x, "x")
+    px, xt, xh = _rows(x, "x", gpu)
     T, H, D = x.shape
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
-    elif out.shape != x.shape or out.dtype != x.dtype:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError("out must have x's shape and type")
-    py, yt, yh = _rows(out, "out", dev)
+    py, yt, yh = _rows(out, "out", gpu)
     n = freq.numel()
-    _call(dev, _lib.mxs_rope, "mxs_rope", px, _dtype(x), T, H, D, xt, xh,
-          _vector(positions, "positions", torch.int64, T, dev), _vector(freq, "freq", torch.float64, n, dev), 2 * n,
+    _call(gpu, _lib.mxs_rope, "mxs_rope", px, _dtype(x), T, H, D, xt, xh,
+          _vector(positions, "positions", torch.int64, T, gpu), _vector(freq, "freq", torch.float64, n, gpu), 2 * n,
           _layout(layout), mscale, py, yt, yh)
     return out
 
@@ -612,7 +620,7 @@ class KV4Cache:
     """A pool of pages of 4-bit keys and values (see mxs_kv4_cache): codes kc,
     vc uint8 [pages, page_size, H, D / 2], E8M0 bytes ks, vs uint8 [pages,
     page_size, H, D / 32], contiguous. Slot = page * page_size + offset.
-    Frozen: the C struct is built once, on first use, and reused."""
+    Frozen: checked and its C struct built once."""
     kc: torch.Tensor
     ks: torch.Tensor
     vc: torch.Tensor
@@ -627,15 +635,11 @@ class KV4Cache:
                     or t.device != self.kc.device:
                 raise ValueError("cache planes must be contiguous uint8 [pages, page_size, H, D / 2] codes and "
                                  "[pages, page_size, H, D / 32] scales on one GPU")
-
-    def c_struct(self):
-        c = self.__dict__.get("_c")
-        if c is None:
-            P, S, H, h = self.kc.shape
-            c = _Kv4Cache(P, S, H, 2 * h, 0, self.kc.data_ptr(), self.ks.data_ptr(), self.vc.data_ptr(),
-                          self.vs.data_ptr())
-            object.__setattr__(self, "_c", c)
-        return c
+        c = _Kv4Cache(P, S, H, 2 * h, 0, self.kc.data_ptr(), self.ks.data_ptr(), self.vc.data_ptr(),
+                      self.vs.data_ptr())
+        for k, v in (("_c", c), ("_ref", ctypes.pointer(c)), ("gpu", self.kc.get_device()), ("page_size", S),
+                     ("H", H), ("D", 2 * h)):
+            object.__setattr__(self, k, v)
 
 
 def kv4_cache_alloc(pages: int, page_size: int, H: int, D: int, device="cuda") -> KV4Cache:
@@ -646,11 +650,10 @@ def kv4_cache_alloc(pages: int, page_size: int, H: int, D: int, device="cuda") -
     return KV4Cache(*(torch.empty((pages, page_size, H, D // w), **kw) for w in (2, 32, 2, 32)))
 
 
-def _kv_rows(cache: KV4Cache, t: torch.Tensor, name: str, T: int, dtype, dev):
-    H, h = cache.kc.shape[2:]
-    if t.dtype != dtype or tuple(t.shape) != (T, H, 2 * h):
-        raise ValueError(f"{name} must be a {dtype} [{T}, {H}, {2 * h}] tensor")
-    return _rows(t, name, dev)
+def _kv_rows(cache: KV4Cache, t: torch.Tensor, name: str, T: int, dtype):
+    if t.dtype is not dtype or t.shape != (T, cache.H, cache.D):
+        raise ValueError(f"{name} must be a {dtype} [{T}, {cache.H}, {cache.D}] tensor")
+    return _rows(t, name, cache.gpu)
 
 
 def mxs_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -659,18 +662,17 @@ def mxs_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: tor
     """Quantises k, v [T, H, D] into the cache at slots [T] (int64, distinct;
     negative or past the pool: skipped). With positions and freq, the keys are
     rotated first, as by mxs_rope but without rounding in between."""
-    dev = _gpu(cache.kc, "cache")
-    T = slots.numel()
-    pk, kt, kh = _kv_rows(cache, k, "k", T, k.dtype, dev)
-    pv, vt, vh = _kv_rows(cache, v, "v", T, k.dtype, dev)
+    gpu, T = cache.gpu, slots.numel()
+    pk, kt, kh = _kv_rows(cache, k, "k", T, k.dtype)
+    pv, vt, vh = _kv_rows(cache, v, "v", T, k.dtype)
     if (positions is None) != (freq is None):
         raise ValueError("positions and freq go together")
     n, pp, pf = 0, None, None
     if positions is not None:
         n = freq.numel()
-        pp, pf = _vector(positions, "positions", torch.int64, T, dev), _vector(freq, "freq", torch.float64, n, dev)
-    _call(dev, _lib.mxs_kv4_append, "mxs_kv4_append", ctypes.byref(cache.c_struct()), pk, pv, _dtype(k), T, kt, kh, vt,
-          vh, _vector(slots, "slots", torch.int64, T, dev), pp, pf, 2 * n, _layout(layout), mscale)
+        pp, pf = _vector(positions, "positions", torch.int64, T, gpu), _vector(freq, "freq", torch.float64, n, gpu)
+    _call(gpu, _lib.mxs_kv4_append, "mxs_kv4_append", cache._ref, pk, pv, _dtype(k), T, kt, kh, vt, vh,
+          _vector(slots, "slots", torch.int64, T, gpu), pp, pf, 2 * n, _layout(layout), mscale)
 
 
 def mxs_kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
@@ -678,19 +680,17 @@ def mxs_kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torc
     """(k, v), each [T, H, D]: the values of slots [T] (int64), exact. Rows of
     slots that are negative or past the pool are left as they were (zero in
     outputs that the call allocates). dtype is that of outputs not given."""
-    dev = _gpu(cache.kc, "cache")
-    T = slots.numel()
+    gpu, T = cache.gpu, slots.numel()
     if k_out is not None or v_out is not None:
         dtype = (k_out if k_out is not None else v_out).dtype
-    H, h = cache.kc.shape[2:]
     if k_out is None:
-        k_out = torch.zeros((T, H, 2 * h), dtype=dtype, device=dev)
+        k_out = torch.zeros((T, cache.H, cache.D), dtype=dtype, device=cache.kc.device)
     if v_out is None:
-        v_out = torch.zeros((T, H, 2 * h), dtype=dtype, device=dev)
-    pk, kt, kh = _kv_rows(cache, k_out, "k_out", T, dtype, dev)
-    pv, vt, vh = _kv_rows(cache, v_out, "v_out", T, dtype, dev)
-    _call(dev, _lib.mxs_kv4_read, "mxs_kv4_read", ctypes.byref(cache.c_struct()),
-          _vector(slots, "slots", torch.int64, T, dev), T, _dtype(k_out), pk, kt, kh, pv, vt, vh)
+        v_out = torch.zeros((T, cache.H, cache.D), dtype=dtype, device=cache.kc.device)
+    pk, kt, kh = _kv_rows(cache, k_out, "k_out", T, dtype)
+    pv, vt, vh = _kv_rows(cache, v_out, "v_out", T, dtype)
+    _call(gpu, _lib.mxs_kv4_read, "mxs_kv4_read", cache._ref, _vector(slots, "slots", torch.int64, T, gpu), T,
+          _dtype(k_out), pk, kt, kh, pv, vt, vh)
     return k_out, v_out
 
 
@@ -713,43 +713,40 @@ def mxs_attend_kv4_tree(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, l
     sequence (default: total_q and what the table can hold); tight bounds give
     a better split. Rows of no sequence are left as they were in `out` (zero in
     an output that the call allocates)."""
-    dev = _gpu(q, "q")
-    pq, qt, qh = _rows(q, "q", dev)
+    gpu = _gpu(q, "q")
+    pq, qt, qh = _rows(q, "q", gpu)
     total, Hq, D = q.shape
-    if qh != D and Hq > 1:
-        raise ValueError("q's heads must be adjacent")
     if out is None:
-        out = torch.zeros((total, Hq, D), dtype=q.dtype, device=dev)
-    elif out.shape != q.shape or out.dtype != q.dtype:
+        out = torch.zeros((total, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError("out must have q's shape and type")
-    po, ot, oh = _rows(out, "out", dev)
-    if oh != D and Hq > 1:
-        raise ValueError("out's heads must be adjacent")
-    P, S, H, h = cache.kc.shape
-    if 2 * h != D or cache.kc.device != dev:
+    po, ot, oh = _rows(out, "out", gpu)
+    if (qh != D or oh != D) and Hq > 1:
+        raise ValueError("the heads of q and of out must be adjacent")
+    if cache.D != D or cache.gpu != gpu:
         raise ValueError("q and the cache must have one head dimension and one device")
-    if table.dtype != torch.int32 or table.dim() != 2 or table.device != dev or not table.is_contiguous():
-        raise ValueError(f"table must be a contiguous int32 [B, pages] tensor on {dev}")
+    if table.dtype is not torch.int32 or table.dim() != 2 or table.get_device() != gpu or not table.is_contiguous():
+        raise ValueError(f"table must be a contiguous int32 [B, pages] tensor on cuda:{gpu}")
     B, width = table.shape
-    words = 0
+    pm, words = None, 0
     if mask is not None:
-        if mask.dtype != torch.int64 or mask.dim() != 2 or mask.shape[0] != total or mask.device != dev \
+        if mask.dtype is not torch.int64 or mask.dim() != 2 or mask.shape[0] != total or mask.get_device() != gpu \
                 or not mask.is_contiguous():
-            raise ValueError(f"mask must be a contiguous int64 [total_q, words] tensor on {dev}")
-        words = mask.shape[1]
+            raise ValueError(f"mask must be a contiguous int64 [total_q, words] tensor on cuda:{gpu}")
+        pm, words = mask.data_ptr(), mask.shape[1]
     if max_q is None:
         max_q = total
     if max_len is None:
-        max_len = width * S
+        max_len = width * cache.page_size
     dt = _dtype(q)
     if ws is None:
-        p, n = _workspace(int(_lib.mxs_attend_kv4_tree_workspace(dt, B, total, max_q, max_len, Hq, H, D)), dev, None)
+        p, n = _workspace(int(_lib.mxs_attend_kv4_tree_workspace(dt, B, total, max_q, max_len, Hq, cache.H, D)),
+                          q.device, None)
     else:
-        if ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"ws must be a contiguous tensor on {dev}")
+        if ws.get_device() != gpu or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on cuda:{gpu}")
         p, n = ws.data_ptr(), ws.numel() * ws.element_size()
-    _call(dev, _lib.mxs_attend_kv4_tree, "mxs_attend_kv4_tree", pq, dt, qt, ctypes.byref(cache.c_struct()),
-          table.data_ptr(), width, _vector(lens, "lens", torch.int32, B, dev),
-          _vector(cu, "cu", torch.int32, B + 1, dev), None if mask is None else mask.data_ptr(), words, B, total,
+    _call(gpu, _lib.mxs_attend_kv4_tree, "mxs_attend_kv4_tree", pq, dt, qt, cache._ref, table.data_ptr(), width,
+          _vector(lens, "lens", torch.int32, B, gpu), _vector(cu, "cu", torch.int32, B + 1, gpu), pm, words, B, total,
           max_q, max_len, Hq, scale, po, ot, p, n)
     return out

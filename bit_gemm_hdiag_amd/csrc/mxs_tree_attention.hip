@@ -57,6 +57,7 @@ constexpr int kStep = 16 * kNTL;     // tokens of a stage
 struct TreeArgs {
     const void *q;
     int64_t ldq;                     // elements between query tokens (heads D apart)
+    bool qvec;                       // query rows 16-byte aligned
     const uint8_t *kc, *ks, *vc, *vs;
     int64_t pages;
     const int32_t *table;
@@ -328,35 +329,58 @@ __device__ __forceinline__ uint64_t mask_window(const TreeArgs &a, const Place &
 }
 
 // Query rows of a wave as B operands: lane (r, c), step b holds the dims of
-// word c NDP + b of row r (zero past the rows and past D)
+// word c NDP + b of row r (zero past the rows and past D). All loads are issued
+// before the first is used; 16 bytes each where the rows are aligned (qvec).
 template <int NDP, int CT, int PARTS>
 __device__ __forceinline__ void load_queries(const TreeArgs &a, const Place &p, int g, int row0, int lane,
                                              bf8 qf[CT][NDP][PARTS]) {
+    typedef std::conditional_t<PARTS == 1, uint16_t, float> T;
+    constexpr int N = PARTS == 1 ? 1 : 2;                // 16-byte loads of 8 elements
     const int r = lane & 15, c = lane >> 4;
+    u4 raw[CT][NDP][N];
+    bool on[CT];
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
         const int row = row0 + 16 * t + r;
-        const bool on = row < p.n * a.G;
-        const int i = on ? row / a.G : 0, h = on ? g * a.G + row - i * a.G : 0;
-        const int64_t at = (int64_t)(on ? p.q0 + i : 0) * a.ldq + (int64_t)h * a.D;
+        on[t] = row < p.n * a.G;
+        const int i = on[t] ? row / a.G : 0, h = on[t] ? g * a.G + row - i * a.G : 0;
+        const T *q = static_cast<const T *>(a.q) + (int64_t)(p.q0 + i) * a.ldq + (int64_t)h * a.D;
 #pragma unroll
         for (int b = 0; b < NDP; ++b) {
             const int d0 = 8 * (c * NDP + b);
-            const bool in = on && d0 < a.D;
+            const T *e = q + (d0 < a.D ? d0 : 0);
+            if (a.qvec) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) raw[t][b][k] = reinterpret_cast<const u4 *>(e)[k];
+            } else if constexpr (PARTS == 1) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) raw[t][b][0][k] = e[2 * k] | (uint32_t)e[2 * k + 1] << 16;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) raw[t][b][k >> 2][k & 3] = __float_as_uint(e[k]);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+        for (int b = 0; b < NDP; ++b) {
+            const bool in = on[t] && 8 * (c * NDP + b) < a.D;
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
-                const int64_t e = at + (in ? d0 + word_dim(s) : 0);
-                float x = 0.f;
-                if (in) x = PARTS == 1 ? bf16_bits_to_f32(static_cast<const uint16_t *>(a.q)[e])
-                                       : static_cast<const float *>(a.q)[e];
-                if (a.negate) x = -x;
+                const int d = word_dim(s);
+                float x;
+                if constexpr (PARTS == 1)
+                    x = __uint_as_float(d & 1 ? raw[t][b][0][d >> 1] & 0xFFFF0000u : raw[t][b][0][d >> 1] << 16);
+                else
+                    x = __uint_as_float(raw[t][b][d >> 2][d & 3]);
+                x = in ? (a.negate ? -x : x) : 0.f;
                 __bf16 part[PARTS];
                 split_bf16<PARTS>(x, part);
 #pragma unroll
                 for (int k = 0; k < PARTS; ++k) qf[t][b][k][s] = part[k];
             }
         }
-    }
 }
 
 // Operands that take the offset of 8 codes out of the scores: A = the scales of
@@ -897,8 +921,11 @@ __global__ __launch_bounds__(64 * rows_waves(NDP, CT)) void k_tree_rows(TreeArgs
 
         int lt = p.t0 + part * STEP;
         if (lt < p.t1) {
+            int pages[SETS];
+#pragma unroll
+            for (int j = 0; j < SETS; ++j) pages[j] = page_at(lt + j * turn);
             unroll_sets<SETS>([&](auto J) {
-                const int row = rows_of(J, lt + J * turn, page_at(lt + J * turn));
+                const int row = rows_of(J, lt + J * turn, pages[J]);
                 valid[J] = __ballot(row >= 0);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 load_ks(J, row);
@@ -1126,66 +1153,79 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
 }
 
 // Rows of tiles that lie in several shares: out = sum_s O_s 2^(m_s - M) 2^9 /
-// sum_s l_s 2^(m_s - M), pieces in order. Workgroup (p, y): the tile that starts
-// in share p, if it ends in another, JR of its rows from y JR on, one wave a row;
-// lane s holds the weight of piece s of a run of 64, and four dims (D <= 256).
+// sum_s l_s 2^(m_s - M). Workgroup (p, y): the tile that starts in share p, if it
+// ends in another, JR of its rows from y JR on. A group of LR >= D / 4 lanes holds
+// a row (four dims a lane) and every SL-th piece; the SL groups of a row are
+// added in LDS in order. Few pieces: many rows at a time; many: many groups a row.
 template <typename T>
 __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
-    const int lane = threadIdx.x & 63, p0 = blockIdx.x;
+    __shared__ __attribute__((aligned(16))) f4 so[256];
+    __shared__ float2 sml[32];
+    const int p0 = blockIdx.x, tid = threadIdx.x;
     const int shares = a.todo[8 * a.P];
     const JoinOf t = {a.todo[8 * p0], a.todo[8 * p0 + 1], a.todo[8 * p0 + 2], a.todo[8 * p0 + 3], a.todo[8 * p0 + 4]};
     if (p0 >= shares || t.last <= p0) return;
-    const int SR = a.HG * a.R;
-    const int d = 4 * lane < a.D ? 4 * lane : 0;
-    const int64_t one = (int64_t)SR * a.D;               // a slot
-    for (int k = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); k < a.JR; k += 4) {
+    const int SR = a.HG * a.R, ns = t.last - p0 + 1;
+    const int LR = a.D <= 32 ? 8 : (a.D <= 64 ? 16 : (a.D <= 128 ? 32 : 64)), groups = 256 / LR;
+    int SL = 1;
+    while (4 * SL < ns && 2 * SL <= groups) SL *= 2;
+    const int grp = tid / LR, sl = grp % SL, d = 4 * (tid % LR) < a.D ? 4 * (tid % LR) : 0;
+    const bool mine = 4 * (tid % LR) < a.D;
+    for (int k = grp / SL; k < a.JR; k += groups / SL) {
         const int in = blockIdx.y * a.JR + k;
         const int gi = in / a.R, row = t.row + in - gi * a.R;
-        if (in >= SR || row >= t.n * a.G) continue;
-        const int i = row / a.G, h = (t.g + gi) * a.G + row - i * a.G;
+        const bool on = in < SR && row < t.n * a.G;
         float M = -INFINITY, L = 0.f;
         f4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int q = p0; q <= t.last; q += 64) {
-            const int ns = t.last - q + 1 < 64 ? t.last - q + 1 : 64;
-            // slot 1 of the tile's first share, slot 0 of the others
-            const int me = q + (lane < ns ? lane : 0);
-            const int64_t at = (2 * (int64_t)me + (me == p0 ? 1 : 0)) * SR + in;
-            float m = -INFINITY, lsum = 0.f;
-            if (lane < ns) {
-                m = a.pml[2 * at];
-                lsum = a.pml[2 * at + 1];
-            }
-            float Mn = m;
+        if (on)
+            for (int s0 = sl; s0 < ns; s0 += 4 * SL) {
+                float m[4], l[4];
+                f4 v[4];
 #pragma unroll
-            for (int j = 32; j; j >>= 1) Mn = fmaxf(Mn, __shfl_xor(Mn, j));
-            Mn = fmaxf(M, Mn);
-            const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - Mn);
-            const float old = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(M - Mn);
-            float ls = lsum * f;
-#pragma unroll
-            for (int j = 32; j; j >>= 1) ls += __shfl_xor(ls, j);
-            L = L * old + ls;
-            o *= old;
-            M = Mn;
-            const float *po = a.po + d + 2 * (int64_t)q * one + (int64_t)in * a.D;
-            for (int j0 = 0; j0 < ns; j0 += 8) {
-                f4 v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int pk = j0 + j < ns ? j0 + j : ns - 1;
-                    v[j] = *reinterpret_cast<const f4 *>(po + 2 * pk * one + (q + pk == p0 ? one : 0));
+                for (int j = 0; j < 4; ++j) {
+                    const int s = s0 + j * SL < ns ? s0 + j * SL : ns - 1;
+                    // slot 1 of the tile's first share, slot 0 of the others
+                    const int64_t at = (2 * (int64_t)(p0 + s) + (s == 0 ? 1 : 0)) * SR + in;
+                    const float2 ml = reinterpret_cast<const float2 *>(a.pml)[at];
+                    m[j] = s0 + j * SL < ns ? ml.x : -INFINITY;
+                    l[j] = ml.y;
+                    v[j] = *reinterpret_cast<const f4 *>(a.po + at * a.D + d);
                 }
+                const float Mn = fmaxf(fmaxf(fmaxf(M, m[0]), fmaxf(m[1], m[2])), m[3]);
+                const float f0 = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(M - Mn);
+                L *= f0;
+                o *= f0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float fk =
-                        __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(f), j0 + j < ns ? j0 + j : 0));
-                    if (j0 + j < ns) o += v[j] * fk;
+                for (int j = 0; j < 4; ++j) {
+                    if (s0 + j * SL >= ns) continue;
+                    const float f = m[j] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[j] - Mn);
+                    L += l[j] * f;
+                    o += v[j] * f;
+                }
+                M = Mn;
+            }
+        if (SL > 1) {
+            so[tid] = o;
+            if (tid % LR == 0) sml[grp] = make_float2(M, L);
+            __syncthreads();
+            if (sl == 0) {
+                for (int j = 1; j < SL; ++j) M = fmaxf(M, sml[grp + j].x);
+                const float own = sml[grp].x, f0 = own == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(own - M);
+                L *= f0;
+                o *= f0;
+                for (int j = 1; j < SL; ++j) {
+                    const float2 ml = sml[grp + j];
+                    const float f = ml.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml.x - M);
+                    L += ml.y * f;
+                    o += so[tid + j * LR] * f;
                 }
             }
+            __syncthreads();
         }
-        const float norm = M == -INFINITY ? 0.f : 512.f / L;
-        T *out = static_cast<T *>(a.out) + ((int64_t)t.q0 + i) * a.ldo + (int64_t)h * a.D + d;
-        if (4 * lane < a.D) {
+        if (on && mine && sl == 0) {
+            const int i = row / a.G, h = (t.g + gi) * a.G + row - i * a.G;
+            const float norm = M == -INFINITY ? 0.f : 512.f / L;
+            T *out = static_cast<T *>(a.out) + ((int64_t)t.q0 + i) * a.ldo + (int64_t)h * a.D + d;
 #pragma unroll
             for (int j = 0; j < 4; ++j) out[j] = (T)(o[j] * norm);
         }
@@ -1212,10 +1252,18 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
         p.CT = rows > 16 ? 2 : 1;
         p.R = 16 * p.CT;
         const int nw = rows_waves(p.NDP, p.CT);
-        p.HG = nw;
-        while (Hkv % p.HG) p.HG /= 2;
+        // heads that fill a 128-byte line of codes
+        p.HG = D <= 32 ? 8 : (D <= 64 ? 4 : (D <= 128 ? 2 : 1));
+        if (getenv("HG")) p.HG = atoi(getenv("HG"));
+        while (p.HG > nw || Hkv % p.HG) p.HG /= 2;
         p.U = nw / p.HG * 16 * kRowTiles;
         p.minu = 1;
+        if (getenv("MU")) p.minu = atoi(getenv("MU"));
+        const int lim = getenv("LIM") ? atoi(getenv("LIM")) : 512;
+        if (max_len <= lim) {
+            p.HG = 1;
+            p.U = ceil_div(max_len > 0 ? max_len : 1, (int64_t)64) * 64;
+        }
         slots = 256;
     } else {
         p.CT = bf ? 2 : 1;
@@ -1223,7 +1271,8 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
         p.R = 16 * p.CT * (kWaves / p.WT);
         p.HG = 1;
         p.U = kStep;
-        p.minu = 2;
+        p.minu = 8;
+        if (getenv("MT")) p.minu = atoi(getenv("MT"));
         slots = p.NDP == 8 ? 256 : 512;
     }
     const int64_t T = max_len > 0 ? ceil_div(max_len, (int64_t)p.U) : 1;
@@ -1287,7 +1336,9 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
                                   hipStream_t st) {
     const TreePlan p = tree_plan(dt, B, max_q, max_len, Hq, c.H, c.D);
     TreeArgs a{};
-    a.q = q; a.ldq = ldq; a.kc = c.kc; a.ks = c.ks; a.vc = c.vc; a.vs = c.vs; a.pages = c.pages;
+    const int es = dt == MXS_BF16 ? 2 : 4;
+    a.q = q; a.ldq = ldq;
+    a.qvec = reinterpret_cast<uintptr_t>(q) % 16 == 0 && (ldq * es % 16 == 0 || total_q == 1); a.kc = c.kc; a.ks = c.ks; a.vc = c.vc; a.vs = c.vs; a.pages = c.pages;
     a.table = table; a.ldt = ldt; a.lens = lens; a.cu = cu; a.mask = mask; a.words = (int)words;
     a.B = (int)B; a.Hq = (int)Hq; a.Hkv = c.H; a.G = (int)(Hq / c.H); a.D = c.D;
     a.total_q = (int)total_q; a.max_q = (int)max_q; a.max_len = (int)max_len; a.ps = c.page_size;
@@ -1306,8 +1357,8 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     a.pml = a.po + (int64_t)(2 * p.P) * p.HG * p.R * c.D;
     a.todo = reinterpret_cast<int *>(a.pml + (int64_t)(2 * p.P) * p.HG * p.R * 2);
     a.join = p.join;
-    // one row a wave where that makes few workgroups, else four
-    a.JR = (int64_t)p.P * p.HG * p.R <= 32768 ? 4 : 16;
+    a.JR = (int)ceil_div((int64_t)p.P * p.HG * p.R, 4096);      // about 4096 workgroups
+    if (getenv("JR")) a.JR = atoi(getenv("JR"));
     const unsigned grid = (unsigned)p.P;
     hipError_t e;
     const bool f32 = dt == MXS_F32;
