@@ -15,5 +15,6 @@ def __getattr__(name):
     if name.startswith("mxs_") or name in ("MxsError", "QMat", "qmat_alloc", "library_path",
                                           "STATUS", "NOALLOC_SCRATCH_BYTES", "KV4Cache", "kv4_cache_alloc"):
         from . import binding
-        return getattr(binding, name)
+        globals()[name] = value = getattr(binding, name)     # found directly from now on
+        return value
     raise AttributeError(name)

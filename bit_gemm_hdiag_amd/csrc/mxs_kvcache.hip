@@ -13,6 +13,7 @@
 // accuracy. The cosines and sines of a workgroup's tokens are computed once
 // into LDS and shared by all its heads.
 #include <cmath>
+#include <type_traits>
 
 #include "mxs_device.h"
 #include "mxs_internal.h"
@@ -190,19 +191,32 @@ struct AppendArgs {
     int H, D, half;
     int TB;
     Div16 words, hwords;            // 8-element words of a token row, of a head
+    Div16 chunk;                    // words of a token row that a workgroup takes
     float mscale;
 };
 
-// Element d of head row r, rotated in fp64 (partner element inside the row)
-template <typename T, bool PAIRS>
-__device__ __forceinline__ double rotated(const T *r, int d, int half, const double *c, const double *s) {
-    const double x = (double)load1<T>(r + d);
-    if (d >= 2 * half) return x;
-    const int i = PAIRS ? d >> 1 : (d < half ? d : d - half);
-    const bool first = PAIRS ? !(d & 1) : d < half;
-    const double y = (double)load1<T>(r + (PAIRS ? d ^ 1 : (first ? d + half : d - half)));
-    return first ? x * c[i] - y * s[i] : x * c[i] + y * s[i];
-}
+// The 8 elements of a word and, for a rotation of halves, the 8 that they pair
+// with, as the loads left them (widening waits for them)
+template <typename T, bool VEC>
+struct Eight {
+    static constexpr int N = VEC ? (int)sizeof(T) / 2 : 8;
+    typedef std::conditional_t<VEC, u32x4, T> E;
+    E e[N];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = reinterpret_cast<const E *>(p)[i];
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (!VEC) {
+            return load1<T>(&e[i]);
+        } else if constexpr (sizeof(T) == 2) {
+            const uint32_t w = e[0][i >> 1];
+            return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+        } else {
+            return __uint_as_float(e[i >> 2][i & 3]);
+        }
+    }
+};
 
 // MXINT4 of one quad's 32 fp64 values, 8 a lane: the rule of quantize_pack8
 // without its rounding to fp32, so that a rotated key's code depends on no
@@ -233,17 +247,52 @@ __device__ __forceinline__ uint32_t pack8_f64(const double v[8], uint32_t &byte)
     return bad ? 0u : w;
 }
 
-template <typename T, bool VEC, int ROT>        // ROT 0 none, 1 halves, 2 pairs
+// ROT 0: none; 1: halves, whole words pair with whole words (half % 8 == 0); 2:
+// pairs; 3: halves of any size (the partners are loaded one by one). A thread
+// takes WPT words, all loaded before the first is quantised; the cosines and
+// sines of the workgroup's tokens are formed while the loads are in flight.
+template <typename T, bool VEC, int ROT, int WPT>
 __global__ __launch_bounds__(256) void k_kv4_append(AppendArgs a) {
     extern __shared__ __attribute__((aligned(16))) double cs64[];
     const int tid = threadIdx.x, half = a.half;
     const int64_t t0 = (int64_t)blockIdx.x * a.TB;
     const int nt = a.T - t0 < a.TB ? (int)(a.T - t0) : a.TB;
+    const bool isv = blockIdx.y != 0;
+    const bool rot = ROT != 0 && !isv;
+    const T *x = static_cast<const T *>(isv ? a.v : a.k);
+    const int64_t xt = isv ? a.vt : a.kt, xh = isv ? a.vh : a.kh;
+    uint8_t *codes = isv ? a.vc : a.kc, *scales = isv ? a.vs : a.ks;
+    // a quad's four lanes hold one 32-block of one token: the words of a head
+    // are a multiple of four, so every branch below is taken by whole quads
+    const uint32_t w0 = blockIdx.z * a.chunk.d;
+    Eight<T, VEC> own[WPT], other[WPT];
+    int64_t slot[WPT];
+    uint32_t tl[WPT], w[WPT], wd[WPT];
+#pragma unroll
+    for (int k = 0; k < WPT; ++k) {
+        const uint32_t e = tid + 256u * k;
+        tl[k] = quot(e, a.chunk);
+        w[k] = w0 + e - tl[k] * a.chunk.d;
+        const bool on = tl[k] < (uint32_t)nt && w[k] < a.words.d;
+        if (!on) {
+            tl[k] = 0;
+            w[k] = w0;
+        }
+        slot[k] = on ? a.slots[t0 + tl[k]] : -1;
+        const uint32_t h = quot(w[k], a.hwords);
+        wd[k] = w[k] - h * a.hwords.d;
+        const T *r = x + (t0 + tl[k]) * xt + (int64_t)h * xh;
+        own[k].load(r + 8 * wd[k]);
+        if (ROT == 1 && !isv) {
+            const int d = 8 * (int)wd[k];
+            other[k].load(r + (d < half ? d + half : (d < 2 * half ? d - half : d)));
+        }
+    }
     double *sn64 = cs64 + a.TB * half;
-    if constexpr (ROT != 0) {
+    if (rot) {
         for (int e = tid; e < nt * half; e += 256) {
-            const int tl = e / half, i = e - tl * half;
-            const double turns = (double)a.pos[t0 + tl] * (a.freq[i] * kInv2Pi);
+            const int l = e / half, i = e - l * half;
+            const double turns = (double)a.pos[t0 + l] * (a.freq[i] * kInv2Pi);
             double s, c;
             sincospi(2.0 * (turns - rint(turns)), &s, &c);
             cs64[e] = c * (double)a.mscale;
@@ -251,54 +300,75 @@ __global__ __launch_bounds__(256) void k_kv4_append(AppendArgs a) {
         }
         __syncthreads();
     }
-    const bool isv = blockIdx.y != 0;
-    const T *x = static_cast<const T *>(isv ? a.v : a.k);
-    const int64_t xt = isv ? a.vt : a.kt, xh = isv ? a.vh : a.kh;
-    uint8_t *codes = isv ? a.vc : a.kc, *scales = isv ? a.vs : a.ks;
-    // a quad's four lanes hold one 32-block of one token: the words of a head
-    // are a multiple of four, so every branch below is taken by whole quads
-    const uint32_t total = (uint32_t)nt * a.words.d;
-    for (uint32_t e = tid; e < total; e += 256) {
-        const uint32_t tl = quot(e, a.words), w = e - tl * a.words.d;
-        const int64_t slot = a.slots[t0 + tl];
-        if ((uint64_t)slot >= (uint64_t)a.nslots) continue;
-        const uint32_t h = quot(w, a.hwords), wd = w - h * a.hwords.d;
-        const T *r = x + (t0 + tl) * xt + (int64_t)h * xh;
-        const int d0 = 8 * (int)wd;
-        uint32_t word, byte;
-        if (ROT != 0 && !isv) {
-            double v[8];
-            const double *c = cs64 + tl * half, *s = sn64 + tl * half;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = rotated<T, ROT == 2>(r, d0 + i, half, c, s);
+    for (int k = 0; k < WPT; ++k) {
+        if ((uint64_t)slot[k] >= (uint64_t)a.nslots) continue;
+        const int d0 = 8 * (int)wd[k];
+        uint32_t word, byte;
+        if (rot) {
+            double v[8];
+            const double *c = cs64 + tl[k] * half, *s = sn64 + tl[k] * half;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int d = d0 + i;
+                const double p = (double)own[k].get(i);
+                v[i] = p;
+                if (d >= 2 * half) continue;
+                if constexpr (ROT == 2) {
+                    const double q = (double)own[k].get(i ^ 1);
+                    v[i] = i & 1 ? p * c[d >> 1] + q * s[d >> 1] : p * c[d >> 1] - q * s[d >> 1];
+                } else {
+                    const bool first = d < half;
+                    const int j = first ? d : d - half;
+                    double q;
+                    if constexpr (ROT == 1) {
+                        q = (double)other[k].get(i);
+                    } else {
+                        const uint32_t h = quot(w[k], a.hwords);
+                        q = (double)load1<T>(x + (t0 + tl[k]) * xt + (int64_t)h * xh + (first ? d + half : d - half));
+                    }
+                    v[i] = first ? p * c[j] - q * s[j] : p * c[j] + q * s[j];
+                }
+            }
             word = pack8_f64(v, byte);
         } else {
             float v[8];
-            load8<T, VEC>(r + d0, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = own[k].get(i);
             word = (uint32_t)quantize_pack8(v, 4, byte);
         }
-        const int64_t cw = slot * a.words.d + w;          // word of the pool
+        const int64_t cw = slot[k] * a.words.d + w[k];    // word of the pool
         reinterpret_cast<uint32_t *>(codes)[cw] = word;
-        if ((w & 3) == 0) scales[cw >> 2] = (uint8_t)byte;
+        if ((w[k] & 3) == 0) scales[cw >> 2] = (uint8_t)byte;
     }
+}
+
+template <typename T, bool VEC, int ROT>
+hipError_t append_go(AppendArgs a, hipStream_t st) {
+    // one word a thread until the chip is full, then four; whole tokens (and
+    // their cosines and sines in LDS, 16 bytes a token and pair), or a chunk of one
+    const int64_t words = a.words.d;
+    const int wpt = 2 * a.T * words <= 4 * 256 * 2048 ? 1 : 4;
+    int64_t tb = 256 * wpt / words;
+    const int64_t cap = ROT ? 2048 / a.half : tb;
+    tb = tb > cap ? cap : tb;
+    a.TB = (int)(tb < 1 ? 1 : tb);
+    a.chunk = div16((uint32_t)(words < 256 * wpt ? words : 256 * wpt));
+    const dim3 grid((unsigned)ceil_div(a.T, (int64_t)a.TB), 2, (unsigned)ceil_div(words, (int64_t)a.chunk.d));
+    const size_t lds = ROT ? (size_t)a.TB * a.half * 16 : 0;
+    if (wpt == 1) hipLaunchKernelGGL((k_kv4_append<T, VEC, ROT, 1>), grid, dim3(256), lds, st, a);
+    else hipLaunchKernelGGL((k_kv4_append<T, VEC, ROT, 4>), grid, dim3(256), lds, st, a);
+    return hipGetLastError();
 }
 
 template <typename T>
 hipError_t append_type(const AppendArgs &a, bool vec, int rot, hipStream_t st) {
-    const dim3 grid((unsigned)ceil_div(a.T, (int64_t)a.TB), 2);
-    const size_t lds = rot ? (size_t)a.TB * a.half * 16 : 0;
-#define MXS_APPEND(VEC, ROT) hipLaunchKernelGGL((k_kv4_append<T, VEC, ROT>), grid, dim3(256), lds, st, a)
-    if (vec) {
-        if (rot == 0) MXS_APPEND(true, 0);
-        else if (rot == 1) MXS_APPEND(true, 1);
-        else MXS_APPEND(true, 2);
-    } else {
-        if (rot == 0) MXS_APPEND(false, 0);
-        else if (rot == 1) MXS_APPEND(false, 1);
-        else MXS_APPEND(false, 2);
+    switch (rot) {
+        case 0: return vec ? append_go<T, true, 0>(a, st) : append_go<T, false, 0>(a, st);
+        case 1: return vec ? append_go<T, true, 1>(a, st) : append_go<T, false, 1>(a, st);
+        case 2: return vec ? append_go<T, true, 2>(a, st) : append_go<T, false, 2>(a, st);
+        default: return vec ? append_go<T, true, 3>(a, st) : append_go<T, false, 3>(a, st);
     }
-#undef MXS_APPEND
-    return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------- read
@@ -308,10 +378,12 @@ struct ReadArgs {
     void *k, *v;
     int64_t T, kt, kh, vt, vh, nslots;
     int TB;
-    Div16 words, hwords;
+    Div16 words, hwords, chunk;
 };
 
-template <typename T, bool VEC>
+// A thread takes WPT words (8 values each); all its codes and scales are loaded
+// before the first is widened
+template <typename T, bool VEC, int WPT>
 __global__ __launch_bounds__(256) void k_kv4_read(ReadArgs a) {
     const bool isv = a.k == nullptr || blockIdx.y != 0;
     const uint32_t *codes = reinterpret_cast<const uint32_t *>(isv ? a.vc : a.kc);
@@ -320,20 +392,36 @@ __global__ __launch_bounds__(256) void k_kv4_read(ReadArgs a) {
     const int64_t yt = isv ? a.vt : a.kt, yh = isv ? a.vh : a.kh;
     const int64_t t0 = (int64_t)blockIdx.x * a.TB;
     const int nt = a.T - t0 < a.TB ? (int)(a.T - t0) : a.TB;
-    const uint32_t total = (uint32_t)nt * a.words.d;
-#pragma unroll 4
-    for (uint32_t e = threadIdx.x; e < total; e += 256) {
-        const uint32_t tl = quot(e, a.words), w = e - tl * a.words.d;
-        const int64_t slot = a.slots[t0 + tl];
-        if ((uint64_t)slot >= (uint64_t)a.nslots) continue;
-        const int64_t cw = slot * a.words.d + w;
-        const uint32_t c = codes[cw];
-        const float s = e8m0_to_f32(scales[cw >> 2]);
-        const uint32_t h = quot(w, a.hwords), wd = w - h * a.hwords.d;
+    const uint32_t w0 = blockIdx.z * a.chunk.d;
+    int64_t slot[WPT];
+    uint32_t tl[WPT], w[WPT], c[WPT], b[WPT];
+#pragma unroll
+    for (int k = 0; k < WPT; ++k) {
+        const uint32_t e = threadIdx.x + 256u * k;
+        tl[k] = quot(e, a.chunk);
+        w[k] = w0 + e - tl[k] * a.chunk.d;
+        const bool on = tl[k] < (uint32_t)nt && w[k] < a.words.d;
+        if (!on) {
+            tl[k] = 0;
+            w[k] = w0;
+        }
+        slot[k] = on ? a.slots[t0 + tl[k]] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < WPT; ++k) {
+        const int64_t cw = ((uint64_t)slot[k] < (uint64_t)a.nslots ? slot[k] : 0) * a.words.d + w[k];
+        c[k] = codes[cw];
+        b[k] = scales[cw >> 2];
+    }
+#pragma unroll
+    for (int k = 0; k < WPT; ++k) {
+        if ((uint64_t)slot[k] >= (uint64_t)a.nslots) continue;
+        const uint32_t h = quot(w[k], a.hwords), wd = w[k] - h * a.hwords.d;
+        const float s = e8m0_to_f32(b[k]);
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = (float)((int32_t)(c << (28 - 4 * i)) >> 28) * s;
-        T *r = y + (t0 + tl) * yt + (int64_t)h * yh + 8 * wd;
+        for (int i = 0; i < 8; ++i) f[i] = (float)((int32_t)(c[k] << (28 - 4 * i)) >> 28) * s;
+        T *r = y + (t0 + tl[k]) * yt + (int64_t)h * yh + 8 * wd;
         if constexpr (VEC) {
             put<T, 16 / sizeof(T)>(r, f);
             if constexpr (sizeof(T) == 4) put<T, 4>(r + 4, f + 4);
@@ -342,6 +430,25 @@ __global__ __launch_bounds__(256) void k_kv4_read(ReadArgs a) {
             for (int i = 0; i < 8; ++i) put<T, 1>(r + i, f + i);
         }
     }
+}
+
+template <typename T>
+hipError_t read_type(ReadArgs a, bool vec, hipStream_t st) {
+    const int64_t words = a.words.d;
+    const int wpt = 2 * a.T * words <= 4 * 256 * 2048 ? 1 : 4;       // as in append_go
+    const int64_t tb = 256 * wpt / words;
+    a.TB = (int)(tb < 1 ? 1 : tb);
+    a.chunk = div16((uint32_t)(words < 256 * wpt ? words : 256 * wpt));
+    const dim3 grid((unsigned)ceil_div(a.T, (int64_t)a.TB), a.k && a.v ? 2 : 1,
+                    (unsigned)ceil_div(words, (int64_t)a.chunk.d));
+    if (wpt == 1) {
+        if (vec) hipLaunchKernelGGL((k_kv4_read<T, true, 1>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_kv4_read<T, false, 1>), grid, dim3(256), 0, st, a);
+    } else {
+        if (vec) hipLaunchKernelGGL((k_kv4_read<T, true, 4>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_kv4_read<T, false, 4>), grid, dim3(256), 0, st, a);
+    }
+    return hipGetLastError();
 }
 
 bool rows16(const void *p, int64_t a, int64_t b, int es) {
@@ -390,14 +497,9 @@ hipError_t launch_kv4_append(const mxs_kv4_cache &c, const void *k, const void *
     a.H = c.H; a.D = c.D; a.half = positions ? rot / 2 : 0; a.mscale = mscale;
     a.words = div16(c.H * (c.D / 8));
     a.hwords = div16(c.D / 8);
-    int64_t tb = 1024 / a.words.d;                     // four words a thread
-    if (T * a.words.d < 256 * 1024) tb = 256 / a.words.d;
-    const int64_t cap = a.half ? 2048 / a.half : 64;   // LDS: 16 bytes a token and pair
-    tb = tb > cap ? cap : tb;
-    a.TB = (int)(tb < 1 ? 1 : tb);
     const int es = dt == MXS_BF16 ? 2 : 4;
     const bool vec = rows16(k, ldkt, ldkh, es) && rows16(v, ldvt, ldvh, es);
-    const int r = a.half == 0 ? 0 : (layout == MXS_ROPE_PAIRS ? 2 : 1);
+    const int r = a.half == 0 ? 0 : (layout == MXS_ROPE_PAIRS ? 2 : (a.half % 8 == 0 ? 1 : 3));
     return dt == MXS_BF16 ? append_type<uint16_t>(a, vec, r, st) : append_type<float>(a, vec, r, st);
 }
 
@@ -408,20 +510,9 @@ hipError_t launch_kv4_read(const mxs_kv4_cache &c, const int64_t *slots, int64_t
     a.kt = ldkt; a.kh = ldkh; a.vt = ldvt; a.vh = ldvh; a.nslots = c.pages * c.page_size;
     a.words = div16(c.H * (c.D / 8));
     a.hwords = div16(c.D / 8);
-    int64_t tb = 1024 / a.words.d;
-    if (T * a.words.d < 256 * 1024) tb = 256 / a.words.d;
-    a.TB = (int)(tb < 1 ? 1 : (tb > 64 ? 64 : tb));
     const int es = dt == MXS_BF16 ? 2 : 4;
     const bool vec = (!k || rows16(k, ldkt, ldkh, es)) && (!v || rows16(v, ldvt, ldvh, es));
-    const dim3 grid((unsigned)ceil_div(T, (int64_t)a.TB), k && v ? 2 : 1);
-    if (dt == MXS_BF16) {
-        if (vec) hipLaunchKernelGGL((k_kv4_read<uint16_t, true>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((k_kv4_read<uint16_t, false>), grid, dim3(256), 0, st, a);
-    } else {
-        if (vec) hipLaunchKernelGGL((k_kv4_read<float, true>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((k_kv4_read<float, false>), grid, dim3(256), 0, st, a);
-    }
-    return hipGetLastError();
+    return dt == MXS_BF16 ? read_type<uint16_t>(a, vec, st) : read_type<float>(a, vec, st);
 }
 
 }  // namespace mxs
