@@ -70,14 +70,18 @@ struct TreeArgs {
     uint32_t pmul, pshift;           // t / ps
     float scale2;                    // |scale| log2(e) 2^9
     bool negate;                     // scale < 0: queries enter negated
-    int R, U, P, minu;               // rows of a tile, tokens of a unit, workgroups, units of a share (at least)
+    int R, U, P;                     // rows of a tile, tokens of a unit, workgroups: powers of two
+    int Rs, Us, Ps;                  // their logarithms
+    int ms, cap;                     // a share has at least 2^ms units, and a tile's 2^-cap
     int HG;                          // KV heads of a tile
+    int nrt;                         // row tiles of a head at most
     int join;                        // a k_tree_join follows
     int JR;                          // its rows of a workgroup
     void *out;
     int64_t ldo;
     float *po, *pml;                 // [2 share + k, HG, R, D], [2 share + k, HG, R, (m, l)]
-    int *todo;                       // [8 share + .]: see JoinOf
+    int *todo;                       // [8 entry + .]: see JoinOf
+    int NT;                          // tiles at most, where they are no more than P: a todo entry each, else 0
 };
 
 // t / ps for 0 <= t < 2^31: pmul = ceil(2^(31 + l) / ps), l = ceil(log2 ps)
@@ -163,8 +167,8 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs &a, int b) {
     q1 = q1 < q0 ? q0 : (q1 > a.total_q ? a.total_q : q1);
     s.q0 = q0;
     s.n = q1 - q0 > a.max_q ? a.max_q : q1 - q0;
-    s.nrt = ((uint32_t)(s.n * a.G) + a.R - 1) / (uint32_t)a.R;
-    s.T = s.len > 0 ? ((uint32_t)s.len + a.U - 1) / (uint32_t)a.U : 1u;
+    s.nrt = ((uint32_t)(s.n * a.G) + a.R - 1) >> a.Rs;
+    s.T = s.len > 0 ? ((uint32_t)s.len + a.U - 1) >> a.Us : 1u;
     return s;
 }
 __device__ __forceinline__ uint32_t units_of(const TreeArgs &a, const Seq &s) {
@@ -183,11 +187,15 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
 }
 
 struct Shares {
-    uint32_t W, P, q, r;             // units, shares, W / P, W % P
-    __device__ __forceinline__ uint32_t start(uint32_t p) const { return p * q + p * r / P; }      // floor(p W / P)
-    // the share of unit x: the last p with p W < (x + 1) P
+    uint32_t W, P;                   // units, shares
+    int shift;                       // little work: shares of 2^shift units; else -1 and P = 2^Ps
+    int Ps;
+    __device__ __forceinline__ uint32_t start(uint32_t p) const {
+        return shift >= 0 ? (p < P ? p << shift : W) : (uint32_t)(((uint64_t)p * W) >> Ps);    // floor(p W / P)
+    }
+    // the share of unit x (else the last p with p W < (x + 1) P)
     __device__ __forceinline__ uint32_t owner(uint32_t x) const {
-        return (uint32_t)(((double)(x + 1) * (double)P - 1.0) / (double)W);
+        return shift >= 0 ? x >> shift : (uint32_t)(((double)(x + 1) * (double)P - 1.0) / (double)W);
     }
 };
 
@@ -233,15 +241,21 @@ __device__ __forceinline__ Shares shares_of(const TreeArgs &a, Window &w, int la
     Shares h;
     w.load(a, 0, 0, lane);
     h.W = w.last();
+    uint32_t T = w.units ? w.s.T : 0u;
     for (int b = 64; b < a.B; b += 64) {
         Window v;
         v.load(a, b, h.W, lane);
         h.W = v.last();
+        T = v.units && v.s.T > T ? v.s.T : T;
     }
-    const uint32_t most = (h.W + a.minu - 1) / (uint32_t)a.minu;
-    h.P = most < (uint32_t)a.P ? most : (uint32_t)a.P;
-    h.q = h.P ? h.W / h.P : 0;
-    h.r = h.P ? h.W % h.P : 0;
+    // the longest tile in at most 2^cap shares: a join of many small pieces
+    // costs more than it gains
+    int sh = a.ms;
+    while (__ballot(T > (1u << (sh + a.cap)))) ++sh;
+    const uint32_t most = (h.W + (1u << sh) - 1) >> sh;
+    h.shift = most <= (uint32_t)a.P ? sh : -1;
+    h.P = h.shift >= 0 ? most : (uint32_t)a.P;
+    h.Ps = a.Ps;
     return h;
 }
 
@@ -253,10 +267,13 @@ struct Place {
     int64_t slot;                    // workspace slot, -1: the whole tile
 };
 
-// What k_tree_join finds at todo + 8 p: the tile whose first piece is the end of
-// share p, if there is one (last > p)
+// What k_tree_join finds in a todo entry. Entries are those of the tiles ((b,
+// head group, row tile), NT > 0) or of the shares that hold a tile's first piece
+// but not its last; an entry with last <= first needs no join. Entry 0 of a
+// share is written by the share, that of a tile by the share of its first unit;
+// entries of no tile are left, and told by the sequence's n.
 struct JoinOf {
-    int last;                        // share of its last piece
+    int first, last;                 // shares of its first and last piece
     int q0, n, g, row;               // Place's
 };
 
@@ -268,11 +285,9 @@ __device__ __forceinline__ void for_each_piece(const TreeArgs &a, int lane, F f)
     Window win;
     const Shares h = shares_of(a, win, lane);
     const uint32_t per = (h.P + 7) / 8, p = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (a.join) {                    // no tile to join yet; todo[8 P] = the number of shares
-        if (threadIdx.x == 0) {
-            if ((blockIdx.x >> 3) < per && p < h.P) a.todo[8 * p] = 0;
-            if (blockIdx.x == 0) a.todo[8 * a.P] = (int)h.P;
-        }
+    if (a.join && a.NT == 0 && threadIdx.x == 0) {       // nothing to join yet; the number of shares
+        if ((blockIdx.x >> 3) < per && p < h.P) a.todo[8 * p + 1] = -1;
+        if (blockIdx.x == 0) a.todo[8 * a.P] = (int)h.P;
     }
     if ((blockIdx.x >> 3) >= per || p >= h.P) return;
     uint32_t x = h.start(p);
@@ -283,13 +298,14 @@ __device__ __forceinline__ void for_each_piece(const TreeArgs &a, int lane, F f)
         const Seq s = win.seq(l);
         const int b = win.b0 + l;
         const uint32_t first = win.first(l);
-        const uint32_t tile = (x - first) / s.T, u0 = (x - first) - tile * s.T;
+        const uint32_t tile = s.T == 1 ? x - first : (x - first) / s.T, u0 = (x - first) - tile * s.T;
+        const uint32_t gt = s.nrt == 1 ? tile : tile / s.nrt;
         const uint32_t u1 = s.T - u0 < end - x ? s.T : u0 + (end - x);
         auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
         Place pl;
         pl.b = uni(b);
-        pl.g = uni((int)(tile / s.nrt) * a.HG);
-        pl.row = uni((int)(tile % s.nrt) * a.R);
+        pl.g = uni((int)gt * a.HG);
+        pl.row = uni((int)(tile - gt * s.nrt) * a.R);
         pl.len = uni(s.len);
         pl.n = uni(s.n);
         pl.q0 = uni(s.q0);
@@ -297,13 +313,15 @@ __device__ __forceinline__ void for_each_piece(const TreeArgs &a, int lane, F f)
         pl.t0 = uni((int)u0 * a.U);
         pl.t1 = uni(u1 == s.T ? s.len : (int)u1 * a.U);
         pl.slot = u0 == 0 && u1 == s.T ? -1 : 2 * (int64_t)p + (u0 > 0 ? 0 : 1);
-        if (u0 == 0 && u1 < s.T && threadIdx.x == 0) {
-            int *t = a.todo + 8 * p;
-            t[0] = (int)h.owner(x + s.T - 1);
-            t[1] = pl.q0;
-            t[2] = pl.n;
-            t[3] = pl.g;
-            t[4] = pl.row;
+        if (a.join && u0 == 0 && (u1 < s.T || a.NT) && threadIdx.x == 0) {
+            const int64_t entry = a.NT ? ((int64_t)b * (a.Hkv / a.HG) + gt) * a.nrt + (tile - gt * s.nrt) : p;
+            int *t = a.todo + 8 * entry;
+            t[0] = (int)p;
+            t[1] = u1 < s.T ? (int)h.owner(x + s.T - 1) : -1;
+            t[2] = pl.q0;
+            t[3] = pl.n;
+            t[4] = pl.g;
+            t[5] = pl.row;
         }
         f(pl);
         x += u1 - u0;
@@ -328,60 +346,65 @@ __device__ __forceinline__ uint64_t mask_window(const TreeArgs &a, const Place &
     return w;
 }
 
-// Query rows of a wave as B operands: lane (r, c), step b holds the dims of
-// word c NDP + b of row r (zero past the rows and past D). All loads are issued
-// before the first is used; 16 bytes each where the rows are aligned (qvec).
+// Query rows of a wave, as the loads leave them: 16 bytes each where the rows
+// are aligned (qvec). Lane (r, c), step b: the dims of word c NDP + b of row r.
 template <int NDP, int CT, int PARTS>
-__device__ __forceinline__ void load_queries(const TreeArgs &a, const Place &p, int g, int row0, int lane,
-                                             bf8 qf[CT][NDP][PARTS]) {
+struct RawQueries {
     typedef std::conditional_t<PARTS == 1, uint16_t, float> T;
-    constexpr int N = PARTS == 1 ? 1 : 2;                // 16-byte loads of 8 elements
-    const int r = lane & 15, c = lane >> 4;
+    static constexpr int N = PARTS == 1 ? 1 : 2;                // 16-byte loads of 8 elements
     u4 raw[CT][NDP][N];
-    bool on[CT];
+    int i[CT];                                                   // query token of the column, -1: no row
+    __device__ __forceinline__ void load(const TreeArgs &a, const Place &p, int g, int row0, int lane) {
+        const int r = lane & 15, c = lane >> 4;
 #pragma unroll
-    for (int t = 0; t < CT; ++t) {
-        const int row = row0 + 16 * t + r;
-        on[t] = row < p.n * a.G;
-        const int i = on[t] ? row / a.G : 0, h = on[t] ? g * a.G + row - i * a.G : 0;
-        const T *q = static_cast<const T *>(a.q) + (int64_t)(p.q0 + i) * a.ldq + (int64_t)h * a.D;
+        for (int t = 0; t < CT; ++t) {
+            const int row = row0 + 16 * t + r;
+            const bool on = row < p.n * a.G;
+            const int tok = on ? row / a.G : 0, h = on ? g * a.G + row - tok * a.G : 0;
+            i[t] = on ? tok : -1;
+            const T *q = static_cast<const T *>(a.q) + (int64_t)(p.q0 + tok) * a.ldq + (int64_t)h * a.D;
 #pragma unroll
-        for (int b = 0; b < NDP; ++b) {
-            const int d0 = 8 * (c * NDP + b);
-            const T *e = q + (d0 < a.D ? d0 : 0);
-            if (a.qvec) {
+            for (int b = 0; b < NDP; ++b) {
+                const int d0 = 8 * (c * NDP + b);
+                const T *e = q + (d0 < a.D ? d0 : 0);
+                if (a.qvec) {
 #pragma unroll
-                for (int k = 0; k < N; ++k) raw[t][b][k] = reinterpret_cast<const u4 *>(e)[k];
-            } else if constexpr (PARTS == 1) {
+                    for (int k = 0; k < N; ++k) raw[t][b][k] = reinterpret_cast<const u4 *>(e)[k];
+                } else if constexpr (PARTS == 1) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) raw[t][b][0][k] = e[2 * k] | (uint32_t)e[2 * k + 1] << 16;
-            } else {
+                    for (int k = 0; k < 4; ++k) raw[t][b][0][k] = e[2 * k] | (uint32_t)e[2 * k + 1] << 16;
+                } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) raw[t][b][k >> 2][k & 3] = __float_as_uint(e[k]);
+                    for (int k = 0; k < 8; ++k) raw[t][b][k >> 2][k & 3] = __float_as_uint(e[k]);
+                }
             }
         }
     }
+    // as B operands, zero past the rows and past D
+    __device__ __forceinline__ void operands(const TreeArgs &a, int lane, bf8 qf[CT][NDP][PARTS]) const {
+        const int c = lane >> 4;
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
+        for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int b = 0; b < NDP; ++b) {
-            const bool in = on[t] && 8 * (c * NDP + b) < a.D;
+            for (int b = 0; b < NDP; ++b) {
+                const bool in = i[t] >= 0 && 8 * (c * NDP + b) < a.D;
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int d = word_dim(s);
-                float x;
-                if constexpr (PARTS == 1)
-                    x = __uint_as_float(d & 1 ? raw[t][b][0][d >> 1] & 0xFFFF0000u : raw[t][b][0][d >> 1] << 16);
-                else
-                    x = __uint_as_float(raw[t][b][d >> 2][d & 3]);
-                x = in ? (a.negate ? -x : x) : 0.f;
-                __bf16 part[PARTS];
-                split_bf16<PARTS>(x, part);
+                for (int s = 0; s < 8; ++s) {
+                    const int d = word_dim(s);
+                    float x;
+                    if constexpr (PARTS == 1)
+                        x = __uint_as_float(d & 1 ? raw[t][b][0][d >> 1] & 0xFFFF0000u : raw[t][b][0][d >> 1] << 16);
+                    else
+                        x = __uint_as_float(raw[t][b][d >> 2][d & 3]);
+                    x = in ? (a.negate ? -x : x) : 0.f;
+                    __bf16 part[PARTS];
+                    split_bf16<PARTS>(x, part);
 #pragma unroll
-                for (int k = 0; k < PARTS; ++k) qf[t][b][k][s] = part[k];
+                    for (int k = 0; k < PARTS; ++k) qf[t][b][k][s] = part[k];
+                }
             }
-        }
-}
+    }
+};
 
 // Operands that take the offset of 8 codes out of the scores: A = the scales of
 // a lane's K blocks as bf16, three times each (a 0xFF byte gives Inf, and NaN in
@@ -924,6 +947,8 @@ __global__ __launch_bounds__(64 * rows_waves(NDP, CT)) void k_tree_rows(TreeArgs
             int pages[SETS];
 #pragma unroll
             for (int j = 0; j < SETS; ++j) pages[j] = page_at(lt + j * turn);
+            RawQueries<NDP, CT, PARTS> rq;
+            rq.load(a, p, g, p.row, lane);
             unroll_sets<SETS>([&](auto J) {
                 const int row = rows_of(J, lt + J * turn, pages[J]);
                 valid[J] = __ballot(row >= 0);
@@ -932,11 +957,10 @@ __global__ __launch_bounds__(64 * rows_waves(NDP, CT)) void k_tree_rows(TreeArgs
                 load_vs(J);
             });
             page = page_at(lt + SETS * turn);
-            load_queries<NDP, CT, PARTS>(a, p, g, p.row, lane, qf);
+            rq.operands(a, lane, qf);
 #pragma unroll
             for (int t = 0; t < CT; ++t) {
-                const int rw = p.row + 16 * t + i;
-                iq[t] = rw < p.n * a.G ? rw / a.G : 0;
+                iq[t] = max(rq.i[t], 0);
                 if constexpr (OFF) qoff[t] = query_sums<NDP>(qf[t]);
             }
             for (; lt < p.t1; lt += SETS * turn)
@@ -1034,17 +1058,17 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
             }
         };
 
-        int row = row_at(p.t0, page_at(p.t0));
+        int page = page_at(p.t0);
+        RawQueries<NDP, CT, PARTS> rq;
+        rq.load(a, p, p.g, row0, lane);
+        int row = row_at(p.t0, page);
         load(row);
-        int page = page_at(p.t0 + kStep);
+        page = page_at(p.t0 + kStep);
         bf8 qf[CT][NDP][PARTS];
-        load_queries<NDP, CT, PARTS>(a, p, p.g, row0, lane, qf);
+        rq.operands(a, lane, qf);
         int iq[CT];
 #pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            const int rw = row0 + 16 * t + i;
-            iq[t] = rw < p.n * a.G ? rw / a.G : 0;
-        }
+        for (int t = 0; t < CT; ++t) iq[t] = max(rq.i[t], 0);
 
         int buf = 0;
         for (int lt = p.t0; lt < p.t1; lt += kStep, buf ^= 1) {
@@ -1153,18 +1177,25 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
 }
 
 // Rows of tiles that lie in several shares: out = sum_s O_s 2^(m_s - M) 2^9 /
-// sum_s l_s 2^(m_s - M). Workgroup (p, y): the tile that starts in share p, if it
-// ends in another, JR of its rows from y JR on. A group of LR >= D / 4 lanes holds
+// sum_s l_s 2^(m_s - M). Workgroup (x, y): the tile of todo entry x, JR of its
+// rows from y JR on. A group of LR >= D / 4 lanes holds
 // a row (four dims a lane) and every SL-th piece; the SL groups of a row are
 // added in LDS in order. Few pieces: many rows at a time; many: many groups a row.
 template <typename T>
 __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
     __shared__ __attribute__((aligned(16))) f4 so[256];
     __shared__ float2 sml[32];
-    const int p0 = blockIdx.x, tid = threadIdx.x;
-    const int shares = a.todo[8 * a.P];
-    const JoinOf t = {a.todo[8 * p0], a.todo[8 * p0 + 1], a.todo[8 * p0 + 2], a.todo[8 * p0 + 3], a.todo[8 * p0 + 4]};
-    if (p0 >= shares || t.last <= p0) return;
+    const int tid = threadIdx.x;
+    const int *e = a.todo + 8 * (int64_t)blockIdx.x;
+    const JoinOf t = {e[0], e[1], e[2], e[3], e[4], e[5]};
+    if (a.NT) {                                          // is there such a tile?
+        const int per = a.Hkv / a.HG * a.nrt, b = blockIdx.x / per, rt = blockIdx.x % a.nrt;
+        if ((uint32_t)rt >= seq_of(a, b).nrt) return;
+    } else if ((int)blockIdx.x >= a.todo[8 * a.P]) {
+        return;
+    }
+    const int p0 = t.first;
+    if (t.last <= p0) return;
     const int SR = a.HG * a.R, ns = t.last - p0 + 1;
     const int LR = a.D <= 32 ? 8 : (a.D <= 64 ? 16 : (a.D <= 128 ? 32 : 64)), groups = 256 / LR;
     int SL = 1;
@@ -1234,7 +1265,8 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
 
 struct TreePlan {
     int NDP, CT, WT;                 // WT 0: k_tree_rows
-    int R, U, P, minu, HG;
+    int R, U, P, HG;
+    int ms, cap, nrt;
     int64_t bound;                   // units at most
     int join;                        // some tile may lie in several shares
 };
@@ -1252,17 +1284,18 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
         p.CT = rows > 16 ? 2 : 1;
         p.R = 16 * p.CT;
         const int nw = rows_waves(p.NDP, p.CT);
-        // heads that fill a 128-byte line of codes
-        p.HG = D <= 32 ? 8 : (D <= 64 ? 4 : (D <= 128 ? 2 : 1));
+        // heads that fill two 128-byte lines of codes; fewer where that would
+        // leave less than 256 workgroups at 32 pieces a tile
+        p.ms = getenv("MU") ? atoi(getenv("MU")) : 0;
+        p.cap = getenv("CAP") ? atoi(getenv("CAP")) : 5;
+        p.HG = D <= 64 ? 8 : (D <= 128 ? 4 : 2);
+        while (p.HG > 1 && (p.HG > nw || Hkv % p.HG || (B * (Hkv / p.HG) << p.cap) < 256)) p.HG /= 2;
         if (getenv("HG")) p.HG = atoi(getenv("HG"));
-        while (p.HG > nw || Hkv % p.HG) p.HG /= 2;
         p.U = nw / p.HG * 16 * kRowTiles;
-        p.minu = 1;
-        if (getenv("MU")) p.minu = atoi(getenv("MU"));
         const int lim = getenv("LIM") ? atoi(getenv("LIM")) : 512;
         if (max_len <= lim) {
             p.HG = 1;
-            p.U = ceil_div(max_len > 0 ? max_len : 1, (int64_t)64) * 64;
+            for (p.U = 64; p.U < max_len; p.U *= 2) {}
         }
         slots = 256;
     } else {
@@ -1271,14 +1304,14 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
         p.R = 16 * p.CT * (kWaves / p.WT);
         p.HG = 1;
         p.U = kStep;
-        p.minu = 8;
-        if (getenv("MT")) p.minu = atoi(getenv("MT"));
+        p.ms = getenv("MT") ? atoi(getenv("MT")) : 1;
+        p.cap = getenv("CAPT") ? atoi(getenv("CAPT")) : 4;
         slots = p.NDP == 8 ? 256 : 512;
     }
     const int64_t T = max_len > 0 ? ceil_div(max_len, (int64_t)p.U) : 1;
-    p.bound = B * (Hkv / p.HG) * ceil_div(rows, (int64_t)p.R) * T;
-    const int64_t most = ceil_div(ceil_div(p.bound, (int64_t)p.minu), (int64_t)8) * 8;
-    p.P = (int)(most < slots ? most : slots);
+    p.nrt = (int)ceil_div(rows, (int64_t)p.R);
+    p.bound = B * (Hkv / p.HG) * p.nrt * T;
+    for (p.P = 8; p.P < slots && ((int64_t)p.P << p.ms) < p.bound;) p.P *= 2;
     p.join = T > 1;
     return p;
 }
@@ -1351,14 +1384,20 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     // at least 2^-126, so that a hidden score stays -inf at scale 0
     a.scale2 = fmaxf((float)(fabs((double)scale) * 1.4426950408889634074 * 512.0), 1.17549435e-38f);
     a.negate = std::signbit(scale);
-    a.R = p.R; a.U = p.U; a.P = p.P; a.minu = p.minu; a.HG = p.HG;
+    a.R = p.R; a.U = p.U; a.P = p.P; a.ms = p.ms; a.HG = p.HG;
+    a.Rs = __builtin_ctz(p.R); a.Us = __builtin_ctz(p.U); a.Ps = __builtin_ctz(p.P);
     a.out = out; a.ldo = ldo;
     a.po = static_cast<float *>(ws);
     a.pml = a.po + (int64_t)(2 * p.P) * p.HG * p.R * c.D;
     a.todo = reinterpret_cast<int *>(a.pml + (int64_t)(2 * p.P) * p.HG * p.R * 2);
     a.join = p.join;
-    a.JR = (int)ceil_div((int64_t)p.P * p.HG * p.R, 4096);      // about 4096 workgroups
-    if (getenv("JR")) a.JR = atoi(getenv("JR"));
+    a.nrt = p.nrt;
+    a.cap = p.cap;
+    const int64_t tiles = B * (c.H / p.HG) * p.nrt;
+    a.NT = tiles <= p.P ? (int)tiles : 0;
+    const int64_t entries = a.NT ? a.NT : p.P;
+    a.JR = (int)ceil_div(entries * p.HG * p.R, 2048);            // about 2048 workgroups, at most 16 rows each
+    a.JR = a.JR > 16 ? 16 : a.JR;
     const unsigned grid = (unsigned)p.P;
     hipError_t e;
     const bool f32 = dt == MXS_F32;
@@ -1366,7 +1405,7 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     else if (p.NDP == 4) e = tree_go<4>(p, a, grid, f32, st);
     else e = tree_go<8>(p, a, grid, f32, st);
     if (e != hipSuccess || !p.join) return e;
-    const dim3 jg((unsigned)p.P, (unsigned)ceil_div(p.HG * p.R, a.JR));
+    const dim3 jg((unsigned)entries, (unsigned)ceil_div(p.HG * p.R, a.JR));
     if (f32) hipLaunchKernelGGL((k_tree_join<float>), jg, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((k_tree_join<__bf16>), jg, dim3(256), 0, st, a);
     return hipGetLastError();
