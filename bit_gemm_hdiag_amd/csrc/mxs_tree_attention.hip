@@ -992,6 +992,20 @@ __global__ __launch_bounds__(64 * rows_waves(NDP, CT)) void k_tree_rows(TreeArgs
     });
 }
 
+// Order of a block of N LDS reads that feed M matrix instructions each: six
+// reads ahead. Left alone, the compiler reads each operand right before its use
+// and waits out the LDS latency every time.
+template <int N, int M>
+__device__ __forceinline__ void pipeline() {
+    constexpr int AHEAD = N < 6 ? N : 6;
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+    unroll_sets<N - AHEAD>([](auto) {
+        __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    });
+    __builtin_amdgcn_sched_group_barrier(0x008, M * AHEAD, 0);
+}
+
 // Many rows: the four waves of a workgroup share every 64-token stage. Each
 // dequantises one 16-token tile of K and of V into LDS, in the operands' own
 // lane order (64 lanes x 16 bytes an operand: reads and writes without bank
@@ -1123,6 +1137,12 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
                             sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][j], sc[t][u], 0, 0, 0);
                 }
             }
+            pipeline<NTW * NDP, CT * PARTS>();
+            bf8 vf[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                vf[n] = *reinterpret_cast<const bf8 *>(lds.v[buf][wt * NTW / 2 * NT + n][lane]);
+            __builtin_amdgcn_sched_barrier(0);
             const uint64_t valid = (uint64_t)(lds.valid[buf][0] | lds.valid[buf][1] << 16) |
                                    (uint64_t)(lds.valid[buf][2] | lds.valid[buf][3] << 16) << 32;
             if (valid != ~0ull || edge) {
@@ -1153,7 +1173,9 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const bf8 vv = *reinterpret_cast<const bf8 *>(lds.v[buf][(wt * NTW + u) / 2 * NT + n][lane]);
+                    const bf8 vv = vf[n];
+                    if (u + 2 < NTW)
+                        vf[n] = *reinterpret_cast<const bf8 *>(lds.v[buf][(wt * NTW + u + 2) / 2 * NT + n][lane]);
 #pragma unroll
                     for (int t = 0; t < CT; ++t)
 #pragma unroll
