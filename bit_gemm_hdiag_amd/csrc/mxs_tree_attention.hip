@@ -48,7 +48,6 @@ typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4;            // waves of a workgroup; they share its tokens
 constexpr int kRowTiles = 2;         // 16-token tiles of a wave's step in k_tree_rows
 constexpr int kRowSets = 3;          // steps whose codes a wave holds or has in flight
 constexpr int kNTL = 4;              // 16-token tiles of a stage in k_tree_tile
@@ -739,6 +738,21 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, co
     }
 }
 
+// The offset of 8 codes leaves the outputs. Blocks of byte 0 (zeros) leave up
+// to l 2^-133: outputs of at most 2^-123 are 0.
+template <int NDP, int CT>
+__device__ __forceinline__ void take_offset(State<NDP, CT> &st) {
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+        for (int n = 0; n < 2 * NDP; ++n) {
+            st.acc[t][n] -= st.w[t] * 0.015625f;                      // 8 / 2^9
+#pragma unroll
+            for (int rr = 0; rr < 4; ++rr)
+                st.acc[t][n][rr] = fabsf(st.acc[t][n][rr]) <= st.l[t][0] * 0x1p-132f ? 0.f : st.acc[t][n][rr];
+        }
+}
+
 // States of two waves over the same rows, through LDS in lane order (CT (2 NDP
 // + 1) KiB): M = max m, sums and outputs scaled by 2^((m - M) scale2)
 template <int NDP, int CT>
@@ -968,18 +982,7 @@ __global__ __launch_bounds__(64 * rows_waves(NDP, CT)) void k_tree_rows(TreeArgs
                     if (J == 0 || lt + J * turn < p.t1) step(J, lt + J * turn);
                 });
         }
-        if constexpr (OFF) {
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    st.acc[t][n] -= st.w[t] * 0.015625f;                                // 8 / 2^9
-                    // blocks of byte 0 (zeros) leave up to l 2^-133: outputs of 2^-124 are 0
-#pragma unroll
-                    for (int rr = 0; rr < 4; ++rr)
-                        st.acc[t][n][rr] = fabsf(st.acc[t][n][rr]) <= st.l[t][0] * 0x1p-132f ? 0.f : st.acc[t][n][rr];
-                }
-        }
+        if constexpr (OFF) take_offset<NDP, CT>(st);
         give_nan<NDP, CT>(st);
 
         for (int half = parts / 2; half; half /= 2) {
@@ -1008,12 +1011,11 @@ __device__ __forceinline__ void pipeline() {
 
 // Many rows: the four waves of a workgroup share every 64-token stage. Each
 // dequantises one 16-token tile of K and of V into LDS, in the operands' own
-// lane order (64 lanes x 16 bytes an operand: reads and writes without bank
-// conflicts), then multiplies all of the stage (or half of it, WT = 2) with its
-// own 16 CT rows. Two LDS buffers: one barrier a stage, the next stage's codes
-// in flight meanwhile. With WT = 2 the two waves of a row tile are merged at
-// the end.
-template <int NDP, int CT, int WT, int PARTS>
+// lane order (64 lanes x 16 bytes an operand: reads without bank conflicts),
+// then multiplies all of the stage (or half of it, WT = 2) with its own 16 CT
+// rows. Two LDS buffers: one barrier a stage, the next stage's codes in flight
+// meanwhile. With WT = 2 the two waves of a row tile are merged at the end.
+template <int NDP>
 struct TileLds {
     static constexpr int NT = 2 * NDP, TILES = kStep / 16;
     uint32_t k[2][TILES * NDP][64][4];
@@ -1023,11 +1025,11 @@ struct TileLds {
 };
 
 template <int NDP, int CT, int WT, int PARTS>
-__global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(TreeArgs a) {
-    constexpr int PP = PARTS, NT = 2 * NDP, WR = kWaves / WT, NTW = kNTL / WT;
+__global__ __launch_bounds__(256, NDP == 8 ? 1 : 2) void k_tree_tile(TreeArgs a) {
+    constexpr int PP = PARTS, NT = 2 * NDP, WR = 4 / WT, NTW = kNTL / WT;
     constexpr int KB = Raw<NDP>::KB, VW = Raw<NDP>::VW;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-    auto &lds = *reinterpret_cast<TileLds<NDP, CT, WT, PARTS> *>(lds_raw);
+    auto &lds = *reinterpret_cast<TileLds<NDP> *>(lds_raw);
     const int lane = threadIdx.x & 63, i = lane & 15, c = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wr = w % WR, wt = w / WR;
@@ -1083,13 +1085,17 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
         int iq[CT];
 #pragma unroll
         for (int t = 0; t < CT; ++t) iq[t] = max(rq.i[t], 0);
-
         int buf = 0;
         for (int lt = p.t0; lt < p.t1; lt += kStep, buf ^= 1) {
             // this wave's tiles into LDS
             const uint32_t ok = (uint32_t)__ballot(row >= 0) & 0xFFFFu;
             const bool edge = lt + kStep > p.ctx || lt + kStep > p.t1;
             if (lane == 0) lds.valid[buf][w] = ok;
+#pragma unroll
+            for (int b = 0; b < NDP; ++b)
+                *reinterpret_cast<bf8 *>(lds.k[buf][w * NDP + b][lane]) =
+                    word_values<false>(k[b], scale_of(kb[KB == 2 ? b >> 2 : 0]));
+            __builtin_amdgcn_sched_barrier(0);
             if (edge || ok != 0xFFFFu) {
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
@@ -1100,11 +1106,6 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
                     }
                 }
             }
-#pragma unroll
-            for (int b = 0; b < NDP; ++b)
-                *reinterpret_cast<bf8 *>(lds.k[buf][w * NDP + b][lane]) =
-                    word_values<false>(k[b], scale_of(kb[KB == 2 ? b >> 2 : 0]));
-            __builtin_amdgcn_sched_barrier(0);
             {
                 uint32_t o[NT][2];
                 float vsc[4];
@@ -1138,10 +1139,14 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
                 }
             }
             pipeline<NTW * NDP, CT * PARTS>();
-            bf8 vf[NT];
+            // V operand j = (tiles, n) of the wave's tokens, VP of them read ahead
+            constexpr int VP = 4;
+            auto v_at = [&](int j) {
+                return *reinterpret_cast<const bf8 *>(lds.v[buf][(wt * NTW / 2 + j / NT) * NT + j % NT][lane]);
+            };
+            bf8 vf[VP];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                vf[n] = *reinterpret_cast<const bf8 *>(lds.v[buf][wt * NTW / 2 * NT + n][lane]);
+            for (int j = 0; j < VP; ++j) vf[j] = v_at(j);
             __builtin_amdgcn_sched_barrier(0);
             const uint64_t valid = (uint64_t)(lds.valid[buf][0] | lds.valid[buf][1] << 16) |
                                    (uint64_t)(lds.valid[buf][2] | lds.valid[buf][3] << 16) << 32;
@@ -1173,14 +1178,14 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const bf8 vv = vf[n];
-                    if (u + 2 < NTW)
-                        vf[n] = *reinterpret_cast<const bf8 *>(lds.v[buf][(wt * NTW + u + 2) / 2 * NT + n][lane]);
+                    const int j = u / 2 * NT + n;
+                    const bf8 vv = vf[j % VP];
+                    if (j + VP < NTW / 2 * NT) vf[j % VP] = v_at(j + VP);
 #pragma unroll
                     for (int t = 0; t < CT; ++t)
 #pragma unroll
-                        for (int j = 0; j < PP; ++j)
-                            st.acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[t][j], st.acc[t][n], 0, 0, 0);
+                        for (int k = 0; k < PP; ++k)
+                            st.acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[t][k], st.acc[t][n], 0, 0, 0);
                 }
             }
         }
@@ -1195,6 +1200,233 @@ __global__ __launch_bounds__(64 * kWaves, NDP == 8 ? 1 : 2) void k_tree_tile(Tre
     }
     if (busy && wt == 0) store_rows<NDP, CT, PARTS>(a, p, st, p.g, row0, lane);
     __syncthreads();                 // the next piece writes the same LDS
+    });
+}
+
+// Most rows: eight waves, 256 (CT 1: 128) rows. Two halves of the workgroup take
+// turns: in every phase one half feeds the matrix cores (p V of the stage before
+// and the scores of this one, all from LDS) while the other half uses the vector
+// ALU (softmax, dequantising the next stage, addresses), and a barrier swaps
+// them. Left to themselves the waves run through the same kind of work
+// together, and each unit idles in turn. Half 0 dequantises K, half 1 V:
+//   phase  2 k      half 0: PV(k - 1), QK(k)          half 1: softmax(k - 1), V(k)
+//   phase  2 k + 1  half 0: softmax(k), K(k + 1)      half 1: PV(k - 1), QK(k)
+// so two LDS buffers serve: K(k) is read in phases 2 k and 2 k + 1 and written
+// again in 2 k + 3; V(k) is read in 2 k + 2 and 2 k + 3, written again in 2 k + 4.
+template <int NDP, int CT, int PARTS>
+__global__ __launch_bounds__(512) void k_tree_pair(TreeArgs a) {
+    constexpr int PP = PARTS, NT = 2 * NDP, NTW = kNTL;
+    constexpr int KB = Raw<NDP>::KB, VW = Raw<NDP>::VW, VP = 4;
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+    auto &lds = *reinterpret_cast<TileLds<NDP> *>(lds_raw);
+    const int lane = threadIdx.x & 63, i = lane & 15, c = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = w >> 2, tw = w & 3;                 // the tile of K or V that this wave dequantises
+    for_each_piece(a, lane, [&](const Place &p) {
+        const int row0 = p.row + w * 16 * CT;
+        const bool busy = row0 < p.n * a.G;
+        State<NDP, CT> st;
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            st.m[t] = -INFINITY;
+            st.l[t] = f4{0.f, 0.f, 0.f, 0.f};
+            st.w[t] = f4{0.f, 0.f, 0.f, 0.f};
+            st.nan[t] = 0;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) st.acc[t][n] = f4{0.f, 0.f, 0.f, 0.f};
+        }
+        if (p.t0 < p.t1) {
+            const LaneAt<NDP> at(lane, a.D);
+            const uint8_t *codes = (half ? a.vc : a.kc) + p.g * (a.D / 2);
+            const uint8_t *scales = (half ? a.vs : a.ks) + p.g * (a.D / 32);
+            const int32_t *table = a.table + (int64_t)p.b * a.ldt;
+            const uint32_t cs = (uint32_t)a.Hkv * (a.D / 2), ss = (uint32_t)a.Hkv * (a.D / 32);
+            const int N = (p.t1 - p.t0 + kStep - 1) / kStep;             // stages
+            auto page_at = [&](int lt) { return table[page_of(a, min(lt + 16 * tw + i, p.t1 - 1))]; };
+            auto row_at = [&](int lt, int page) {
+                const int t = lt + 16 * tw + i;
+                return t < p.t1 && (uint32_t)page < (uint64_t)a.pages ? page * a.ps + (t - page_of(a, t) * a.ps) : -1;
+            };
+            // codes and scales of this wave's tile: K as the lane's words of one
+            // token, V as the lane's words of four
+            constexpr int RW = NDP > 4 * VW ? NDP : 4 * VW;
+            uint32_t raw[RW], rb[4];
+            auto load = [&](int row) {
+                if (half == 0) {
+                    const uint64_t r = (uint32_t)max(row, 0);
+                    load_k<NDP>(raw, codes + r * cs, at);
+#pragma unroll
+                    for (int b = 0; b < KB; ++b) rb[b] = scales[r * ss + at.kb[b]];
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint64_t r = (uint32_t)max(__shfl(row, 4 * c + s), 0);
+                        load_v<NDP>(raw + s * VW, codes + r * cs, at);
+                        rb[s] = scales[r * ss + at.vb];
+                    }
+                }
+            };
+            int page = page_at(p.t0);
+            RawQueries<NDP, CT, PARTS> rq;
+            rq.load(a, p, p.g, row0, lane);
+            int row = row_at(p.t0, page);
+            load(row);
+            page = page_at(p.t0 + kStep);
+            bf8 qf[CT][NDP][PARTS];
+            rq.operands(a, lane, qf);
+            int iq[CT];
+#pragma unroll
+            for (int t = 0; t < CT; ++t) iq[t] = max(rq.i[t], 0);
+
+            // stage k's tile of this wave into LDS, stage k + 1's loads under way
+            auto stage = [&](int k) {
+                const int lt = p.t0 + k * kStep, buf = k & 1;
+                const uint32_t ok = (uint32_t)__ballot(row >= 0) & 0xFFFFu;
+                if (half == 0) {
+                    if (lane == 0) lds.valid[buf][tw] = ok;
+#pragma unroll
+                    for (int b = 0; b < NDP; ++b)
+                        *reinterpret_cast<bf8 *>(lds.k[buf][tw * NDP + b][lane]) =
+                            word_values<false>(raw[b], scale_of(rb[KB == 2 ? b >> 2 : 0]));
+                } else {
+                    if (lt + kStep > p.ctx || lt + kStep > p.t1 || ok != 0xFFFFu) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            if (!((ok >> (4 * c + s)) & 1)) rb[s] = 0;
+                            if (lt + kStep > p.ctx || lt + kStep > p.t1) {
+                                const uint64_t bad = take_nan(rb[s]);
+                                if (lane == 0) lds.nan[buf][tw][s] = bad;
+                            }
+                        }
+                    }
+                    uint32_t v[4][VW], o[NT][2];
+                    float vsc[4];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        vsc[s] = scale_of(rb[s]);
+#pragma unroll
+                        for (int b = 0; b < VW; ++b) v[s][b] = raw[s * VW + b];
+                    }
+                    v_pairs<NDP, false>(v, vsc, o);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        *reinterpret_cast<u2 *>(&lds.v[buf][(tw >> 1) * NT + n][lane][2 * (tw & 1)]) = u2{o[n][0], o[n][1]};
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                row = row_at(lt + kStep, page);
+                page = page_at(lt + 2 * kStep);
+                load(row);
+            };
+
+            f4 sc[CT][NTW];
+            bf8 pf[NTW / 2][CT][PP];
+            // p V of a stage
+            auto values = [&](int vbuf) {
+                auto v_at = [&](int j) { return *reinterpret_cast<const bf8 *>(lds.v[vbuf][j / NT * NT + j % NT][lane]); };
+                {
+                    bf8 vf[VP];
+#pragma unroll
+                    for (int j = 0; j < VP; ++j) vf[j] = v_at(j);
+#pragma unroll
+                    for (int u = 0; u < NTW / 2; ++u) {
+#pragma unroll
+                        for (int t = 0; t < CT; ++t)
+#pragma unroll
+                            for (int j = 0; j < PP; ++j)
+                                st.l[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones(), pf[u][t][j], st.l[t], 0, 0, 0);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const int j = u * NT + n;
+                            const bf8 vv = vf[j % VP];
+                            if (j + VP < NTW / 2 * NT) vf[j % VP] = v_at(j + VP);
+#pragma unroll
+                            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                                for (int q = 0; q < PP; ++q)
+                                    st.acc[t][n] =
+                                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[u][t][q], st.acc[t][n], 0, 0, 0);
+                        }
+                    }
+                }
+            };
+            // scores of a stage
+            auto scores = [&](int kb) {
+                auto k_at = [&](int j) { return *reinterpret_cast<const bf8 *>(lds.k[kb][j / NDP * NDP + j % NDP][lane]); };
+                {
+                    bf8 kf[VP];
+#pragma unroll
+                    for (int j = 0; j < VP; ++j) kf[j] = k_at(j);
+#pragma unroll
+                    for (int u = 0; u < NTW; ++u) {
+#pragma unroll
+                        for (int t = 0; t < CT; ++t) sc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int b = 0; b < NDP; ++b) {
+                            const int j = u * NDP + b;
+                            const bf8 kv = kf[j % VP];
+                            if (j + VP < NTW * NDP) kf[j % VP] = k_at(j + VP);
+#pragma unroll
+                            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                                for (int q = 0; q < PARTS; ++q)
+                                    sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][q], sc[t][u], 0, 0, 0);
+                        }
+                    }
+                }
+            };
+            // vector half of stage k: its softmax
+            auto weigh = [&](int k) {
+                const int lt = p.t0 + k * kStep, buf = k & 1;
+                const bool edge = lt + kStep > p.ctx || lt + kStep > p.t1;
+                const uint64_t valid = (uint64_t)(lds.valid[buf][0] | lds.valid[buf][1] << 16) |
+                                       (uint64_t)(lds.valid[buf][2] | lds.valid[buf][3] << 16) << 32;
+                if (valid != ~0ull || edge) {
+                    uint64_t seen[CT];
+#pragma unroll
+                    for (int t = 0; t < CT; ++t) seen[t] = valid & mask_window(a, p, iq[t], lt);
+                    hide<CT, NTW>(sc, seen, c);
+                    if (edge)
+                        for (int u = 0; u < NTW; ++u)
+                            for (int s = 0; s < 4; ++s) {
+                                const uint64_t bad = lds.nan[buf][u][s];
+                                if (bad)
+                                    for (int j = 0; j < 4; ++j)
+                                        note_nan<NDP, CT>(st, (uint32_t)(bad >> (16 * j)) & 0xFFFFu, 16 * u + 4 * j + s,
+                                                          seen, c);
+                            }
+                }
+                soften<NDP, CT, NTW, PARTS == 3>(st, sc, a.scale2);
+#pragma unroll
+                for (int u = 0; u < NTW; u += 2)
+#pragma unroll
+                    for (int t = 0; t < CT; ++t) p_operands<PP>(sc[t][u], sc[t][u + 1], pf[u / 2][t]);
+            };
+
+            stage(0);
+            // every wave meets the same 2 N + 2 barriers; half 1 is a phase behind
+            if (half) lds_barrier();
+            lds_barrier();
+            scores(0);
+            lds_barrier();
+            weigh(0);
+            stage(1);
+            for (int k = 1; k < N; ++k) {
+                lds_barrier();
+                __builtin_amdgcn_s_setprio(1);       // the matrix half issues first
+                values((k & 1) ^ 1);
+                scores(k & 1);
+                __builtin_amdgcn_s_setprio(0);
+                lds_barrier();
+                weigh(k);
+                stage(k + 1);        // past the last stage: its rows are clamped, its tiles not read
+            }
+            lds_barrier();
+            values((N & 1) ^ 1);
+            if (!half) lds_barrier();
+        }
+        give_nan<NDP, CT>(st);
+        if (busy) store_rows<NDP, CT, PARTS>(a, p, st, p.g, row0, lane);
+        __syncthreads();                 // the next piece writes the same LDS
     });
 }
 
@@ -1286,7 +1518,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
 }
 
 struct TreePlan {
-    int NDP, CT, WT;                 // WT 0: k_tree_rows
+    int NDP, CT, NW, WT;             // WT 0: k_tree_rows; NW 8: k_tree_pair
     int R, U, P, HG;
     int ms, cap, nrt;
     int64_t bound;                   // units at most
@@ -1320,13 +1552,14 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
         slots = 256;
     } else {
         p.CT = bf ? 2 : 1;
+        p.NW = rows > 64 * p.CT && p.NDP <= 4 ? 8 : 4;
         p.WT = rows <= 32 * p.CT ? 2 : 1;
-        p.R = 16 * p.CT * (kWaves / p.WT);
+        p.R = 16 * p.CT * (p.NW / p.WT);
         p.HG = 1;
         p.U = kStep;
         p.ms = 1;
         p.cap = 5;
-        slots = p.NDP == 8 ? 256 : 512;
+        slots = p.NDP == 8 || p.NW == 8 ? 256 : 512;
     }
     const int64_t T = max_len > 0 ? ceil_div(max_len, (int64_t)p.U) : 1;
     p.nrt = (int)ceil_div(rows, (int64_t)p.R);
@@ -1348,23 +1581,28 @@ hipError_t rows_go(const TreeArgs &a, unsigned grid, hipStream_t st) {
 }
 template <int NDP, int CT, int WT, int PARTS>
 hipError_t tile_go(const TreeArgs &a, unsigned grid, hipStream_t st) {
-    constexpr size_t lds = sizeof(TileLds<NDP, CT, WT, PARTS>);
-    static_assert(WT == 1 || lds >= (size_t)(kWaves / 2) * CT * (2 * NDP + 1) * 1024, "merge space");
-    hipLaunchKernelGGL((k_tree_tile<NDP, CT, WT, PARTS>), dim3(grid), dim3(64 * kWaves), lds, st, a);
+    constexpr size_t lds = sizeof(TileLds<NDP>);
+    static_assert(WT == 1 || lds >= (size_t)2 * CT * (2 * NDP + 1) * 1024, "merge space");
+    hipLaunchKernelGGL((k_tree_tile<NDP, CT, WT, PARTS>), dim3(grid), dim3(256), lds, st, a);
     return hipGetLastError();
+}
+template <int NDP, int CT, int PARTS>
+hipError_t tile_go(const TreePlan &p, const TreeArgs &a, unsigned grid, hipStream_t st) {
+    if constexpr (NDP <= 4)
+        if (p.NW == 8) {
+            hipLaunchKernelGGL((k_tree_pair<NDP, CT, PARTS>), dim3(grid), dim3(512),
+                               sizeof(TileLds<NDP>), st, a);
+            return hipGetLastError();
+        }
+    return p.WT == 1 ? tile_go<NDP, CT, 1, PARTS>(a, grid, st) : tile_go<NDP, CT, 2, PARTS>(a, grid, st);
 }
 template <int NDP>
 hipError_t tree_go(const TreePlan &p, const TreeArgs &a, unsigned grid, bool f32, hipStream_t st) {
-    if (f32) {
-        if (p.WT == 0) return rows_go<NDP, 1, 3>(a, grid, st);
-        return p.WT == 1 ? tile_go<NDP, 1, 1, 3>(a, grid, st) : tile_go<NDP, 1, 2, 3>(a, grid, st);
-    }
-    if (p.WT == 0) {
-        if constexpr (NDP <= 4)
-            if (p.CT == 2) return rows_go<NDP, 2, 1>(a, grid, st);
-        return rows_go<NDP, 1, 1>(a, grid, st);
-    }
-    return p.WT == 1 ? tile_go<NDP, 2, 1, 1>(a, grid, st) : tile_go<NDP, 2, 2, 1>(a, grid, st);
+    if (f32) return p.WT == 0 ? rows_go<NDP, 1, 3>(a, grid, st) : tile_go<NDP, 1, 3>(p, a, grid, st);
+    if (p.WT) return tile_go<NDP, 2, 1>(p, a, grid, st);
+    if constexpr (NDP <= 4)
+        if (p.CT == 2) return rows_go<NDP, 2, 1>(a, grid, st);
+    return rows_go<NDP, 1, 1>(a, grid, st);
 }
 
 }  // namespace
