@@ -29,10 +29,27 @@
 // the factors 2^9 go into the score scale and the final normalisation.
 // A block with byte 0xFF is NaN. bf16 queries enter as they are; fp32 queries
 // as the exact sum of three bf16 parts, and so do their softmax weights p. For
-// bf16 queries p is rounded to one bf16 (2^-9 of each p, independent from token
-// to token, against the output's own rounding of 2^-9; two parts took PPP),
-// and the sum that normalises is that of the rounded values, so one dominant
-// token gives its V exactly. Maxima, sums and outputs are fp32.
+// bf16 queries p is rounded to one bf16: the error is independent from token to
+// token, and of the size of the output's own rounding (0.0017 instead of 0.0016
+// root mean square over the output at 8 x 26 drafted tokens). Two parts cost a
+// third of the time where arithmetic counts: 708 against 583 us at 16 trees of
+// 64 tokens over up to 16384. The sum that normalises is that of the rounded
+// values, so one dominant token gives its V exactly. Maxima, sums and outputs
+// are fp32.
+//
+// Kernels, by the rows n G of a KV head (tree_plan; bf16 / fp32 queries):
+//   k_tree_rows  up to 32 (D <= 128) or 16 / 16: every wave its own tokens
+//   k_tree_tile  up to 128 / 64, D > 128: four waves share stages in LDS
+//   k_tree_pair  more: eight waves share stages and take turns
+// A device-side schedule (below) cuts the work into equal shares.
+// Measured (MI355X, 8 KV heads, D = 128, pages of 64 tokens):
+//   32 sequences, one token, 4 query heads a KV head, 4915 to 16384 cached
+//   tokens: 96 us, 3.9 TB/s of codes and scales (loads alone: 88 us)
+//   one sequence of 8192, 32768 tokens, 8 query heads: 14.6, 26.8 us
+//   8 x 26 drafted tokens, 8 query heads, up to 8192 tokens: 93 us, 356 TFLOP/s
+//   16 x 64, up to 16384 tokens: 470 us, 653 TFLOP/s; the LDS reads of the
+//   operands bound it (a wave reads the whole stage for 32 rows; 64 rows a wave
+//   need more registers than there are)
 #include <cmath>
 #include <type_traits>
 
@@ -49,7 +66,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 constexpr int kRowTiles = 2;         // 16-token tiles of a wave's step in k_tree_rows
-constexpr int kRowSets = 3;          // steps whose codes a wave holds or has in flight
+constexpr int kRowSets = 3;          // steps whose codes a wave holds or has in flight (one or two: within 2 %)
 constexpr int kNTL = 4;              // 16-token tiles of a stage in k_tree_tile
 constexpr int kStep = 16 * kNTL;     // tokens of a stage
 
@@ -72,7 +89,7 @@ struct TreeArgs {
     int R, U, P;                     // rows of a tile, tokens of a unit, workgroups: powers of two
     int Rs, Us, Ps;                  // their logarithms
     int ms, cap;                     // a share has at least 2^ms units, and a tile's 2^-cap
-    int HG;                          // KV heads of a tile
+    int HG, groups;                  // KV heads of a tile, Hkv / HG
     int nrt;                         // row tiles of a head at most
     int join;                        // a k_tree_join follows
     int JR;                          // its rows of a workgroup
@@ -171,7 +188,7 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs &a, int b) {
     return s;
 }
 __device__ __forceinline__ uint32_t units_of(const TreeArgs &a, const Seq &s) {
-    return (uint32_t)(a.Hkv / a.HG) * s.nrt * s.T;
+    return (uint32_t)a.groups * s.nrt * s.T;
 }
 
 // inclusive sum over the wave's lanes
@@ -313,7 +330,7 @@ __device__ __forceinline__ void for_each_piece(const TreeArgs &a, int lane, F f)
         pl.t1 = uni(u1 == s.T ? s.len : (int)u1 * a.U);
         pl.slot = u0 == 0 && u1 == s.T ? -1 : 2 * (int64_t)p + (u0 > 0 ? 0 : 1);
         if (a.join && u0 == 0 && (u1 < s.T || a.NT) && threadIdx.x == 0) {
-            const int64_t entry = a.NT ? ((int64_t)b * (a.Hkv / a.HG) + gt) * a.nrt + (tile - gt * s.nrt) : p;
+            const int64_t entry = a.NT ? ((int64_t)b * a.groups + gt) * a.nrt + (tile - gt * s.nrt) : p;
             int *t = a.todo + 8 * entry;
             t[0] = (int)p;
             t[1] = u1 < s.T ? (int)h.owner(x + s.T - 1) : -1;
@@ -785,7 +802,8 @@ __device__ __forceinline__ void take_state(State<NDP, CT> &st, const float *ex, 
 // tile's HG heads and turns of 16 NTL tokens, which it dequantises in registers.
 // The heads of a token lie side by side in its cache row: read together they
 // use whole 128-byte lines (a head alone has 64 bytes of codes and 4 of scales in
-// a row at D = 128, and its neighbours would fetch the lines again: NNN). The
+// a row at D = 128, and its neighbours would fetch the lines again: 135 against
+// 102 us for 32 sequences of up to 16384 tokens). The
 // parts of a head are merged in LDS, the upper half into the lower, by halves.
 // Lane = token finds the pool rows and loads both scale rows, one load each,
 // and passes them to the lanes that need them through LDS.
@@ -1443,7 +1461,7 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
     const int *e = a.todo + 8 * (int64_t)blockIdx.x;
     const JoinOf t = {e[0], e[1], e[2], e[3], e[4], e[5]};
     if (a.NT) {                                          // is there such a tile?
-        const int per = a.Hkv / a.HG * a.nrt, b = blockIdx.x / per, rt = blockIdx.x % a.nrt;
+        const int per = a.groups * a.nrt, b = blockIdx.x / per, rt = blockIdx.x % a.nrt;
         if ((uint32_t)rt >= seq_of(a, b).nrt) return;
     } else if ((int)blockIdx.x >= a.todo[8 * a.P]) {
         return;
@@ -1642,7 +1660,7 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     // at least 2^-126, so that a hidden score stays -inf at scale 0
     a.scale2 = fmaxf((float)(fabs((double)scale) * 1.4426950408889634074 * 512.0), 1.17549435e-38f);
     a.negate = std::signbit(scale);
-    a.R = p.R; a.U = p.U; a.P = p.P; a.ms = p.ms; a.HG = p.HG;
+    a.R = p.R; a.U = p.U; a.P = p.P; a.ms = p.ms; a.HG = p.HG; a.groups = c.H / p.HG;
     a.Rs = __builtin_ctz(p.R); a.Us = __builtin_ctz(p.U); a.Ps = __builtin_ctz(p.P);
     a.out = out; a.ldo = ldo;
     a.po = static_cast<float *>(ws);

@@ -537,17 +537,22 @@ mxs_status mxs_kv4_read(const mxs_kv4_cache *cache, const int64_t *slots, int64_
  * of its ancestors and itself. Tokens in no valid page (table entry negative or
  * past the pool) are seen by no row; what an unseen token's K and V hold, NaN
  * included, does not reach the output.
- * fp32 queries: exact products, fp32 sums, fp32 output. bf16 queries: softmax
- * weights to 2^-17, fp32 sums, output rounded once. Every sum has a fixed
- * order: the result is deterministic and independent of the other sequences'
- * contents (not of B, max_q and max_len, which choose the split). Scale bytes
- * 0 to 2 (values below 2^-122) are read to 2^-124.
+ * fp32 queries: exact products, fp32 sums, fp32 output. bf16 queries: exact
+ * scores up to the fp32 sums, softmax weights rounded to bf16 (in the products
+ * and in the sum that normalises alike), fp32 sums, output rounded once;
+ * outputs of magnitude up to 2^-123 are returned as 0. Every sum has an order
+ * fixed by the arguments, lens and cu: the result is deterministic, and what the
+ * other sequences hold does not change it (their lengths move the split, and
+ * with it the rounding). Scale bytes 0 to 2 (values below 2^-122) are read to
+ * 2^-124.
  * q: [total_q, Hq, D] of `dtype`, ldq elements between tokens; out the same
  * with ldo; rows of no sequence are left as they were. table: [B, ldt] int32;
  * lens: [B] int32; cu: [B + 1] int32, ascending from 0, at most total_q; mask:
  * [total_q, mask_words] uint64 or NULL. max_q and max_len are upper bounds of
- * n and lens known to the host (they size the launch, so that a captured graph
- * serves any lens up to max_len): longer ones are cut off at the bound. All
+ * n and lens known to the host (they choose the kernel and the number of
+ * workgroups; the work is divided among those on the device by the lens and cu
+ * found there, so that a captured graph serves any lens up to max_len): longer
+ * ones are cut off at the bound. All
  * device memory except the cache struct. ws: >= mxs_attend_kv4_tree_workspace
  * bytes of device memory, 16-byte aligned, contents scratch (NULL if 0); calls
  * that may overlap need one each. D <= 256, max_len <= 2^30 and <= ldt *

@@ -190,13 +190,15 @@ def test_tree_attention_errors(lib):
 
 def test_tree_workspace(lib):
     w = lib.mxs_attend_kv4_tree_workspace
-    assert w(1, 64, 64, 1, 160, 4, 2, 64) == 0                    # one token range
+    assert w(1, 64, 64, 1, 160, 4, 2, 64) == 0                    # short contexts: nothing to join
     for bad in ((7, 1, 1, 1, 1 << 20, 4, 2, 64), (1, 0, 1, 1, 1 << 20, 4, 2, 64), (1, 1, 0, 1, 1 << 20, 4, 2, 64),
                 (1, 1, 1, 0, 1 << 20, 4, 2, 64), (1, 1, 1, 1, -1, 4, 2, 64), (1, 1, 1, 1, 1 << 20, 3, 2, 64),
                 (1, 1, 1, 1, 1 << 20, 4, 2, 48), (1, 1, 1, 1, 1 << 20, 4, 2, 288), (1, 1, 1, 1, 1 << 20, 4, 0, 64)):
         assert w(*bad) == 0
-    n = w(1, 1, 3, 3, 100000, 8, 2, 128)
-    assert n > 0 and n < 1 << 28
+    # pieces are kept per workgroup, not per row and range: bounded for any batch
+    for args in ((1, 1, 3, 3, 100000, 8, 2, 128), (1, 256, 1 << 16, 256, 1 << 17, 64, 8, 128),
+                 (0, 64, 1 << 14, 256, 1 << 20, 128, 8, 256)):
+        assert 0 < w(*args) < 1 << 28
 
 
 def test_binding_refuses_host_tensors():

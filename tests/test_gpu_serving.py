@@ -415,6 +415,65 @@ def test_tree_attention(mx, lens, ns, Hq, Hkv, D, page, mask, dtype):
     b.check(out)
 
 
+# batches of more than 64 sequences (the schedule reads them 64 at a time), some
+# without tokens or without queries: more tiles than workgroups, long tiles that
+# lie in several shares, and one very long sequence among short ones
+@pytest.mark.parametrize("case", ["short", "many", "ragged", "wide"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tree_attention_large_batches(mx, dtype, case):
+    rng = np.random.default_rng(5)
+    B, L, n, Hq, Hkv, D = {"short": (200, 40, 3, 2, 1, 32), "many": (150, 700, 1, 4, 4, 64),
+                           "ragged": (70, 90, 2, 4, 2, 64), "wide": (66, 130, 70, 2, 1, 32)}[case]
+    lens = rng.integers(1, L + 1, B)
+    ns = np.minimum(rng.integers(0, n + 1, B), lens)
+    lens[3] = ns[3] = 0
+    ns[5:9] = 0
+    if case == "ragged":
+        lens[66], ns[66] = 6000, 2
+    ns[B - 1], lens[B - 1] = min(n, L), L
+    b = Batch(mx, lens.tolist(), ns.tolist(), Hq, Hkv, D, 16, dtype, "tree", 90 + B)
+    got = b.run(mx)
+    b.check(got)
+    assert torch.equal(got, b.run(mx, max_len=None if case == "short" else int(lens.max())))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,n", [(128, 1, 64, 1), (8, 8, 128, 1), (12, 12, 32, 2), (6, 6, 256, 1), (64, 8, 128, 1),
+                                        (64, 2, 128, 5), (64, 1, 128, 9), (32, 1, 32, 40)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tree_attention_head_groups(mx, dtype, Hq, Hkv, D, n):
+    """Every grouping of heads: one KV head to one a query head, over tiles that several shares hold."""
+    b = Batch(mx, [1300, 60], [n, n], Hq, Hkv, D, 64, dtype, "tree", Hq + D)
+    b.check(b.run(mx))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tree_attention_long_shares(mx, dtype):
+    """More work than the workgroups take in one piece of a tile each."""
+    b = Batch(mx, [9000, 8500, 7000, 8999], [1, 1, 1, 1], 8, 8, 128, 64, dtype, "causal", 61)
+    b.check(b.run(mx))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tree_attention_mask_words(mx, dtype):
+    """Bits past the drafted tokens and words past the mask do not count; unaligned query rows."""
+    b = Batch(mx, [150, 90], [70, 10], 4, 2, 64, 16, dtype, "tree", 33)
+    ref = b.run(mx)
+    wide = torch.full((80, 5), -1, dtype=torch.int64, device=DEV)
+    wide[:, :2] = b.bits
+    n = torch.tensor([70] * 70 + [10] * 10)
+    for r in range(80):                                          # set every bit from n on
+        k = int(n[r])
+        wide[r, 0] |= (-1 << k) if k < 64 else 0
+        wide[r, 1] |= (-1 << max(0, k - 64)) if k >= 64 else -1
+    assert torch.equal(b.run(mx, mask=wide), ref)
+    b.seen[:70, 64:] = False                                     # one word: tokens 64 .. 69 unseen
+    b.check(b.run(mx, mask=b.bits[:, :1].contiguous()))
+    rows = torch.zeros(80, 4 * 64 + 3, dtype=dtype, device=DEV)
+    rows[:, 1:257] = b.q.view(80, 256)
+    odd = rows[:, 1:257].unflatten(1, (4, 64))
+    assert odd.data_ptr() % 16 and torch.equal(b.run(mx, q=odd), ref)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_tree_attention_of_one_token_agrees_with_attend_kv4(mx, dtype):
     b = Batch(mx, [1000], [1], 16, 2, 128, 1000, dtype, "causal", 4, spare=0)
@@ -667,6 +726,31 @@ def test_two_streams_at_once(mx):
     torch.cuda.synchronize()
     for o, r in zip(outs, refs):
         assert torch.equal(o, r)
+
+
+def test_two_graphs_share_a_workspace(mx):
+    """Two captured calls over one workspace, replayed in turn and mixed with eager ones."""
+    bs = [Batch(mx, [3000, 40], [5, 3], 8, 2, 64, 64, BF, "tree", 70), Batch(mx, [700], [40], 8, 2, 64, 16, BF, "tree", 71)]
+    args = [b.args() for b in bs]
+    need = max(mx.mxs_attend_kv4_tree_workspace(BF, len(b.lens), b.q.shape[0], max(b.ns), max(b.lens), 8, 2, 64) for b in bs)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    outs = [torch.empty_like(b.q) for b in bs]
+    call = lambda i: mx.mxs_attend_kv4_tree(bs[i].q, bs[i].cache, out=outs[i], ws=ws, **args[i])
+    refs = [call(i).clone() for i in range(2)]
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(i)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        for o in outs:
+            o.fill_(float("nan"))
+        graphs[i].replay()
+        call(1 - i)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], refs[0]) and torch.equal(outs[1], refs[1])
 
 
 def test_slots_past_four_gigabytes(mx):
