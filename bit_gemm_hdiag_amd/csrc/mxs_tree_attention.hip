@@ -1227,10 +1227,15 @@ __global__ __launch_bounds__(256, NDP == 8 ? 1 : 2) void k_tree_tile(TreeArgs a)
 // ALU (softmax, dequantising the next stage, addresses), and a barrier swaps
 // them. Left to themselves the waves run through the same kind of work
 // together, and each unit idles in turn. Half 0 dequantises K, half 1 V:
-//   phase  2 k      half 0: PV(k - 1), QK(k)          half 1: softmax(k - 1), V(k)
-//   phase  2 k + 1  half 0: softmax(k), K(k + 1)      half 1: PV(k - 1), QK(k)
+//   phase  2 k      half 0: PV(k - 1), QK(k)          half 1: V(k), softmax(k - 1)
+//   phase  2 k + 1  half 0: K(k + 1), softmax(k)      half 1: PV(k - 1), QK(k)
 // so two LDS buffers serve: K(k) is read in phases 2 k and 2 k + 1 and written
 // again in 2 k + 3; V(k) is read in 2 k + 2 and 2 k + 3, written again in 2 k + 4.
+// 16 x 64 drafted tokens over up to 16384 (8 query heads): four waves without
+// turns 500 us; eight waves without turns, one barrier a stage, 488; turns 516,
+// with the matrix half's waves first in issue 470; on a slower card 500, with the
+// next stage's tiles written before the softmax 474. Of a turn of 5900 cycles
+// the operands' LDS reads (256 KiB a stage) take most.
 template <int NDP, int CT, int PARTS>
 __global__ __launch_bounds__(512) void k_tree_pair(TreeArgs a) {
     constexpr int PP = PARTS, NT = 2 * NDP, NTW = kNTL;
@@ -1426,8 +1431,8 @@ __global__ __launch_bounds__(512) void k_tree_pair(TreeArgs a) {
             lds_barrier();
             scores(0);
             lds_barrier();
-            weigh(0);
             stage(1);
+            weigh(0);
             for (int k = 1; k < N; ++k) {
                 lds_barrier();
                 __builtin_amdgcn_s_setprio(1);       // the matrix half issues first
@@ -1435,8 +1440,8 @@ __global__ __launch_bounds__(512) void k_tree_pair(TreeArgs a) {
                 scores(k & 1);
                 __builtin_amdgcn_s_setprio(0);
                 lds_barrier();
-                weigh(k);
                 stage(k + 1);        // past the last stage: its rows are clamped, its tiles not read
+                weigh(k);
             }
             lds_barrier();
             values((N & 1) ^ 1);
