@@ -1345,55 +1345,51 @@ __global__ __launch_bounds__(512) void k_tree_pair(TreeArgs a) {
             bf8 pf[NTW / 2][CT][PP];
             // p V of a stage
             auto values = [&](int vbuf) {
-                auto v_at = [&](int j) { return *reinterpret_cast<const bf8 *>(lds.v[vbuf][j / NT * NT + j % NT][lane]); };
-                {
-                    bf8 vf[VP];
+                auto v_at = [&](int j) { return *reinterpret_cast<const bf8 *>(lds.v[vbuf][j][lane]); };
+                bf8 vf[VP];
 #pragma unroll
-                    for (int j = 0; j < VP; ++j) vf[j] = v_at(j);
+                for (int j = 0; j < VP; ++j) vf[j] = v_at(j);
 #pragma unroll
-                    for (int u = 0; u < NTW / 2; ++u) {
+                for (int u = 0; u < NTW / 2; ++u) {
+#pragma unroll
+                    for (int t = 0; t < CT; ++t)
+#pragma unroll
+                        for (int j = 0; j < PP; ++j)
+                            st.l[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones(), pf[u][t][j], st.l[t], 0, 0, 0);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int j = u * NT + n;
+                        const bf8 vv = vf[j % VP];
+                        if (j + VP < NTW / 2 * NT) vf[j % VP] = v_at(j + VP);
 #pragma unroll
                         for (int t = 0; t < CT; ++t)
 #pragma unroll
-                            for (int j = 0; j < PP; ++j)
-                                st.l[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones(), pf[u][t][j], st.l[t], 0, 0, 0);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const int j = u * NT + n;
-                            const bf8 vv = vf[j % VP];
-                            if (j + VP < NTW / 2 * NT) vf[j % VP] = v_at(j + VP);
-#pragma unroll
-                            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                                for (int q = 0; q < PP; ++q)
-                                    st.acc[t][n] =
-                                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[u][t][q], st.acc[t][n], 0, 0, 0);
-                        }
+                            for (int q = 0; q < PP; ++q)
+                                st.acc[t][n] =
+                                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pf[u][t][q], st.acc[t][n], 0, 0, 0);
                     }
                 }
             };
             // scores of a stage
             auto scores = [&](int kb) {
-                auto k_at = [&](int j) { return *reinterpret_cast<const bf8 *>(lds.k[kb][j / NDP * NDP + j % NDP][lane]); };
-                {
-                    bf8 kf[VP];
+                auto k_at = [&](int j) { return *reinterpret_cast<const bf8 *>(lds.k[kb][j][lane]); };
+                bf8 kf[VP];
 #pragma unroll
-                    for (int j = 0; j < VP; ++j) kf[j] = k_at(j);
+                for (int j = 0; j < VP; ++j) kf[j] = k_at(j);
 #pragma unroll
-                    for (int u = 0; u < NTW; ++u) {
+                for (int u = 0; u < NTW; ++u) {
 #pragma unroll
-                        for (int t = 0; t < CT; ++t) sc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
+                    for (int t = 0; t < CT; ++t) sc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int b = 0; b < NDP; ++b) {
-                            const int j = u * NDP + b;
-                            const bf8 kv = kf[j % VP];
-                            if (j + VP < NTW * NDP) kf[j % VP] = k_at(j + VP);
+                    for (int b = 0; b < NDP; ++b) {
+                        const int j = u * NDP + b;
+                        const bf8 kv = kf[j % VP];
+                        if (j + VP < NTW * NDP) kf[j % VP] = k_at(j + VP);
 #pragma unroll
-                            for (int t = 0; t < CT; ++t)
+                        for (int t = 0; t < CT; ++t)
 #pragma unroll
-                                for (int q = 0; q < PARTS; ++q)
-                                    sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][q], sc[t][u], 0, 0, 0);
-                        }
+                            for (int q = 0; q < PARTS; ++q)
+                                sc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[t][b][q], sc[t][u], 0, 0, 0);
                     }
                 }
             };
