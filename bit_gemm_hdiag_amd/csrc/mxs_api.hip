@@ -133,7 +133,8 @@ mxs_status check_rotation(const char *where, const double *freq, int64_t rot, in
     return MXS_OK;
 }
 
-constexpr int64_t kMaxTokens = 0x7FFFFFFF;
+// a grid has fewer than 2^32 threads along an axis, and a workgroup of 256 may hold one token
+constexpr int64_t kMaxTokens = 0xFFFFFF;
 
 }  // namespace
 

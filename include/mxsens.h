@@ -481,7 +481,7 @@ mxs_status mxs_rope_frequencies(int32_t rot, double base, int32_t scaling, doubl
  * and ldh (heads) and adjacent dims; y may be x (same strides); they must not
  * overlap otherwise. positions: [T] int64 device (any sign); freq: [rot/2]
  * fp64 device. 16-byte aligned rows whose halves are whole 16-byte vectors
- * are faster. D <= 4096, H <= 65535, T <= 2^31 - 1. T = 0 or H = 0 is a no-op.
+ * are faster. D <= 4096, H <= 65535, T < 2^24. T = 0 or H = 0 is a no-op.
  * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE (sizes negative, rot odd, < 2 or > D,
  * strides < D, rows of y that overlap, y == x with other strides),
  * MXS_ERR_UNSUPPORTED, MXS_ERR_DEVICE.
@@ -501,7 +501,7 @@ mxs_status mxs_rope(const void *x, mxs_dtype dtype, int64_t T, int64_t H, int64_
  * unspecified mix of the two tokens, other slots are unaffected. Slots not
  * named keep their contents.
  * k, v: [T, H, D] device arrays of `dtype` with element strides as in
- * mxs_rope. T = 0 is a no-op.
+ * mxs_rope. T < 2^24. T = 0 is a no-op.
  * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE (T < 0, strides < D, rot, the cache's
  * sizes), MXS_ERR_UNSUPPORTED (alignment, sizes), MXS_ERR_DEVICE.
  */
@@ -516,7 +516,7 @@ mxs_status mxs_kv4_append(const mxs_kv4_cache *cache, const void *k, const void 
  * Rows whose slot is negative or past the pool are left as they were. Slots
  * may repeat. k or v may be NULL (not both): that one is not read.
  * k, v: [T, H, D] device arrays of `dtype`, element strides as in mxs_rope,
- * rows not overlapping. T = 0 is a no-op.
+ * rows not overlapping. T < 2^24. T = 0 is a no-op.
  * Errors: as mxs_kv4_append.
  */
 mxs_status mxs_kv4_read(const mxs_kv4_cache *cache, const int64_t *slots, int64_t T, mxs_dtype dtype, void *k,

@@ -156,6 +156,13 @@ def test_read_errors(lib):
     assert call(slots=P(0x10004)) == UNSUPPORTED
 
 
+def test_more_tokens_than_a_grid_holds_are_refused(lib):
+    big = 1 << 24                # one token a workgroup of 256 threads would pass 2^32 threads
+    assert lib.mxs_rope(A, 1, big, 2, 64, 128, 64, A, A, 64, 0, 1.0, P(0x90000), 128, 64, None) == UNSUPPORTED
+    assert lib.mxs_kv4_append(cache(), A, A, 1, big, 128, 64, 128, 64, A, None, None, 0, 0, 1.0, None) == UNSUPPORTED
+    assert lib.mxs_kv4_read(cache(), A, big, 1, A, 128, 64, A, 128, 64, None) == UNSUPPORTED
+
+
 def test_tree_attention_errors(lib):
     def call(q=A, dt=1, ldq=256, c=cache(), table=A, ldt=10, lens=A, cu=A, mask=None, words=0, B=2, tq=4, mq=4, ml=160,
              Hq=4, s=0.125, out=A, ldo=256, ws=A, n=1 << 30):
