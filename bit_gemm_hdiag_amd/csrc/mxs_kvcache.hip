@@ -82,6 +82,10 @@ struct RopeArgs {
     float mscale;
 };
 
+// Bound by HBM: x read and y written once, the angles are one fp64 product and
+// one sincospi a token and pair, shared by the heads. 2048 tokens of 64 heads of
+// 128 bf16 take 11.5 us (5.8 TB/s, against 5.0 of a 2 GiB copy: the caches hold
+// part of it), 64 tokens 2.7 us, of which the launch is most.
 // One unit is V elements of the first and V of the second half of a head's
 // rotated part (PAIRS: 2 V consecutive elements of V pairs; V = 1: one pair),
 // or V elements that pass through.
@@ -156,9 +160,11 @@ __global__ __launch_bounds__(256) void k_rope(RopeArgs a) {
 template <typename T, int V, bool PAIRS>
 hipError_t rope_go(RopeArgs a, hipStream_t st) {
     const int units = a.half / V + (a.D - 2 * a.half) / V;
-    // about 1024 units in a workgroup (four a thread), whole heads first,
-    // then tokens; few units altogether are spread over the chip instead
-    const int64_t want = a.T * a.H * units >= 256 * 1024 ? 1024 : 256;
+    // 256 units in a workgroup, one a thread, whole heads first, then tokens.
+    // Four a thread (and a quarter of the sines and cosines) are slower at any
+    // number of tokens: 3.7 against 2.6 us at 8 tokens of 64 heads of 128 bf16,
+    // 22.0 against 20.9 at 4096.
+    const int64_t want = 256;
     a.HB = a.H;
     while (a.HB > 1 && (int64_t)a.HB * units > want) a.HB = (a.HB + 1) / 2;
     int64_t tb = a.HB == a.H ? want / ((int64_t)a.HB * units) : 1;
@@ -247,6 +253,11 @@ __device__ __forceinline__ uint32_t pack8_f64(const double v[8], uint32_t &byte)
     return bad ? 0u : w;
 }
 
+// K and V are read once and 17/64 (bf16) of their bytes written. Without rotation
+// bound by HBM: 32768 tokens of 8 heads of 128 bf16 29.0 us (5.9 TB/s; cold, 41.6).
+// With it the fp64 sincospi of every token and pair (computed once for the heads)
+// and the fp64 products add 1.6 us at 2048 tokens (5.4 us) and 23 us at 32768; fp32
+// would put keys near a rounding border on either side of it.
 // ROT 0: none; 1: halves, whole words pair with whole words (half % 8 == 0); 2:
 // pairs; 3: halves of any size (the partners are loaded one by one). A thread
 // takes WPT words, all loaded before the first is quantised; the cosines and
@@ -345,10 +356,13 @@ __global__ __launch_bounds__(256) void k_kv4_append(AppendArgs a) {
 
 template <typename T, bool VEC, int ROT>
 hipError_t append_go(AppendArgs a, hipStream_t st) {
-    // one word a thread until the chip is full, then four; whole tokens (and
-    // their cosines and sines in LDS, 16 bytes a token and pair), or a chunk of one
+    // One word a thread until the chip is full four times over, then four. Graph
+    // replays at 8 heads of 128 bf16, one against four words: 8 tokens 2.3 against
+    // 3.1 us (rotated 3.2, 6.9), 4096 tokens 5.3, 5.5 (8.6, 9.6), 8192 9.6, 8.7
+    // (15.3, 16.0), 32768 31.4, 29.0 (52.4, 51.5). Whole tokens to a workgroup (and
+    // their cosines and sines in LDS, 16 bytes a token and pair), or a chunk of one.
     const int64_t words = a.words.d;
-    const int wpt = 2 * a.T * words <= 4 * 256 * 2048 ? 1 : 4;
+    const int wpt = 2 * a.T * words < 4 * 256 * 2048 ? 1 : 4;
     int64_t tb = 256 * wpt / words;
     const int64_t cap = ROT ? 2048 / a.half : tb;
     tb = tb > cap ? cap : tb;
@@ -381,6 +395,8 @@ struct ReadArgs {
     Div16 words, hwords, chunk;
 };
 
+// Bound by the writes: 65536 rows of 8 heads of 128 bf16 take 60 us cold (5.6
+// TB/s), 32768 rows 28 us when the caches hold part of them.
 // A thread takes WPT words (8 values each); all its codes and scales are loaded
 // before the first is widened
 template <typename T, bool VEC, int WPT>
@@ -435,7 +451,9 @@ __global__ __launch_bounds__(256) void k_kv4_read(ReadArgs a) {
 template <typename T>
 hipError_t read_type(ReadArgs a, bool vec, hipStream_t st) {
     const int64_t words = a.words.d;
-    const int wpt = 2 * a.T * words <= 4 * 256 * 2048 ? 1 : 4;       // as in append_go
+    // as in append_go; one against four words: 8 tokens 2.3 against 2.9 us, 4096
+    // 5.8, 6.0, 8192 9.2, 9.0, 16384 16.2, 15.3
+    const int wpt = 2 * a.T * words < 4 * 256 * 2048 ? 1 : 4;
     const int64_t tb = 256 * wpt / words;
     a.TB = (int)(tb < 1 ? 1 : tb);
     a.chunk = div16((uint32_t)(words < 256 * wpt ? words : 256 * wpt));
