@@ -38,7 +38,8 @@
 // are fp32.
 //
 // Kernels, by the rows n G of a KV head (tree_plan; bf16 / fp32 queries):
-//   k_tree_rows  up to 32 (D <= 128) or 16 / 16: every wave its own tokens
+//   k_tree_rows  up to 16 (D <= 128, large batches: 32) / 16: every wave its own
+//                tokens
 //   k_tree_tile  up to 128 / 64, D > 128: four waves share stages in LDS
 //   k_tree_pair  more: eight waves share stages and take turns
 // A device-side schedule (below) cuts the work into equal shares.
@@ -1552,7 +1553,13 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
     const int64_t rows = max_q * (Hq / Hkv);
     const bool bf = dt == MXS_BF16;
     int64_t slots;
-    if (rows <= (bf && p.NDP <= 4 ? 32 : 16)) {
+    // Up to 16 rows every wave takes its own tokens (against stages in LDS at 8
+    // sequences of 8192 tokens, 8 heads of 128 bf16: 8 rows 27.3, 41.4 us, 16 rows
+    // 29.5, 42.2; fp32 38.4, 42.6). From 17 to 32 the batch decides: 24 rows of 32
+    // sequences of 500 and 16384 tokens take 17.5 against 23.6 and 217 against 246
+    // us (heads of 64: 130, 187), but 8 sequences of 500 and 2048 17.4 against
+    // 16.2 and 28.3 against 23.5, for a stage feeds four waves from few tokens.
+    if (rows <= 16 || (rows <= 32 && bf && p.NDP <= 4 && B * Hkv >= 256)) {
         p.WT = 0;
         p.CT = rows > 16 ? 2 : 1;
         p.R = 16 * p.CT;
@@ -1570,6 +1577,10 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
         }
         slots = 256;
     } else {
+        // Graph replays at 8 sequences of 8192 tokens, heads of 128: 64 bf16 rows in
+        // two row groups of two waves each 51.4 us, in four of one 60.0 (fp32, 32
+        // rows: 49.8, 63.1); 256 rows by pairs of waves 103.0, by four waves 113.0
+        // (fp32, 128 rows: 110, 118), 128 rows alike.
         p.CT = bf ? 2 : 1;
         p.NW = rows > 64 * p.CT && p.NDP <= 4 ? 8 : 4;
         p.WT = rows <= 32 * p.CT ? 2 : 1;

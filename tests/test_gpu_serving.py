@@ -437,6 +437,22 @@ def test_tree_attention_large_batches(mx, dtype, case):
     assert torch.equal(got, b.run(mx, max_len=None if case == "short" else int(lens.max())))
 
 
+# 17 to 32 query rows a KV head in batches with many KV heads, and in the same batches with few
+@pytest.mark.parametrize("D,longest", [(32, 300), (64, 1200), (96, 300), (128, 1200)])
+@pytest.mark.parametrize("Hkv", [1, 4])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tree_attention_drafts_of_large_batches(mx, dtype, Hkv, D, longest):
+    rng = np.random.default_rng(D)
+    lens = rng.integers(0, 80, 68)
+    lens[[7, 66]] = longest, longest - 1
+    ns = np.minimum(rng.integers(0, 4, 68), lens)
+    ns[[7, 66]] = 3
+    b = Batch(mx, lens.tolist(), ns.tolist(), 10 * Hkv, Hkv, D, 16, dtype, "tree", 300 + D)
+    got = b.run(mx)
+    b.check(got)
+    assert torch.equal(got, b.run(mx))
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,n", [(128, 1, 64, 1), (8, 8, 128, 1), (12, 12, 32, 2), (6, 6, 256, 1), (64, 8, 128, 1),
                                         (64, 2, 128, 5), (64, 1, 128, 9), (32, 1, 32, 40)])
 @pytest.mark.parametrize("dtype", [BF, F32])
