@@ -254,7 +254,7 @@ __device__ __forceinline__ uint32_t pack8_f64(const double v[8], uint32_t &byte)
 }
 
 // K and V are read once and 17/64 (bf16) of their bytes written. Without rotation
-// bound by HBM: 32768 tokens of 8 heads of 128 bf16 29.0 us (5.9 TB/s; cold, 41.6).
+// bound by HBM: 32768 tokens of 8 heads of 128 bf16 29.0 us (5.9 TB/s; cold, 42 to 46).
 // With it the fp64 sincospi of every token and pair (computed once for the heads)
 // and the fp64 products add 1.6 us at 2048 tokens (5.4 us) and 23 us at 32768; fp32
 // would put keys near a rounding border on either side of it.

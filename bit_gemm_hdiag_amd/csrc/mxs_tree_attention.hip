@@ -47,8 +47,8 @@
 //   32 sequences, one token, 4 query heads a KV head, 4915 to 16384 cached
 //   tokens: 96 us, 3.9 TB/s of codes and scales (loads alone: 88 us)
 //   one sequence of 8192, 32768 tokens, 8 query heads: 14.6, 26.8 us
-//   8 x 26 drafted tokens, 8 query heads, up to 8192 tokens: 93 us, 356 TFLOP/s
-//   16 x 64, up to 16384 tokens: 470 us, 653 TFLOP/s; the LDS reads of the
+//   8 x 26 drafted tokens, 8 query heads, up to 8192 tokens: 90 us, 368 TFLOP/s
+//   16 x 64, up to 16384 tokens: 475 us, 648 TFLOP/s; the LDS reads of the
 //   operands bound it (a wave reads the whole stage for 32 rows; 64 rows a wave
 //   need more registers than there are)
 #include <cmath>
