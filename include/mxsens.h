@@ -530,7 +530,8 @@ mxs_status mxs_kv4_read(const mxs_kv4_cache *cache, const int64_t *slots, int64_
  * before this call). Query token i sees all of the first lens[b] - n tokens
  * and, of the last n, those j with bit j % 64 of mask[row, j / 64] set (bits
  * past mask_words count as clear; a token sees itself only if its own bit is
- * set); with mask NULL the j <= i. Over the tokens it sees, with g = h / (Hq / H),
+ * set); with mask NULL the j <= i. Where lens[b] < n, the cached tokens are the
+ * first lens[b] of the n, and the others are seen by no row. Over the tokens it sees, with g = h / (Hq / H),
  *     out[row, h] = sum_t p_t V[t, g],  p = softmax_t(scale q[row, h] . K[t, g]),
  * and 0 if it sees none. Plain decode is n = 1 with mask NULL; a chunk of a
  * prompt is n tokens with mask NULL; a drafted tree gives every token the bits

@@ -570,6 +570,19 @@ def test_tree_attention_reads_padded_batches_in_bounds(mx):
     assert torch.equal(got[:2], ref[:2]) and not got[2:].any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [5, 70])
+def test_tree_attention_fewer_cached_tokens_than_queries(mx, dtype, n):
+    """Three cached tokens: rows 0 to 2 see up to themselves, later rows all three."""
+    b = Batch(mx, [n], [n], 4, 2, 64, 16, dtype, "causal", 9)
+    bound = dict(max_q=n, max_len=n)
+    got = b.run(mx, lens=b.dev([3]), **bound)
+    first = b.run(mx, q=b.q[:3].contiguous(), lens=b.dev([3]), cu=b.dev([0, 3]), **bound)
+    rest = b.run(mx, q=b.q[3:].contiguous(), lens=b.dev([3] * (n - 3)), cu=b.dev(range(n - 2)),
+                 table=b.dev(np.repeat(b.table, n - 3, 0)), **bound)
+    assert torch.equal(got, torch.cat([first, rest]))
+
+
 def test_tree_attention_arguments_are_checked(mx):
     b = Batch(mx, [64, 64], [2, 2], 4, 2, 64, 16, F32, "tree", 8)
     for bad in (dict(table=b.dev(b.table).long()), dict(lens=b.dev([64])), dict(cu=b.dev([0, 2])),
