@@ -143,11 +143,14 @@ def _ptr(t):
 
 
 def _workspace(nbytes: int, dev, ws):
+    """(tensor, pointer, bytes). The caller keeps the tensor until the library
+    function has returned: given back earlier, the block could go to a call of
+    another thread that enqueues between this call's launches."""
     if nbytes == 0:
-        return None, 0
+        return ws, None, 0
     if ws is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 # --------------------------------------------------------------------- plain calls
@@ -185,7 +188,7 @@ def mxs_calibrate(X: torch.Tensor, hdiag: torch.Tensor | None = None, ws=None) -
         hdiag = torch.zeros(K, dtype=torch.float64, device=X.device)
     if hdiag.dtype != torch.float64 or not hdiag.is_contiguous() or hdiag.numel() != K:
         raise ValueError("hdiag must be a contiguous fp64 [K] tensor")
-    pw, nw = _workspace(mxs_calibrate_workspace(M, K), X.device, ws)
+    ws, pw, nw = _workspace(mxs_calibrate_workspace(M, K), X.device, ws)
     _check(_lib.mxs_calibrate(px, _dtype(X), M, K, ldx, hdiag.data_ptr(), pw, nw, _stream(X.device)),
            "mxs_calibrate")
     return hdiag
@@ -199,7 +202,7 @@ def mxs_score(W: torch.Tensor, hdiag: torch.Tensor, score: torch.Tensor | None =
         score = torch.empty(K, dtype=torch.float64, device=W.device)
     if hdiag.dtype != torch.float64 or not hdiag.is_contiguous() or hdiag.numel() != K:
         raise ValueError("hdiag must be a contiguous fp64 [K] tensor")
-    p, n = _workspace(mxs_score_workspace(N, K), W.device, ws)
+    ws, p, n = _workspace(mxs_score_workspace(N, K), W.device, ws)
     _check(_lib.mxs_score(pw_, _dtype(W), N, K, ldw, hdiag.data_ptr(), score.data_ptr(), p, n,
                           _stream(W.device)), "mxs_score")
     return score
@@ -295,7 +298,7 @@ def _gemm(fn, wsfn, name, A: QMat, W: QMat, Y, ws) -> torch.Tensor:
     py, ldy = _dev2d(Y, "Y")
     a, w = ctypes.byref(A.c_struct()), ctypes.byref(W.c_struct())
     if ws is None:
-        p, n = _workspace(int(wsfn(a, w)), dev, None)
+        ws, p, n = _workspace(int(wsfn(a, w)), dev, None)
     else:
         p, n = ws.data_ptr(), ws.numel() * ws.element_size()
     _check(fn(a, w, py, ldy, p, n, _stream(dev)), name)
@@ -350,7 +353,7 @@ def mxs_mixed_gemm_fused(X: torch.Tensor, perm: torch.Tensor | None, W: QMat, Y:
     w = W.c_struct()
     dt = _dtype(X)
     if ws is None:
-        p, n = _workspace(int(_lib.mxs_mixed_gemm_fused_workspace(M, dt, ctypes.byref(w))), X.device, None)
+        ws, p, n = _workspace(int(_lib.mxs_mixed_gemm_fused_workspace(M, dt, ctypes.byref(w))), X.device, None)
     else:
         p, n = ws.data_ptr(), ws.numel() * ws.element_size()
     _check(_lib.mxs_mixed_gemm_fused(px, dt, M, ldx, _ptr(perm), ctypes.byref(w), py, ldy, p, n,
@@ -391,7 +394,7 @@ def mxs_mixed_gemm_prepared(A: QMat, W: QMat, wprep: torch.Tensor, Y: torch.Tens
     py, ldy = _dev2d(Y, "Y")
     a, w = ctypes.byref(A.c_struct()), ctypes.byref(W.c_struct())
     if ws is None:
-        p, n = _workspace(int(_lib.mxs_mixed_gemm_prepared_workspace(a, w)), dev, None)
+        ws, p, n = _workspace(int(_lib.mxs_mixed_gemm_prepared_workspace(a, w)), dev, None)
     else:
         p, n = ws.data_ptr(), ws.numel() * ws.element_size()
     _check(_lib.mxs_mixed_gemm_prepared(a, w, wprep.data_ptr(), wprep.numel() * wprep.element_size(), py, ldy,
@@ -411,8 +414,8 @@ def mxs_mixed_gemm_fused_prepared(X: torch.Tensor, perm: torch.Tensor | None, W:
     w = W.c_struct()
     dt = _dtype(X)
     if ws is None:
-        p, n = _workspace(int(_lib.mxs_mixed_gemm_fused_prepared_workspace(M, dt, ctypes.byref(w))), X.device,
-                          None)
+        ws, p, n = _workspace(int(_lib.mxs_mixed_gemm_fused_prepared_workspace(M, dt, ctypes.byref(w))), X.device,
+                              None)
     else:
         p, n = ws.data_ptr(), ws.numel() * ws.element_size()
     _check(_lib.mxs_mixed_gemm_fused_prepared(px, dt, M, ldx, _ptr(perm), ctypes.byref(w), wprep.data_ptr(),
@@ -479,7 +482,7 @@ def mxs_output_error(X: torch.Tensor, W: torch.Tensor, Yq: torch.Tensor, err=Non
         raise ValueError("shapes do not match: X [M, K], W [N, K], Yq [M, N]")
     if err is None:
         err = torch.empty(1, dtype=torch.float64, device=X.device)
-    p, n = _workspace(mxs_output_error_workspace(M, N), X.device, ws)
+    ws, p, n = _workspace(mxs_output_error_workspace(M, N), X.device, ws)
     _check(_lib.mxs_output_error(px, pw, _dtype(X), M, N, K, ldx, ldw, py, ldy, err.data_ptr(), p, n,
                                  _stream(X.device)), "mxs_output_error")
     return err
@@ -522,7 +525,7 @@ def mxs_attend_kv4(q: torch.Tensor, k_cache, v_cache, scale: float, out=None, ws
         raise ValueError("cache shapes do not match q")
     if out is None:
         out = torch.empty((Hq, D), dtype=torch.float32, device=q.device)
-    p, n = _workspace(mxs_attend_kv4_workspace(T, Hq, Hkv, D), q.device, ws)
+    ws, p, n = _workspace(mxs_attend_kv4_workspace(T, Hq, Hkv, D), q.device, ws)
     _check(_lib.mxs_attend_kv4(q.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), T, Hq,
                                Hkv, D, float(scale), out.data_ptr(), p, n, _stream(q.device)), "mxs_attend_kv4")
     return out
@@ -740,8 +743,8 @@ def mxs_attend_kv4_tree(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, l
         max_len = width * cache.page_size
     dt = _dtype(q)
     if ws is None:
-        p, n = _workspace(int(_lib.mxs_attend_kv4_tree_workspace(dt, B, total, max_q, max_len, Hq, cache.H, D)),
-                          q.device, None)
+        ws, p, n = _workspace(int(_lib.mxs_attend_kv4_tree_workspace(dt, B, total, max_q, max_len, Hq, cache.H, D)),
+                              q.device, None)
     else:
         if ws.get_device() != gpu or not ws.is_contiguous():
             raise ValueError(f"ws must be a contiguous tensor on cuda:{gpu}")
