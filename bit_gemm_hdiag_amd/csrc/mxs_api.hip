@@ -136,6 +136,11 @@ mxs_status check_rotation(const char *where, const double *freq, int64_t rot, in
 // a grid has fewer than 2^32 threads along an axis, and a workgroup of 256 may hold one token
 constexpr int64_t kMaxTokens = 0xFFFFFF;
 
+// sizes that mxs_attend_kv4_tree does not take, whatever the others are
+bool past_tree_limits(int64_t B, int64_t total_q, int64_t max_q, int64_t max_len, int64_t Hq, int64_t D) {
+    return D > 256 || B > 65535 || Hq > 65535 || max_len > (1 << 30) || max_q > (1 << 20) || total_q > (1 << 24);
+}
+
 }  // namespace
 
 extern "C" {
@@ -551,7 +556,7 @@ mxs_status mxs_kv4_read(const mxs_kv4_cache *cache, const int64_t *slots, int64_
 size_t mxs_attend_kv4_tree_workspace(mxs_dtype dtype, int64_t B, int64_t total_q, int64_t max_q, int64_t max_len,
                                      int64_t Hq, int64_t Hkv, int64_t D) {
     if (!dtype_ok(dtype) || B <= 0 || total_q <= 0 || max_q <= 0 || max_len < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv ||
-        D < 32 || D % 32 || D > 256)
+        D < 32 || D % 32 || past_tree_limits(B, total_q, max_q, max_len, Hq, D))
         return 0;
     return mxs::attend_kv4_tree_workspace(dtype, B, max_q, max_len, Hq, Hkv, D);
 }
@@ -571,8 +576,7 @@ mxs_status mxs_attend_kv4_tree(const void *q, mxs_dtype dtype, int64_t ldq, cons
         return fail(MXS_ERR_SHAPE, "attend_kv4_tree: B=%lld total_q=%lld max_q=%lld max_len=%lld Hq=%lld H=%lld",
                     (long long)B, (long long)total_q, (long long)max_q, (long long)max_len, (long long)Hq,
                     (long long)H);
-    if (D > 256 || B > 65535 || Hq > 65535 || max_len > (1 << 30) || max_q > (1 << 20) || total_q > (1 << 24) ||
-        mask_words > (1 << 20) || ldt > (1 << 30))
+    if (past_tree_limits(B, total_q, max_q, max_len, Hq, D) || mask_words > (1 << 20) || ldt > (1 << 30))
         return fail(MXS_ERR_UNSUPPORTED, "attend_kv4_tree: D=%lld B=%lld Hq=%lld max_len=%lld max_q=%lld total_q=%lld",
                     (long long)D, (long long)B, (long long)Hq, (long long)max_len, (long long)max_q,
                     (long long)total_q);

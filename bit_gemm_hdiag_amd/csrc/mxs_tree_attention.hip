@@ -1540,17 +1540,26 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
 struct TreePlan {
     int NDP, CT, NW, WT;             // WT 0: k_tree_rows; NW 8: k_tree_pair
     int R, U, P, HG;
-    int ms, cap, nrt;
-    int64_t bound;                   // units at most
+    int ms, cap;
+    int64_t nrt;
+    int64_t bound;                   // units at most (kMostUnits + 1: more than the device counts)
     int join;                        // some tile may lie in several shares
 };
+
+// The device counts rows and units in 32 bits. Sizes that are each allowed have
+// products past 64 bits, so the host stops counting at kMostUnits + 1.
+constexpr int64_t kMostUnits = 1 << 30;
+int64_t count(int64_t a, int64_t b) {
+    int64_t r;
+    return __builtin_mul_overflow(a, b, &r) || r > kMostUnits ? kMostUnits + 1 : r;
+}
 
 // Kernel, tile and number of workgroups from what the host knows: eight waves
 // (four where one needs more than 256 registers) fit on each of the 256 CUs.
 TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv, int64_t D) {
     TreePlan p;
     p.NDP = D <= 64 ? 2 : (D <= 128 ? 4 : 8);
-    const int64_t rows = max_q * (Hq / Hkv);
+    const int64_t rows = count(max_q, Hq / Hkv);
     const bool bf = dt == MXS_BF16;
     int64_t slots;
     // Up to 16 rows every wave takes its own tokens (against stages in LDS at 8
@@ -1592,8 +1601,8 @@ TreePlan tree_plan(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int6
         slots = p.NDP == 8 || p.NW == 8 ? 256 : 512;
     }
     const int64_t T = max_len > 0 ? ceil_div(max_len, (int64_t)p.U) : 1;
-    p.nrt = (int)ceil_div(rows, (int64_t)p.R);
-    p.bound = B * (Hkv / p.HG) * p.nrt * T;
+    p.nrt = ceil_div(rows, (int64_t)p.R);
+    p.bound = count(count(count(B, Hkv / p.HG), p.nrt), T);
     for (p.P = 8; p.P < slots && ((int64_t)p.P << p.ms) < p.bound;) p.P *= 2;
     p.join = T > 1;
     return p;
@@ -1646,8 +1655,7 @@ size_t attend_kv4_tree_workspace(mxs_dtype dt, int64_t B, int64_t max_q, int64_t
 
 bool attend_kv4_tree_supported(mxs_dtype dt, int64_t B, int64_t max_q, int64_t max_len, int64_t Hq, int64_t Hkv,
                                int64_t D) {
-    const int64_t rows = max_q * (Hq / Hkv);
-    return rows <= (1 << 30) && tree_plan(dt, B, max_q, max_len, Hq, Hkv, D).bound <= (1 << 30);
+    return count(max_q, Hq / Hkv) <= kMostUnits && tree_plan(dt, B, max_q, max_len, Hq, Hkv, D).bound <= kMostUnits;
 }
 
 hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, const mxs_kv4_cache &c,
@@ -1679,7 +1687,7 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
     a.pml = a.po + (int64_t)(2 * p.P) * p.HG * p.R * c.D;
     a.todo = reinterpret_cast<int *>(a.pml + (int64_t)(2 * p.P) * p.HG * p.R * 2);
     a.join = p.join;
-    a.nrt = p.nrt;
+    a.nrt = (int)p.nrt;
     a.cap = p.cap;
     const int64_t tiles = B * (c.H / p.HG) * p.nrt;
     a.NT = tiles <= p.P ? (int)tiles : 0;

@@ -555,8 +555,9 @@ mxs_status mxs_kv4_read(const mxs_kv4_cache *cache, const int64_t *slots, int64_
  * found there, so that a captured graph serves any lens up to max_len): longer
  * ones are cut off at the bound. All
  * device memory except the cache struct. ws: >= mxs_attend_kv4_tree_workspace
- * bytes of device memory, 16-byte aligned, contents scratch (NULL if 0); calls
- * that may overlap need one each. D <= 256, max_len <= 2^30 and <= ldt *
+ * bytes of device memory, 16-byte aligned, contents scratch (NULL if 0; the
+ * query gives 0 for sizes that the call refuses); calls that may overlap need
+ * one each. D <= 256, max_len <= 2^30 and <= ldt *
  * page_size. total_q = 0, max_q = 0 or B = 0 is a no-op.
  * Errors: MXS_ERR_ARG (NULL, unknown dtype, scale not finite), MXS_ERR_SHAPE
  * (sizes, Hq % H, strides, ldt * page_size < max_len), MXS_ERR_UNSUPPORTED

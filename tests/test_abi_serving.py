@@ -225,3 +225,26 @@ def test_binding_refuses_host_tensors():
         mx.kv4_cache_alloc(2, 16, 2, 64, device="cpu")
     with pytest.raises(ValueError):
         mx.mxs_attend_kv4_tree(x, None, None, None, None, 1.0)
+
+
+def test_work_that_wraps_64_bits_is_refused(lib):
+    """Every size is allowed by itself; the count of work units is past 2^64, and
+    wraps to a negative number, to zero or to a few units."""
+    def call(B, Hq, H, max_q, max_len, dt=1):
+        c = cache(pages=1 << 20, H=H, D=32)
+        return lib.mxs_attend_kv4_tree(A, dt, Hq * 32, c, A, 1 << 26, A, A, None, 0, B, 1 << 24, max_q, max_len, Hq, 1.0, A,
+                                       Hq * 32, A, 1 << 40, None)
+    assert call(65535, 16383, 16383, 1 << 20, 1 << 30) == UNSUPPORTED
+    assert call(1 << 15, 1 << 13, 1 << 13, 1 << 20, 1 << 30) == UNSUPPORTED       # 2^64 units
+    assert call(1 << 15, 1 << 13, 1 << 13, 1 << 20, (1 << 30) - 64) == UNSUPPORTED
+    for dt in (0, 1):
+        for B in (1 << 12, 1 << 14, 65535):
+            for heads in (1 << 12, 12345, 16383):
+                for max_q in (1, 300, 1 << 20):
+                    assert call(B, heads, heads, max_q, 1 << 30, dt) == UNSUPPORTED, (dt, B, heads, max_q)
+    w = lib.mxs_attend_kv4_tree_workspace
+    big = (1 << 63) - 1
+    assert w(1, 1, 1, 1 << 20, 1 << 30, 65535, 1, 32) > 0
+    for bad in ((1, big, 1, 1, 1 << 30, 4, 2, 64), (1, 1, big, 1, 1 << 30, 4, 2, 64), (1, 1, 1, big, 1 << 30, 4, 2, 64),
+                (1, 1, 1, 1, big, 4, 2, 64), (1, 1, 1, 1, 1 << 30, big - 1, 2, 64), (1, 1, 1, 1, 1 << 30, big, big, 64)):
+        assert w(*bad) == 0                                       # sizes that the call refuses
