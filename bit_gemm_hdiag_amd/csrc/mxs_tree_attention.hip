@@ -1476,10 +1476,11 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
     while (4 * SL < ns && 2 * SL <= groups) SL *= 2;
     const int grp = tid / LR, sl = grp % SL, d = 4 * (tid % LR) < a.D ? 4 * (tid % LR) : 0;
     const bool mine = 4 * (tid % LR) < a.D;
-    for (int k = grp / SL; k < a.JR; k += groups / SL) {
-        const int in = blockIdx.y * a.JR + k;
+    // every thread makes the same number of turns: the barriers are inside
+    for (int k0 = 0; k0 < a.JR; k0 += groups / SL) {
+        const int k = k0 + grp / SL, in = blockIdx.y * a.JR + k;
         const int gi = in / a.R, row = t.row + in - gi * a.R;
-        const bool on = in < SR && row < t.n * a.G;
+        const bool on = k < a.JR && in < SR && row < t.n * a.G;
         float M = -INFINITY, L = 0.f;
         f4 o = {0.f, 0.f, 0.f, 0.f};
         if (on)
