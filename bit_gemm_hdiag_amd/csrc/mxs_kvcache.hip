@@ -433,7 +433,8 @@ __global__ __launch_bounds__(256) void k_kv4_read(ReadArgs a) {
     for (int k = 0; k < WPT; ++k) {
         if ((uint64_t)slot[k] >= (uint64_t)a.nslots) continue;
         const uint32_t h = quot(w[k], a.hwords), wd = w[k] - h * a.hwords.d;
-        const float s = e8m0_to_f32(b[k]);
+        // a marked block is NaN whatever its codes (Inf would do for zeros only)
+        const float s = b[k] == 0xFFu ? NAN : e8m0_to_f32(b[k]);
         float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = (float)((int32_t)(c[k] << (28 - 4 * i)) >> 28) * s;

@@ -512,7 +512,8 @@ mxs_status mxs_kv4_append(const mxs_kv4_cache *cache, const void *k, const void 
 
 /*
  * The cache read back: row t of k and v receives the values of slot slots[t],
- * code * 2^(byte - 127), exact in both types (a block marked 0xFF gives NaN).
+ * code * 2^(byte - 127), exact in both types (a block marked 0xFF gives NaN,
+ * whatever its codes; 2^128 and more, which no quantised block holds, Inf).
  * Rows whose slot is negative or past the pool are left as they were. Slots
  * may repeat. k or v may be NULL (not both): that one is not read.
  * k, v: [T, H, D] device arrays of `dtype`, element strides as in mxs_rope,

@@ -1,0 +1,54 @@
+"""The serving calls at the ends of what a cache can hold."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_serving import BF, DEV, F32, Batch, n64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mx():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import bit_gemm_hdiag_amd as mx
+    return mx
+
+
+# ----------------------------------------------- blocks marked 0xFF that hold codes
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [40, 9000])                        # one and four words a thread
+def test_read_of_marked_blocks_is_nan_whatever_their_codes(mx, dtype, T):
+    H, D = 8, 128
+    c = mx.kv4_cache_alloc(-(-T // 16), 16, H, D)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    for t in (c.kc, c.vc):
+        t.copy_(torch.randint(0, 256, t.shape, generator=g, device=DEV, dtype=torch.uint8))
+    marked = []
+    for t in (c.ks, c.vs):
+        m = torch.rand(t.shape, generator=g, device=DEV) < 0.25
+        t.copy_(torch.where(m, 255, 120))
+        marked.append(m.view(-1, H, D // 32)[:T].repeat_interleave(32, -1))
+    for got, m in zip(mx.mxs_kv4_read(c, torch.arange(T, device=DEV), dtype), marked):
+        assert int((torch.isnan(got) != m).sum()) == 0
+        assert int((~torch.isfinite(got[~m])).sum()) == 0
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("n,G", [(1, 1), (1, 8), (3, 8), (12, 8), (40, 8)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_of_marked_blocks_is_nan_whatever_their_codes(mx, dtype, n, G, D):
+    """Blocks with byte 0xFF and codes of either sign, in the context and among the drafted tokens."""
+    b = Batch(mx, [700, 90, 60], [n, min(n, 5), min(n, 5)], 2 * G, 2, D, 16, dtype, "causal", 50 + D)
+    c = b.cache
+    last = lambda plane, s, t: plane[int(b.table[s, t // 16]), t % 16]
+    for s, t, head, planes in ((0, 333, 0, ("vs", "vc")), (0, 700 - 1, 1, ("vs", "vc")), (1, 17, 0, ("ks", "kc")),
+                               (1, 89, 1, ("ks", "kc"))):
+        last(getattr(c, planes[0]), s, t)[head, 1] = 255
+        codes = last(getattr(c, planes[1]), s, t)[head, 16:32]
+        codes.copy_(torch.tensor([0x11, 0x77, 0x99, 0xF8] * 4, dtype=torch.uint8, device=DEV))
+    got = b.run(mx)
+    ref, _ = b.reference()
+    assert np.isnan(ref).any() and not np.isnan(ref).all()
+    assert np.array_equal(np.isnan(n64(got)), np.isnan(ref))
+    b.check(got)
