@@ -546,7 +546,7 @@ struct State {
     f4 acc[CT][2 * NDP];
     float m[CT];
     f4 l[CT];
-    f4 w[CT];                        // Offset: sum of p 2^s of the lane's V block
+    f4 w[CT];                        // sum of p times the offset's value 8 2^(s - 9) of the lane's V block
     uint32_t nan[CT];                // bit rr: the output's dims of register rr are NaN (see give_nan)
 };
 
@@ -638,10 +638,13 @@ __device__ __forceinline__ void v_pairs(const uint32_t v[4][Raw<NDP>::VW], const
     }
 }
 // The 2 NDP V operands of two tiles (tile n = dim i DL + n of lane (i, c)); OFF:
-// `off` is the operand of the lane's scales
+// `off` is the operand of a code of 0 in the lane's blocks, converted as the
+// codes are. It has their range and rounding: no sum of it overflows where theirs
+// does not, and zeros cancel to the last bit at any scale.
 template <int NDP, bool OFF>
 __device__ __forceinline__ void v_operands(const uint32_t v[2][4][Raw<NDP>::VW], const uint32_t vb[2][4],
                                            bf8 out[2 * NDP], bf8 &off) {
+    constexpr uint32_t kZero = 0x0808u;                               // two codes of 0, 8 added
     uint32_t o[2][2 * NDP][2], w[2][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -651,7 +654,9 @@ __device__ __forceinline__ void v_operands(const uint32_t v[2][4][Raw<NDP>::VW],
         v_pairs<NDP, OFF>(v[u], sc, o[u]);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            w[u][s] = __builtin_amdgcn_perm(__float_as_uint(sc[2 * s + 1]), __float_as_uint(sc[2 * s]), 0x07060302u);
+            w[u][s] = OFF ? __builtin_amdgcn_perm(cvt2<false>(kZero, sc[2 * s + 1]), cvt2<false>(kZero, sc[2 * s]),
+                                                  0x05040100u)
+                          : 0u;
     }
 #pragma unroll
     for (int n = 0; n < 2 * NDP; ++n) out[n] = __builtin_bit_cast(bf8, u4{o[0][n][0], o[0][n][1], o[1][n][0], o[1][n][1]});
@@ -756,19 +761,13 @@ __device__ __forceinline__ void store_rows(const TreeArgs &a, const Place &p, co
     }
 }
 
-// The offset of 8 codes leaves the outputs. Blocks of byte 0 (zeros) leave up
-// to l 2^-133: outputs of at most 2^-123 are 0.
+// The offset of 8 codes leaves the outputs
 template <int NDP, int CT>
 __device__ __forceinline__ void take_offset(State<NDP, CT> &st) {
 #pragma unroll
     for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int n = 0; n < 2 * NDP; ++n) {
-            st.acc[t][n] -= st.w[t] * 0.015625f;                      // 8 / 2^9
-#pragma unroll
-            for (int rr = 0; rr < 4; ++rr)
-                st.acc[t][n][rr] = fabsf(st.acc[t][n][rr]) <= st.l[t][0] * 0x1p-132f ? 0.f : st.acc[t][n][rr];
-        }
+        for (int n = 0; n < 2 * NDP; ++n) st.acc[t][n] -= st.w[t];
 }
 
 // States of two waves over the same rows, through LDS in lane order (CT (2 NDP
@@ -812,7 +811,7 @@ __device__ __forceinline__ void take_state(State<NDP, CT> &st, const float *ex, 
 // e4m3 pattern is the number itself: K enters as (code + 8) 2^(s - 9) and a
 // product of the lane's block scales with -8 times the sum of its query dims
 // (in three bf16 parts) takes the excess out of the scores; V enters likewise,
-// and a product of p with the block scales (State::w) takes it out at the end.
+// and a product of p with the offsets (State::w) takes it out at the end.
 // fp32 queries keep the exact codes.
 __host__ __device__ constexpr int rows_waves(int NDP, int CT) { return NDP * CT <= 4 ? 8 : 4; }
 // f(0), f(1), ... f(N - 1) with constant arguments

@@ -541,12 +541,13 @@ mxs_status mxs_kv4_read(const mxs_kv4_cache *cache, const int64_t *slots, int64_
  * included, does not reach the output.
  * fp32 queries: exact products, fp32 sums, fp32 output. bf16 queries: exact
  * scores up to the fp32 sums, softmax weights rounded to bf16 (in the products
- * and in the sum that normalises alike), fp32 sums, output rounded once;
- * outputs of magnitude up to 2^-123 are returned as 0. Every sum has an order
- * fixed by the arguments, lens and cu: the result is deterministic, and what the
- * other sequences hold does not change it (their lengths move the split, and
- * with it the rounding). Scale bytes 0 to 2 (values below 2^-122) are read to
- * 2^-124.
+ * and in the sum that normalises alike), fp32 sums, output rounded once. Every
+ * sum has an order fixed by the arguments, lens and cu: the result is
+ * deterministic, and what the other sequences hold does not change it (their
+ * lengths move the split, and with it the rounding). Scale bytes 0 to 2 (values
+ * below 2^-122) are read to 2^-124. The sums hold p V / 2^9 with weights p of up
+ * to 2^6 and codes of up to 15 (8 added), so they are finite wherever V's
+ * largest scale 2^(byte - 127) times the tokens seen is at most 2^127.
  * q: [total_q, Hq, D] of `dtype`, ldq elements between tokens; out the same
  * with ldo; rows of no sequence are left as they were. table: [B, ldt] int32;
  * lens: [B] int32; cu: [B + 1] int32, ascending from 0, at most total_q; mask:

@@ -52,3 +52,50 @@ def test_attention_of_marked_blocks_is_nan_whatever_their_codes(mx, dtype, n, G,
     assert np.isnan(ref).any() and not np.isnan(ref).all()
     assert np.array_equal(np.isnan(n64(got)), np.isnan(ref))
     b.check(got)
+
+
+# --------------------------------------------------------------- values near the largest
+@pytest.mark.parametrize("rows", [1, 8, 24, 40, 300])
+@pytest.mark.parametrize("byte", [240, 250, 252, 254])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_of_large_values_is_finite(mx, dtype, D, byte, rows):
+    """Codes of 1 and 0 at scales up to 2^127: over equal scores the output is the value itself, while
+    sums of p 2^s are up to 60 times 2^127 (and of p 2^(s - 9), which the kernels keep, below 2^127)."""
+    L = 60
+    n = min(rows, L)
+    G = rows // n
+    B = 260 if rows == 24 else 3                                 # 24 rows: a kernel for few sequences, one for many
+    b = Batch(mx, [L] * B, [n] * B, G, 1, D, 16, dtype, "causal", 4)
+    b.q.zero_()
+    c = b.cache
+    c.vs.fill_(byte)
+    c.vc.fill_(0x01)                                             # even dims 1, odd dims 0
+    out = b.run(mx).double()
+    assert int((~torch.isfinite(out)).sum()) == 0
+    # sums of up to 60 weights of 1, exact; division and product round twice, then the output
+    want = 2.0 ** (byte - 127)
+    assert ((out[..., 0::2] - want).abs() <= (2 * 2.0 ** -24 + 2.0 ** -8 * (dtype == BF)) * want).all()
+    assert not out[..., 1::2].any()
+
+
+@pytest.mark.parametrize("rows", [1, 8, 24, 40, 300])
+@pytest.mark.parametrize("byte", [0, 1, 2, 3, 4, 6, 9, 20])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_of_tiny_values(mx, dtype, byte, rows):
+    """Codes 0 to 7 at the smallest scales, the same in every token, over equal scores."""
+    L, D = 40, 64
+    n = min(rows, L)
+    B = 260 if rows == 24 else 3
+    b = Batch(mx, [L] * B, [n] * B, rows // n, 1, D, 16, dtype, "causal", 4)
+    b.q.zero_()
+    c = b.cache
+    c.vs.fill_(byte)
+    codes = torch.arange(D, device=DEV) % 8
+    c.vc.copy_((codes[0::2] | codes[1::2] << 4).to(torch.uint8))
+    out = b.run(mx).double()
+    want = codes.double() * 2.0 ** (byte - 127)
+    # bytes 0 to 2 are read to multiples of 2^-124; a type's subnormals have one step
+    low = 2.0 ** -125 if byte < 3 else 0.0
+    step = {BF: 2.0 ** -134, F32: 2.0 ** -150}[dtype]
+    assert ((out - want).abs() <= low + step + (2 * 2.0 ** -24 + 2.0 ** -8 * (dtype == BF)) * (want + low)).all()
