@@ -536,6 +536,13 @@ ROPE_LAYOUTS = {"half": 0, "pairs": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 
 
+def _int32(n: int, name: str) -> int:
+    """n, which the C interface takes in 32 bits (a larger one would lose its upper half)."""
+    if n > 0x7FFFFFFF:
+        raise ValueError(f"{name} must be less than 2^31")
+    return n
+
+
 def mxs_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                          low: float = 1.0, high: float = 4.0, original_length: float = 8192.0,
                          device="cuda") -> torch.Tensor:
@@ -546,7 +553,7 @@ def mxs_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none",
     original_length tokens (none above `high` turns, all below `low`)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
-    out = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64)
+    out = torch.empty(max(_int32(int(rot), "rot") // 2, 1), dtype=torch.float64)
     _check(_lib.mxs_rope_frequencies(rot, base, ROPE_SCALINGS[scaling], factor, low, high, original_length,
                                      out.data_ptr()), "mxs_rope_frequencies")
     return out.to(device)
@@ -612,8 +619,8 @@ def mxs_rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, layou
     py, yt, yh = _rows(out, "out", gpu)
     n = freq.numel()
     _call(gpu, _lib.mxs_rope, "mxs_rope", px, _dtype(x), T, H, D, xt, xh,
-          _vector(positions, "positions", torch.int64, T, gpu), _vector(freq, "freq", torch.float64, n, gpu), 2 * n,
-          _layout(layout), mscale, py, yt, yh)
+          _vector(positions, "positions", torch.int64, T, gpu), _vector(freq, "freq", torch.float64, n, gpu),
+          _int32(2 * n, "2 * len(freq)"), _layout(layout), mscale, py, yt, yh)
     return out
 
 
@@ -638,8 +645,8 @@ class KV4Cache:
                     or t.device != self.kc.device:
                 raise ValueError("cache planes must be contiguous uint8 [pages, page_size, H, D / 2] codes and "
                                  "[pages, page_size, H, D / 32] scales on one GPU")
-        c = _Kv4Cache(P, S, H, 2 * h, 0, self.kc.data_ptr(), self.ks.data_ptr(), self.vc.data_ptr(),
-                      self.vs.data_ptr())
+        c = _Kv4Cache(P, _int32(S, "page_size"), _int32(H, "H"), _int32(2 * h, "D"), 0, self.kc.data_ptr(),
+                      self.ks.data_ptr(), self.vc.data_ptr(), self.vs.data_ptr())
         for k, v in (("_c", c), ("_ref", ctypes.pointer(c)), ("gpu", self.kc.get_device()), ("page_size", S),
                      ("H", H), ("D", 2 * h)):
             object.__setattr__(self, k, v)
@@ -675,7 +682,7 @@ def mxs_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: tor
         n = freq.numel()
         pp, pf = _vector(positions, "positions", torch.int64, T, gpu), _vector(freq, "freq", torch.float64, n, gpu)
     _call(gpu, _lib.mxs_kv4_append, "mxs_kv4_append", cache._ref, pk, pv, _dtype(k), T, kt, kh, vt, vh,
-          _vector(slots, "slots", torch.int64, T, gpu), pp, pf, 2 * n, _layout(layout), mscale)
+          _vector(slots, "slots", torch.int64, T, gpu), pp, pf, _int32(2 * n, "2 * len(freq)"), _layout(layout), mscale)
 
 
 def mxs_kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
