@@ -286,9 +286,10 @@ struct Place {
 
 // What k_tree_join finds in a todo entry. Entries are those of the tiles ((b,
 // head group, row tile), NT > 0) or of the shares that hold a tile's first piece
-// but not its last; an entry with last <= first needs no join. Entry 0 of a
-// share is written by the share, that of a tile by the share of its first unit;
-// entries of no tile are left, and told by the sequence's n.
+// but not its last; an entry with last <= first needs no join. The entry of a
+// share is written by the share ((0, -1) where no tile starts that it does not
+// end), that of a tile by the share of its first unit; entries of no tile are
+// left, and told by the sequence's n. What no one wrote is not read.
 struct JoinOf {
     int first, last;                 // shares of its first and last piece
     int q0, n, g, row;               // Place's
@@ -303,7 +304,10 @@ __device__ __forceinline__ void for_each_piece(const TreeArgs &a, int lane, F f)
     const Shares h = shares_of(a, win, lane);
     const uint32_t per = (h.P + 7) / 8, p = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if (a.join && a.NT == 0 && threadIdx.x == 0) {       // nothing to join yet; the number of shares
-        if ((blockIdx.x >> 3) < per && p < h.P) a.todo[8 * p + 1] = -1;
+        if ((blockIdx.x >> 3) < per && p < h.P) {
+            a.todo[8 * p] = 0;                           // both: the workspace holds anything, and the join
+            a.todo[8 * p + 1] = -1;                      // compares them
+        }
         if (blockIdx.x == 0) a.todo[8 * a.P] = (int)h.P;
     }
     if ((blockIdx.x >> 3) >= per || p >= h.P) return;
