@@ -686,21 +686,25 @@ def mxs_kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: tor
 
 
 def mxs_kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
-                 k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None):
+                 k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, keys: bool = True,
+                 values: bool = True):
     """(k, v), each [T, H, D]: the values of slots [T] (int64), exact. Rows of
     slots that are negative or past the pool are left as they were (zero in
-    outputs that the call allocates). dtype is that of outputs not given."""
+    outputs that the call allocates). dtype is that of outputs not given. keys
+    or values False: that one is not read, and None is returned for it."""
     gpu, T = cache.gpu, slots.numel()
+    if not (keys or values) or (k_out is not None and not keys) or (v_out is not None and not values):
+        raise ValueError("keys, values or both are read, and no output is given for what is not")
     if k_out is not None or v_out is not None:
         dtype = (k_out if k_out is not None else v_out).dtype
-    if k_out is None:
+    if keys and k_out is None:
         k_out = torch.zeros((T, cache.H, cache.D), dtype=dtype, device=cache.kc.device)
-    if v_out is None:
+    if values and v_out is None:
         v_out = torch.zeros((T, cache.H, cache.D), dtype=dtype, device=cache.kc.device)
-    pk, kt, kh = _kv_rows(cache, k_out, "k_out", T, dtype)
-    pv, vt, vh = _kv_rows(cache, v_out, "v_out", T, dtype)
+    pk, kt, kh = _kv_rows(cache, k_out, "k_out", T, dtype) if keys else (None, 0, 0)
+    pv, vt, vh = _kv_rows(cache, v_out, "v_out", T, dtype) if values else (None, 0, 0)
     _call(gpu, _lib.mxs_kv4_read, "mxs_kv4_read", cache._ref, _vector(slots, "slots", torch.int64, T, gpu), T,
-          _dtype(k_out), pk, kt, kh, pv, vt, vh)
+          _dtype(k_out if keys else v_out), pk, kt, kh, pv, vt, vh)
     return k_out, v_out
 
 

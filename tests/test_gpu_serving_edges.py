@@ -54,6 +54,29 @@ def test_attention_of_marked_blocks_is_nan_whatever_their_codes(mx, dtype, n, G,
     b.check(got)
 
 
+# ------------------------------------------------------------------ one of the two read
+@pytest.mark.parametrize("T", [9, 9000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_read_of_keys_or_of_values_alone(mx, T, dtype):
+    H, D = 3, 96
+    c = mx.kv4_cache_alloc(-(-T // 17), 17, H, D)
+    g = torch.Generator().manual_seed(T)
+    slots = torch.randperm(T, generator=g).to(DEV)
+    k, v = (torch.randn(T, H, D, generator=g).to(DEV) for _ in range(2))
+    mx.mxs_kv4_append(c, k, v, slots)
+    both = mx.mxs_kv4_read(c, slots, dtype)
+    ko, none = mx.mxs_kv4_read(c, slots, dtype, values=False)
+    assert none is None and torch.equal(ko, both[0])
+    none, vo = mx.mxs_kv4_read(c, slots, dtype, keys=False)
+    assert none is None and torch.equal(vo, both[1])
+    rows = torch.full((T, 2 * H, D), 7.0, dtype=dtype, device=DEV)        # the other half is left as it was
+    mx.mxs_kv4_read(c, slots, v_out=rows[:, H:], keys=False)
+    assert torch.equal(rows[:, H:], both[1]) and bool((rows[:, :H] == 7.0).all())
+    for bad in (dict(keys=False, values=False), dict(keys=False, k_out=rows[:, :H]), dict(values=False, v_out=rows[:, H:])):
+        with pytest.raises(ValueError):
+            mx.mxs_kv4_read(c, slots, **bad)
+
+
 # --------------------------------------------------------------- values near the largest
 @pytest.mark.parametrize("rows", [1, 8, 24, 40, 300])
 @pytest.mark.parametrize("byte", [240, 250, 252, 254])
