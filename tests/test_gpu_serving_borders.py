@@ -159,3 +159,57 @@ def test_join_takes_every_piece_once(mx, D, L, dtype):
         p = Pinned(mx, [L], [n], 1, G, D, 64, dtype, L + D, anchors=[L // 2 + 3])
         step = 64 if L < 4000 else 256
         p.sweep([near(L, step)[::1 if n * G > 1 else 3]])
+
+
+# (lens, ns, Hkv, G, D, page): every kernel, tiles whole and in pieces, pages that
+# end inside stages, ragged batches (shares end anywhere), rows past the last tile
+SWEEPS = {
+    "rows, decode": ([1500, 333, 65], [1, 1, 1], 8, 8, 128, 64),
+    "rows, one head a group": ([1100, 700], [1, 1], 1, 16, 64, 17),
+    "rows, chain": ([900, 1290], [4, 2], 2, 4, 96, 16),
+    "rows, D 256": ([1300], [2], 2, 8, 256, 64),
+    "rows, short": ([500, 1, 257], [1, 1, 1], 4, 8, 128, 16),
+    "rows, D 32": ([2100], [1], 4, 16, 32, 1),
+    "tile, two waves a row group": ([1000, 203], [5, 3], 2, 8, 128, 64),
+    "tile, four row groups": ([777, 130], [12, 5], 1, 8, 64, 16),
+    "tile, D 224": ([700, 513], [9, 2], 1, 8, 224, 33),
+    "pair": ([1030, 450, 129], [40, 17, 33], 2, 8, 128, 64),
+    "pair, odd": ([640, 900], [129, 70], 3, 2, 64, 7),
+    "pair, prompt from nothing": ([400], [400], 2, 4, 96, 16),
+    "tile, prompt from nothing": ([200, 90], [200, 90], 2, 1, 160, 64),
+}
+
+
+@pytest.mark.parametrize("case", SWEEPS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_every_token_counts_once(mx, case, dtype):
+    lens, ns, Hkv, G, D, page = SWEEPS[case]
+    # a token that every row sees: any of the context, else the first
+    rng = np.random.default_rng(len(case))
+    anchors = [int(rng.integers(0, L - n + 1)) for L, n in zip(lens, ns)]
+    if case == "rows, short":                                    # a sequence of one token has no other to pin
+        lens, ns, anchors = [lens[0], lens[2]], [1, 1], [anchors[0], anchors[2]]
+    Pinned(mx, lens, ns, Hkv, G, D, page, dtype, 7 * D + page, anchors).sweep()
+
+
+# many sequences: more tiles than workgroups, long ones among short, and (17 to
+# 32 rows a KV head) the kernel of two column tiles a wave
+@pytest.mark.parametrize("n,G,Hkv,D", [(1, 4, 8, 128), (3, 8, 4, 64), (3, 8, 4, 128), (9, 4, 4, 64)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_every_token_counts_once_in_large_batches(mx, n, G, Hkv, D, dtype):
+    rng = np.random.default_rng(n * D)
+    B = 70
+    lens = rng.integers(n + 1, 90, B)
+    lens[[5, 66]] = (1200, 641) if n > 1 else (500, 301)
+    ns = rng.integers(1, n + 1, B)
+    ns[[5, 66]] = n
+    Pinned(mx, lens.tolist(), ns.tolist(), Hkv, G, D, 16, dtype, n + D).sweep()
+
+
+@pytest.mark.parametrize("L", [17001, 33000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tokens_at_borders_of_long_contexts(mx, L, dtype):
+    p = Pinned(mx, [L, 2049], [1, 1], 2, 16, 128, 64, dtype, L, anchors=[L // 3, 5])
+    p.sweep([near(L, 128), near(2049, 32)])
+    p = Pinned(mx, [L], [20], 1, 8, 64, 256, dtype, L + 1, anchors=[7])
+    p.sweep([near(L, 64)])
