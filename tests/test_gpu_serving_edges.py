@@ -72,7 +72,8 @@ def test_read_of_keys_or_of_values_alone(mx, T, dtype):
     rows = torch.full((T, 2 * H, D), 7.0, dtype=dtype, device=DEV)        # the other half is left as it was
     mx.mxs_kv4_read(c, slots, v_out=rows[:, H:], keys=False)
     assert torch.equal(rows[:, H:], both[1]) and bool((rows[:, :H] == 7.0).all())
-    for bad in (dict(keys=False, values=False), dict(keys=False, k_out=rows[:, :H]), dict(values=False, v_out=rows[:, H:])):
+    for bad in (dict(keys=False, values=False), dict(keys=False, k_out=rows[:, :H]),
+                dict(values=False, v_out=rows[:, H:])):
         with pytest.raises(ValueError):
             mx.mxs_kv4_read(c, slots, **bad)
 
@@ -122,3 +123,27 @@ def test_attention_of_tiny_values(mx, dtype, byte, rows):
     low = 2.0 ** -125 if byte < 3 else 0.0
     step = {BF: 2.0 ** -134, F32: 2.0 ** -150}[dtype]
     assert ((out - want).abs() <= low + step + (2 * 2.0 ** -24 + 2.0 ** -8 * (dtype == BF)) * (want + low)).all()
+
+
+# ------------------------------------------------------------ caches that others wrote
+@pytest.mark.parametrize("Hq,Hkv,D,n", [(1, 1, 32, 1), (8, 2, 64, 1), (16, 2, 128, 1), (6, 2, 96, 9), (16, 1, 128, 12),
+                                        (8, 2, 160, 7), (4, 1, 256, 3), (16, 2, 128, 40)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_over_any_codes(mx, dtype, Hq, Hkv, D, n):
+    """Every code, -8 among them, which no quantised block holds, and blocks of differing scales."""
+    b = Batch(mx, [300, 70], [n, n], Hq, Hkv, D, 16, dtype, "tree", 60 + D)
+    g = torch.Generator(device=DEV).manual_seed(D)
+    for t in (b.cache.kc, b.cache.vc):
+        t.copy_(torch.randint(0, 256, t.shape, generator=g, device=DEV, dtype=torch.uint8))
+    for t in (b.cache.ks, b.cache.vs):
+        t.copy_(torch.randint(118, 127, t.shape, generator=g, device=DEV, dtype=torch.uint8))
+    b.check(b.run(mx))
+
+
+def test_attention_over_no_pages(mx):
+    """A table without columns: nothing is cached, every row is 0."""
+    b = Batch(mx, [40, 3], [2, 1], 4, 2, 64, 16, BF, "causal", 3)
+    out = torch.full_like(b.q, 5.0)
+    none = torch.empty(2, 0, dtype=torch.int32, device=DEV)
+    got = mx.mxs_attend_kv4_tree(b.q, b.cache, none, b.dev([0, 0]), b.dev([0, 2, 3]), 0.125, out=out)
+    assert got is out and not out.any()

@@ -60,3 +60,30 @@ def test_workspace_may_hold_anything(mx, dtype, shape):
         ws[need:].fill_(0xA5)
         assert torch.equal(run(), ref), fill
         assert bool((ws[need:] == 0xA5).all())                   # nothing written past it
+
+
+def test_two_threads_on_one_stream(mx):
+    """Calls without a workspace of their own, whose two launches interleave with the other thread's."""
+    import threading
+    bs = [Batch(mx, [3000], [4], 8, 2, 128, 64, BF, "tree", 80 + i) for i in range(2)]
+    args = [b.args() for b in bs]
+    refs = [mx.mxs_attend_kv4_tree(b.q, b.cache, **a) for b, a in zip(bs, args)]
+    outs = [[torch.empty_like(b.q) for _ in range(50)] for b in bs]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            for o in outs[i]:
+                mx.mxs_attend_kv4_tree(bs[i].q, bs[i].cache, out=o, **args[i])
+        except Exception as e:                                   # shown by the main thread
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for got, ref in zip(outs, refs):
+        assert all(torch.equal(o, ref) for o in got)
