@@ -724,9 +724,10 @@ def mxs_attend_kv4_tree(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, l
     [total_q, words] int64 holds, for every row, the bits of the drafted tokens
     it sees (None: those up to itself). table [B, pages], lens [B] and cu
     [B + 1] are int32. max_q and max_len bound the query and cached tokens of a
-    sequence (default: total_q and what the table can hold); tight bounds give
-    a better split. Rows of no sequence are left as they were in `out` (zero in
-    an output that the call allocates)."""
+    sequence (default: total_q and what the table can hold). max_q chooses the
+    kernel: plain decode of a batch should pass max_q=1 (with the default, 32
+    sequences take more than twice the time). Rows of no sequence are left as
+    they were in `out` (zero in an output that the call allocates)."""
     gpu = _gpu(q, "q")
     pq, qt, qh = _rows(q, "q", gpu)
     total, Hq, D = q.shape

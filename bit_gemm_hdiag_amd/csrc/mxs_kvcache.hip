@@ -85,7 +85,9 @@ struct RopeArgs {
 // Bound by HBM: x read and y written once, the angles are one fp64 product and
 // one sincospi a token and pair, shared by the heads. 2048 tokens of 64 heads of
 // 128 bf16 take 11.5 us (5.8 TB/s, against 5.0 of a 2 GiB copy: the caches hold
-// part of it), 64 tokens 2.7 us, of which the launch is most.
+// part of it), 64 tokens 2.7 us, of which the launch is most. Rows that no 16-byte
+// access fits (V = 1) take 29.9 us there, and 54.7 where 20 of the 128 dims turn
+// and the rest is copied element by element.
 // One unit is V elements of the first and V of the second half of a head's
 // rotated part (PAIRS: 2 V consecutive elements of V pairs; V = 1: one pair),
 // or V elements that pass through.
@@ -256,8 +258,10 @@ __device__ __forceinline__ uint32_t pack8_f64(const double v[8], uint32_t &byte)
 // K and V are read once and 17/64 (bf16) of their bytes written. Without rotation
 // bound by HBM: 32768 tokens of 8 heads of 128 bf16 29.0 us (5.9 TB/s; cold, 42 to 46).
 // With it the fp64 sincospi of every token and pair (computed once for the heads)
-// and the fp64 products add 1.6 us at 2048 tokens (5.4 us) and 23 us at 32768; fp32
-// would put keys near a rounding border on either side of it.
+// and the fp64 products, behind a barrier between loads and stores in the K
+// workgroups, add 1.5 us at 2048 tokens (5.7 us) and 24 us at 32768 (52.7); fp32
+// would put keys near a rounding border on either side of it. fp32 inputs: 48.1 us
+// at 32768 tokens, rotated 67.6.
 // ROT 0: none; 1: halves, whole words pair with whole words (half % 8 == 0); 2:
 // pairs; 3: halves of any size (the partners are loaded one by one). A thread
 // takes WPT words, all loaded before the first is quantised; the cosines and
@@ -359,7 +363,9 @@ hipError_t append_go(AppendArgs a, hipStream_t st) {
     // One word a thread until the chip is full four times over, then four. Graph
     // replays at 8 heads of 128 bf16, one against four words: 8 tokens 2.3 against
     // 3.1 us (rotated 3.2, 6.9), 4096 tokens 5.3, 5.5 (8.6, 9.6), 8192 9.6, 8.7
-    // (15.3, 16.0), 32768 31.4, 29.0 (52.4, 51.5). Whole tokens to a workgroup (and
+    // (15.3, 16.0), 16384 (27.6, 28.0), 32768 31.4, 29.0 (52.4, 51.5). The border is
+    // the unrotated call's; a rotated one would gain up to 4 % between 8192 and
+    // 16384 tokens by a later one. Whole tokens to a workgroup (and
     // their cosines and sines in LDS, 16 bytes a token and pair), or a chunk of one.
     const int64_t words = a.words.d;
     const int wpt = 2 * a.T * words < 4 * 256 * 2048 ? 1 : 4;
@@ -396,7 +402,7 @@ struct ReadArgs {
 };
 
 // Bound by the writes: 65536 rows of 8 heads of 128 bf16 take 60 us cold (5.6
-// TB/s), 32768 rows 28 us when the caches hold part of them.
+// TB/s), 32768 rows 28 us when the caches hold part of them; 32768 rows of fp32 78.
 // A thread takes WPT words (8 values each); all its codes and scales are loaded
 // before the first is widened
 template <typename T, bool VEC, int WPT>

@@ -30,27 +30,38 @@
 // A block with byte 0xFF is NaN. bf16 queries enter as they are; fp32 queries
 // as the exact sum of three bf16 parts, and so do their softmax weights p. For
 // bf16 queries p is rounded to one bf16: the error is independent from token to
-// token, and of the size of the output's own rounding (0.0017 instead of 0.0016
-// root mean square over the output at 8 x 26 drafted tokens). Two parts cost a
-// third of the time where arithmetic counts: 708 against 583 us at 16 trees of
-// 64 tokens over up to 16384. The sum that normalises is that of the rounded
-// values, so one dominant token gives its V exactly. Maxima, sums and outputs
-// are fp32.
+// token, and of the size of the output's own rounding (together 0.0016 to 0.0022
+// root mean square of the output, by shape and inputs, where two parts give 0.0015
+// to 0.0018). Two parts cost 3 % in decode (100.4 against 97.7
+// us at 32 ragged sequences), 14 % at 8 x 26 drafted tokens (103 against 90.5) and
+// 18 % at 16 x 64 (556 against 470). A caller who wants whole weights passes the
+// same queries as fp32 (8 sequences of 8192 tokens: 36 against 28 us). The sum
+// that normalises is that of the rounded values, so one dominant token gives its V
+// exactly. Maxima, sums and outputs are fp32.
 //
 // Kernels, by the rows n G of a KV head (tree_plan; bf16 / fp32 queries):
 //   k_tree_rows  up to 16 (D <= 128, large batches: 32) / 16: every wave its own
 //                tokens
 //   k_tree_tile  up to 128 / 64, D > 128: four waves share stages in LDS
 //   k_tree_pair  more: eight waves share stages and take turns
+// One kernel serves a call, chosen by max_q: a prompt chunk among decoding
+// sequences puts those into its tiles too (31 single tokens on 4096 and a chunk of
+// 512: 315 us together, 45 + 135 in two calls).
 // A device-side schedule (below) cuts the work into equal shares.
-// Measured (MI355X, 8 KV heads, D = 128, pages of 64 tokens):
+// Measured (MI355X, 8 KV heads, D = 128, pages of 64 tokens; bf16, fp32 queries):
 //   32 sequences, one token, 4 query heads a KV head, 4915 to 16384 cached
 //   tokens: 96 us, 3.9 TB/s of codes and scales (loads alone: 88 us)
-//   one sequence of 8192, 32768 tokens, 8 query heads: 14.6, 26.8 us
+//   one sequence of 2048, 8192, 32768 tokens, 8 query heads: 13.4, 14.7, 27.0 us
+//   (15.4, 16.9, 31.6): the schedule and the join are most of the short ones
 //   8 x 26 drafted tokens, 8 query heads, up to 8192 tokens: 90 us, 368 TFLOP/s
-//   16 x 64, up to 16384 tokens: 475 us, 648 TFLOP/s; the LDS reads of the
-//   operands bound it (a wave reads the whole stage for 32 rows; 64 rows a wave
-//   need more registers than there are)
+//   (all of 8192: 100, 203 us)
+//   16 x 64, up to 16384 tokens: 470 us, 655 TFLOP/s (see k_tree_pair)
+//   chunk of 512 behind 8192: 209 us (415); 4096 from nothing: 1405 us (2398)
+// Registers: k_tree_rows of fp32 queries at D = 128 spills 28 bytes a lane (at
+// D = 96, 60), k_tree_tile of bf16 at D > 128 48; the others no vector registers,
+// all three kernels 76 to 157 scalar ones. 64 rows a wave (k_tree_tile with CT = 4)
+// would halve the LDS reads of the many-row kernels; in the present order of work
+// it spills 110 registers and is slower.
 #include <cmath>
 #include <type_traits>
 
@@ -67,7 +78,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 constexpr int kRowTiles = 2;         // 16-token tiles of a wave's step in k_tree_rows
-constexpr int kRowSets = 3;          // steps whose codes a wave holds or has in flight (one or two: within 2 %)
+constexpr int kRowSets = 3;          // steps whose codes a wave holds or has in flight (bf16: one or two within 2 %)
 constexpr int kNTL = 4;              // 16-token tiles of a stage in k_tree_tile
 constexpr int kStep = 16 * kNTL;     // tokens of a stage
 
@@ -168,7 +179,11 @@ __device__ __forceinline__ float col_max(float x) {
 // no tokens has one empty unit a tile, which writes its zeros). It is cut into
 // P' equal shares, one a workgroup, from the lengths that the call finds on the
 // device: ragged batches are balanced, and a captured graph stays so when its
-// lengths change. A tile that lies in one share is written to `out`; the
+// lengths change. Every row tile of a sequence has the units of its whole length:
+// where there is no mask, tokens past a tile's last row are computed and hidden,
+// so a prompt from nothing does twice the work that its rows see (196 TFLOP/s of
+// the seen pairs at 4096 tokens, 679 for a chunk of 512 behind 8192).
+// A tile that lies in one share is written to `out`; the
 // pieces of the others go to the workspace (a share has at most two: the end of
 // a tile, k = 0, and the start of one, k = 1) and k_tree_join adds them.
 struct Seq {
@@ -1238,8 +1253,12 @@ __global__ __launch_bounds__(256, NDP == 8 ? 1 : 2) void k_tree_tile(TreeArgs a)
 // 16 x 64 drafted tokens over up to 16384 (8 query heads): four waves without
 // turns 500 us; eight waves without turns, one barrier a stage, 488; turns 516,
 // with the matrix half's waves first in issue 470; on a slower card 500, with the
-// next stage's tiles written before the softmax 474. Of a turn of 5900 cycles
-// the operands' LDS reads (256 KiB a stage) take most.
+// next stage's tiles written before the softmax 474. No unit is near its limit:
+// of the call's 1.03 million cycles the matrix cores are busy in 37 %, the vector
+// ALU issues in at most 53 %, LDS serves the operands (256 KiB a stage) in 27 %.
+// The phases overlap too little. Waves whose rows lie past the tile's end go
+// through the same work (8 x 26 drafted tokens: 208 rows at most in tiles of 256,
+// 31 % of the cycles matrix, 50 % vector, 22 % LDS).
 template <int NDP, int CT, int PARTS>
 __global__ __launch_bounds__(512) void k_tree_pair(TreeArgs a) {
     constexpr int PP = PARTS, NT = 2 * NDP, NTW = kNTL;
