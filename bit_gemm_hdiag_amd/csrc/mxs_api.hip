@@ -556,7 +556,8 @@ mxs_status mxs_kv4_read(const mxs_kv4_cache *cache, const int64_t *slots, int64_
 size_t mxs_attend_kv4_tree_workspace(mxs_dtype dtype, int64_t B, int64_t total_q, int64_t max_q, int64_t max_len,
                                      int64_t Hq, int64_t Hkv, int64_t D) {
     if (!dtype_ok(dtype) || B <= 0 || total_q <= 0 || max_q <= 0 || max_len < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv ||
-        D < 32 || D % 32 || past_tree_limits(B, total_q, max_q, max_len, Hq, D))
+        D < 32 || D % 32 || past_tree_limits(B, total_q, max_q, max_len, Hq, D) ||
+        !mxs::attend_kv4_tree_supported(dtype, B, max_q, max_len, Hq, Hkv, D))
         return 0;
     return mxs::attend_kv4_tree_workspace(dtype, B, max_q, max_len, Hq, Hkv, D);
 }

@@ -244,7 +244,7 @@ def test_work_that_wraps_64_bits_is_refused(lib):
                     assert call(B, heads, heads, max_q, 1 << 30, dt) == UNSUPPORTED, (dt, B, heads, max_q)
     w = lib.mxs_attend_kv4_tree_workspace
     big = (1 << 63) - 1
-    assert w(1, 1, 1, 1 << 20, 1 << 30, 65535, 1, 32) > 0
+    assert w(1, 1, 1, 1 << 14, 1 << 30, 65535, 1, 32) == 0 and w(1, 1, 1, 1 << 10, 1 << 16, 65535, 1, 32) > 0
     for bad in ((1, big, 1, 1, 1 << 30, 4, 2, 64), (1, 1, big, 1, 1 << 30, 4, 2, 64), (1, 1, 1, big, 1 << 30, 4, 2, 64),
                 (1, 1, 1, 1, big, 4, 2, 64), (1, 1, 1, 1, 1 << 30, big - 1, 2, 64), (1, 1, 1, 1, 1 << 30, big, big, 64)):
         assert w(*bad) == 0                                       # sizes that the call refuses
