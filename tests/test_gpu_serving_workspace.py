@@ -87,3 +87,36 @@ def test_two_threads_on_one_stream(mx):
     assert not failed
     for got, ref in zip(outs, refs):
         assert all(torch.equal(o, ref) for o in got)
+
+
+@pytest.mark.parametrize("B,n,Hq,Hkv,D", [(70, 9, 16, 4, 64), (150, 1, 4, 4, 128), (5, 40, 8, 2, 128)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_graph_replays_of_ragged_batches(mx, dtype, B, n, Hq, Hkv, D):
+    """Captured once; lengths, query counts and the workspace's bytes change between replays."""
+    L = 900
+    b = Batch(mx, [L] * B, [n] * B, Hq, Hkv, D, 16, dtype, "causal", B + D)
+    args = b.args()
+    need = mx.mxs_attend_kv4_tree_workspace(dtype, B, B * n, n, L, Hq, Hkv, D)
+    ws, ews = (torch.zeros(need, dtype=torch.uint8, device=DEV) for _ in range(2))
+    out, eager = torch.empty_like(b.q), torch.empty_like(b.q)
+    run = lambda o, w: mx.mxs_attend_kv4_tree(b.q, b.cache, out=o, ws=w, **args)
+    run(out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(out, ws)
+    rng = np.random.default_rng(B)
+    for rep, (lo, hi) in enumerate(((L, L), (0, 0), (0, L), (0, 70), (L - 3, L), (1, 2))):
+        lens = rng.integers(lo, hi + 1, B)
+        ns = np.minimum(rng.integers(0, n + 1, B), lens)
+        args["lens"].copy_(b.dev(lens))
+        args["cu"].copy_(b.dev(np.concatenate([[0], np.cumsum(ns)])))
+        for w, byte in ((ws, 0x80 + rep), (ews, 0)):
+            w.fill_(byte)
+        for o in (out, eager):
+            o.fill_(7.0)
+        graph.replay()
+        run(eager, ews)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), rep
+        assert bool((out[int(ns.sum()):] == 7.0).all())          # rows of no sequence
