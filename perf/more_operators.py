@@ -201,7 +201,7 @@ def _prepare_pages(case, g, cpu):
         path[int(cu[b]):int(cu[b]) + len(kept)] = torch.tensor(kept, dtype=torch.int32)
         count[b] = len(kept)
     st = dict(planes=_planes(pages, page, case["H"], case["D"], g), table=table.cuda(), lens=lens.cuda(),
-              refs=refs.cuda(), cu=cu.cuda(), path=path.cuda(), count=count.cuda(), max_n=max(ns),
+              refs=refs.cuda(), cu=cu.cuda(), path=path.cuda(), count=count.cuda(),
               src=torch.arange(F, dtype=torch.int32).cuda(), dst=torch.arange(B, rows, dtype=torch.int32).cuda(),
               keep=lens.cuda(), grown=torch.empty(rows, dtype=torch.int32, device="cuda"),
               kept=torch.empty(rows, dtype=torch.int32, device="cuda"),
@@ -366,10 +366,8 @@ def run(st):
     cache, refs, table = st["cache"], st["refs"], st["table"]
     if st["src"].numel():
         mx.mxs_kv4_fork(cache, refs, table, st["lens"], st["src"], st["dst"])
-    mx.mxs_kv4_reserve(cache, refs, table, st["lens"], st["cu"], max_n=st["max_n"], slots=st["slots"],
-                       lens_out=st["grown"], ws=st["ws"])
-    mx.mxs_kv4_compact(cache, table, st["grown"], st["cu"], st["path"], st["count"], max_n=st["max_n"],
-                       lens_out=st["kept"])
+    mx.mxs_kv4_reserve(cache, refs, table, st["lens"], st["cu"], slots=st["slots"], lens_out=st["grown"], ws=st["ws"])
+    mx.mxs_kv4_compact(cache, table, st["grown"], st["cu"], st["path"], st["count"], lens_out=st["kept"])
     mx.mxs_kv4_release(cache, refs, table, st["kept"], st["keep"], lens_out=st["left"])
     return [st["slots"], st["grown"], st["kept"], st["left"], refs, table, *st["planes"]]
 
