@@ -90,6 +90,12 @@ def _load():
         "mxs_kv4_append": (S, [P, P, P, c_int32, c_int64, c_int64, c_int64, c_int64, c_int64, P, P, P, c_int32, c_int32,
                                c_float, P]),
         "mxs_kv4_read": (S, [P, P, c_int64, c_int32, P, c_int64, c_int64, P, c_int64, c_int64, P]),
+        "mxs_kv4_copy": (S, [P, P, P, P, c_int64, P]),
+        "mxs_kv4_fork": (S, [P, P, P, c_int64, c_int64, P, P, P, c_int64, P]),
+        "mxs_kv4_reserve_workspace": (c_size_t, [c_int64, c_int64]),
+        "mxs_kv4_reserve": (S, [P, P, P, c_int64, c_int64, P, P, c_int64, P, P, P, c_size_t, P]),
+        "mxs_kv4_compact": (S, [P, P, c_int64, c_int64, P, P, P, P, c_int64, P, P]),
+        "mxs_kv4_release": (S, [P, P, P, c_int64, c_int64, P, P, P, P]),
         "mxs_attend_kv4_tree_workspace": (c_size_t, [c_int32] + [c_int64] * 7),
         "mxs_attend_kv4_tree": (S, [P, c_int32, c_int64, P, P, c_int64, P, P, P, c_int64, c_int64, c_int64, c_int64,
                                     c_int64, c_int64, c_float, P, c_int64, P, c_size_t, P]),
@@ -110,7 +116,8 @@ EXPORTED = ("mxs_status_string", "mxs_last_error", "mxs_version", "mxs_budget_bl
             "mxs_prepare_weights_size", "mxs_prepare_weights", "mxs_mixed_gemm_prepared_workspace",
             "mxs_mixed_gemm_prepared", "mxs_mixed_gemm_fused_prepared_workspace", "mxs_mixed_gemm_fused_prepared",
             "mxs_rope_frequencies", "mxs_rope", "mxs_kv4_append", "mxs_kv4_read", "mxs_attend_kv4_tree_workspace",
-            "mxs_attend_kv4_tree")
+            "mxs_attend_kv4_tree", "mxs_kv4_copy", "mxs_kv4_fork", "mxs_kv4_reserve_workspace", "mxs_kv4_reserve",
+            "mxs_kv4_compact", "mxs_kv4_release")
 
 
 def _check(status: int, where: str):
@@ -706,6 +713,115 @@ def mxs_kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torc
     _call(gpu, _lib.mxs_kv4_read, "mxs_kv4_read", cache._ref, _vector(slots, "slots", torch.int64, T, gpu), T,
           _dtype(k_out if keys else v_out), pk, kt, kh, pv, vt, vh)
     return k_out, v_out
+
+
+# ------------------------------------------------------------ pages of the cache
+def _table(cache: KV4Cache, table: torch.Tensor):
+    """(pointer, width, rows) of a page table."""
+    if table.dtype is not torch.int32 or table.dim() != 2 or table.get_device() != cache.gpu \
+            or not table.is_contiguous():
+        raise ValueError(f"table must be a contiguous int32 [B, pages] tensor on cuda:{cache.gpu}")
+    B, width = table.shape
+    return table.data_ptr(), width, B
+
+
+def _given_ws(ws, nbytes: int, gpu: int, dev):
+    """(tensor, pointer, bytes) of a workspace, allocated if the caller passes none."""
+    if ws is None:
+        return _workspace(nbytes, dev, None)
+    if ws.get_device() != gpu or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on cuda:{gpu}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def mxs_kv4_copy(dst: KV4Cache, dst_slots: torch.Tensor, src: KV4Cache, src_slots: torch.Tensor) -> None:
+    """Copies the tokens of src_slots [T] in one pool to dst_slots [T] in another
+    or the same (int64; pairs with a negative or too large slot are skipped).
+    Destinations are distinct and, in one pool, no token's source."""
+    gpu, T = dst.gpu, src_slots.numel()
+    if src.gpu != gpu:
+        raise ValueError("both pools must be on one GPU")
+    _call(gpu, _lib.mxs_kv4_copy, "mxs_kv4_copy", dst._ref, _vector(dst_slots, "dst_slots", torch.int64, T, gpu),
+          src._ref, _vector(src_slots, "src_slots", torch.int64, T, gpu), T)
+
+
+def mxs_kv4_fork(cache: KV4Cache, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, src: torch.Tensor,
+                 dst: torch.Tensor) -> None:
+    """Row dst[i] of the page table becomes a fork of row src[i]: the same pages
+    for its tokens (refs [pages] counts them), the same length. The rows dst
+    hold no pages before. table [B, pages], lens [B], src and dst [n] int32."""
+    gpu, n = cache.gpu, src.numel()
+    pt, width, B = _table(cache, table)
+    _call(gpu, _lib.mxs_kv4_fork, "mxs_kv4_fork", cache._ref,
+          _vector(refs, "refs", torch.int32, cache.kc.shape[0], gpu), pt, width, B,
+          _vector(lens, "lens", torch.int32, B, gpu), _vector(src, "src", torch.int32, n, gpu),
+          _vector(dst, "dst", torch.int32, n, gpu), n)
+
+
+def mxs_kv4_reserve_workspace(pages: int, B: int) -> int:
+    return int(_lib.mxs_kv4_reserve_workspace(pages, B))
+
+
+def mxs_kv4_reserve(cache: KV4Cache, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
+                    total: int | None = None, slots: torch.Tensor | None = None, lens_out: torch.Tensor | None = None,
+                    ws=None):
+    """(slots [total] int64, lens_out [B] int32): room for cu[b + 1] - cu[b] tokens
+    behind the lens[b] of every sequence, in the lowest free pages (refs 0) where
+    its row of the table has none or shares one (whose tokens are copied first).
+    slots are those of the new tokens, -1 where the pool or the row has no room
+    (that sequence is left as it was). total: the rows of slots, needed where the
+    call allocates them. lens_out may be lens."""
+    gpu, dev = cache.gpu, cache.kc.device
+    pt, width, B = _table(cache, table)
+    pages = cache.kc.shape[0]
+    if slots is None:
+        if total is None:
+            raise ValueError("total or slots must be given")
+        slots = torch.full((total,), -1, dtype=torch.int64, device=dev)
+    elif total is not None and total != slots.numel():
+        raise ValueError("slots must have total elements")
+    n = slots.numel()
+    if lens_out is None:
+        lens_out = torch.empty(B, dtype=torch.int32, device=dev)
+    ws, p, nbytes = _given_ws(ws, int(_lib.mxs_kv4_reserve_workspace(pages, B)), gpu, dev)
+    _call(gpu, _lib.mxs_kv4_reserve, "mxs_kv4_reserve", cache._ref, _vector(refs, "refs", torch.int32, pages, gpu), pt,
+          width, B, _vector(lens, "lens", torch.int32, B, gpu), _vector(cu, "cu", torch.int32, B + 1, gpu), n,
+          _vector(slots, "slots", torch.int64, n, gpu), _vector(lens_out, "lens_out", torch.int32, B, gpu), p, nbytes)
+    return slots, lens_out
+
+
+def mxs_kv4_compact(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor, path: torch.Tensor,
+                    count: torch.Tensor, lens_out: torch.Tensor | None = None) -> torch.Tensor:
+    """lens_out [B]: of the last cu[b + 1] - cu[b] tokens of every sequence, those
+    numbered path[cu[b]] .. path[cu[b] + count[b] - 1] (ascending) are moved together
+    behind the others, and the length ends there. path and count as
+    mxs_verify_tree returns them. lens_out may be lens."""
+    gpu = cache.gpu
+    pt, width, B = _table(cache, table)
+    total = path.numel()
+    if lens_out is None:
+        lens_out = torch.empty(B, dtype=torch.int32, device=cache.kc.device)
+    _call(gpu, _lib.mxs_kv4_compact, "mxs_kv4_compact", cache._ref, pt, width, B,
+          _vector(lens, "lens", torch.int32, B, gpu), _vector(cu, "cu", torch.int32, B + 1, gpu),
+          _vector(path, "path", torch.int32, total, gpu), _vector(count, "count", torch.int32, B, gpu), total,
+          _vector(lens_out, "lens_out", torch.int32, B, gpu))
+    return lens_out
+
+
+def mxs_kv4_release(cache: KV4Cache, refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, keep: torch.Tensor,
+                    lens_out: torch.Tensor | None = None) -> torch.Tensor:
+    """lens_out [B] = min(lens, keep): the pages behind the first keep[b] tokens of
+    every sequence are given back (0 frees it, a negative keep leaves it as it
+    is). lens_out may be lens."""
+    gpu = cache.gpu
+    pt, width, B = _table(cache, table)
+    if lens_out is None:
+        lens_out = torch.empty(B, dtype=torch.int32, device=cache.kc.device)
+    _call(gpu, _lib.mxs_kv4_release, "mxs_kv4_release", cache._ref,
+          _vector(refs, "refs", torch.int32, cache.kc.shape[0], gpu), pt, width, B,
+          _vector(lens, "lens", torch.int32, B, gpu), _vector(keep, "keep", torch.int32, B, gpu),
+          _vector(lens_out, "lens_out", torch.int32, B, gpu))
+    return lens_out
 
 
 # ------------------------------------------- attention of drafted tokens over it

@@ -603,4 +603,101 @@ mxs_status mxs_attend_kv4_tree(const void *q, mxs_dtype dtype, int64_t ldq, cons
                          "attend_kv4_tree");
 }
 
+// Sizes and pointers of a page table over a cache
+static mxs_status check_table(const mxs_kv4_cache *cache, const void *refs, bool with_refs, const void *table,
+                              int64_t ldt, int64_t B, const void *lens, const char *name) {
+    const mxs_status r = check_cache(cache, name);
+    if (r != MXS_OK) return r;
+    if (B < 0 || ldt < 0) return fail(MXS_ERR_SHAPE, "%s: B=%lld ldt=%lld", name, (long long)B, (long long)ldt);
+    if (B > 65535 || ldt > (1 << 30))
+        return fail(MXS_ERR_UNSUPPORTED, "%s: B=%lld ldt=%lld", name, (long long)B, (long long)ldt);
+    if (B > 0 && ((with_refs && !refs) || (ldt > 0 && !table) || !lens))
+        return fail(MXS_ERR_ARG, "%s: NULL pointer", name);
+    if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(lens, 4))
+        return fail(MXS_ERR_UNSUPPORTED, "%s: misaligned pointer", name);
+    return MXS_OK;
+}
+
+mxs_status mxs_kv4_copy(const mxs_kv4_cache *dst, const int64_t *dst_slots, const mxs_kv4_cache *src,
+                        const int64_t *src_slots, int64_t T, hipStream_t stream) {
+    mxs_status r = check_cache(dst, "kv4_copy");
+    if (r != MXS_OK || (r = check_cache(src, "kv4_copy")) != MXS_OK) return r;
+    if (T < 0 || dst->H != src->H || dst->D != src->D)
+        return fail(MXS_ERR_SHAPE, "kv4_copy: T=%lld, pools of %d x %d and %d x %d", (long long)T, src->H, src->D,
+                    dst->H, dst->D);
+    if (T > kMaxTokens) return fail(MXS_ERR_UNSUPPORTED, "kv4_copy: T=%lld", (long long)T);
+    if (T == 0) return ok();
+    if (!dst_slots || !src_slots) return fail(MXS_ERR_ARG, "kv4_copy: NULL pointer");
+    if (!aligned(dst_slots, 8) || !aligned(src_slots, 8))
+        return fail(MXS_ERR_UNSUPPORTED, "kv4_copy: misaligned pointer");
+    return device_status(mxs::launch_kv4_copy(*dst, dst_slots, *src, src_slots, T, stream), "kv4_copy");
+}
+
+mxs_status mxs_kv4_fork(const mxs_kv4_cache *cache, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
+                        int32_t *lens, const int32_t *src, const int32_t *dst, int64_t n, hipStream_t stream) {
+    const mxs_status r = check_table(cache, refs, true, table, ldt, B, lens, "kv4_fork");
+    if (r != MXS_OK) return r;
+    if (n < 0) return fail(MXS_ERR_SHAPE, "kv4_fork: n=%lld", (long long)n);
+    if (n > 65535) return fail(MXS_ERR_UNSUPPORTED, "kv4_fork: n=%lld", (long long)n);
+    if (n == 0 || B == 0) return ok();
+    if (!src || !dst) return fail(MXS_ERR_ARG, "kv4_fork: NULL pointer");
+    if (!aligned(src, 4) || !aligned(dst, 4)) return fail(MXS_ERR_UNSUPPORTED, "kv4_fork: misaligned pointer");
+    return device_status(mxs::launch_kv4_fork(*cache, refs, table, ldt, B, lens, src, dst, n, stream), "kv4_fork");
+}
+
+constexpr int64_t kMaxPages = 1 << 24;      // of a pool whose free pages are looked for
+
+size_t mxs_kv4_reserve_workspace(int64_t pages, int64_t B) {
+    if (pages < 1 || pages > kMaxPages || B < 1 || B > 65535) return 0;
+    return mxs::kv4_reserve_workspace(pages, B);
+}
+
+mxs_status mxs_kv4_reserve(const mxs_kv4_cache *cache, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
+                           const int32_t *lens, const int32_t *cu, int64_t total, int64_t *slots, int32_t *lens_out,
+                           void *ws, size_t ws_bytes, hipStream_t stream) {
+    const mxs_status r = check_table(cache, refs, true, table, ldt, B, lens, "kv4_reserve");
+    if (r != MXS_OK) return r;
+    if (total < 0) return fail(MXS_ERR_SHAPE, "kv4_reserve: total=%lld", (long long)total);
+    if (total > kMaxTokens || cache->pages > kMaxPages)
+        return fail(MXS_ERR_UNSUPPORTED, "kv4_reserve: total=%lld pages=%lld", (long long)total,
+                    (long long)cache->pages);
+    if (B == 0) return ok();
+    if (!cu || !lens_out || (total > 0 && !slots)) return fail(MXS_ERR_ARG, "kv4_reserve: NULL pointer");
+    if (!aligned(cu, 4) || !aligned(lens_out, 4) || !aligned(slots, 8))
+        return fail(MXS_ERR_UNSUPPORTED, "kv4_reserve: misaligned pointer");
+    const size_t need = mxs::kv4_reserve_workspace(cache->pages, B);
+    if (!ws || ws_bytes < need || !aligned(ws, 16))
+        return fail(MXS_ERR_WORKSPACE, "kv4_reserve: workspace of %zu bytes, needs %zu, 16-byte aligned", ws_bytes,
+                    need);
+    return device_status(mxs::launch_kv4_reserve(*cache, refs, table, ldt, B, lens, cu, total, slots, lens_out, ws,
+                                                 stream), "kv4_reserve");
+}
+
+mxs_status mxs_kv4_compact(const mxs_kv4_cache *cache, const int32_t *table, int64_t ldt, int64_t B,
+                           const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
+                           int64_t total, int32_t *lens_out, hipStream_t stream) {
+    const mxs_status r = check_table(cache, nullptr, false, table, ldt, B, lens, "kv4_compact");
+    if (r != MXS_OK) return r;
+    if (total < 0) return fail(MXS_ERR_SHAPE, "kv4_compact: total=%lld", (long long)total);
+    if (total > kMaxTokens) return fail(MXS_ERR_UNSUPPORTED, "kv4_compact: total=%lld", (long long)total);
+    if (B == 0) return ok();
+    if (!cu || !count || !lens_out || (total > 0 && !path)) return fail(MXS_ERR_ARG, "kv4_compact: NULL pointer");
+    if (!aligned(cu, 4) || !aligned(count, 4) || !aligned(path, 4) || !aligned(lens_out, 4))
+        return fail(MXS_ERR_UNSUPPORTED, "kv4_compact: misaligned pointer");
+    return device_status(mxs::launch_kv4_compact(*cache, table, ldt, B, lens, cu, path, count, total, lens_out,
+                                                 stream), "kv4_compact");
+}
+
+mxs_status mxs_kv4_release(const mxs_kv4_cache *cache, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
+                           const int32_t *lens, const int32_t *keep, int32_t *lens_out, hipStream_t stream) {
+    const mxs_status r = check_table(cache, refs, true, table, ldt, B, lens, "kv4_release");
+    if (r != MXS_OK) return r;
+    if (B == 0) return ok();
+    if (!keep || !lens_out) return fail(MXS_ERR_ARG, "kv4_release: NULL pointer");
+    if (!aligned(keep, 4) || !aligned(lens_out, 4))
+        return fail(MXS_ERR_UNSUPPORTED, "kv4_release: misaligned pointer");
+    return device_status(mxs::launch_kv4_release(*cache, refs, table, ldt, B, lens, keep, lens_out, stream),
+                         "kv4_release");
+}
+
 }  // extern "C"

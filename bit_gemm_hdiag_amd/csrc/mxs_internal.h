@@ -87,4 +87,19 @@ hipError_t launch_attend_kv4_tree(const void *q, mxs_dtype dt, int64_t ldq, cons
                                   int64_t max_len, int64_t Hq, float scale, void *out, int64_t ldo, void *ws,
                                   hipStream_t st);
 
+// pages of the cache (mxs_pages.hip)
+size_t kv4_reserve_workspace(int64_t pages, int64_t B);
+hipError_t launch_kv4_copy(const mxs_kv4_cache &dst, const int64_t *dst_slots, const mxs_kv4_cache &src,
+                           const int64_t *src_slots, int64_t T, hipStream_t st);
+hipError_t launch_kv4_fork(const mxs_kv4_cache &c, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
+                           int32_t *lens, const int32_t *src, const int32_t *dst, int64_t n, hipStream_t st);
+hipError_t launch_kv4_reserve(const mxs_kv4_cache &c, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
+                              const int32_t *lens, const int32_t *cu, int64_t total, int64_t *slots,
+                              int32_t *lens_out, void *ws, hipStream_t st);
+hipError_t launch_kv4_compact(const mxs_kv4_cache &c, const int32_t *table, int64_t ldt, int64_t B,
+                              const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
+                              int64_t total, int32_t *lens_out, hipStream_t st);
+hipError_t launch_kv4_release(const mxs_kv4_cache &c, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
+                              const int32_t *lens, const int32_t *keep, int32_t *lens_out, hipStream_t st);
+
 }  // namespace mxs

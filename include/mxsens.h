@@ -580,6 +580,100 @@ mxs_status mxs_attend_kv4_tree(const void *q, mxs_dtype dtype, int64_t ldq, cons
                                int64_t max_len, int64_t Hq, float scale, void *out, int64_t ldo, void *ws,
                                size_t ws_bytes, hipStream_t stream);
 
+/*
+ * Pages of the cache, for a server that gives sequences pages as they grow. The
+ * caller keeps, in device memory, the page table (table [B, ldt] int32: entry j of
+ * a row is the page of tokens j page_size .. (j + 1) page_size - 1; a negative
+ * entry, or one past the pool, is none), lens [B] int32 and refs [pages] int32:
+ * how many table entries hold each page. A page with 0 is free; a negative count
+ * keeps a page from being given out. A new pool has refs 0 and tables of -1. The
+ * calls below keep refs and table in step, on the device, so that a step of a
+ * server needs no copy to the host and can be captured. A row of no tokens may
+ * still hold pages (room for more); entries of one row, and of rows that were
+ * not forked from each other, name different pages.
+ */
+
+/*
+ * Tokens copied between pools: slot dst_slots[i] of dst receives the codes and
+ * scale bytes of slot src_slots[i] of src, as they are. dst and src may be one
+ * pool; then no destination is another token's source. Pairs with a negative or
+ * too large slot are skipped. Destinations differ from one another; a source may
+ * repeat. The pools have the same H and D. T < 2^24. T = 0 is a no-op.
+ * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE (T < 0, the caches' sizes, differing H or
+ * D), MXS_ERR_UNSUPPORTED (alignment, sizes), MXS_ERR_DEVICE.
+ */
+mxs_status mxs_kv4_copy(const mxs_kv4_cache *dst, const int64_t *dst_slots, const mxs_kv4_cache *src,
+                        const int64_t *src_slots, int64_t T, hipStream_t stream);
+
+/*
+ * Sequences forked: for every i < n, row dst[i] of the table receives the entries
+ * of row src[i] that hold tokens (j page_size < lens[src[i]]) and none behind
+ * them, refs counts one more for each, and lens[dst[i]] = lens[src[i]]. No token
+ * moves: mxs_kv4_reserve copies a shared page before it is written. Rows dst[i]
+ * hold no pages before the call (mxs_kv4_release), differ from one another and
+ * are no source; a source may repeat. Pairs with a row outside [0, B), or of a
+ * row with itself, are skipped. n = 0 is a no-op.
+ * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE (negative sizes), MXS_ERR_UNSUPPORTED (B or
+ * n > 65535, ldt > 2^30, alignment), MXS_ERR_DEVICE.
+ */
+mxs_status mxs_kv4_fork(const mxs_kv4_cache *cache, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
+                        int32_t *lens, const int32_t *src, const int32_t *dst, int64_t n, hipStream_t stream);
+
+/*
+ * Room for new tokens: sequence b is about to receive n = cu[b + 1] - cu[b] tokens
+ * behind its lens[b]. Every table entry of positions lens[b] .. lens[b] + n - 1
+ * that is empty, or whose page other sequences hold too, takes the lowest free
+ * page that no earlier entry took (sequences in order, then positions); refs of
+ * the new page is 1. A shared page that is replaced loses one reference, and its
+ * tokens before lens[b] are copied first. (Where all holders of a page write to
+ * it, each takes a copy and the page is free after the call.)
+ * slots[cu[b] + i] receives the slot of token lens[b] + i, for mxs_kv4_append and
+ * lens_out[b] = lens[b] + n, for mxs_attend_kv4_tree (lens_out may be lens).
+ * A sequence whose table row is too short (lens[b] + n > ldt page_size, or lens[b]
+ * < 0) is refused: its slots are -1, its table is left and lens_out[b] = lens[b].
+ * So is, once the free pages run out, the first sequence that they do not serve
+ * whole, and every later one that needs a page.
+ * cu: [B + 1] int32 ascending from 0, cu[B] <= total; slots: [total] int64, those of no
+ * sequence are left as they were. At most 2^24 pages, B <= 65535. ws: >=
+ * mxs_kv4_reserve_workspace(pages, B) bytes, 16-byte aligned, contents scratch.
+ * B = 0 is a no-op.
+ * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE (negative sizes), MXS_ERR_UNSUPPORTED
+ * (sizes, alignment), MXS_ERR_WORKSPACE, MXS_ERR_DEVICE.
+ */
+size_t mxs_kv4_reserve_workspace(int64_t pages, int64_t B);
+mxs_status mxs_kv4_reserve(const mxs_kv4_cache *cache, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
+                           const int32_t *lens, const int32_t *cu, int64_t total, int64_t *slots, int32_t *lens_out,
+                           void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The accepted tokens of a drafted tree moved together: of the last n = cu[b + 1]
+ * - cu[b] cached tokens of sequence b, number path[cu[b] + i] becomes number i for
+ * i < count[b] (as mxs_verify_tree leaves them: path ascends, path[cu[b]] is the
+ * root's 0), and lens_out[b] = lens[b] - n + count[b]; lens_out may be lens. The
+ * pages behind stay with the sequence as room for the next step. A path that
+ * does not ascend leaves an unspecified order, entries outside [i, n) and
+ * tokens in no page are skipped; counts are taken between 0 and n. A sequence
+ * with fewer than n cached tokens is left as it is, lens_out[b] = lens[b]. Tokens
+ * are moved where they lie: the pages of the last n tokens are not shared (as
+ * mxs_kv4_reserve leaves them). path: [total] int32, cu as above.
+ * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE, MXS_ERR_UNSUPPORTED (B > 65535, ldt > 2^30,
+ * alignment), MXS_ERR_DEVICE.
+ */
+mxs_status mxs_kv4_compact(const mxs_kv4_cache *cache, const int32_t *table, int64_t ldt, int64_t B,
+                           const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
+                           int64_t total, int32_t *lens_out, hipStream_t stream);
+
+/*
+ * Pages given back: every page of row b behind the first keep[b] tokens (entries
+ * j with j page_size >= keep[b]) loses one reference and its entry becomes -1;
+ * lens_out[b] = min(lens[b], keep[b]) (lens_out may be lens). keep 0 frees the
+ * sequence, keep = lens gives back unused room; a negative keep leaves row and
+ * length as they are.
+ * Errors: as mxs_kv4_fork.
+ */
+mxs_status mxs_kv4_release(const mxs_kv4_cache *cache, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
+                           const int32_t *lens, const int32_t *keep, int32_t *lens_out, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
