@@ -96,6 +96,9 @@ def _load():
         "mxs_kv4_reserve": (S, [P, P, P, c_int64, c_int64, P, P, c_int64, P, P, P, c_size_t, P]),
         "mxs_kv4_compact": (S, [P, P, c_int64, c_int64, P, P, P, P, c_int64, P, P]),
         "mxs_kv4_release": (S, [P, P, P, c_int64, c_int64, P, P, P, P]),
+        "mxs_verify_tree_workspace": (c_size_t, [c_int64] * 4),
+        "mxs_verify_tree": (S, [P, c_int32, c_int64, c_int64, P, P, P, c_int64, c_int64, c_int64, P, c_int64, c_int32,
+                                P, P, P, P, P, P, c_size_t, P]),
         "mxs_attend_kv4_tree_workspace": (c_size_t, [c_int32] + [c_int64] * 7),
         "mxs_attend_kv4_tree": (S, [P, c_int32, c_int64, P, P, c_int64, P, P, P, c_int64, c_int64, c_int64, c_int64,
                                     c_int64, c_int64, c_float, P, c_int64, P, c_size_t, P]),
@@ -117,7 +120,7 @@ EXPORTED = ("mxs_status_string", "mxs_last_error", "mxs_version", "mxs_budget_bl
             "mxs_mixed_gemm_prepared", "mxs_mixed_gemm_fused_prepared_workspace", "mxs_mixed_gemm_fused_prepared",
             "mxs_rope_frequencies", "mxs_rope", "mxs_kv4_append", "mxs_kv4_read", "mxs_attend_kv4_tree_workspace",
             "mxs_attend_kv4_tree", "mxs_kv4_copy", "mxs_kv4_fork", "mxs_kv4_reserve_workspace", "mxs_kv4_reserve",
-            "mxs_kv4_compact", "mxs_kv4_release")
+            "mxs_kv4_compact", "mxs_kv4_release", "mxs_verify_tree_workspace", "mxs_verify_tree")
 
 
 def _check(status: int, where: str):
@@ -881,3 +884,66 @@ def mxs_attend_kv4_tree(q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, l
           _vector(lens, "lens", torch.int32, B, gpu), _vector(cu, "cu", torch.int32, B + 1, gpu), pm, words, B, total,
           max_q, max_len, Hq, scale, po, ot, p, n)
     return out
+
+
+# ------------------------------------------------- verification of drafted tokens
+def mxs_verify_tree_workspace(B: int, total: int, max_n: int, V: int) -> int:
+    return int(_lib.mxs_verify_tree_workspace(B, total, max_n, V))
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, gpu: int):
+    """(pointer, row stride) of a [rows, cols] tensor on that GPU with adjacent columns."""
+    if t.dim() != 2 or t.shape != (rows, cols) or t.get_device() != gpu or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a [{rows}, {cols}] tensor on cuda:{gpu} with unit column stride")
+    return t.data_ptr(), t.stride(0)
+
+
+def mxs_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, cu: torch.Tensor, uniform: torch.Tensor,
+                    parents: torch.Tensor | None = None, draft: torch.Tensor | None = None, replacement: bool = False,
+                    temperature: torch.Tensor | None = None, max_n: int | None = None,
+                    path: torch.Tensor | None = None, count: torch.Tensor | None = None,
+                    next_token: torch.Tensor | None = None, ws=None):
+    """(path int32 [total], count int32 [B], next_token int64 [B]): drafted tokens
+    accepted or rejected against the target's logits [total, V] (bf16 or fp32), so
+    that every token is distributed as the target alone would draw it.
+
+    Rows cu[b] .. cu[b + 1] - 1 (cu int32 [B + 1]) are the nodes of sequence b: its
+    last token, then the drafted ones, tokens [total] (int64) below parents [total]
+    (int32, counted within the sequence; None: a chain). draft [total, V] (fp32):
+    row i is the distribution from which the children of node i were drawn, without
+    replacement unless `replacement` is set; None: they were proposed without one.
+    temperature [B] (fp32; 0: greedy; None: 1). uniform [total] (fp64, in [0, 1)):
+    the number that decides on each node; the root's draws the next token. max_n
+    bounds a sequence's nodes (default: total, and at most 1024).
+    path holds the kept nodes of each sequence, the root first, then -1; count
+    their number; next_token what follows the last of them."""
+    gpu = _gpu(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be a [total, V] tensor")
+    total, V = logits.shape
+    pl, ldl = _matrix(logits, "logits", total, V, gpu)
+    dt, dev, B = _dtype(logits), logits.device, cu.numel() - 1
+    if B < 0:
+        raise ValueError("cu must have B + 1 elements")
+    pd, ldd = None, 0
+    if draft is not None:
+        if draft.dtype is not torch.float32:
+            raise TypeError("draft must be fp32")
+        pd, ldd = _matrix(draft, "draft", total, V, gpu)
+    if max_n is None:
+        max_n = total
+    if path is None:
+        path = torch.full((total,), -1, dtype=torch.int32, device=dev)
+    if count is None:
+        count = torch.empty(B, dtype=torch.int32, device=dev)
+    if next_token is None:
+        next_token = torch.empty(B, dtype=torch.int64, device=dev)
+    ws, p, n = _given_ws(ws, int(_lib.mxs_verify_tree_workspace(B, total, max_n, V)), gpu, dev)
+    _call(gpu, _lib.mxs_verify_tree, "mxs_verify_tree", pl, dt, ldl, V,
+          _vector(tokens, "tokens", torch.int64, total, gpu),
+          None if parents is None else _vector(parents, "parents", torch.int32, total, gpu),
+          _vector(cu, "cu", torch.int32, B + 1, gpu), B, total, max_n, pd, ldd, int(bool(replacement)),
+          None if temperature is None else _vector(temperature, "temperature", torch.float32, B, gpu),
+          _vector(uniform, "uniform", torch.float64, total, gpu), _vector(path, "path", torch.int32, total, gpu),
+          _vector(count, "count", torch.int32, B, gpu), _vector(next_token, "next_token", torch.int64, B, gpu), p, n)
+    return path, count, next_token

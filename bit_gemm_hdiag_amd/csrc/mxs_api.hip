@@ -700,4 +700,44 @@ mxs_status mxs_kv4_release(const mxs_kv4_cache *cache, int32_t *refs, int32_t *t
                          "kv4_release");
 }
 
+constexpr int64_t kMaxVocab = 1 << 20, kMaxNodeRows = 1 << 22, kMaxTree = 1024;
+
+size_t mxs_verify_tree_workspace(int64_t B, int64_t total, int64_t max_n, int64_t V) {
+    if (B < 1 || B > 65535 || total < 0 || total > kMaxNodeRows || max_n < 0 || max_n > kMaxTree || V < 1 ||
+        V > kMaxVocab)
+        return 0;
+    return mxs::verify_tree_workspace(B, total, V);
+}
+
+mxs_status mxs_verify_tree(const void *logits, mxs_dtype dtype, int64_t ldl, int64_t V, const int64_t *tokens,
+                           const int32_t *parents, const int32_t *cu, int64_t B, int64_t total, int64_t max_n,
+                           const float *draft, int64_t ldd, int32_t replacement, const float *temperature,
+                           const double *uniform, int32_t *path, int32_t *count, int64_t *next, void *ws,
+                           size_t ws_bytes, hipStream_t stream) {
+    if (!dtype_ok(dtype)) return fail(MXS_ERR_ARG, "verify_tree: unknown dtype %d", (int)dtype);
+    if (replacement != 0 && replacement != 1)
+        return fail(MXS_ERR_ARG, "verify_tree: replacement %d is neither 0 nor 1", (int)replacement);
+    if (B < 0 || total < 0 || max_n < 0 || V < 1 || (total > 1 && (ldl < V || (draft && ldd < V))) ||
+        ldl > ((int64_t)1 << 40) || (draft && ldd > ((int64_t)1 << 40)))
+        return fail(MXS_ERR_SHAPE, "verify_tree: B=%lld total=%lld max_n=%lld V=%lld ldl=%lld ldd=%lld", (long long)B,
+                    (long long)total, (long long)max_n, (long long)V, (long long)ldl, (long long)ldd);
+    if (B > 65535 || total > kMaxNodeRows || max_n > kMaxTree || V > kMaxVocab)
+        return fail(MXS_ERR_UNSUPPORTED, "verify_tree: B=%lld total=%lld max_n=%lld V=%lld", (long long)B,
+                    (long long)total, (long long)max_n, (long long)V);
+    if (B == 0) return ok();
+    if (!cu || !count || !next || (total > 0 && (!logits || !tokens || !uniform || !path)))
+        return fail(MXS_ERR_ARG, "verify_tree: NULL pointer");
+    if (!aligned(logits, dtype == MXS_BF16 ? 2 : 4) || !aligned(tokens, 8) || !aligned(parents, 4) ||
+        !aligned(cu, 4) || !aligned(draft, 4) || !aligned(temperature, 4) || !aligned(uniform, 8) ||
+        !aligned(path, 4) || !aligned(count, 4) || !aligned(next, 8))
+        return fail(MXS_ERR_UNSUPPORTED, "verify_tree: misaligned pointer");
+    const size_t need = mxs::verify_tree_workspace(B, total, V);
+    if (!ws || ws_bytes < need || !aligned(ws, 16))
+        return fail(MXS_ERR_WORKSPACE, "verify_tree: workspace of %zu bytes, needs %zu, 16-byte aligned", ws_bytes,
+                    need);
+    return device_status(mxs::launch_verify_tree(logits, dtype, ldl, V, tokens, parents, cu, B, total, max_n, draft,
+                                                 ldd, replacement, temperature, uniform, path, count, next, ws,
+                                                 stream), "verify_tree");
+}
+
 }  // extern "C"

@@ -102,4 +102,12 @@ hipError_t launch_kv4_compact(const mxs_kv4_cache &c, const int32_t *table, int6
 hipError_t launch_kv4_release(const mxs_kv4_cache &c, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
                               const int32_t *lens, const int32_t *keep, int32_t *lens_out, hipStream_t st);
 
+// verification of drafted tokens (mxs_verify.hip)
+size_t verify_tree_workspace(int64_t B, int64_t total, int64_t V);
+hipError_t launch_verify_tree(const void *logits, mxs_dtype dt, int64_t ldl, int64_t V, const int64_t *tokens,
+                              const int32_t *parents, const int32_t *cu, int64_t B, int64_t total, int64_t max_n,
+                              const float *draft, int64_t ldd, int32_t replacement, const float *temperature,
+                              const double *uniform, int32_t *path, int32_t *count, int64_t *next, void *ws,
+                              hipStream_t st);
+
 }  // namespace mxs
