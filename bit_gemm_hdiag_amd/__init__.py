@@ -13,7 +13,8 @@ _BINDING_NAMES = None
 
 def __getattr__(name):
     if name.startswith("mxs_") or name in ("MxsError", "QMat", "qmat_alloc", "library_path",
-                                          "STATUS", "NOALLOC_SCRATCH_BYTES", "KV4Cache", "kv4_cache_alloc"):
+                                          "STATUS", "NOALLOC_SCRATCH_BYTES", "KV4Cache", "kv4_cache_alloc",
+                                          "LoraSet"):
         from . import binding
         globals()[name] = value = getattr(binding, name)     # found directly from now on
         return value

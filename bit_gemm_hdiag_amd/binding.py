@@ -36,6 +36,11 @@ class _QMat(Structure):
                 ("q4", c_void_p), ("ld4", c_int64), ("sc", c_void_p), ("lds", c_int64)]
 
 
+class _Lora(Structure):
+    _fields_ = [("K", c_int64), ("N", c_int64), ("n", c_int32), ("R", c_int32), ("dtype", c_int32),
+                ("reserved", c_int32), ("A", c_void_p), ("B", c_void_p), ("scale", c_void_p), ("rank", c_void_p)]
+
+
 class _Kv4Cache(Structure):
     _fields_ = [("pages", c_int64), ("page_size", c_int32), ("H", c_int32), ("D", c_int32), ("reserved", c_int32),
                 ("kc", c_void_p), ("ks", c_void_p), ("vc", c_void_p), ("vs", c_void_p)]
@@ -99,6 +104,8 @@ def _load():
         "mxs_verify_tree_workspace": (c_size_t, [c_int64] * 4),
         "mxs_verify_tree": (S, [P, c_int32, c_int64, c_int64, P, P, P, c_int64, c_int64, c_int64, P, c_int64, c_int32,
                                 P, P, P, P, P, P, c_size_t, P]),
+        "mxs_lora_add_workspace": (c_size_t, [c_int64, P]),
+        "mxs_lora_add": (S, [P, c_int64, c_int64, P, P, P, c_int64, P, c_size_t, P]),
         "mxs_attend_kv4_tree_workspace": (c_size_t, [c_int32] + [c_int64] * 7),
         "mxs_attend_kv4_tree": (S, [P, c_int32, c_int64, P, P, c_int64, P, P, P, c_int64, c_int64, c_int64, c_int64,
                                     c_int64, c_int64, c_float, P, c_int64, P, c_size_t, P]),
@@ -120,7 +127,8 @@ EXPORTED = ("mxs_status_string", "mxs_last_error", "mxs_version", "mxs_budget_bl
             "mxs_mixed_gemm_prepared", "mxs_mixed_gemm_fused_prepared_workspace", "mxs_mixed_gemm_fused_prepared",
             "mxs_rope_frequencies", "mxs_rope", "mxs_kv4_append", "mxs_kv4_read", "mxs_attend_kv4_tree_workspace",
             "mxs_attend_kv4_tree", "mxs_kv4_copy", "mxs_kv4_fork", "mxs_kv4_reserve_workspace", "mxs_kv4_reserve",
-            "mxs_kv4_compact", "mxs_kv4_release", "mxs_verify_tree_workspace", "mxs_verify_tree")
+            "mxs_kv4_compact", "mxs_kv4_release", "mxs_verify_tree_workspace", "mxs_verify_tree",
+            "mxs_lora_add_workspace", "mxs_lora_add")
 
 
 def _check(status: int, where: str):
@@ -947,3 +955,51 @@ def mxs_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, cu: torch.Tensor
           _vector(uniform, "uniform", torch.float64, total, gpu), _vector(path, "path", torch.int32, total, gpu),
           _vector(count, "count", torch.int32, B, gpu), _vector(next_token, "next_token", torch.int64, B, gpu), p, n)
     return path, count, next_token
+
+
+# ------------------------------------------- adapters beside a shared projection
+@dataclass(frozen=True)
+class LoraSet:
+    """Low-rank adapters of one linear layer (see mxs_lora): A [n, R, K] and B
+    [n, N, R] (bf16 or fp32), scale fp32 [n] (None: 1), rank int32 [n] (None: R),
+    contiguous, on one GPU. Frozen: checked and its C struct built once."""
+    A: torch.Tensor
+    B: torch.Tensor
+    scale: torch.Tensor | None = None
+    rank: torch.Tensor | None = None
+
+    def __post_init__(self):
+        A, B = self.A, self.B
+        gpu = _gpu(A, "A")
+        if A.dim() != 3 or B.dim() != 3 or B.dtype is not A.dtype or B.get_device() != gpu \
+                or not A.is_contiguous() or not B.is_contiguous():
+            raise ValueError("A [n, R, K] and B [n, N, R] must be contiguous tensors of one type on one GPU")
+        n, R, K = A.shape
+        N = B.shape[1]
+        if B.shape[0] != n or B.shape[2] != R:
+            raise ValueError("A [n, R, K] and B [n, N, R] do not match")
+        c = _Lora(K, N, _int32(n, "n"), _int32(R, "R"), _dtype(A), 0, _ptr(A), _ptr(B),
+                  None if self.scale is None else _vector(self.scale, "scale", torch.float32, n, gpu),
+                  None if self.rank is None else _vector(self.rank, "rank", torch.int32, n, gpu))
+        for k, v in (("_c", c), ("_ref", ctypes.pointer(c)), ("gpu", gpu), ("K", K), ("N", N)):
+            object.__setattr__(self, k, v)
+
+
+def mxs_lora_add_workspace(M: int, adapters: LoraSet) -> int:
+    return int(_lib.mxs_lora_add_workspace(M, adapters._ref))
+
+
+def mxs_lora_add(Y: torch.Tensor, X: torch.Tensor, ids: torch.Tensor, adapters: LoraSet, ws=None) -> torch.Tensor:
+    """Y[t] += scale[a] B[a] (A[a] X[t]) with a = ids[t] (int32 [M]; outside the
+    set: the row is left as it was). X [M, K] of the adapters' type, Y [M, N] fp32,
+    as mxs_mixed_gemm writes it. Returns Y."""
+    gpu = adapters.gpu
+    M = ids.numel()
+    if X.dtype is not adapters.A.dtype or Y.dtype is not torch.float32:
+        raise TypeError("X must have the adapters' type, and Y must be fp32")
+    px, ldx = _matrix(X, "X", M, adapters.K, gpu)
+    py, ldy = _matrix(Y, "Y", M, adapters.N, gpu)
+    ws, p, n = _given_ws(ws, int(_lib.mxs_lora_add_workspace(M, adapters._ref)), gpu, Y.device)
+    _call(gpu, _lib.mxs_lora_add, "mxs_lora_add", px, M, ldx, _vector(ids, "ids", torch.int32, M, gpu), adapters._ref, py,
+          ldy, p, n)
+    return Y

@@ -16,7 +16,7 @@ LIB = os.path.join(OUT_DIR, "libmxsens.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["mxs_colsum.hip", "mxs_allocate.hip", "mxs_quantize.hip", "mxs_gemm.hip", "mxs_layerwise.hip", "mxs_attention.hip",
-           "mxs_kvcache.hip", "mxs_pages.hip", "mxs_verify.hip",
+           "mxs_kvcache.hip", "mxs_pages.hip", "mxs_verify.hip", "mxs_lora.hip",
            "mxs_tree_attention.hip", "mxs_api.hip"]
 # packed fp32 instructions are disabled for all device code; common-code
 # sinking is off because merging the tails of per-width branches turned

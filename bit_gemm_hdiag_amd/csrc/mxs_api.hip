@@ -740,4 +740,43 @@ mxs_status mxs_verify_tree(const void *logits, mxs_dtype dtype, int64_t ldl, int
                                                  stream), "verify_tree");
 }
 
+// Sizes of a set of adapters and of the rows they are added to
+static bool lora_shape(const mxs_lora *s, int64_t M) {
+    return s->K > 0 && s->K % 32 == 0 && s->N >= 0 && s->n >= 0 && s->R > 0 && M >= 0;
+}
+static bool lora_past_limits(const mxs_lora *s, int64_t M) {
+    return s->R > 128 || s->n > 8192 || M > ((int64_t)1 << 22) || s->K > ((int64_t)1 << 24) ||
+           s->N > ((int64_t)1 << 24);
+}
+
+size_t mxs_lora_add_workspace(int64_t M, const mxs_lora *set) {
+    if (!set || !dtype_ok((mxs_dtype)set->dtype) || !lora_shape(set, M) || lora_past_limits(set, M) || M == 0 ||
+        set->N == 0 || set->n == 0)
+        return 0;
+    return mxs::lora_add_workspace(M, *set);
+}
+
+mxs_status mxs_lora_add(const void *X, int64_t M, int64_t ldx, const int32_t *ids, const mxs_lora *set, float *Y,
+                        int64_t ldy, void *ws, size_t ws_bytes, hipStream_t stream) {
+    if (!set) return fail(MXS_ERR_ARG, "lora_add: set is NULL");
+    if (set->reserved != 0) return fail(MXS_ERR_ARG, "lora_add: reserved field must be 0");
+    if (!dtype_ok((mxs_dtype)set->dtype)) return fail(MXS_ERR_ARG, "lora_add: unknown dtype %d", (int)set->dtype);
+    if (!lora_shape(set, M) || (M > 1 && (ldx < set->K || ldy < set->N)) || ldx > ((int64_t)1 << 40) ||
+        ldy > ((int64_t)1 << 40))
+        return fail(MXS_ERR_SHAPE, "lora_add: M=%lld K=%lld N=%lld n=%d R=%d ldx=%lld ldy=%lld", (long long)M,
+                    (long long)set->K, (long long)set->N, set->n, set->R, (long long)ldx, (long long)ldy);
+    if (lora_past_limits(set, M))
+        return fail(MXS_ERR_UNSUPPORTED, "lora_add: M=%lld K=%lld N=%lld n=%d R=%d", (long long)M, (long long)set->K,
+                    (long long)set->N, set->n, set->R);
+    if (M == 0 || set->N == 0 || set->n == 0) return ok();
+    if (!X || !ids || !Y || !set->A || !set->B) return fail(MXS_ERR_ARG, "lora_add: NULL pointer");
+    if (!aligned(X, set->dtype == MXS_BF16 ? 2 : 4) || !aligned(ids, 4) || !aligned(Y, 4) || !aligned(set->A, 16) ||
+        !aligned(set->B, 16) || !aligned(set->scale, 4) || !aligned(set->rank, 4))
+        return fail(MXS_ERR_UNSUPPORTED, "lora_add: misaligned pointer");
+    const size_t need = mxs::lora_add_workspace(M, *set);
+    if (!ws || ws_bytes < need || !aligned(ws, 256))
+        return fail(MXS_ERR_WORKSPACE, "lora_add: workspace of %zu bytes, needs %zu, 256-byte aligned", ws_bytes, need);
+    return device_status(mxs::launch_lora_add(X, M, ldx, ids, *set, Y, ldy, ws, stream), "lora_add");
+}
+
 }  // extern "C"

@@ -110,4 +110,9 @@ hipError_t launch_verify_tree(const void *logits, mxs_dtype dt, int64_t ldl, int
                               const double *uniform, int32_t *path, int32_t *count, int64_t *next, void *ws,
                               hipStream_t st);
 
+// low-rank adapters (mxs_lora.hip)
+size_t lora_add_workspace(int64_t M, const mxs_lora &set);
+hipError_t launch_lora_add(const void *X, int64_t M, int64_t ldx, const int32_t *ids, const mxs_lora &set, float *Y,
+                           int64_t ldy, void *ws, hipStream_t st);
+
 }  // namespace mxs

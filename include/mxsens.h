@@ -721,6 +721,47 @@ mxs_status mxs_verify_tree(const void *logits, mxs_dtype dtype, int64_t ldl, int
                            const double *uniform, int32_t *path, int32_t *count, int64_t *next, void *ws,
                            size_t ws_bytes, hipStream_t stream);
 
+/*
+ * Low-rank adapters of one linear layer, for the requests of a batch: adapter a
+ * adds scale[a] B[a] A[a] to the shared weight. A: [n, R, K], B: [n, N, R],
+ * contiguous, of `dtype`, 16-byte aligned; scale: [n] fp32 or NULL (1); rank: [n]
+ * int32 or NULL (R): adapter a uses its first rank[a] rows of A and columns of B
+ * (taken between 0 and R); what lies behind them does not matter. Device memory
+ * owned by the caller. Host struct, read during the call.
+ */
+typedef struct mxs_lora {
+    int64_t K, N;
+    int32_t n, R;       /* adapters (at most 8192), stored rank (at most 128) */
+    int32_t dtype;      /* mxs_dtype of A and B, and of the X they multiply   */
+    int32_t reserved;   /* must be 0                                          */
+    const void *A, *B;
+    const float *scale;
+    const int32_t *rank;
+} mxs_lora;
+
+/*
+ * Adapters beside a shared projection: with a = ids[t],
+ *     Y[t] += scale[a] B[a] (A[a] X[t]);
+ * rows whose id is outside [0, n), or of rank 0, are left as they were. Y is the
+ * fp32 output of the mxs_mixed_gemm calls over the same tokens; X is the layer's
+ * input in its own channel order (no permutation) and does not overlap Y. Exact
+ * products of the inputs with fp32 sums; A X is kept in fp32 (it enters the bf16
+ * matrix cores as exact three-part sums) and the result is scaled and added in
+ * fp32. Every sum has an order fixed by the sizes: the result is deterministic,
+ * and what the other rows hold does not change a row (their number moves the
+ * split of K, and with it the rounding).
+ * X: [M, ldx >= K] of set->dtype; ids: [M] int32; Y: [M, ldy >= N] fp32 (rows of
+ * 16-byte alignment are faster, as are ranks of whole 16-byte vectors). K % 32
+ * == 0, M <= 2^22. ws: >= mxs_lora_add_workspace bytes (0 for sizes that the
+ * call refuses), 256-byte aligned, contents scratch; calls that may overlap need
+ * one each. M = 0, N = 0 or n = 0 is a no-op.
+ * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE, MXS_ERR_UNSUPPORTED (sizes, alignment),
+ * MXS_ERR_WORKSPACE, MXS_ERR_DEVICE.
+ */
+size_t mxs_lora_add_workspace(int64_t M, const mxs_lora *set);
+mxs_status mxs_lora_add(const void *X, int64_t M, int64_t ldx, const int32_t *ids, const mxs_lora *set, float *Y,
+                        int64_t ldy, void *ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
