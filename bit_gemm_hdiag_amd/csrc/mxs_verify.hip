@@ -20,68 +20,179 @@ namespace mxs {
 
 namespace {
 
-constexpr int kWave = 1024;             // logits of a chunk: 16 of each lane
+constexpr int kPiece = 1024;            // logits of a wave: 16 of each lane
 constexpr int kMaxNodes = 1024;
+constexpr int kMaxChunks = 64;          // of a row: one of each lane
 
-// Element k of a lane's 16 is number 256 (k / 4) + 4 lane + k % 4 of the chunk
-__device__ __forceinline__ int chunk_index(int lane, int k) { return 256 * (k >> 2) + 4 * lane + (k & 3); }
+// A row is cut into at most 64 chunks of 4096 (up to 2^18 tokens) or 16384 logits.
+// The large ones are a tenth quicker to sum (57 against 64 us for 794 rows of 128000
+// bf16, half of them greedy) and twice as slow to draw from (22 against 13 us).
+inline int chunk_size(int64_t V) { return V <= 4096 * kMaxChunks ? 4096 : 16384; }
 
-// Four consecutive logits at p, of which `left` exist (NaN and what is missing: -inf)
+// Element k of a lane's 16 within a piece: whole 16-byte vectors
 template <typename T>
-__device__ __forceinline__ void load4(const T *p, int64_t left, float v[4]) {
-    if (left >= 4) {
-        if constexpr (sizeof(T) == 2) {
-            uint32_t w[2];
-            __builtin_memcpy(w, p, 8);
-            v[0] = __uint_as_float(w[0] << 16);
-            v[1] = __uint_as_float(w[0] & 0xFFFF0000u);
-            v[2] = __uint_as_float(w[1] << 16);
-            v[3] = __uint_as_float(w[1] & 0xFFFF0000u);
-        } else {
-            __builtin_memcpy(v, p, 16);
+__device__ __forceinline__ int piece_index(int lane, int k) {
+    constexpr int E = 16 / sizeof(T);
+    return 64 * E * (k / E) + E * lane + k % E;
+}
+
+// A lane's 16 logits of a whole piece as they lie in memory, and as numbers
+template <typename T>
+struct Piece {
+    static constexpr int E = 16 / sizeof(T), N = 16 / E;
+    u32x4 w[N];
+    __device__ __forceinline__ void load(const T *p, int lane) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) __builtin_memcpy(&w[k], p + 64 * E * k + E * lane, 16);
+    }
+    __device__ __forceinline__ void get(float v[16]) const {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            if constexpr (sizeof(T) == 2) {
+                const uint32_t u = w[k / 8][k % 8 / 2];
+                v[k] = __uint_as_float(k & 1 ? u & 0xFFFF0000u : u << 16);
+            } else {
+                v[k] = __uint_as_float(w[k / 4][k % 4]);
+            }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = i < left ? load1<T>(p + i) : -INFINITY;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = v[i] == v[i] ? v[i] : -INFINITY;
-}
+};
 
-template <typename T>
-__device__ __forceinline__ void load_chunk(const T *row, int64_t V, int64_t at, int lane, float v[16]) {
-#pragma unroll
-    for (int k = 0; k < 16; k += 4) {
-        const int64_t i = at + chunk_index(lane, k);
-        load4<T>(row + i, V - i, v + k);
+// exp((l - m) / T) for l <= m as 2^n p(f), n + f = (l - m) log2(e) / T, |f| <=
+// 1/2, with p the polynomial of degree 8 that interpolates 2^f at the Chebyshev
+// points: relative error below 1.1e-12, so of 2^17 tokens the draw of one in ten
+// million could move to a neighbour; p(0) = 1. n is taken from the low bits of
+// 1.5 2^52 + (l - m) log2(e) / T.
+struct Scale {
+    double c, lo;                       // log2(e) / T; (l - m) below which a weight counts as 0 (2^-1000)
+    __device__ __forceinline__ explicit Scale(float t) {
+        const bool greedy = !(t > 0.f);
+        c = greedy ? 1.0 : 1.4426950408889634074 / (double)t;
+        lo = -693.14718055994530942 * (greedy ? 1.0 : (double)t);
     }
+};
+// p <- p f + c for four numbers, c a constant in scalar registers (the compiler
+// would copy it into the result's registers first, an instruction more each time)
+__device__ __forceinline__ void horner4(double p[4], const double f[4], double c) {
+    asm("v_fma_f64 %0, %0, %4, %8\n\tv_fma_f64 %1, %1, %5, %8\n\tv_fma_f64 %2, %2, %6, %8\n\tv_fma_f64 %3, %3, %7, %8"
+        : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3])
+        : "v"(f[0]), "v"(f[1]), "v"(f[2]), "v"(f[3]), "s"(c));
 }
-
-// exp((l - m) / T); l <= m. m = +inf leaves 1 where l is +inf too, m = -inf
-// nothing; l = -inf is 0 at any T (at T = inf all other weights are 1)
-__device__ __forceinline__ double weight(float l, float m, double inv) {
-    const double e = exp(((double)l - (double)m) * inv);
-    return l == -INFINITY ? 0.0 : (l == m ? 1.0 : (m == INFINITY ? 0.0 : e));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// p 2^n for the n in the low bits of kn
+__device__ __forceinline__ double scaled(double p, double kn) {
+    u32x2 u = __builtin_bit_cast(u32x2, p);
+    u.y += __builtin_bit_cast(u32x2, kn).x << 20;
+    return __builtin_bit_cast(double, u);
 }
-
-__device__ __forceinline__ float wave_max(float v) {
+constexpr double kMagic = 6755399441055744.0;
+constexpr double kP8 = 1.3255224884799127e-06, kP7 = 1.5310079402383103e-05, kP6 = 0.00015403455852419016,
+                 kP5 = 0.0013333450568000008, kP4 = 0.00961812915940262, kP3 = 0.05550410941205934,
+                 kP2 = 0.2402265069581299, kP1 = 0.6931471805459335;
+struct Weight {
+    double m, c, lo;
+    float low;
+    __device__ __forceinline__ Weight(float mx, Scale t) : m((double)mx), c(t.c), lo(t.lo), low((float)((double)mx + t.lo)) {}
+    // Where sums need none of the exceptions below: a finite maximum, T < inf, and
+    // an fp32 number near m + lo. Weights below that one's, about 2^-1000, those of
+    // NaN and -inf among them, count as that (the median of three is the smallest
+    // where one is NaN).
+    __device__ __forceinline__ bool plain() const {
+        const double d = (double)low - m;
+        return c > 0.0 && fabs(m) < INFINITY && d <= 0.9 * lo && d >= 1.02 * lo;
+    }
+    __device__ __forceinline__ void raw4(const float l[4], double w[4]) const {
+        double kn[4], f[4];
 #pragma unroll
-    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
+        for (int k = 0; k < 4; ++k) {
+            const double d = (double)__builtin_amdgcn_fmed3f(l[k], low, INFINITY) - m;
+            kn[k] = fma(d, c, kMagic);
+            f[k] = fma(d, c, -(kn[k] - kMagic));
+            w[k] = fma(kP8, f[k], kP7);
+        }
+        horner4(w, f, kP6);
+        horner4(w, f, kP5);
+        horner4(w, f, kP4);
+        horner4(w, f, kP3);
+        horner4(w, f, kP2);
+        horner4(w, f, kP1);
 #pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+        for (int k = 0; k < 4; ++k) w[k] = scaled(fma(w[k], f[k], 1.0), kn[k]);
+    }
+    __device__ __forceinline__ double power(double d) const {
+        const double kn = fma(d, c, kMagic), f = fma(d, c, -(kn - kMagic));
+        double p = fma(kP8, f, kP7);
+        p = fma(p, f, kP6);
+        p = fma(p, f, kP5);
+        p = fma(p, f, kP4);
+        p = fma(p, f, kP3);
+        p = fma(p, f, kP2);
+        p = fma(p, f, kP1);
+        return scaled(fma(p, f, 1.0), kn);
+    }
+    // Weights below 2^-1000 are 0. m = +inf leaves 1 where l is +inf too, m = -inf
+    // nothing; NaN is 0, and -inf at any T (at T = inf all other weights are 1)
+    __device__ __forceinline__ double operator()(float l) const {
+        const double d = (double)l - m;
+        return !(l > -INFINITY) ? 0.0 : ((double)l == m || c == 0.0 ? (m < INFINITY || (double)l == m ? 1.0 : 0.0) : (m == INFINITY || d < lo ? 0.0 : power(d)));
+    }
+};
+
+// Sums, maxima and running sums over the lanes of a wave by moves within the
+// vector unit: the last lane of each 16 passes its total on
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+    return __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
 }
 __device__ __forceinline__ double wave_scan(double v) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double y = __shfl_up(v, o);
-        if ((int)(threadIdx.x & 63) >= o) v += y;
-    }
+    v += moved<0x111, 0xF>(v);          // the lane 1, 2, 4, 8 before this one within 16
+    v += moved<0x112, 0xF>(v);
+    v += moved<0x114, 0xF>(v);
+    v += moved<0x118, 0xF>(v);
+    v += moved<0x142, 0xA>(v);          // lane 15 and 47 to the 16 behind them
+    v += moved<0x143, 0xC>(v);          // lane 31 to the 32 behind it
     return v;
 }
+__device__ __forceinline__ double lane_of(double v, int lane) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ double wave_sum(double v) { return lane_of(wave_scan(v), 63); }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float larger(float v) {
+    const int u = __float_as_int(v);
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(u, u, CTRL, ROWS, 0xF, false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = larger<0x111, 0xF>(v);
+    v = larger<0x112, 0xF>(v);
+    v = larger<0x114, 0xF>(v);
+    v = larger<0x118, 0xF>(v);
+    v = larger<0x142, 0xA>(v);
+    v = larger<0x143, 0xC>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int smaller(int v) {
+    const int u = __builtin_amdgcn_update_dpp(v, v, CTRL, ROWS, 0xF, false);
+    return u < v ? u : v;
+}
+__device__ __forceinline__ int wave_min(int v) {
+    v = smaller<0x111, 0xF>(v);
+    v = smaller<0x112, 0xF>(v);
+    v = smaller<0x114, 0xF>(v);
+    v = smaller<0x118, 0xF>(v);
+    v = smaller<0x142, 0xA>(v);
+    v = smaller<0x143, 0xC>(v);
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
+__device__ __forceinline__ int64_t ceil_div_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Args {
     const void *logits;
@@ -94,8 +205,8 @@ struct Args {
     int64_t *next;
     float *mx;              // [total, C] maximum of each chunk
     double *sum;            // [total, C] its weights' sum; greedy rows: index of the maximum
-    double *rest;           // [B, C] sums of a remainder's chunks
-    int C, max_n, replacement;
+    int C, chunk, max_n, replacement;
+    bool direct;            // grid of k_row_stats: (chunk, node, sequence) instead of (chunk, row)
 };
 
 // The sequence of a row (the number of sequences that end at or before it), B if none
@@ -110,357 +221,440 @@ __device__ __forceinline__ int64_t sequence_of(const Args &a, int64_t row, int l
     return b;
 }
 
-// A wave a chunk of a row: its maximum, and the sum of the weights against it
-template <typename T>
+__device__ __forceinline__ double clean(float q) { return q > 0.f && q < INFINITY ? (double)q : 0.0; }
+
+// A workgroup a chunk of a row: its maximum, and the sum of the weights against it
+// (greedy rows: the lowest index of the maximum). A wave takes G pieces, all loaded
+// before the first is used. The piece that passes the end of the row is loaded from
+// 1024 logits before the end, less those that the piece before it has.
+// Bound by fp64 arithmetic: 17 instructions a logit.
+template <typename T, int G>
 __global__ __launch_bounds__(256) void k_row_stats(Args a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = blockIdx.y + (int64_t)blockIdx.z * 65535;
-    const int c = blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= a.total || c >= a.C) return;
-    double inv = 1.0;
-    bool greedy = false;
-    if (a.temperature) {
-        const int64_t b = sequence_of(a, row, lane);
-        if (b >= a.B) return;
-        const float t = a.temperature[b];
-        greedy = !(t > 0.f);
-        inv = greedy ? 1.0 : 1.0 / (double)t;
-    }
-    float v[16];
-    load_chunk<T>(static_cast<const T *>(a.logits) + row * a.ldl, a.V, (int64_t)c * kWave, lane, v);
-    float m = v[0];
-#pragma unroll
-    for (int k = 1; k < 16; ++k) m = fmaxf(m, v[k]);
-    m = wave_max(m);
-    double s = 0.0;
-    if (greedy) {
-        int at = kWave;
-#pragma unroll
-        for (int k = 15; k >= 0; --k)
-            if (v[k] == m) at = chunk_index(lane, k);
-#pragma unroll
-        for (int o = 32; o; o >>= 1) {
-            const int y = __shfl_xor(at, o);
-            at = y < at ? y : at;
-        }
-        s = (double)((int64_t)c * kWave + at);
+    __shared__ float ms[4];
+    __shared__ double ss[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = blockIdx.x;
+    int64_t row, b;
+    if (a.direct) {
+        b = blockIdx.z;
+        const int c0 = a.cu[b], c1 = a.cu[b + 1];
+        row = (int64_t)c0 + blockIdx.y;
+        if (c0 < 0 || row >= c1 || row >= a.total) return;
     } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) s += weight(v[k], m, inv);
-        s = wave_sum(s);
+        row = blockIdx.y + (int64_t)blockIdx.z * 65535;
+        if (row >= a.total) return;
+        b = sequence_of(a, row, lane);
+        if (b >= a.B) return;
     }
+    const T *p = static_cast<const T *>(a.logits) + row * a.ldl;
+    const int V = (int)a.V, from = (c * 4 * G + wave) * kPiece;      // pieces from, from + 4, ..
+    Piece<T> w[G];
+    if (V >= kPiece) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int at = from + 4 * g * kPiece;
+            if (at < V) w[g].load(p + (at + kPiece <= V ? at : V - kPiece), lane);
+        }
+    }
+    const float t = a.temperature ? a.temperature[b] : 1.f;
+    const bool greedy = !(t > 0.f);
+    const Scale sc(t);
+    float m = -INFINITY;
+    double s = 0.0;
+    int best = 0x7FFFFFFF;
+    if (V >= kPiece) {
+        float v[G][16];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int at = from + 4 * g * kPiece;
+            if (at >= V) break;
+            w[g].get(v[g]);
+            if (at + kPiece > V) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[g][k] = V - kPiece + piece_index<T>(lane, k) < at ? -INFINITY : v[g][k];
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) m = fmaxf(m, v[g][k]);      // ignores NaN
+        }
+        m = wave_max(m);
+        const Weight e(m, sc);
+        if (greedy) {
+#pragma unroll
+            for (int g = G - 1; g >= 0; --g) {
+                const int at = from + 4 * g * kPiece, first = at + kPiece <= V ? at : V - kPiece;
+                if (at >= V) continue;
+#pragma unroll
+                for (int k = 15; k >= 0; --k) best = v[g][k] == m ? first + piece_index<T>(lane, k) : best;
+            }
+        } else if (e.plain()) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                if (from + 4 * g * kPiece >= V) break;
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    double r[4];
+                    e.raw4(v[g] + k, r);
+                    s += (r[0] + r[1]) + (r[2] + r[3]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+    } else if (wave == 0) {
+        for (int i = lane; i < V; i += 64) m = fmaxf(m, load1<T>(p + i));
+        m = wave_max(m);
+        for (int i = V - 1 - lane; i >= 0 && greedy; i -= 64) best = load1<T>(p + i) == m ? i : best;
+    }
+    const Weight e(m, sc);
+    if (!greedy && !(V >= kPiece && e.plain())) {         // few tokens, or what the quick sum cannot take
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+            const int at = from + 4 * g * kPiece;
+#pragma unroll 1
+            for (int i = at + lane; i < at + kPiece && i < V; i += 64) s += e(load1<T>(p + i));
+        }
+    }
+    s = greedy ? (double)wave_min(best) : wave_sum(s);
     if (lane == 0) {
-        a.mx[row * a.C + c] = m;
-        a.sum[row * a.C + c] = s;
+        ms[wave] = m;
+        ss[wave] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const float mm = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+        double r = greedy ? 2147483647.0 : 0.0;
+        const Weight all(mm, sc);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            if (greedy) r = ms[i] == mm && ss[i] < r ? ss[i] : r;
+            else r += ss[i] * all(ms[i]);
+        }
+        a.mx[row * a.C + c] = mm;
+        a.sum[row * a.C + c] = r;
     }
 }
 
-struct Walk {
-    double S, R, left;
-    int cur, i, kept, gone;             // node, next child to try, kept nodes, children of cur taken out (no draft)
-    int done;
-};
+// Four consecutive logits (or draft probabilities) at p, of which `left` exist
+template <typename T>
+__device__ __forceinline__ f32x4 load4(const T *p, int64_t left, float missing) {
+    f32x4 v;
+    if (left >= 4) {
+        if constexpr (sizeof(T) == 2) {
+            uint32_t u[2];
+            __builtin_memcpy(u, p, 8);
+            v = f32x4{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xFFFF0000u), __uint_as_float(u[1] << 16),
+                      __uint_as_float(u[1] & 0xFFFF0000u)};
+        } else {
+            __builtin_memcpy(&v, p, 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = i < left ? load1<T>(p + i) : missing;
+    }
+    return v;
+}
 
-// One workgroup a sequence walks its tree. The walk itself is one thread's; the
-// workgroup prepares what it reads (maximum and sum of every node's row, weight
-// and draft probability of every token) and forms the sums of remainders.
+// One workgroup a sequence walks its tree. The first wave tries the children; the
+// workgroup prepares what that reads (maximum and sum of every node's row, weight
+// and draft probability of every token), forms the sums of remainders, a wave a
+// piece, and draws the next token: the chunk or piece where the cumulated sum
+// crosses the random number, then the token in it. The code runs once or twice a
+// call, so its loops stay rolled: fetching instructions costs more than running them.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_walk(Args a) {
     __shared__ float node_m[kMaxNodes], node_q[kMaxNodes];
     __shared__ double node_z[kMaxNodes], node_e[kMaxNodes], node_u[kMaxNodes];
-    __shared__ int node_p[kMaxNodes];
-    __shared__ int node_best[kMaxNodes];
-    __shared__ uint8_t node_out[kMaxNodes];       // taken out of its parent's row
-    __shared__ Walk w;
-    __shared__ double part[16];
+    __shared__ int node_p[kMaxNodes];             // parent of a node that can be accepted, else -1
+    __shared__ int node_best[kMaxNodes], node_x[kMaxNodes];
+    __shared__ int gone[kMaxNodes];               // children of the current node that were taken out (no draft)
+    __shared__ double sums[1024], wsum[16];
+    __shared__ int firsts[16], lasts[16];
+    __shared__ struct {
+        double S, target, before;
+        int cur, kept, gone, sum, at, past;
+    } w;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t b = blockIdx.x;
     int c0 = a.cu[b], c1 = a.cu[b + 1];
+    const float t = a.temperature ? a.temperature[b] : 1.f;
     c0 = c0 < 0 ? 0 : c0;
     c1 = c1 > a.total ? (int)a.total : c1;
     const int rows = c1 > c0 ? c1 - c0 : 0;
     const int n = rows < a.max_n ? rows : a.max_n;
+    for (int i = tid; i < rows; i += 1024) a.path[c0 + i] = i == 0 && n > 0 ? 0 : -1;
     if (n == 0) {
-        for (int i = tid; i < rows; i += 1024) a.path[c0 + i] = -1;
         if (tid == 0) {
             a.count[b] = 0;
             a.next[b] = -1;
         }
         return;
     }
-    const float t = a.temperature ? a.temperature[b] : 1.f;
     const bool greedy = !(t > 0.f);
-    const double inv = greedy ? 1.0 : 1.0 / (double)t;
+    const Scale sc(t);
     const T *logits = static_cast<const T *>(a.logits) + (int64_t)c0 * a.ldl;
     const float *draft = a.draft && !greedy ? a.draft + (int64_t)c0 * a.ldd : nullptr;
 
     // maximum and sum of every row, from its chunks
     for (int i = wave; i < n; i += 16) {
-        const float *mc = a.mx + (int64_t)(c0 + i) * a.C;
-        const double *sc = a.sum + (int64_t)(c0 + i) * a.C;
-        float m = -INFINITY;
-        for (int c = lane; c < a.C; c += 64) m = fmaxf(m, mc[c]);
-        m = wave_max(m);
-        double z = 0.0;
+        const int64_t at = (int64_t)(c0 + i) * a.C + lane;
+        const float mc = lane < a.C ? a.mx[at] : -INFINITY;
+        const double zc = lane < a.C ? a.sum[at] : 0.0;
+        const float m = wave_max(mc);
+        double z;
         int best = 0x7FFFFFFF;
-        for (int c = lane; c < a.C; c += 64) {
-            if (greedy) {
-                if (mc[c] == m && (int)sc[c] < best) best = (int)sc[c];
-            } else {
-                z += sc[c] * weight(mc[c], m, inv);
-            }
-        }
-        z = wave_sum(z);
-        for (int o = 32; o; o >>= 1) {
-            const int y = __shfl_xor(best, o);
-            best = y < best ? y : best;
+        if (greedy) {
+            best = wave_min(mc == m ? (int)zc : best);
+            z = m == -INFINITY ? 0.0 : 1.0;
+        } else {
+            z = wave_sum(zc * Weight(m, sc)(mc));
         }
         if (lane == 0) {
             node_m[i] = m;
-            node_z[i] = greedy ? (m == -INFINITY ? 0.0 : 1.0) : z;
+            node_z[i] = z;
             node_best[i] = m == -INFINITY ? -1 : best;
         }
     }
-    __syncthreads();
+    // the tokens' own logits, while the maxima are on their way to LDS
     for (int i = tid; i < n; i += 1024) {
         const int p = a.parents ? a.parents[c0 + i] : i - 1;
         const int64_t x = a.tokens[c0 + i];
         const bool ok = i > 0 && p >= 0 && p < i && x >= 0 && x < a.V;
-        double e = -1.0;                            // never accepted
-        float q = 1.f;
-        if (ok) {
-            if (greedy) {
-                e = x == node_best[p] ? 1.0 : 0.0;
-            } else {
-                float l = load1<T>(logits + p * a.ldl + x);
-                l = l == l ? l : -INFINITY;
-                e = weight(l, node_m[p], inv);
-            }
-            if (draft) {
-                q = draft[p * a.ldd + x];
-                q = q > 0.f && q < INFINITY ? q : 0.f;
-            }
-        }
-        node_p[i] = i > 0 && p >= 0 && p < i ? p : -1;
-        node_e[i] = e;
-        node_q[i] = q;
         node_u[i] = a.uniform[c0 + i];
-        node_out[i] = 0;
+        node_p[i] = ok ? p : -1;
+        node_x[i] = ok ? (int)x : -1;
+        node_e[i] = ok && !greedy ? (double)load1<T>(logits + p * a.ldl + x) : 0.0;
+        node_q[i] = ok && draft ? (float)clean(draft[p * a.ldd + x]) : 1.f;
     }
-    for (int i = tid; i < rows; i += 1024) a.path[c0 + i] = i == 0 ? 0 : -1;
-    if (tid == 0) {
-        w.S = 0.0;
-        w.left = 1.0;
-        w.cur = 0;
-        w.i = 1;
-        w.kept = 1;
-        w.gone = 0;
-        w.done = 0;
+    if (tid == 0) w.gone = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += 1024) {
+        const int p = node_p[i];
+        if (p >= 0) node_e[i] = greedy ? (node_x[i] == node_best[p] ? 1.0 : 0.0) : Weight(node_m[p], sc)((float)node_e[i]);
     }
     __syncthreads();
-    if (tid == 0) w.R = node_z[0];
-    double *rest = a.rest + b * a.C;
+
+    // the walk: all lanes of the first wave go the same way
+    int cur = 0, next_child = 1, kept = 1;
+    double S = 0.0, R = node_z[0], left = 1.0;
+    const int pieces = (int)ceil_div_dev(a.V, kPiece);
     for (;;) {
-        if (tid == 0) {
-            // until a remainder has to be summed, or no child is left
-            int i = w.i, cur = w.cur;
+        if (wave == 0) {
             bool sum = false;
-            for (; i < n && !sum; ++i) {
-                if (node_p[i] != cur || node_e[i] < 0.0) continue;
-                const double e = node_e[i], q = (double)node_q[i];
+            int ngone = w.gone;
+            while (!sum) {
+                // the next child of cur
+                int i = -1;
+                for (int i0 = next_child & ~63; i0 < n && i < 0; i0 += 64) {
+                    const int j = i0 + lane;
+                    const uint64_t kids = __ballot(j < n && j >= next_child && node_p[j] == cur);
+                    if (kids) i = i0 + __ffsll((long long)kids) - 1;
+                }
+                if (i < 0) break;
+                next_child = i + 1;
+                const double e = node_e[i], q = (double)node_q[i], u = node_u[i];
                 bool ok;
                 if (greedy) {
                     ok = e > 0.0;
                 } else if (draft) {
-                    const double r = e - w.S * q;
-                    ok = w.left > 0.0 && node_u[i] * q * w.R < (r > 0.0 ? r : 0.0) * w.left;
+                    ok = left > 0.0 && u * q * R < fmax(e - S * q, 0.0) * left;
+                    if (!ok && left > 0.0) {
+                        S += R / left;
+                        if (!a.replacement) left -= q;
+                        sum = true;
+                    }
                 } else {
                     double r = e;
-                    for (int j = cur + 1; j < i; ++j)             // the same token among its elder siblings
-                        if (node_out[j] && node_p[j] == cur && a.tokens[c0 + j] == a.tokens[c0 + i]) r = 0.0;
-                    ok = node_u[i] * w.R < r;
+                    for (int k = 0; k < ngone; ++k)               // the same token among its elder siblings
+                        if (node_x[gone[k]] == node_x[i]) r = 0.0;
+                    ok = u * R < r;
                     if (!ok && r > 0.0) {
-                        node_out[i] = 1;
-                        w.gone = 1;
-                        w.R = w.R > r ? w.R - r : 0.0;
+                        if (lane == 0) gone[ngone] = i;
+                        ++ngone;
+                        R = R > r ? R - r : 0.0;
                     }
                 }
                 if (ok) {
-                    a.path[c0 + w.kept] = i;
-                    ++w.kept;
+                    if (lane == 0) a.path[c0 + kept] = i;
+                    ++kept;
                     cur = i;
-                    w.S = 0.0;
-                    w.left = 1.0;
-                    w.R = node_z[i];
-                    w.gone = 0;
-                } else if (draft && w.left > 0.0) {
-                    w.S += w.R / w.left;
-                    if (!a.replacement) w.left -= q;
-                    sum = true;
+                    S = 0.0;
+                    left = 1.0;
+                    R = node_z[i];
+                    ngone = 0;
                 }
             }
-            w.i = i;
-            w.cur = cur;
-            w.done = !sum;
+            if (lane == 0) {
+                w.S = S;
+                w.cur = cur;
+                w.kept = kept;
+                w.gone = ngone;
+                w.sum = sum;
+            }
         }
         __syncthreads();
-        if (w.done) break;
-        // the remainder's sum, chunk by chunk
+        if (!w.sum) break;
+        // the remainder's sum, piece by piece, four values of a lane at a time; the
+        // next four are loaded before these are used
         const T *row = logits + (int64_t)w.cur * a.ldl;
         const float *qrow = draft + (int64_t)w.cur * a.ldd;
-        const float m = node_m[w.cur];
-        const double S = w.S;
-        for (int c = wave; c < a.C; c += 16) {
-            float v[16], q[16];
-            load_chunk<T>(row, a.V, (int64_t)c * kWave, lane, v);
-            load_chunk<float>(qrow, a.V, (int64_t)c * kWave, lane, q);
-            double s = 0.0;
+        const Weight e(node_m[w.cur], sc);
+        const double s0 = w.S;
+        const int turns = 4 * ((pieces - wave + 15) / 16);
+        auto place = [&](int j) { return (int64_t)(wave + 16 * (j >> 2)) * kPiece + 256 * (j & 3) + 4 * lane; };
+        f32x4 v = load4<T>(row + place(0), a.V - place(0), -INFINITY), q = load4<float>(qrow + place(0), a.V - place(0), 0.f);
+        double s = 0.0;
+#pragma unroll 1
+        for (int j = 0; j < turns; ++j) {
+            const f32x4 v0 = v, q0 = q;
+            const int64_t at = place(j + 1 < turns ? j + 1 : j);
+            v = load4<T>(row + at, a.V - at, -INFINITY);
+            q = load4<float>(qrow + at, a.V - at, 0.f);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const double qk = q[k] > 0.f && q[k] < INFINITY ? (double)q[k] : 0.0;
-                const double r = weight(v[k], m, inv) - S * qk;
-                s += r > 0.0 ? r : 0.0;
+            for (int k = 0; k < 4; ++k) s += fmax(e(v0[k]) - s0 * clean(q0[k]), 0.0);
+            if ((j & 3) == 3) {
+                s = wave_sum(s);
+                if (lane == 0) sums[wave + 16 * (j >> 2)] = s;
+                s = 0.0;
             }
-            s = wave_sum(s);
-            if (lane == 0) rest[c] = s;
         }
         __syncthreads();
         if (wave == 0) {
-            double s = 0.0;
-            for (int c = lane; c < a.C; c += 64) s += rest[c];
-            s = wave_sum(s);
-            if (lane == 0) w.R = s;
+            s = 0.0;
+            for (int c = lane; c < pieces; c += 64) s += sums[c];
+            R = wave_sum(s);
         }
-        __syncthreads();
     }
-    const int cur = w.cur;
-    const float m = node_m[cur];
+    cur = w.cur;
+    const int ngone = w.gone;
     if (tid == 0) a.count[b] = w.kept;
     if (greedy || node_z[cur] == 0.0) {
         if (tid == 0) a.next[b] = greedy ? node_best[cur] : -1;
         return;
     }
-    // sums of the chunks of what is left: the target's own, less the tokens taken
-    // out, unless a remainder was summed
-    const bool rem = draft && w.S > 0.0;
-    if (!rem) {
-        for (int c = tid; c < a.C; c += 1024)
-            rest[c] = a.sum[(int64_t)(c0 + cur) * a.C + c] * weight(a.mx[(int64_t)(c0 + cur) * a.C + c], m, inv);
-        __syncthreads();
-        if (tid == 0 && w.gone)
-            for (int j = cur + 1; j < n; ++j)
-                if (node_out[j] && node_p[j] == cur) {
-                    const int c = (int)(a.tokens[c0 + j] / kWave);
-                    const double r = rest[c] - node_e[j];
-                    rest[c] = r > 0.0 ? r : 0.0;
-                }
-        __syncthreads();
-    }
-    if (wave != 0) return;
-    // the first wave: total, chunk, token
-    const int per = (a.C + 63) / 64;
-    bool whole = false;                           // nothing left: the target's own weights
+    // What is drawn from: the sums of a remainder's pieces, or those of the row's
+    // chunks less the tokens taken out; the row's own where nothing is left of it
+    const Weight e(node_m[cur], sc);
+    const T *row = logits + (int64_t)cur * a.ldl;
+    bool own = !(draft && w.S > 0.0), whole = false;
+#pragma unroll 1
     for (;;) {
-        double mine = 0.0;
-        for (int c = lane * per; c < (lane + 1) * per && c < a.C; ++c)
-            mine += whole ? a.sum[(int64_t)(c0 + cur) * a.C + c] * weight(a.mx[(int64_t)(c0 + cur) * a.C + c], m, inv) : rest[c];
-        const double upto = wave_scan(mine);
-        const double total = __shfl(upto, 63);
-        if (!(total > 0.0) && !whole) {
-            whole = true;
-            continue;
-        }
-        const double target = node_u[0] * total;
-        // first chunk whose inclusive sum is past the target, else the last one that holds anything
-        int at = a.C, last = -1;
-        double before = 0.0, run = upto - mine;
-        for (int c = lane * per; c < (lane + 1) * per && c < a.C; ++c) {
-            const double s = whole ? a.sum[(int64_t)(c0 + cur) * a.C + c] * weight(a.mx[(int64_t)(c0 + cur) * a.C + c], m, inv) : rest[c];
-            if (s > 0.0) last = c;
-            if (s > 0.0 && run + s > target && at == a.C) {
-                at = c;
-                before = run;
+        const int size = own ? a.chunk : kPiece, count = own ? a.C : pieces;
+        if (own) {
+            if (tid < a.C) {
+                const int64_t at = (int64_t)(c0 + cur) * a.C + tid;
+                double s = a.sum[at] * e(a.mx[at]);
+                if (!whole)
+                    for (int k = 0; k < ngone; ++k)
+                        if (node_x[gone[k]] / a.chunk == tid) s = fmax(s - node_e[gone[k]], 0.0);
+                sums[tid] = s;
             }
-            run += s;
+            __syncthreads();
         }
-        const uint64_t found = __ballot(at < a.C);
-        bool past = false;
-        if (found) {
-            const int f = __ffsll((long long)found) - 1;
-            at = __shfl(at, f);
-            before = __shfl(before, f);
-        } else {
-            const uint64_t any = __ballot(last >= 0);
-            if (!any) {
-                if (lane == 0) a.next[b] = -1;
-                return;
-            }
-            at = __shfl(last, 63 - __clzll((long long)any));
-            past = true;
-        }
-        // the token within the chunk
-        float v[16], q[16];
-        load_chunk<T>(logits + (int64_t)cur * a.ldl, a.V, (int64_t)at * kWave, lane, v);
-        if (rem && !whole) load_chunk<float>(draft + (int64_t)cur * a.ldd, a.V, (int64_t)at * kWave, lane, q);
-        double r[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const int64_t x = (int64_t)at * kWave + chunk_index(lane, k);
-            r[k] = weight(v[k], m, inv);
-            if (rem && !whole) {
-                const double qk = q[k] > 0.f && q[k] < INFINITY ? (double)q[k] : 0.0;
-                r[k] -= w.S * qk;
-                r[k] = r[k] > 0.0 ? r[k] : 0.0;
-            }
-            if (w.gone && !whole)
-                for (int j = cur + 1; j < n; ++j)
-                    if (node_out[j] && node_p[j] == cur && a.tokens[c0 + j] == x) r[k] = 0.0;
-        }
-        int64_t first = INT64_MAX, final_ = -1;
-        double base = before;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {             // elements in the order of their index
-            const double quad = ((r[4 * g] + r[4 * g + 1]) + r[4 * g + 2]) + r[4 * g + 3];
-            const double inc = wave_scan(quad);
-            double s = base + (inc - quad);
-#pragma unroll
-            for (int k = 4 * g; k < 4 * g + 4; ++k) {
-                const int64_t x = (int64_t)at * kWave + chunk_index(lane, k);
-                s += r[k];
-                if (r[k] > 0.0) {
-                    if (s > target && x < first) first = x;
-                    if (x > final_) final_ = x;
+        if (wave == 0) {
+            const int per = (count + 63) / 64;
+            double mine = 0.0;
+            for (int c = lane * per; c < (lane + 1) * per && c < count; ++c) mine += sums[c];
+            const double upto = wave_scan(mine), target = node_u[0] * lane_of(upto, 63);
+            // first one whose inclusive sum is past the target, else the last that holds anything
+            int at = -1, last = -1;
+            double before = 0.0, run = upto - mine;
+            for (int c = lane * per; c < (lane + 1) * per && c < count; ++c) {
+                const double s = sums[c];
+                if (s > 0.0) {
+                    last = c;
+                    if (run + s > target && at < 0) {
+                        at = c;
+                        before = run;
+                    }
                 }
+                run += s;
             }
-            base += __shfl(inc, 63);
+            const uint64_t found = __ballot(at >= 0), any = __ballot(last >= 0);
+            if (found) {
+                const int f = __ffsll((long long)found) - 1;
+                at = __builtin_amdgcn_readlane(at, f);
+                before = lane_of(before, f);
+            } else if (any) {
+                at = __builtin_amdgcn_readlane(last, 63 - __clzll((long long)any));
+            }
+            if (lane == 0) {
+                w.at = at;
+                w.before = before;
+                w.target = target;
+                w.past = !found;
+            }
         }
-        for (int o = 32; o; o >>= 1) {
-            const int64_t y = __shfl_xor(first, o), z = __shfl_xor(final_, o);
-            first = y < first ? y : first;
-            final_ = z > final_ ? z : final_;
+        __syncthreads();
+        // 4096 tokens at a time, four of a thread
+        int first = 0x7FFFFFFF, last = -1;
+        double base = w.before;
+        const double target = w.target;
+        if (w.at >= 0) {
+#pragma unroll 1
+            for (int i = 0; i < size; i += 4096) {
+                const int64_t at = (int64_t)w.at * size + i + 4 * tid;
+                const int64_t there = i + 4 * tid < size ? a.V - at : 0;
+                const f32x4 v = load4<T>(row + at, there, -INFINITY);
+                f32x4 q = {0, 0, 0, 0};
+                if (!own) q = load4<float>(draft + (int64_t)cur * a.ldd + at, there, 0.f);     // own: no q
+                double r[4], part = 0.0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    r[k] = fmax(e(v[k]) - w.S * clean(q[k]), 0.0);
+                    if (!whole)
+                        for (int j = 0; j < ngone; ++j)
+                            if (node_x[gone[j]] == at + k) r[k] = 0.0;
+                    part += r[k];
+                }
+                const double inc = wave_scan(part);
+                if (lane == 63) wsum[wave] = inc;
+                __syncthreads();
+                const double waves = wave_scan(lane < 16 ? wsum[lane] : 0.0);
+                double s = base + (wave ? lane_of(waves, wave - 1) : 0.0) + (inc - part);
+                base += lane_of(waves, 15);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    s += r[k];
+                    if (r[k] > 0.0) {
+                        last = (int)at + k;
+                        if (s > target && first == 0x7FFFFFFF) first = last;
+                    }
+                }
+                __syncthreads();
+            }
         }
-        const int64_t x = past || first == INT64_MAX ? final_ : first;
-        if (x < 0 && !whole) {                    // the chunk's sum was rounding alone
-            whole = true;
-            continue;
+        first = wave_min(first);
+        last = ~wave_min(~last);                      // ~ turns the order round
+        if (lane == 0) {
+            firsts[wave] = first;
+            lasts[wave] = last;
         }
-        if (lane == 0) a.next[b] = x;
-        return;
+        __syncthreads();
+        first = wave_min(firsts[lane & 15]);
+        last = ~wave_min(~lasts[lane & 15]);
+        const int x = w.past || first == 0x7FFFFFFF ? last : first;
+        if (x >= 0 || whole) {
+            if (tid == 0) a.next[b] = x;
+            return;
+        }
+        own = whole = true;                           // nothing but rounding was left
+        __syncthreads();
     }
 }
 
-size_t layout(int64_t B, int64_t total, int64_t V, size_t *sum, size_t *rest, int *C) {
-    const int64_t c = ceil_div(V, (int64_t)kWave);
-    const size_t mx = ((size_t)total * c * 4 + 15) / 16 * 16, s = (size_t)total * c * 8;
+size_t layout(int64_t total, int64_t V, size_t *sum, int *C) {
+    const int64_t c = ceil_div(V, (int64_t)chunk_size(V));
+    const size_t mx = ((size_t)total * c * 4 + 15) / 16 * 16;
     if (sum) *sum = mx;
-    if (rest) *rest = mx + s;
     if (C) *C = (int)c;
-    return mx + s + (size_t)B * c * 8;
+    return mx + (size_t)total * c * 8 + 16;
 }
 
 }  // namespace
 
-size_t verify_tree_workspace(int64_t B, int64_t total, int64_t V) { return layout(B, total, V, nullptr, nullptr, nullptr); }
+size_t verify_tree_workspace(int64_t B, int64_t total, int64_t V) {
+    (void)B;
+    return layout(total, V, nullptr, nullptr);
+}
 
 hipError_t launch_verify_tree(const void *logits, mxs_dtype dt, int64_t ldl, int64_t V, const int64_t *tokens,
                               const int32_t *parents, const int32_t *cu, int64_t B, int64_t total, int64_t max_n,
@@ -472,17 +666,26 @@ hipError_t launch_verify_tree(const void *logits, mxs_dtype dt, int64_t ldl, int
     a.tokens = tokens; a.parents = parents; a.cu = cu; a.draft = draft; a.temperature = temperature;
     a.uniform = uniform; a.path = path; a.count = count; a.next = next;
     a.max_n = (int)max_n; a.replacement = replacement;
-    size_t sum, rest;
-    layout(B, total, V, &sum, &rest, &a.C);
+    size_t sum;
+    layout(total, V, &sum, &a.C);
+    a.chunk = chunk_size(V);
     uint8_t *w = static_cast<uint8_t *>(ws);
     a.mx = reinterpret_cast<float *>(w);
     a.sum = reinterpret_cast<double *>(w + sum);
-    a.rest = reinterpret_cast<double *>(w + rest);
     if (total > 0 && max_n > 0) {
-        const dim3 grid((unsigned)ceil_div(a.C, 4), (unsigned)(total < 65535 ? total : 65535),
-                        (unsigned)ceil_div(total, (int64_t)65535));
-        if (dt == MXS_BF16) hipLaunchKernelGGL(k_row_stats<uint16_t>, grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL(k_row_stats<float>, grid, dim3(256), 0, st, a);
+        // a workgroup a node and chunk, unless a loose max_n would leave most of them without a node: then a row
+        // and chunk, and its sequence is looked for
+        a.direct = B * max_n <= 2 * total + 64;
+        const dim3 grid = a.direct ? dim3((unsigned)a.C, (unsigned)max_n, (unsigned)B)
+                                   : dim3((unsigned)a.C, (unsigned)(total < 65535 ? total : 65535),
+                                          (unsigned)ceil_div(total, (int64_t)65535));
+        if (a.chunk == 4096) {
+            if (dt == MXS_BF16) hipLaunchKernelGGL((k_row_stats<uint16_t, 1>), grid, dim3(256), 0, st, a);
+            else hipLaunchKernelGGL((k_row_stats<float, 1>), grid, dim3(256), 0, st, a);
+        } else {
+            if (dt == MXS_BF16) hipLaunchKernelGGL((k_row_stats<uint16_t, 4>), grid, dim3(256), 0, st, a);
+            else hipLaunchKernelGGL((k_row_stats<float, 4>), grid, dim3(256), 0, st, a);
+        }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
