@@ -33,7 +33,7 @@ struct LoraArgs {
     int64_t M, K, N, ldx, ldy;
     int n, R, Rp;                       // adapters, stored rank, rank rounded up to 16
     int splits;
-    int64_t kper;                       // K of a slice (a multiple of 128)
+    int64_t kper;                       // K of a slice
     int64_t nper;                       // columns of Y a workgroup takes (a multiple of 64)
     int32_t *order;                     // rows by adapter
     Tile *tiles;
@@ -41,6 +41,19 @@ struct LoraArgs {
 };
 
 // ----------------------------------------------------------------- the groups
+// cnt[id] before this row is added. The rows of a prompt have one id: lanes that
+// all have the same are added by one of them (64 additions to one place take turns).
+__device__ __forceinline__ int count_rows(int32_t *cnt, int32_t id) {
+    const uint64_t on = __ballot(1);
+    if (__builtin_amdgcn_readfirstlane(id) == id && __ballot(1) == on) {
+        const int lane = threadIdx.x & 63, before = __popcll(on & ((1ull << lane) - 1));
+        int at = 0;
+        if (before == 0) at = atomicAdd(&cnt[id], __popcll(on));
+        return __builtin_amdgcn_readfirstlane(at) + before;
+    }
+    return atomicAdd(&cnt[id], 1);
+}
+
 // One workgroup: rows counted by adapter, adapters cut into tiles, rows put in
 // place. The order of the rows of one adapter is left to the atomics: no value
 // depends on it.
@@ -50,9 +63,14 @@ __global__ __launch_bounds__(1024) void k_lora_group(LoraArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int i = tid; i < a.n; i += 1024) cnt[i] = 0;
     __syncthreads();
-    for (int64_t t = tid; t < a.M; t += 1024) {
-        const int32_t id = a.ids[t];
-        if ((uint32_t)id < (uint32_t)a.n) atomicAdd(&cnt[id], 1);
+    // 4096 rows at a time: one wait for their ids
+    for (int64_t t0 = tid; t0 < a.M; t0 += 4096) {
+        int32_t id[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) id[k] = t0 + 1024 * k < a.M ? a.ids[t0 + 1024 * k] : -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((uint32_t)id[k] < (uint32_t)a.n) count_rows(cnt, id[k]);
     }
     __syncthreads();
     const int per = (a.n + 1023) / 1024;
@@ -89,9 +107,13 @@ __global__ __launch_bounds__(1024) void k_lora_group(LoraArgs a) {
     }
     if (tid == 1023) *a.ntiles = s;
     __syncthreads();
-    for (int64_t t = tid; t < a.M; t += 1024) {
-        const int32_t id = a.ids[t];
-        if ((uint32_t)id < (uint32_t)a.n) a.order[atomicAdd(&cnt[id], 1)] = (int32_t)t;
+    for (int64_t t0 = tid; t0 < a.M; t0 += 4096) {
+        int32_t id[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) id[k] = t0 + 1024 * k < a.M ? a.ids[t0 + 1024 * k] : -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((uint32_t)id[k] < (uint32_t)a.n) a.order[count_rows(cnt, id[k])] = (int32_t)(t0 + 1024 * k);
     }
 }
 
@@ -245,97 +267,170 @@ struct Parts {
     static constexpr int E = 16 / sizeof(T);
 };
 
-// Elements r0 .. r0 + E - 1 of row n of B; zeros from the rank on
-template <typename T, bool VEC>
+// Elements r0 .. r0 + E - 1 of a row of B; zeros from the rank on
+template <typename T>
 __device__ __forceinline__ u32x4 load_b(const T *row, int r0, int rank) {
     constexpr int E = 16 / sizeof(T);
     u32x4 v = {0, 0, 0, 0};
-    if (r0 >= rank) return v;
-    if (VEC && r0 + E <= rank) return load16(row + r0);
-    T e[E];
+    if (r0 + E <= rank) return load16(row + r0);
+    if (r0 < rank) {
+        T e[E];
 #pragma unroll
-    for (int j = 0; j < E; ++j) e[j] = r0 + j < rank ? row[r0 + j] : T(0);
-    __builtin_memcpy(&v, e, 16);
+        for (int j = 0; j < E; ++j) e[j] = r0 + j < rank ? row[r0 + j] : T(0);
+        __builtin_memcpy(&v, e, 16);
+    }
     return v;
 }
 
-template <typename T, bool VECB, bool VECY>
+// A wave takes CT tiles of 16 columns at a time: their rows of B are loaded before
+// anything waits, then V's parts are read from LDS once for all of them, while
+// the next 16 tokens' part of Y is on its way.
+template <typename T, int STEPS, int CT>
+struct Columns {
+    u32x4 b[CT][STEPS];
+    __device__ __forceinline__ void load(const LoraArgs &a, int64_t c, int adapter, int rank) {
+        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < CT; ++i) {
+            const int64_t n = c + 16 * i + col < a.N ? c + 16 * i + col : a.N - 1;
+            const T *row = static_cast<const T *>(a.B) + ((int64_t)adapter * a.N + n) * a.R;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) b[i][s] = load_b<T>(row, s * Parts<T>::D + Parts<T>::E * g, rank);
+        }
+    }
+};
+
+template <int CT>
+__device__ __forceinline__ void load_y(const float *y, int64_t left, f32x4 v[CT]) {
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+        if (left >= 16 * i + 4) {
+            __builtin_memcpy(&v[i], y + 16 * i, 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = 16 * i + j < left ? y[16 * i + j] : 0.f;
+        }
+    }
+}
+template <int CT>
+__device__ __forceinline__ void store_y(float *y, int64_t left, const f32x4 v[CT]) {
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+        if (left >= 16 * i + 4) {
+            __builtin_memcpy(y + 16 * i, &v[i], 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (16 * i + j < left) y[16 * i + j] = v[i][j];
+        }
+    }
+}
+
+template <typename T, int STEPS, int CT>
+struct Expand {
+    Columns<T, STEPS, CT> w;
+    f32x4 y[CT], later[CT];
+    // the rows of B and the first 16 tokens' part of Y at columns c
+    __device__ __forceinline__ void load(const LoraArgs &a, const int32_t *rows, int adapter, int count, int rank, int64_t c) {
+        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+        w.load(a, c, adapter, rank);
+        if (col < count) load_y<CT>(a.Y + (int64_t)rows[col] * a.ldy + c + 4 * g, a.N - c - 4 * g, later);
+    }
+    __device__ __forceinline__ void run(const LoraArgs &a, const T *parts, const int32_t *rows, int adapter, int count,
+                                        int rank, float scale, int64_t c, int64_t c1) {
+        constexpr int P = Parts<T>::P, D = Parts<T>::D, E = Parts<T>::E, W = STEPS * D + E;
+        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+        for (; c < c1; c += 64 * CT) {
+            const int64_t at = c + 4 * g, left = a.N - at;
+            auto row = [&](int t) { return a.Y + (int64_t)rows[t + col] * a.ldy + at; };
+#pragma unroll 1
+            for (int t = 0; t < count; t += 16) {
+#pragma unroll
+                for (int i = 0; i < CT; ++i) y[i] = later[i];
+                if (t + 16 + col < count) load_y<CT>(row(t + 16), left, later);
+                f32x4 acc[CT];
+#pragma unroll
+                for (int i = 0; i < CT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                    for (int q = 0; q < P; ++q) {
+                        const u32x4 v = *reinterpret_cast<const u32x4 *>(parts + (q * kTile + t + col) * W + s * D + E * g);
+#pragma unroll
+                        for (int i = 0; i < CT; ++i) acc[i] = mma<T>(w.b[i][s], v, acc[i]);
+                    }
+                if (t + 16 >= count && c + 64 * CT < c1) load(a, rows, adapter, count, rank, c + 64 * CT);
+                if (t + col < count) {
+#pragma unroll
+                    for (int i = 0; i < CT; ++i) y[i] += scale * acc[i];
+                    store_y<CT>(row(t), left, y);
+                }
+            }
+        }
+    }
+};
+
+template <typename T, int STEPS, int CT>
 __global__ __launch_bounds__(256) void k_lora_expand(LoraArgs a, bool small) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t raw[];
+    constexpr int P = Parts<T>::P, D = Parts<T>::D, E = Parts<T>::E, Rd = STEPS * D, W = Rd + E;
+    __shared__ __attribute__((aligned(16))) T parts[P * kTile * W];      // a row's place: 16 bytes of padding
     __shared__ int32_t rows[kTile];
-    constexpr int P = Parts<T>::P, D = Parts<T>::D, E = Parts<T>::E;
     int adapter, count;
     if (!find_group(a, small, rows, adapter, count)) return;
     const int rank = rank_of(a, adapter);
     if (rank == 0) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
-    const int steps = (rank + D - 1) / D, Rd = steps * D;
-    const int W = Rd + E;                                   // a row's place in LDS: 16 bytes of padding
-    T *parts = reinterpret_cast<T *>(raw);
-    const int subs = (count + 15) / 16;
+    const int64_t c0 = (int64_t)blockIdx.y * a.nper, c1 = c0 + a.nper < a.N ? c0 + a.nper : a.N;
+    const int64_t c = c0 + 16 * CT * (threadIdx.x >> 6);
     const float scale = a.scale ? a.scale[adapter] : 1.f;
-    for (int e = threadIdx.x; e < subs * 16 * Rd; e += 256) {
-        const int t = e / Rd, r = e - t * Rd;
-        float v = 0.f;
+    // V, four ranks of a token at a time: the slices' sums are loaded eight together
+    const int places = (count + 15) / 16 * 16;
+    for (int e = threadIdx.x; e < places * (Rd / 4); e += 256) {
+        const int t = e / (Rd / 4), r = 4 * (e - t * (Rd / 4));
+        f32x4 v = {0, 0, 0, 0};
         if (r < rank && t < count) {
             const float *p = a.V + (int64_t)rows[t] * a.Rp + r;
-            for (int s = 0; s < a.splits; ++s) v += p[(int64_t)s * a.M * a.Rp];
+            for (int s = 0; s < a.splits; s += 8) {
+                f32x4 part[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    part[j] = f32x4{0, 0, 0, 0};
+                    if (s + j < a.splits) part[j] = *reinterpret_cast<const f32x4 *>(p + (int64_t)(s + j) * a.M * a.Rp);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v += part[j];
+            }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = r + j < rank ? v[j] : 0.f;
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
                 // cut, not rounded: no part overflows, and three of 8 bits hold all 24
-                const uint32_t h = v == v ? __float_as_uint(v) & 0xFFFF0000u : 0x7FC00000u;
-                parts[(q * kTile + t) * W + r] = (uint16_t)(h >> 16);
-                v = __builtin_isinf(v) ? 0.f : v - __uint_as_float(h);
+                uint32_t h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h[j] = v[j] == v[j] ? __float_as_uint(v[j]) & 0xFFFF0000u : 0x7FC00000u;
+                    v[j] = __builtin_isinf(v[j]) ? 0.f : v[j] - __uint_as_float(h[j]);
+                }
+                *reinterpret_cast<uint2 *>(parts + (q * kTile + t) * W + r) = make_uint2(h[0] >> 16 | h[1], h[2] >> 16 | h[3]);
             }
         } else {
-            parts[t * W + r] = v;
+            *reinterpret_cast<f32x4 *>(parts + t * W + r) = v;
         }
     }
+    Expand<T, STEPS, CT> x;
+    if (c < c1) x.load(a, rows, adapter, count, rank, c);
     __syncthreads();
-    const int64_t c0 = (int64_t)blockIdx.y * a.nper, c1 = c0 + a.nper < a.N ? c0 + a.nper : a.N;
-    for (int64_t c = c0 + 16 * wave; c < c1; c += 64) {
-        const int64_t n = c + col < a.N ? c + col : a.N - 1;
-        const T *brow = static_cast<const T *>(a.B) + ((int64_t)adapter * a.N + n) * a.R;
-        f32x4 acc[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) acc[t] = f32x4{0, 0, 0, 0};
-        for (int s = 0; s < steps; ++s) {
-            const u32x4 b = load_b<T, VECB>(brow, s * D + E * g, rank);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (t >= subs) break;
-#pragma unroll
-                for (int q = 0; q < P; ++q) {
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(parts + (q * kTile + 16 * t + col) * W + s * D + E * g);
-                    acc[t] = mma<T>(b, v, acc[t]);
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int i = 16 * t + col;
-            if (i >= count) continue;
-            const int64_t at = c + 4 * g;
-            float *y = a.Y + (int64_t)rows[i] * a.ldy + at;
-            if (VECY && at + 4 <= a.N) {
-                f32x4 v = *reinterpret_cast<f32x4 *>(y);
-                v += scale * acc[t];
-                *reinterpret_cast<f32x4 *>(y) = v;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (at + j < a.N) y[j] += scale * acc[t][j];
-            }
-        }
-    }
+    x.run(a, parts, rows, adapter, count, rank, scale, c, c1);
 }
 
+// Column tiles of a wave
+constexpr int wide_tiles(int steps) { return steps <= 1 ? 4 : (steps <= 4 ? 2 : 1); }
+
 struct Plan {
-    bool small;
+    bool small, wide;                   // wide: four tiles of columns a wave, else one
     int64_t tiles;                      // at most
-    int splits, nt;
+    int splits, nt, steps;
     int64_t kper, nper;
     size_t order, list, ntiles, V, bytes;
     int Rp;
@@ -343,23 +438,31 @@ struct Plan {
 
 Plan plan_of(int64_t M, const mxs_lora &s) {
     Plan p{};
+    const int es = s.dtype == MXS_BF16 ? 2 : 4;
     p.small = M <= kSmall;
-    p.tiles = p.small ? M : ceil_div(M, (int64_t)kTile) + (s.n < M ? s.n : M);
+    const int64_t full = ceil_div(M, (int64_t)kTile), own = s.n < M ? s.n : M;
+    p.tiles = p.small ? M : full + own;
+    const int64_t busy = own > full ? own : full;           // tiles to expect
     p.Rp = (s.R + 15) / 16 * 16;
     p.nt = p.Rp <= 16 ? 1 : (p.Rp <= 32 ? 2 : 4);
+    p.steps = (int)ceil_div(s.R, es == 2 ? 32 : 16);
+    p.steps = p.steps <= 2 ? p.steps : (p.steps <= 4 ? 4 : 8);
     const int64_t ranks = ceil_div(p.Rp, 16 * p.nt);
-    // slices of K until the chip is busy: at least 512 of K each, few where they are read by many
-    const int64_t busy = p.small ? M : ceil_div(M, (int64_t)kTile);
-    int64_t want = ceil_div(512, busy * ranks), most = p.small ? 16 : 4;
-    want = want < most ? want : most;
-    const int64_t fit = ceil_div(s.K, 512);
+    // slices of K until the chip is filled, each a turn of the four waves or more, and
+    // V's partial sums below a thirty-second of X
+    const int64_t turn = 1024 / es;
+    int64_t want = ceil_div(1024, busy * ranks);
+    const int64_t fit = ceil_div(s.K, turn), most = p.small ? 16 : s.K * es / (32 * p.Rp);
     want = want < fit ? want : fit;
-    want = want < 1 ? 1 : want;
-    p.kper = ceil_div(ceil_div(s.K, want), 128) * 128;
+    want = want < most ? want : most;
+    want = want < 1 ? 1 : (want > 64 ? 64 : want);
+    p.kper = ceil_div(ceil_div(s.K, want), turn) * turn;
     p.splits = (int)ceil_div(s.K, p.kper);
-    // columns of Y: 64 and more until there are 1024 workgroups
-    p.nper = 64;
-    while (p.nper < 1024 && busy * ceil_div(s.N, 2 * p.nper) >= 1024) p.nper *= 2;
+    // columns of Y a workgroup takes: 64 where that leaves the chip unfilled, else four
+    // tiles a wave, and several turns of them from 4096 workgroups on
+    p.wide = busy * ceil_div(s.N, (int64_t)256) >= 512;
+    p.nper = p.wide ? 512 : 64;
+    while (p.wide && p.nper < 2048 && busy * ceil_div(s.N, 2 * p.nper) >= 4096) p.nper *= 2;
     while (ceil_div(s.N, p.nper) > 65535) p.nper *= 2;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -377,6 +480,13 @@ Plan plan_of(int64_t M, const mxs_lora &s) {
     return p;
 }
 
+template <typename T, int STEPS>
+void go_expand(const LoraArgs &a, const Plan &p, hipStream_t st) {
+    const dim3 grid((unsigned)p.tiles, (unsigned)ceil_div(a.N, p.nper));
+    if (p.wide) hipLaunchKernelGGL((k_lora_expand<T, STEPS, wide_tiles(STEPS)>), grid, dim3(256), 0, st, a, p.small);
+    else hipLaunchKernelGGL((k_lora_expand<T, STEPS, 1>), grid, dim3(256), 0, st, a, p.small);
+}
+
 template <typename T>
 hipError_t go(LoraArgs a, const Plan &p, hipStream_t st) {
     hipError_t e;
@@ -390,14 +500,13 @@ hipError_t go(LoraArgs a, const Plan &p, hipStream_t st) {
     else if (p.nt == 2) hipLaunchKernelGGL((k_lora_shrink<T, 2>), gs, dim3(256), ls, st, a, p.small);
     else hipLaunchKernelGGL((k_lora_shrink<T, 4>), gs, dim3(256), ls, st, a, p.small);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    constexpr int D = Parts<T>::D, E = Parts<T>::E;
-    const size_t le = (size_t)Parts<T>::P * kTile * (ceil_div(a.R, D) * D + E) * sizeof(T);
-    const dim3 ge((unsigned)p.tiles, (unsigned)ceil_div(a.N, p.nper));
-    const bool vecb = a.R % E == 0, vecy = reinterpret_cast<uintptr_t>(a.Y) % 16 == 0 && a.ldy % 4 == 0;
-    if (vecb && vecy) hipLaunchKernelGGL((k_lora_expand<T, true, true>), ge, dim3(256), le, st, a, p.small);
-    else if (vecb) hipLaunchKernelGGL((k_lora_expand<T, true, false>), ge, dim3(256), le, st, a, p.small);
-    else if (vecy) hipLaunchKernelGGL((k_lora_expand<T, false, true>), ge, dim3(256), le, st, a, p.small);
-    else hipLaunchKernelGGL((k_lora_expand<T, false, false>), ge, dim3(256), le, st, a, p.small);
+    switch (p.steps) {
+        case 1: go_expand<T, 1>(a, p, st); break;
+        case 2: go_expand<T, 2>(a, p, st); break;
+        case 4: go_expand<T, 4>(a, p, st); break;
+        default:                            // fp32 ranks above 64
+            if constexpr (sizeof(T) == 4) go_expand<T, 8>(a, p, st);
+    }
     return hipGetLastError();
 }
 
