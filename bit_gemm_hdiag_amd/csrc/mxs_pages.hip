@@ -13,7 +13,7 @@ namespace mxs {
 
 namespace {
 
-constexpr int kChunkPages = 4096;       // pages of a bitmap chunk: 64 words of 64 bits
+constexpr int kChunkPages = 1024;       // pages of a bitmap chunk: 16 of each lane
 
 struct Planes {
     uint8_t *c[2], *s[2];               // codes and scales of K and V
@@ -30,20 +30,79 @@ Planes planes_of(const mxs_kv4_cache &c) {
     return p;
 }
 
+// n / d for n < 65536, d <= 65536: m = ceil(2^32 / d), 0 for d = 1
+struct Div16 {
+    uint32_t m, d;
+};
+Div16 div16(uint32_t d) { return Div16{d <= 1 ? 0u : (uint32_t)((0x100000000ull + d - 1) / d), d ? d : 1u}; }
+__device__ __forceinline__ uint32_t quot(uint32_t n, Div16 v) { return v.m ? __umulhi(n, v.m) : n; }
+
 // ---------------------------------------------------------------------- copy
+// Bound by HBM: 131072 tokens of 8 heads of 128 take 59 us (4.9 TB/s, the rate of
+// a plain copy). A workgroup takes whole tokens of one plane, or a chunk of one: WPT
+// code words a thread, loaded before the first is stored, and their scale bytes,
+// eight at a time where a token has a multiple of eight. Four words a thread pass the
+// caches by (68 us if not); one, where the tokens are few, does not.
+template <bool WIDE, int WPT>
 __global__ __launch_bounds__(256) void k_kv4_copy(Planes to, const int64_t *to_slots, Planes from,
-                                                  const int64_t *from_slots, int64_t T) {
-    const int nb = to.nb;
-    const int64_t total = T * nb, step = (int64_t)gridDim.x * 256;
-    const int p = blockIdx.y;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += step) {
-        const int64_t t = e / nb;
-        const int u = (int)(e - t * nb);
-        const int64_t d = to_slots[t], s = from_slots[t];
-        if ((uint64_t)d >= (uint64_t)to.slots || (uint64_t)s >= (uint64_t)from.slots) continue;
-        reinterpret_cast<u32x4 *>(to.c[p])[d * nb + u] = reinterpret_cast<const u32x4 *>(from.c[p])[s * nb + u];
-        to.s[p][d * nb + u] = from.s[p][s * nb + u];
+                                                  const int64_t *from_slots, int64_t T, int TB, Div16 chunk) {
+    const int nb = to.nb, p = blockIdx.y;
+    const int64_t t0 = (int64_t)blockIdx.x * TB;
+    const int nt = T - t0 < TB ? (int)(T - t0) : TB;
+    const uint32_t w0 = blockIdx.z * chunk.d;
+    int64_t d[WPT], s[WPT];
+    u32x4 v[WPT];
+    uint8_t b[WPT];
+#pragma unroll
+    for (int k = 0; k < WPT; ++k) {
+        const uint32_t e = threadIdx.x + 256u * k, tl = quot(e, chunk), w = w0 + e - tl * chunk.d;
+        const bool on = tl < (uint32_t)nt && w < (uint32_t)nb;
+        d[k] = on ? to_slots[t0 + tl] : -1;
+        s[k] = on ? from_slots[t0 + tl] : -1;
+        if ((uint64_t)d[k] >= (uint64_t)to.slots || (uint64_t)s[k] >= (uint64_t)from.slots) d[k] = -1;
+        d[k] = d[k] < 0 ? -1 : d[k] * nb + w;
+        s[k] = s[k] * nb + w;
     }
+#pragma unroll
+    for (int k = 0; k < WPT; ++k)
+        if (d[k] >= 0) {
+            const u32x4 *x = reinterpret_cast<const u32x4 *>(from.c[p]) + s[k];
+            v[k] = WPT > 1 ? __builtin_nontemporal_load(x) : *x;
+            if constexpr (!WIDE) b[k] = from.s[p][s[k]];
+        }
+    uint64_t wide = 0;
+    int64_t wd = -1;
+    if constexpr (WIDE) {
+        const uint32_t e = 8u * threadIdx.x, tl = quot(e, chunk), w = w0 + e - tl * chunk.d;
+        if (e < 256 * WPT && tl < (uint32_t)nt && w < (uint32_t)nb) {
+            const int64_t td = to_slots[t0 + tl], ts = from_slots[t0 + tl];
+            if ((uint64_t)td < (uint64_t)to.slots && (uint64_t)ts < (uint64_t)from.slots) {
+                wd = td * nb + w;
+                wide = *reinterpret_cast<const uint64_t *>(from.s[p] + ts * nb + w);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < WPT; ++k)
+        if (d[k] >= 0) {
+            u32x4 *x = reinterpret_cast<u32x4 *>(to.c[p]) + d[k];
+            if constexpr (WPT > 1) __builtin_nontemporal_store(v[k], x);
+            else *x = v[k];
+            if constexpr (!WIDE) to.s[p][d[k]] = b[k];
+        }
+    if (WIDE && wd >= 0) *reinterpret_cast<uint64_t *>(to.s[p] + wd) = wide;
+}
+
+template <int WPT>
+void copy_go(const Planes &to, const int64_t *to_slots, const Planes &from, const int64_t *from_slots, int64_t T,
+             hipStream_t st) {
+    const int nb = to.nb, most = 256 * WPT, tb = nb < most ? most / nb : 1;
+    const Div16 chunk = div16(nb < most ? nb : most);
+    const dim3 grid((unsigned)ceil_div(T, (int64_t)tb), 2, (unsigned)ceil_div(nb, (int64_t)chunk.d));
+    if (nb % 8 == 0)
+        hipLaunchKernelGGL((k_kv4_copy<true, WPT>), grid, dim3(256), 0, st, to, to_slots, from, from_slots, T, tb, chunk);
+    else
+        hipLaunchKernelGGL((k_kv4_copy<false, WPT>), grid, dim3(256), 0, st, to, to_slots, from, from_slots, T, tb, chunk);
 }
 
 // ---------------------------------------------------------------------- fork
@@ -66,7 +125,7 @@ __global__ __launch_bounds__(256) void k_kv4_fork(int32_t *refs, int32_t *table,
 // Workspace: a bitmap of the free pages, their number in each chunk, the pages
 // that each sequence needs (-1: its row is too short), and the pages granted.
 struct Reserve {
-    uint64_t *map;
+    uint16_t *map;
     int32_t *counts, *need, *grant;
     int chunks;
 };
@@ -79,10 +138,10 @@ size_t reserve_layout(int64_t pages, int64_t B, void *ws, Reserve *r) {
         at += (bytes + 15) / 16 * 16;
         return o;
     };
-    const size_t map = take(chunks * 64 * 8), counts = take(chunks * 4), need = take(B * 4), grant = take(pages * 4);
+    const size_t map = take(chunks * 64 * 2), counts = take(chunks * 4), need = take(B * 4), grant = take(pages * 4);
     if (r) {
         uint8_t *w = static_cast<uint8_t *>(ws);
-        r->map = reinterpret_cast<uint64_t *>(w + map);
+        r->map = reinterpret_cast<uint16_t *>(w + map);
         r->counts = reinterpret_cast<int32_t *>(w + counts);
         r->need = reinterpret_cast<int32_t *>(w + need);
         r->grant = reinterpret_cast<int32_t *>(w + grant);
@@ -158,22 +217,53 @@ __global__ __launch_bounds__(256) void k_kv4_need(SeqArgs a, Reserve r, int seq_
     }
     const int chunk = ((int)blockIdx.x - seq_groups) * 4 + wave;
     if (chunk >= r.chunks) return;
-    uint64_t mine = 0;
-    const int64_t p0 = (int64_t)chunk * kChunkPages;
-    for (int k = 0; k < 64; ++k) {
-        const int64_t p = p0 + k * 64 + lane;
-        const uint64_t bits = __ballot(p < a.pages && a.refs[p < a.pages ? p : 0] == 0);
-        if (lane == k) mine = bits;
+    // 16 pages a lane, all loaded at once
+    const int64_t p0 = (int64_t)chunk * kChunkPages + 16 * lane;
+    uint32_t mine = 0;
+    if (p0 + 16 <= a.pages) {
+        int4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) __builtin_memcpy(&v[k], a.refs + p0 + 4 * k, 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            mine |= ((v[k].x == 0) | (v[k].y == 0) << 1 | (v[k].z == 0) << 2 | (v[k].w == 0) << 3) << 4 * k;
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < 16 && p0 + k < a.pages; ++k) mine |= (uint32_t)(a.refs[p0 + k] == 0) << k;
     }
-    r.map[(int64_t)chunk * 64 + lane] = mine;
-    const int c = wave_sum(__popcll(mine));
+    r.map[(int64_t)chunk * 64 + lane] = (uint16_t)mine;
+    const int c = wave_sum(__popc(mine));
     if (lane == 0) r.counts[chunk] = c;
 }
 
+// n bytes, a multiple of 16, at 16-byte places; the loads of a turn go before its stores
+__device__ __forceinline__ void copy16(uint8_t *to, const uint8_t *from, int64_t n) {
+    for (int64_t e = 16 * threadIdx.x; e < n; e += 16 * 1024) {
+        u32x4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (e + 4096 * k < n) v[k] = *reinterpret_cast<const u32x4 *>(from + e + 4096 * k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (e + 4096 * k < n) *reinterpret_cast<u32x4 *>(to + e + 4096 * k) = v[k];
+    }
+}
+// n bytes at any places
+__device__ __forceinline__ void copy_bytes(uint8_t *to, const uint8_t *from, int64_t n) {
+    int64_t done = 0;
+    if ((reinterpret_cast<uintptr_t>(to) | reinterpret_cast<uintptr_t>(from)) % 8 == 0) {
+        done = n / 8 * 8;
+        for (int64_t e = 8 * threadIdx.x; e < done; e += 8 * 256)
+            *reinterpret_cast<uint64_t *>(to + e) = *reinterpret_cast<const uint64_t *>(from + e);
+    }
+    for (int64_t e = done + threadIdx.x; e < n; e += 256) to[e] = from[e];
+}
+
 // A workgroup a sequence: its ranks among the free pages, the pages themselves,
-// then its table entries, the copy of a shared page's tokens, and its slots.
+// then its table entries, its slots, and the copy of a shared page's tokens.
 __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes pl, int64_t *slots, int32_t *lens_out) {
-    __shared__ int part[256], sums[4], found[2], old_last, new_last;
+    __shared__ int sums[3][4], found[2], old_last, new_last;
+    __shared__ int32_t few[256];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t b = blockIdx.x;
     int len, n;
@@ -182,23 +272,24 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
     const int c0 = a.cu[b] < 0 ? 0 : a.cu[b];
     const int need = r.need[b];
     int32_t *row = a.table + b * a.ldt;
-    // pages that earlier sequences need, and all that are free
-    int before = 0, avail = 0;
-    if (need > 0) {
-        for (int64_t i = tid; i < b; i += 256) before += r.need[i] > 0 ? r.need[i] : 0;
-        for (int i = tid; i < r.chunks; i += 256) avail += r.counts[i];
-    }
-    before = wave_sum(before);
-    avail = wave_sum(avail);
-    if (lane == 0) {
-        sums[wave] = before;
-        part[wave] = avail;
-    }
     if (tid == 0) old_last = new_last = -1;
-    __syncthreads();
-    before = sums[0] + sums[1] + sums[2] + sums[3];
-    avail = part[0] + part[1] + part[2] + part[3];
-    __syncthreads();
+    int before = 0, avail = 0, mine = 0, upto = 0;
+    const int per = (r.chunks + 255) / 256;
+    if (need > 0) {
+        // pages that earlier sequences need, and all that are free, a run of chunks a thread
+        for (int64_t i = tid; i < b; i += 256) before += r.need[i] > 0 ? r.need[i] : 0;
+        for (int i = tid * per; i < (tid + 1) * per && i < r.chunks; ++i) mine += r.counts[i];
+        before = wave_sum(before);
+        upto = wave_scan(mine);
+        if (lane == 63) {
+            sums[0][wave] = before;
+            sums[1][wave] = upto;
+        }
+        __syncthreads();
+        before = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
+        avail = sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
+        for (int w = 0; w < wave; ++w) upto += sums[1][w];
+    }
     if (need < 0 || (need > 0 && (int64_t)before + need > avail)) {
         for (int64_t j = tid; j < nj; j += 256)
             if (row[j0 + j] < -1) row[j0 + j] = -2 - row[j0 + j];
@@ -207,32 +298,26 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
         return;
     }
     if (need > 0) {
-        // the chunk that holds rank `before`: each thread sums a run of chunks
-        const int per = (r.chunks + 255) / 256;
-        int s = 0;
-        for (int i = tid * per; i < (tid + 1) * per && i < r.chunks; ++i) s += r.counts[i];
-        part[tid] = s;
-        __syncthreads();
-        int up = 0;
-        for (int i = 0; i < tid; ++i) up += part[i];
-        if (up <= before && before < up + s) {
-            int c = tid * per;
+        // the chunk that holds rank `before`, then the pages of the ranks from there
+        if (upto - mine <= before && before < upto) {
+            int c = tid * per, up = upto - mine;
             while (up + r.counts[c] <= before) up += r.counts[c++];
             found[0] = c;
             found[1] = up;
         }
         __syncthreads();
+        int32_t *grant = need <= 256 ? few : r.grant + before;
         if (wave == 0) {
-            int at = found[1];
-            for (int c = found[0]; c < r.chunks && at < before + need; ++c) {
-                uint64_t bits = r.map[(int64_t)c * 64 + lane];
-                const int cnt = __popcll(bits), inc = wave_scan(cnt);
+            int at = found[1] - before;
+            for (int c = found[0]; c < r.chunks && at < need; ++c) {
+                uint32_t bits = r.map[(int64_t)c * 64 + lane];
+                const int cnt = __popc(bits), inc = wave_scan(cnt);
                 int rank = at + inc - cnt;
-                const int32_t p = c * kChunkPages + lane * 64;
+                const int32_t p = c * kChunkPages + lane * 16;
                 while (bits) {
-                    const int k = __ffsll((long long)bits) - 1;
+                    const int k = __ffs((int)bits) - 1;
                     bits &= bits - 1;
-                    if (rank >= before && rank < before + need) r.grant[rank] = p + k;
+                    if (rank >= 0 && rank < need) grant[rank] = p + k;
                     ++rank;
                 }
                 at += __shfl(inc, 63);
@@ -240,18 +325,18 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
         }
         __syncthreads();
         // entries in order take the granted pages in order
-        int at = before;
+        int at = 0;
         for (int64_t t0 = 0; t0 < nj; t0 += 256) {
             const int64_t j = t0 + tid;
             const int32_t v = j < nj ? row[j0 + j] : 0;
             const uint64_t takes = __ballot(v < 0);
-            if (lane == 0) sums[wave] = __popcll(takes);
+            if (lane == 0) sums[2][wave] = __popcll(takes);
             __syncthreads();
             int rank = at + __popcll(takes & ((1ull << lane) - 1));
-            for (int w = 0; w < wave; ++w) rank += sums[w];
-            at += sums[0] + sums[1] + sums[2] + sums[3];
+            for (int w = 0; w < wave; ++w) rank += sums[2][w];
+            at += sums[2][0] + sums[2][1] + sums[2][2] + sums[2][3];
             if (v < 0) {
-                const int32_t p = r.grant[rank];
+                const int32_t p = grant[rank];
                 row[j0 + j] = p;
                 a.refs[p] = 1;
                 if (v < -1) {
@@ -265,29 +350,31 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
             __syncthreads();
         }
     }
-    // tokens of the last page, before the new ones
-    if (new_last >= 0) {
-        const int64_t units = (int64_t)(len % a.page_size) * pl.nb;
-        const int64_t from = (int64_t)old_last * a.page_size * pl.nb, to = (int64_t)new_last * a.page_size * pl.nb;
-        for (int p = 0; p < 2; ++p)
-            for (int64_t u = tid; u < units; u += 256) {
-                reinterpret_cast<u32x4 *>(pl.c[p])[to + u] = reinterpret_cast<const u32x4 *>(pl.c[p])[from + u];
-                pl.s[p][to + u] = pl.s[p][from + u];
-            }
-    }
     for (int i = tid; i < n; i += 256) {
         const int64_t t = (int64_t)len + i, j = t / a.page_size;
         slots[c0 + i] = (int64_t)row[j] * a.page_size + (t - j * a.page_size);
     }
     if (tid == 0) lens_out[b] = len + n;
+    // tokens of a shared last page before the new ones: one run of bytes a plane
+    if (need > 0 && new_last >= 0) {
+        const int64_t units = (int64_t)(len % a.page_size) * pl.nb, unit = (int64_t)a.page_size * pl.nb;
+        for (int p = 0; p < 2; ++p) {
+            copy16(pl.c[p] + 16 * new_last * unit, pl.c[p] + 16 * old_last * unit, 16 * units);
+            copy_bytes(pl.s[p] + new_last * unit, pl.s[p] + old_last * unit, units);
+        }
+    }
 }
 
 // ------------------------------------------------------------------- compact
-// A workgroup a sequence. Kept tokens are moved in ascending order, a thread a
-// block column: number i lands where no later token is read, because path[i] >= i.
+// A workgroup a sequence. The slots of 256 kept tokens are found first, then tokens
+// are moved 1024 code words (with their scale bytes) at a time, in ascending
+// order: all are read before the first is written, and what a later turn reads no
+// earlier one has written, because path[i] >= i.
 __global__ __launch_bounds__(256) void k_kv4_compact(SeqArgs a, Planes pl, const int32_t *path, const int32_t *count,
                                                      int32_t *lens_out) {
+    __shared__ int32_t from[256], to[256];
     const int64_t b = blockIdx.x;
+    const int tid = threadIdx.x;
     int len = a.lens[b], c0 = a.cu[b], c1 = a.cu[b + 1];
     c0 = c0 < 0 ? 0 : c0;
     c1 = c1 > a.total ? (int)a.total : c1;
@@ -296,27 +383,56 @@ __global__ __launch_bounds__(256) void k_kv4_compact(SeqArgs a, Planes pl, const
     kept = kept < 0 ? 0 : (kept > n ? n : kept);
     const bool moves = len >= n;
     __syncthreads();                            // every thread has read lens before it may be written
-    if (moves) {
-        const int64_t base = (int64_t)len - n;
-        const int32_t *row = a.table + b * a.ldt;
-        auto slot = [&](int64_t t) -> int64_t {
-            const int64_t j = t / a.page_size;
-            const int32_t p = j < a.ldt ? row[j] : -1;
-            return p < 0 || p >= a.pages ? -1 : (int64_t)p * a.page_size + (t - j * a.page_size);
-        };
-        for (int u = threadIdx.x; u < 2 * pl.nb; u += 256) {
-            const int p = u >= pl.nb, w = p ? u - pl.nb : u;
-            for (int i = 0; i < kept; ++i) {
-                const int f = path[c0 + i];
-                if (f <= i || f >= n) continue;
-                const int64_t s = slot(base + f), d = slot(base + i);
-                if (s < 0 || d < 0) continue;
-                reinterpret_cast<u32x4 *>(pl.c[p])[d * pl.nb + w] = reinterpret_cast<const u32x4 *>(pl.c[p])[s * pl.nb + w];
-                pl.s[p][d * pl.nb + w] = pl.s[p][s * pl.nb + w];
-            }
+    if (tid == 0) lens_out[b] = moves ? len - n + kept : len;
+    if (!moves) return;
+    const int64_t base = (int64_t)len - n;
+    const int32_t *row = a.table + b * a.ldt;
+    auto slot = [&](int64_t t) -> int32_t {
+        const int64_t j = t / a.page_size;
+        const int32_t p = j < a.ldt ? row[j] : -1;
+        return p < 0 || p >= a.pages ? -1 : (int32_t)(p * a.page_size + (t - j * a.page_size));
+    };
+    const int words = 2 * pl.nb;                // of a token: K's, then V's
+    for (int i0 = 0; i0 < kept; i0 += 256) {
+        const int m = kept - i0 < 256 ? kept - i0 : 256;
+        if (tid < m) {
+            const int f = path[c0 + i0 + tid];
+            const bool on = f > i0 + tid && f < n;
+            const int32_t s = on ? slot(base + f) : -1, d = on ? slot(base + i0 + tid) : -1;
+            from[tid] = d < 0 ? -1 : s;
+            to[tid] = d;
         }
+        __syncthreads();
+        for (int64_t e0 = 0; e0 < (int64_t)m * words; e0 += 1024) {
+            u32x4 v[4];
+            uint8_t sc[4];
+            int64_t d[4];
+            int pk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t e = e0 + tid + 256 * k;
+                d[k] = -1;
+                if (e < (int64_t)m * words) {
+                    const int i = (int)(e / words), u = (int)(e - (int64_t)i * words), p = u >= pl.nb, w = p ? u - pl.nb : u;
+                    const int32_t s = from[i];
+                    if (s >= 0) {
+                        pk[k] = p;
+                        d[k] = (int64_t)to[i] * pl.nb + w;
+                        v[k] = reinterpret_cast<const u32x4 *>(pl.c[p])[(int64_t)s * pl.nb + w];
+                        sc[k] = pl.s[p][(int64_t)s * pl.nb + w];
+                    }
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (d[k] >= 0) {
+                    reinterpret_cast<u32x4 *>(pl.c[pk[k]])[d[k]] = v[k];
+                    pl.s[pk[k]][d[k]] = sc[k];
+                }
+        }
+        __syncthreads();
     }
-    if (threadIdx.x == 0) lens_out[b] = moves ? len - n + kept : len;
 }
 
 // ------------------------------------------------------------------- release
@@ -349,9 +465,10 @@ size_t kv4_reserve_workspace(int64_t pages, int64_t B) { return reserve_layout(p
 hipError_t launch_kv4_copy(const mxs_kv4_cache &dst, const int64_t *dst_slots, const mxs_kv4_cache &src,
                            const int64_t *src_slots, int64_t T, hipStream_t st) {
     const Planes to = planes_of(dst), from = planes_of(src);
-    const int64_t g = ceil_div(T * to.nb, (int64_t)256);
-    hipLaunchKernelGGL(k_kv4_copy, dim3((unsigned)(g < 65536 ? g : 65536), 2), dim3(256), 0, st, to, dst_slots, from,
-                       src_slots, T);
+    // one word a thread until the chip is full four times over (as the append): 2.6
+    // against 4.2 us at 1901 tokens of 3 heads of 96
+    if (2 * T * to.nb < 4 * 256 * 2048) copy_go<1>(to, dst_slots, from, src_slots, T, st);
+    else copy_go<4>(to, dst_slots, from, src_slots, T, st);
     return hipGetLastError();
 }
 

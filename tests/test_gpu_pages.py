@@ -293,6 +293,13 @@ def test_copy(mx, H, D, page, T, same):
         a.same()
 
 
+@pytest.mark.parametrize("H,D,page,T", [(8, 128, 64, 40000), (3, 96, 17, 130000), (64, 1024, 3, 600), (33, 1024, 5, 5),
+                                        (64, 1024, 3, 7)])
+def test_copy_of_many_words(mx, H, D, page, T):
+    """Four words a thread, tokens of more words than a workgroup takes, with scale bytes by eight and one by one."""
+    test_copy(mx, H, D, page, T, False)
+
+
 def test_copy_of_nothing(mx):
     a = Pool(mx, 2, 4, 1, 32, 1, 1, 1)
     none = dev([], torch.int64)
