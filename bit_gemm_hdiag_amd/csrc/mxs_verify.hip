@@ -194,6 +194,15 @@ __device__ __forceinline__ int wave_min(int v) {
 
 __device__ __forceinline__ int64_t ceil_div_dev(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Where a walk ended: the row of the last kept node, whether its chunks are summed,
+// and what was taken out of it: S q, or `gone` tokens
+struct State {
+    double S;
+    int32_t cur, gone;
+    int32_t sums;           // 0: nothing to draw (no node); else what is left to sum
+};
+enum { kNone = 0, kSummed = 1, kLeaf = 2, kRemainder = 3 };
+
 struct Args {
     const void *logits;
     int64_t ldl, V, B, total, ldd;
@@ -205,6 +214,9 @@ struct Args {
     int64_t *next;
     float *mx;              // [total, C] maximum of each chunk
     double *sum;            // [total, C] its weights' sum; greedy rows: index of the maximum
+    double *rest;           // [B, C] sums of a remainder's chunks
+    struct State *state;    // [B] where the walk ended
+    int32_t *gone;          // [total] tokens taken out of that node's row
     int C, chunk, max_n, replacement;
     bool direct;            // grid of k_row_stats: (chunk, node, sequence) instead of (chunk, row)
 };
@@ -223,40 +235,24 @@ __device__ __forceinline__ int64_t sequence_of(const Args &a, int64_t row, int l
 
 __device__ __forceinline__ double clean(float q) { return q > 0.f && q < INFINITY ? (double)q : 0.0; }
 
-// A workgroup a chunk of a row: its maximum, and the sum of the weights against it
-// (greedy rows: the lowest index of the maximum). A wave takes G pieces, all loaded
-// before the first is used. The piece that passes the end of the row is loaded from
-// 1024 logits before the end, less those that the piece before it has.
-// Bound by fp64 arithmetic: 17 instructions a logit.
-template <typename T, int G>
-__global__ __launch_bounds__(256) void k_row_stats(Args a) {
-    __shared__ float ms[4];
-    __shared__ double ss[4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x;
-    int64_t row, b;
-    if (a.direct) {
-        b = blockIdx.z;
-        const int c0 = a.cu[b], c1 = a.cu[b + 1];
-        row = (int64_t)c0 + blockIdx.y;
-        if (c0 < 0 || row >= c1 || row >= a.total) return;
-    } else {
-        row = blockIdx.y + (int64_t)blockIdx.z * 65535;
-        if (row >= a.total) return;
-        b = sequence_of(a, row, lane);
-        if (b >= a.B) return;
-    }
+// A chunk of a row, by a workgroup of 256 or (WAVE) by one wave: its maximum, and the
+// sum of the weights against it (greedy rows: the lowest index of the maximum). A wave
+// takes G pieces, all loaded before the first is used. The piece that passes the end of the row is
+// loaded from 1024 logits before the end, less those that the piece before it has.
+template <typename T, int G, bool WAVE>
+__device__ __forceinline__ void chunk_stats(const Args &a, int64_t row, int c, float t) {
+    constexpr int WAVES = WAVE ? 1 : 4;
+    const int lane = threadIdx.x & 63, wave = WAVE ? 0 : threadIdx.x >> 6;
     const T *p = static_cast<const T *>(a.logits) + row * a.ldl;
-    const int V = (int)a.V, from = (c * 4 * G + wave) * kPiece;      // pieces from, from + 4, ..
+    const int V = (int)a.V, from = (c * WAVES * G + wave) * kPiece;  // pieces from, from + WAVES, ..
     Piece<T> w[G];
     if (V >= kPiece) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            const int at = from + 4 * g * kPiece;
+            const int at = from + WAVES * g * kPiece;
             if (at < V) w[g].load(p + (at + kPiece <= V ? at : V - kPiece), lane);
         }
     }
-    const float t = a.temperature ? a.temperature[b] : 1.f;
     const bool greedy = !(t > 0.f);
     const Scale sc(t);
     float m = -INFINITY;
@@ -266,7 +262,7 @@ __global__ __launch_bounds__(256) void k_row_stats(Args a) {
         float v[G][16];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            const int at = from + 4 * g * kPiece;
+            const int at = from + WAVES * g * kPiece;
             if (at >= V) break;
             w[g].get(v[g]);
             if (at + kPiece > V) {
@@ -281,7 +277,7 @@ __global__ __launch_bounds__(256) void k_row_stats(Args a) {
         if (greedy) {
 #pragma unroll
             for (int g = G - 1; g >= 0; --g) {
-                const int at = from + 4 * g * kPiece, first = at + kPiece <= V ? at : V - kPiece;
+                const int at = from + WAVES * g * kPiece, first = at + kPiece <= V ? at : V - kPiece;
                 if (at >= V) continue;
 #pragma unroll
                 for (int k = 15; k >= 0; --k) best = v[g][k] == m ? first + piece_index<T>(lane, k) : best;
@@ -289,7 +285,7 @@ __global__ __launch_bounds__(256) void k_row_stats(Args a) {
         } else if (e.plain()) {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                if (from + 4 * g * kPiece >= V) break;
+                if (from + WAVES * g * kPiece >= V) break;
 #pragma unroll
                 for (int k = 0; k < 16; k += 4) {
                     double r[4];
@@ -308,12 +304,21 @@ __global__ __launch_bounds__(256) void k_row_stats(Args a) {
     if (!greedy && !(V >= kPiece && e.plain())) {         // few tokens, or what the quick sum cannot take
 #pragma unroll 1
         for (int g = 0; g < G; ++g) {
-            const int at = from + 4 * g * kPiece;
+            const int at = from + WAVES * g * kPiece;
 #pragma unroll 1
             for (int i = at + lane; i < at + kPiece && i < V; i += 64) s += e(load1<T>(p + i));
         }
     }
     s = greedy ? (double)wave_min(best) : wave_sum(s);
+    if constexpr (WAVE) {
+        if (lane == 0) {
+            a.mx[row * a.C + c] = m;
+            a.sum[row * a.C + c] = s;
+        }
+        return;
+    }
+    __shared__ float ms[4];
+    __shared__ double ss[4];
     if (lane == 0) {
         ms[wave] = m;
         ss[wave] = s;
@@ -331,6 +336,97 @@ __global__ __launch_bounds__(256) void k_row_stats(Args a) {
         a.mx[row * a.C + c] = mm;
         a.sum[row * a.C + c] = r;
     }
+}
+
+// The chunks of every node that has children (16 trees of 64 nodes over 128000 bf16:
+// 64 us with the leaves, 51 without). 18 instructions a logit, most of them fp64: 163
+// rows of 128000 bf16 take 25 us, of which 10 are arithmetic at its full rate and 8 the
+// bytes; the rest is the way to a wave's first logits (cu, parents, row), which the
+// four waves of a SIMD do not hide.
+template <typename T, int G, bool WAVE>
+__global__ __launch_bounds__(256) void k_row_stats(Args a) {
+    int64_t row, b;
+    if (a.direct) {
+        b = blockIdx.z;
+        row = (int64_t)a.cu[b] + blockIdx.y;
+    } else {
+        row = blockIdx.y + (int64_t)blockIdx.z * 65535;
+        if (row >= a.total) return;
+        b = sequence_of(a, row, threadIdx.x & 63);
+        if (b >= a.B) return;
+    }
+    const int c0 = a.cu[b], c1 = a.cu[b + 1] < a.total ? a.cu[b + 1] : (int)a.total;
+    const int n = c1 - c0 < a.max_n ? c1 - c0 : a.max_n, i = (int)(row - c0);
+    if (c0 < 0 || i >= n) return;
+    bool parent = false;
+    if (a.parents) {
+        for (int j = i + 1 + threadIdx.x; j < n; j += 256) parent |= a.parents[c0 + j] == i;
+        parent = __syncthreads_or(parent);
+    } else {
+        parent = i + 1 < n;
+    }
+    if (!parent) return;
+    const int c = WAVE ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if (c < a.C) chunk_stats<T, G, WAVE>(a, row, c, a.temperature ? a.temperature[b] : 1.f);
+}
+
+// What the walks left to be summed, before the next tokens are drawn: the chunks of
+// a last node without children, or those of max(e - S q, 0)
+template <typename T, int G>
+__global__ __launch_bounds__(256) void k_rest(Args a) {
+    __shared__ double ss[4];
+    const int64_t b = blockIdx.y;
+    const State w = a.state[b];
+    if (w.sums < kLeaf) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x;
+    const int64_t row = w.cur;
+    const float t = a.temperature ? a.temperature[b] : 1.f;
+    if (w.sums == kLeaf) {
+        chunk_stats<T, G, false>(a, row, c, t);
+        return;
+    }
+    const T *p = static_cast<const T *>(a.logits) + row * a.ldl;
+    const float *q = a.draft + row * a.ldd;
+    const Weight e(wave_max(lane < a.C ? a.mx[row * a.C + lane] : -INFINITY), Scale(t));
+    const int V = (int)a.V;
+    double s = 0.0;
+    if (V >= kPiece && e.plain()) {
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+            const int at = (c * 4 * G + wave + 4 * g) * kPiece, base = at + kPiece <= V ? at : V - kPiece;
+            if (at >= V) break;
+            Piece<T> w16;
+            w16.load(p + base, lane);
+            f32x4 q4[4];
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) __builtin_memcpy(&q4[k / 4], q + base + piece_index<T>(lane, k), 16);
+            float v[16];
+            w16.get(v);
+            if (at != base) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = base + piece_index<T>(lane, k) < at ? -INFINITY : v[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                double r[4];
+                e.raw4(v + k, r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const double x = r[j] - w.S * clean(q4[k / 4][j]);
+                    s += x > 0.0 ? x : 0.0;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (int i = c * a.chunk + (int)threadIdx.x; i < (c + 1) * a.chunk && i < V; i += 256)
+            s += fmax(e(load1<T>(p + i)) - w.S * clean(q[i]), 0.0);
+    }
+    s = wave_sum(s);
+    if (lane == 0) ss[wave] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) a.rest[b * a.C + c] = ((ss[0] + ss[1]) + ss[2]) + ss[3];
 }
 
 // Four consecutive logits (or draft probabilities) at p, of which `left` exist
@@ -355,10 +451,10 @@ __device__ __forceinline__ f32x4 load4(const T *p, int64_t left, float missing) 
 
 // One workgroup a sequence walks its tree. The first wave tries the children; the
 // workgroup prepares what that reads (maximum and sum of every node's row, weight
-// and draft probability of every token), forms the sums of remainders, a wave a
-// piece, and draws the next token: the chunk or piece where the cumulated sum
-// crosses the random number, then the token in it. The code runs once or twice a
-// call, so its loops stay rolled: fetching instructions costs more than running them.
+// and draft probability of every token), and sums a remainder where there is
+// another child to try. The code runs once or twice a call, so its loops stay rolled:
+// fetching instructions costs more than running them (27 against 13 us, with the draw,
+// for 16 trees of 64 nodes).
 template <typename T>
 __global__ __launch_bounds__(1024) void k_walk(Args a) {
     __shared__ float node_m[kMaxNodes], node_q[kMaxNodes];
@@ -366,11 +462,11 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
     __shared__ int node_p[kMaxNodes];             // parent of a node that can be accepted, else -1
     __shared__ int node_best[kMaxNodes], node_x[kMaxNodes];
     __shared__ int gone[kMaxNodes];               // children of the current node that were taken out (no draft)
-    __shared__ double sums[1024], wsum[16];
-    __shared__ int firsts[16], lasts[16];
+    __shared__ int has_child[kMaxNodes];
+    __shared__ double sums[16];
     __shared__ struct {
-        double S, target, before;
-        int cur, kept, gone, sum, at, past;
+        double S;
+        int cur, gone, sum;
     } w;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t b = blockIdx.x;
@@ -385,6 +481,7 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
         if (tid == 0) {
             a.count[b] = 0;
             a.next[b] = -1;
+            a.state[b].sums = kNone;
         }
         return;
     }
@@ -392,9 +489,23 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
     const Scale sc(t);
     const T *logits = static_cast<const T *>(a.logits) + (int64_t)c0 * a.ldl;
     const float *draft = a.draft && !greedy ? a.draft + (int64_t)c0 * a.ldd : nullptr;
-
-    // maximum and sum of every row, from its chunks
-    for (int i = wave; i < n; i += 16) {
+    for (int i = tid; i < n; i += 1024) has_child[i] = 0;
+    __syncthreads();
+    // the tokens' own logits
+    for (int i = tid; i < n; i += 1024) {
+        const int p = a.parents ? a.parents[c0 + i] : i - 1;
+        const int64_t x = a.tokens[c0 + i];
+        const bool below = i > 0 && p >= 0 && p < i, ok = below && x >= 0 && x < a.V;
+        if (below) has_child[p] = 1;
+        node_u[i] = a.uniform[c0 + i];
+        node_p[i] = ok ? p : -1;
+        node_x[i] = ok ? (int)x : -1;
+        node_e[i] = ok && !greedy ? (double)load1<T>(logits + p * a.ldl + x) : 0.0;
+        node_q[i] = ok && draft ? (float)clean(draft[p * a.ldd + x]) : 1.f;
+    }
+    // maximum and sum of every row from its chunks, by the other waves first (rows
+    // without children have none; what is read there is not used)
+    for (int i = 15 - wave; i < n; i += 16) {
         const int64_t at = (int64_t)(c0 + i) * a.C + lane;
         const float mc = lane < a.C ? a.mx[at] : -INFINITY;
         const double zc = lane < a.C ? a.sum[at] : 0.0;
@@ -413,17 +524,6 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
             node_best[i] = m == -INFINITY ? -1 : best;
         }
     }
-    // the tokens' own logits, while the maxima are on their way to LDS
-    for (int i = tid; i < n; i += 1024) {
-        const int p = a.parents ? a.parents[c0 + i] : i - 1;
-        const int64_t x = a.tokens[c0 + i];
-        const bool ok = i > 0 && p >= 0 && p < i && x >= 0 && x < a.V;
-        node_u[i] = a.uniform[c0 + i];
-        node_p[i] = ok ? p : -1;
-        node_x[i] = ok ? (int)x : -1;
-        node_e[i] = ok && !greedy ? (double)load1<T>(logits + p * a.ldl + x) : 0.0;
-        node_q[i] = ok && draft ? (float)clean(draft[p * a.ldd + x]) : 1.f;
-    }
     if (tid == 0) w.gone = 0;
     __syncthreads();
     for (int i = tid; i < n; i += 1024) {
@@ -440,7 +540,7 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
         if (wave == 0) {
             bool sum = false;
             int ngone = w.gone;
-            while (!sum) {
+            for (;;) {
                 // the next child of cur
                 int i = -1;
                 for (int i0 = next_child & ~63; i0 < n && i < 0; i0 += 64) {
@@ -448,7 +548,11 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
                     const uint64_t kids = __ballot(j < n && j >= next_child && node_p[j] == cur);
                     if (kids) i = i0 + __ffsll((long long)kids) - 1;
                 }
-                if (i < 0) break;
+                if (i < 0) {
+                    sum = false;                      // no other child: the draw sums what is left
+                    break;
+                }
+                if (sum) break;
                 next_child = i + 1;
                 const double e = node_e[i], q = (double)node_q[i], u = node_u[i];
                 bool ok;
@@ -485,15 +589,14 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
             if (lane == 0) {
                 w.S = S;
                 w.cur = cur;
-                w.kept = kept;
                 w.gone = ngone;
                 w.sum = sum;
             }
         }
         __syncthreads();
         if (!w.sum) break;
-        // the remainder's sum, piece by piece, four values of a lane at a time; the
-        // next four are loaded before these are used
+        // the remainder's sum, a wave a piece, four values of a lane at a time; the next
+        // four are loaded before these are used
         const T *row = logits + (int64_t)w.cur * a.ldl;
         const float *qrow = draft + (int64_t)w.cur * a.ldd;
         const Weight e(node_m[w.cur], sc);
@@ -501,81 +604,97 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
         const int turns = 4 * ((pieces - wave + 15) / 16);
         auto place = [&](int j) { return (int64_t)(wave + 16 * (j >> 2)) * kPiece + 256 * (j & 3) + 4 * lane; };
         f32x4 v = load4<T>(row + place(0), a.V - place(0), -INFINITY), q = load4<float>(qrow + place(0), a.V - place(0), 0.f);
+        f32x4 v1 = load4<T>(row + place(1), a.V - place(1), -INFINITY), q1 = load4<float>(qrow + place(1), a.V - place(1), 0.f);
         double s = 0.0;
+        const bool plain = e.plain();
 #pragma unroll 1
         for (int j = 0; j < turns; ++j) {
             const f32x4 v0 = v, q0 = q;
-            const int64_t at = place(j + 1 < turns ? j + 1 : j);
-            v = load4<T>(row + at, a.V - at, -INFINITY);
-            q = load4<float>(qrow + at, a.V - at, 0.f);
+            const int64_t at = place(j + 2 < turns ? j + 2 : j);
+            v = v1;
+            q = q1;
+            v1 = load4<T>(row + at, a.V - at, -INFINITY);
+            q1 = load4<float>(qrow + at, a.V - at, 0.f);
+            double r[4];
+            if (plain) {
+                const float x[4] = {v0[0], v0[1], v0[2], v0[3]};
+                e.raw4(x, r);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s += fmax(e(v0[k]) - s0 * clean(q0[k]), 0.0);
-            if ((j & 3) == 3) {
-                s = wave_sum(s);
-                if (lane == 0) sums[wave + 16 * (j >> 2)] = s;
-                s = 0.0;
+                for (int k = 0; k < 4; ++k) r[k] = e(v0[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const double x = r[k] - s0 * clean(q0[k]);
+                s += x > 0.0 ? x : 0.0;
             }
         }
+        s = wave_sum(s);
+        if (lane == 0) sums[wave] = s;
         __syncthreads();
-        if (wave == 0) {
-            s = 0.0;
-            for (int c = lane; c < pieces; c += 64) s += sums[c];
-            R = wave_sum(s);
-        }
+        R = wave_sum(lane < 16 ? sums[lane] : 0.0);
     }
-    cur = w.cur;
-    const int ngone = w.gone;
-    if (tid == 0) a.count[b] = w.kept;
-    if (greedy || node_z[cur] == 0.0) {
-        if (tid == 0) a.next[b] = greedy ? node_best[cur] : -1;
+    const int end = w.cur, ngone = w.gone;
+    for (int k = tid; k < ngone; k += 1024) a.gone[c0 + k] = node_x[gone[k]];
+    if (tid == 0) {
+        a.count[b] = kept;
+        a.state[b] = State{w.S, c0 + end, ngone, !has_child[end] ? kLeaf : (draft && w.S > 0.0 ? kRemainder : kSummed)};
+    }
+}
+
+// The next token of every sequence: the chunk where the cumulated sum of what is
+// left crosses the random number, then the token in it.
+template <typename T>
+__global__ __launch_bounds__(1024) void k_draw(Args a) {
+    __shared__ double sums[kMaxChunks], wsum[16];
+    __shared__ int firsts[16], lasts[16];
+    __shared__ struct {
+        double target, before;
+        int at, past;
+    } w;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t b = blockIdx.x;
+    const State st = a.state[b];
+    if (st.sums == kNone) return;
+    const float t = a.temperature ? a.temperature[b] : 1.f;
+    const bool greedy = !(t > 0.f);
+    const int c0 = a.cu[b] < 0 ? 0 : a.cu[b];
+    const float mc = lane < a.C ? a.mx[(int64_t)st.cur * a.C + lane] : -INFINITY;
+    const double zc = lane < a.C ? a.sum[(int64_t)st.cur * a.C + lane] : 0.0;
+    const double u = a.uniform[c0];
+    const float m = wave_max(mc);
+    if (greedy || m == -INFINITY) {
+        const int best = wave_min(mc == m ? (int)zc : 0x7FFFFFFF);
+        if (tid == 0) a.next[b] = m == -INFINITY ? -1 : best;
         return;
     }
-    // What is drawn from: the sums of a remainder's pieces, or those of the row's
-    // chunks less the tokens taken out; the row's own where nothing is left of it
-    const Weight e(node_m[cur], sc);
-    const T *row = logits + (int64_t)cur * a.ldl;
-    bool own = !(draft && w.S > 0.0), whole = false;
+    const Weight e(m, Scale(t));
+    const T *row = static_cast<const T *>(a.logits) + (int64_t)st.cur * a.ldl;
+    // the sums of the remainder's chunks, or those of the row's less the tokens taken
+    // out; the row's own where nothing is left of it
+    bool rem = st.sums == kRemainder, whole = false;
 #pragma unroll 1
     for (;;) {
-        const int size = own ? a.chunk : kPiece, count = own ? a.C : pieces;
-        if (own) {
-            if (tid < a.C) {
-                const int64_t at = (int64_t)(c0 + cur) * a.C + tid;
-                double s = a.sum[at] * e(a.mx[at]);
-                if (!whole)
-                    for (int k = 0; k < ngone; ++k)
-                        if (node_x[gone[k]] / a.chunk == tid) s = fmax(s - node_e[gone[k]], 0.0);
-                sums[tid] = s;
-            }
-            __syncthreads();
-        }
         if (wave == 0) {
-            const int per = (count + 63) / 64;
-            double mine = 0.0;
-            for (int c = lane * per; c < (lane + 1) * per && c < count; ++c) mine += sums[c];
-            const double upto = wave_scan(mine), target = node_u[0] * lane_of(upto, 63);
-            // first one whose inclusive sum is past the target, else the last that holds anything
-            int at = -1, last = -1;
-            double before = 0.0, run = upto - mine;
-            for (int c = lane * per; c < (lane + 1) * per && c < count; ++c) {
-                const double s = sums[c];
-                if (s > 0.0) {
-                    last = c;
-                    if (run + s > target && at < 0) {
-                        at = c;
-                        before = run;
+            double s = 0.0;
+            if (lane < a.C) {
+                if (rem) {
+                    s = a.rest[b * a.C + lane];
+                } else {
+                    s = zc * e(mc);
+                    for (int k = 0; k < st.gone && !whole; ++k) {
+                        const int x = a.gone[c0 + k];
+                        if (x / a.chunk == lane) s = fmax(s - e(load1<T>(row + x)), 0.0);
                     }
                 }
-                run += s;
             }
-            const uint64_t found = __ballot(at >= 0), any = __ballot(last >= 0);
-            if (found) {
-                const int f = __ffsll((long long)found) - 1;
-                at = __builtin_amdgcn_readlane(at, f);
-                before = lane_of(before, f);
-            } else if (any) {
-                at = __builtin_amdgcn_readlane(last, 63 - __clzll((long long)any));
-            }
+            const double upto = wave_scan(s), target = u * lane_of(upto, 63);
+            // first one whose inclusive sum is past the target, else the last that holds anything
+            const uint64_t found = __ballot(s > 0.0 && upto > target), any = __ballot(s > 0.0);
+            int at = -1;
+            if (found) at = __ffsll((long long)found) - 1;
+            else if (any) at = 63 - __clzll((long long)any);
+            const double before = lane_of(upto - s, at < 0 ? 0 : at);
             if (lane == 0) {
                 w.at = at;
                 w.before = before;
@@ -590,21 +709,21 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
         const double target = w.target;
         if (w.at >= 0) {
 #pragma unroll 1
-            for (int i = 0; i < size; i += 4096) {
-                const int64_t at = (int64_t)w.at * size + i + 4 * tid;
-                const int64_t there = i + 4 * tid < size ? a.V - at : 0;
-                const f32x4 v = load4<T>(row + at, there, -INFINITY);
+            for (int i = 0; i < a.chunk; i += 4096) {
+                const int64_t at = (int64_t)w.at * a.chunk + i + 4 * tid;
+                const f32x4 v = load4<T>(row + at, a.V - at, -INFINITY);
                 f32x4 q = {0, 0, 0, 0};
-                if (!own) q = load4<float>(draft + (int64_t)cur * a.ldd + at, there, 0.f);     // own: no q
+                if (rem) q = load4<float>(a.draft + (int64_t)st.cur * a.ldd + at, a.V - at, 0.f);
                 double r[4], part = 0.0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    r[k] = fmax(e(v[k]) - w.S * clean(q[k]), 0.0);
-                    if (!whole)
-                        for (int j = 0; j < ngone; ++j)
-                            if (node_x[gone[j]] == at + k) r[k] = 0.0;
-                    part += r[k];
+                for (int k = 0; k < 4; ++k) r[k] = fmax(e(v[k]) - st.S * clean(q[k]), 0.0);
+                for (int j = 0; j < st.gone && !whole; ++j) {
+                    const int64_t k = a.gone[c0 + j] - at;
+#pragma unroll
+                    for (int l = 0; l < 4; ++l) r[l] = k == l ? 0.0 : r[l];
                 }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) part += r[k];
                 const double inc = wave_scan(part);
                 if (lane == 63) wsum[wave] = inc;
                 __syncthreads();
@@ -636,25 +755,38 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
             if (tid == 0) a.next[b] = x;
             return;
         }
-        own = whole = true;                           // nothing but rounding was left
+        rem = false;                                  // nothing but rounding was left
+        whole = true;
         __syncthreads();
     }
 }
 
-size_t layout(int64_t total, int64_t V, size_t *sum, int *C) {
-    const int64_t c = ceil_div(V, (int64_t)chunk_size(V));
-    const size_t mx = ((size_t)total * c * 4 + 15) / 16 * 16;
-    if (sum) *sum = mx;
-    if (C) *C = (int)c;
-    return mx + (size_t)total * c * 8 + 16;
+struct Layout {
+    size_t mx, sum, rest, state, gone, bytes;
+    int C;
+};
+
+Layout layout(int64_t B, int64_t total, int64_t V) {
+    Layout l{};
+    l.C = (int)ceil_div(V, (int64_t)chunk_size(V));
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 15) / 16 * 16;
+        return o;
+    };
+    l.mx = take((size_t)total * l.C * 4);
+    l.sum = take((size_t)total * l.C * 8);
+    l.rest = take((size_t)B * l.C * 8);
+    l.state = take((size_t)B * sizeof(State));
+    l.gone = take((size_t)total * 4);
+    l.bytes = at;
+    return l;
 }
 
 }  // namespace
 
-size_t verify_tree_workspace(int64_t B, int64_t total, int64_t V) {
-    (void)B;
-    return layout(total, V, nullptr, nullptr);
-}
+size_t verify_tree_workspace(int64_t B, int64_t total, int64_t V) { return layout(B, total, V).bytes; }
 
 hipError_t launch_verify_tree(const void *logits, mxs_dtype dt, int64_t ldl, int64_t V, const int64_t *tokens,
                               const int32_t *parents, const int32_t *cu, int64_t B, int64_t total, int64_t max_n,
@@ -666,31 +798,53 @@ hipError_t launch_verify_tree(const void *logits, mxs_dtype dt, int64_t ldl, int
     a.tokens = tokens; a.parents = parents; a.cu = cu; a.draft = draft; a.temperature = temperature;
     a.uniform = uniform; a.path = path; a.count = count; a.next = next;
     a.max_n = (int)max_n; a.replacement = replacement;
-    size_t sum;
-    layout(total, V, &sum, &a.C);
+    const Layout l = layout(B, total, V);
+    a.C = l.C;
     a.chunk = chunk_size(V);
     uint8_t *w = static_cast<uint8_t *>(ws);
-    a.mx = reinterpret_cast<float *>(w);
-    a.sum = reinterpret_cast<double *>(w + sum);
+    a.mx = reinterpret_cast<float *>(w + l.mx);
+    a.sum = reinterpret_cast<double *>(w + l.sum);
+    a.rest = reinterpret_cast<double *>(w + l.rest);
+    a.state = reinterpret_cast<State *>(w + l.state);
+    a.gone = reinterpret_cast<int32_t *>(w + l.gone);
+    hipError_t e;
     if (total > 0 && max_n > 0) {
-        // a workgroup a node and chunk, unless a loose max_n would leave most of them without a node: then a row
-        // and chunk, and its sequence is looked for
+        // a wave a chunk where those alone fill the chip, else a workgroup: 25 us either way
+        // for 32 chains of 8 nodes over 128000 bf16, 40 against 51 for 16 trees of 64
+        const bool by_wave = a.chunk == 4096 && total * a.C >= 4096;
+        const unsigned gx = (unsigned)(by_wave ? ceil_div(a.C, 4) : a.C);
+        // a node and chunk, unless a loose max_n would leave most workgroups without a node:
+        // then a row and chunk, and its sequence is looked for
         a.direct = B * max_n <= 2 * total + 64;
-        const dim3 grid = a.direct ? dim3((unsigned)a.C, (unsigned)max_n, (unsigned)B)
-                                   : dim3((unsigned)a.C, (unsigned)(total < 65535 ? total : 65535),
+        const dim3 grid = a.direct ? dim3(gx, (unsigned)max_n, (unsigned)B)
+                                   : dim3(gx, (unsigned)(total < 65535 ? total : 65535),
                                           (unsigned)ceil_div(total, (int64_t)65535));
-        if (a.chunk == 4096) {
-            if (dt == MXS_BF16) hipLaunchKernelGGL((k_row_stats<uint16_t, 1>), grid, dim3(256), 0, st, a);
-            else hipLaunchKernelGGL((k_row_stats<float, 1>), grid, dim3(256), 0, st, a);
+        if (by_wave) {
+            if (dt == MXS_BF16) hipLaunchKernelGGL((k_row_stats<uint16_t, 4, true>), grid, dim3(256), 0, st, a);
+            else hipLaunchKernelGGL((k_row_stats<float, 4, true>), grid, dim3(256), 0, st, a);
+        } else if (a.chunk == 4096) {
+            if (dt == MXS_BF16) hipLaunchKernelGGL((k_row_stats<uint16_t, 1, false>), grid, dim3(256), 0, st, a);
+            else hipLaunchKernelGGL((k_row_stats<float, 1, false>), grid, dim3(256), 0, st, a);
         } else {
-            if (dt == MXS_BF16) hipLaunchKernelGGL((k_row_stats<uint16_t, 4>), grid, dim3(256), 0, st, a);
-            else hipLaunchKernelGGL((k_row_stats<float, 4>), grid, dim3(256), 0, st, a);
+            if (dt == MXS_BF16) hipLaunchKernelGGL((k_row_stats<uint16_t, 4, false>), grid, dim3(256), 0, st, a);
+            else hipLaunchKernelGGL((k_row_stats<float, 4, false>), grid, dim3(256), 0, st, a);
         }
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (dt == MXS_BF16) hipLaunchKernelGGL(k_walk<uint16_t>, dim3((unsigned)B), dim3(1024), 0, st, a);
     else hipLaunchKernelGGL(k_walk<float>, dim3((unsigned)B), dim3(1024), 0, st, a);
+    if ((e = hipGetLastError()) != hipSuccess || total == 0 || max_n == 0) return e;
+    const dim3 grid((unsigned)a.C, (unsigned)B);
+    if (a.chunk == 4096) {
+        if (dt == MXS_BF16) hipLaunchKernelGGL((k_rest<uint16_t, 1>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_rest<float, 1>), grid, dim3(256), 0, st, a);
+    } else {
+        if (dt == MXS_BF16) hipLaunchKernelGGL((k_rest<uint16_t, 4>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((k_rest<float, 4>), grid, dim3(256), 0, st, a);
+    }
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (dt == MXS_BF16) hipLaunchKernelGGL(k_draw<uint16_t>, dim3((unsigned)B), dim3(1024), 0, st, a);
+    else hipLaunchKernelGGL(k_draw<float>, dim3((unsigned)B), dim3(1024), 0, st, a);
     return hipGetLastError();
 }
 
