@@ -44,8 +44,8 @@ struct LoraArgs {
 // cnt[id] before this row is added. The rows of a prompt have one id: lanes that
 // all have the same are added by one of them (64 additions to one place take turns).
 __device__ __forceinline__ int count_rows(int32_t *cnt, int32_t id) {
-    const uint64_t on = __ballot(1);
-    if (__builtin_amdgcn_readfirstlane(id) == id && __ballot(1) == on) {
+    const uint64_t on = __ballot(1), same = __ballot(__builtin_amdgcn_readfirstlane(id) == id);
+    if (same == on) {
         const int lane = threadIdx.x & 63, before = __popcll(on & ((1ull << lane) - 1));
         int at = 0;
         if (before == 0) at = atomicAdd(&cnt[id], __popcll(on));

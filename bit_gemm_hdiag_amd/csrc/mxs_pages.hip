@@ -150,7 +150,8 @@ size_t reserve_layout(int64_t pages, int64_t B, void *ws, Reserve *r) {
     return at;
 }
 
-__device__ __forceinline__ int wave_sum(int v) {
+template <typename I>
+__device__ __forceinline__ I wave_sum(I v) {
 #pragma unroll
     for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
     return v;
@@ -180,7 +181,7 @@ __device__ __forceinline__ bool write_range(const SeqArgs &a, int64_t b, int &le
     c1 = c1 > a.total ? (int)a.total : c1;
     n = c1 > c0 ? c1 - c0 : 0;
     j0 = nj = 0;
-    if (len < 0 || (int64_t)len + n > a.ldt * a.page_size) return false;
+    if (len < 0 || (int64_t)len + n > a.ldt * a.page_size || (int64_t)len + n > 0x7FFFFFFF) return false;
     if (n == 0) return true;
     j0 = len / a.page_size;
     nj = ((int64_t)len + n - 1) / a.page_size - j0 + 1;
@@ -262,7 +263,8 @@ __device__ __forceinline__ void copy_bytes(uint8_t *to, const uint8_t *from, int
 // A workgroup a sequence: its ranks among the free pages, the pages themselves,
 // then its table entries, its slots, and the copy of a shared page's tokens.
 __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes pl, int64_t *slots, int32_t *lens_out) {
-    __shared__ int sums[3][4], found[2], old_last, new_last;
+    __shared__ int64_t needs[4];
+    __shared__ int sums[2][4], found[2], old_last, new_last;
     __shared__ int32_t few[256];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t b = blockIdx.x;
@@ -273,30 +275,33 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
     const int need = r.need[b];
     int32_t *row = a.table + b * a.ldt;
     if (tid == 0) old_last = new_last = -1;
-    int before = 0, avail = 0, mine = 0, upto = 0;
+    __syncthreads();                            // every thread has read lens before it may be written
+    int64_t wanted = 0;                         // 64 bits: no lens and cu make it wrap
+    int avail = 0, mine = 0, upto = 0;
     const int per = (r.chunks + 255) / 256;
     if (need > 0) {
         // pages that earlier sequences need, and all that are free, a run of chunks a thread
-        for (int64_t i = tid; i < b; i += 256) before += r.need[i] > 0 ? r.need[i] : 0;
+        for (int64_t i = tid; i < b; i += 256) wanted += r.need[i] > 0 ? r.need[i] : 0;
         for (int i = tid * per; i < (tid + 1) * per && i < r.chunks; ++i) mine += r.counts[i];
-        before = wave_sum(before);
+        wanted = wave_sum(wanted);
         upto = wave_scan(mine);
         if (lane == 63) {
-            sums[0][wave] = before;
-            sums[1][wave] = upto;
+            needs[wave] = wanted;
+            sums[0][wave] = upto;
         }
         __syncthreads();
-        before = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
-        avail = sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
-        for (int w = 0; w < wave; ++w) upto += sums[1][w];
+        wanted = needs[0] + needs[1] + needs[2] + needs[3];
+        avail = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
+        for (int w = 0; w < wave; ++w) upto += sums[0][w];
     }
-    if (need < 0 || (need > 0 && (int64_t)before + need > avail)) {
+    if (need < 0 || (need > 0 && wanted + need > avail)) {
         for (int64_t j = tid; j < nj; j += 256)
             if (row[j0 + j] < -1) row[j0 + j] = -2 - row[j0 + j];
         for (int i = tid; i < n; i += 256) slots[c0 + i] = -1;
         if (tid == 0) lens_out[b] = len;
         return;
     }
+    const int before = (int)wanted;             // at most the free pages
     if (need > 0) {
         // the chunk that holds rank `before`, then the pages of the ranks from there
         if (upto - mine <= before && before < upto) {
@@ -330,11 +335,11 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
             const int64_t j = t0 + tid;
             const int32_t v = j < nj ? row[j0 + j] : 0;
             const uint64_t takes = __ballot(v < 0);
-            if (lane == 0) sums[2][wave] = __popcll(takes);
+            if (lane == 0) sums[1][wave] = __popcll(takes);
             __syncthreads();
             int rank = at + __popcll(takes & ((1ull << lane) - 1));
-            for (int w = 0; w < wave; ++w) rank += sums[2][w];
-            at += sums[2][0] + sums[2][1] + sums[2][2] + sums[2][3];
+            for (int w = 0; w < wave; ++w) rank += sums[1][w];
+            at += sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
             if (v < 0) {
                 const int32_t p = grant[rank];
                 row[j0 + j] = p;
