@@ -736,10 +736,10 @@ def _table(cache: KV4Cache, table: torch.Tensor):
     return table.data_ptr(), width, B
 
 
-def _given_ws(ws, nbytes: int, gpu: int, dev):
+def _given_ws(ws, gpu: int, dev, query, *args):
     """(tensor, pointer, bytes) of a workspace, allocated if the caller passes none."""
     if ws is None:
-        return _workspace(nbytes, dev, None)
+        return _workspace(int(query(*args)), dev, None)
     if ws.get_device() != gpu or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on cuda:{gpu}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
@@ -794,7 +794,7 @@ def mxs_kv4_reserve(cache: KV4Cache, refs: torch.Tensor, table: torch.Tensor, le
     n = slots.numel()
     if lens_out is None:
         lens_out = torch.empty(B, dtype=torch.int32, device=dev)
-    ws, p, nbytes = _given_ws(ws, int(_lib.mxs_kv4_reserve_workspace(pages, B)), gpu, dev)
+    ws, p, nbytes = _given_ws(ws, gpu, dev, _lib.mxs_kv4_reserve_workspace, pages, B)
     _call(gpu, _lib.mxs_kv4_reserve, "mxs_kv4_reserve", cache._ref, _vector(refs, "refs", torch.int32, pages, gpu), pt,
           width, B, _vector(lens, "lens", torch.int32, B, gpu), _vector(cu, "cu", torch.int32, B + 1, gpu), n,
           _vector(slots, "slots", torch.int64, n, gpu), _vector(lens_out, "lens_out", torch.int32, B, gpu), p, nbytes)
@@ -946,7 +946,7 @@ def mxs_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, cu: torch.Tensor
         count = torch.empty(B, dtype=torch.int32, device=dev)
     if next_token is None:
         next_token = torch.empty(B, dtype=torch.int64, device=dev)
-    ws, p, n = _given_ws(ws, int(_lib.mxs_verify_tree_workspace(B, total, max_n, V)), gpu, dev)
+    ws, p, n = _given_ws(ws, gpu, dev, _lib.mxs_verify_tree_workspace, B, total, max_n, V)
     _call(gpu, _lib.mxs_verify_tree, "mxs_verify_tree", pl, dt, ldl, V,
           _vector(tokens, "tokens", torch.int64, total, gpu),
           None if parents is None else _vector(parents, "parents", torch.int32, total, gpu),
@@ -999,7 +999,7 @@ def mxs_lora_add(Y: torch.Tensor, X: torch.Tensor, ids: torch.Tensor, adapters: 
         raise TypeError("X must have the adapters' type, and Y must be fp32")
     px, ldx = _matrix(X, "X", M, adapters.K, gpu)
     py, ldy = _matrix(Y, "Y", M, adapters.N, gpu)
-    ws, p, n = _given_ws(ws, int(_lib.mxs_lora_add_workspace(M, adapters._ref)), gpu, Y.device)
+    ws, p, n = _given_ws(ws, gpu, Y.device, _lib.mxs_lora_add_workspace, M, adapters._ref)
     _call(gpu, _lib.mxs_lora_add, "mxs_lora_add", px, M, ldx, _vector(ids, "ids", torch.int32, M, gpu), adapters._ref, py,
           ldy, p, n)
     return Y

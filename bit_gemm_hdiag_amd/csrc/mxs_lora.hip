@@ -449,14 +449,16 @@ Plan plan_of(int64_t M, const mxs_lora &s) {
     p.steps = p.steps <= 2 ? p.steps : (p.steps <= 4 ? 4 : 8);
     const int64_t ranks = ceil_div(p.Rp, 16 * p.nt);
     // slices of K until the chip is filled, each a turn of the four waves or more, and
-    // V's partial sums below a thirty-second of X
-    const int64_t turn = 1024 / es;
+    // V's partial sums below an eighth of X (or 2 MiB)
+    const int64_t turn = 1024 / es, turns = ceil_div(s.K, turn);
+    int64_t most = s.K * es / (32 * p.Rp);
+    const int64_t room = ((int64_t)1 << 19) / (M * p.Rp);
+    most = p.small ? 16 : (most > room ? most : room);
     int64_t want = ceil_div(1024, busy * ranks);
-    const int64_t fit = ceil_div(s.K, turn), most = p.small ? 16 : s.K * es / (32 * p.Rp);
-    want = want < fit ? want : fit;
     want = want < most ? want : most;
     want = want < 1 ? 1 : (want > 64 ? 64 : want);
-    p.kper = ceil_div(ceil_div(s.K, want), turn) * turn;
+    p.kper = turn * (turns > want ? turns / want : 1);
+    while (ceil_div(s.K, p.kper) > 128) p.kper += turn;
     p.splits = (int)ceil_div(s.K, p.kper);
     // columns of Y a workgroup takes: 64 where that leaves the chip unfilled, else four
     // tiles a wave, and several turns of them from 4096 workgroups on
