@@ -9,6 +9,12 @@
 // so that a lane ends with four consecutive elements of one token. A column of a
 // tile depends on its own token alone: columns past a group's end repeat one of
 // its tokens and are not stored, and where a token sits does not change its value.
+//
+// Bound by memory: the adapters' bytes for few rows (64 rows on 32 adapters of rank
+// 64, 28672 x 8192: 16 + 51 us for 33 + 132 MB, half of the copy rate: each workgroup
+// waits for its rows, then V, then B; 34 us of the 51 are B alone), X and Y for prompts
+// (4096 rows of 8192 x 8192 at rank 16: 25 us for 67 MB of X, 69 for 268 MB of Y, 3.9
+// TB/s). 8 rows on 4 adapters take 3.8 + 6.1 us, mostly latency.
 #include "mxs_device.h"
 #include "mxs_internal.h"
 
@@ -174,7 +180,9 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 
 // ---------------------------------------------------------------- V = A X
 // NT tiles of 16 ranks by TT tiles of 16 tokens a wave; the four waves of a
-// workgroup share the slice of K and add their sums in LDS in their order.
+// workgroup share the slice of K and add their sums in LDS in their order. X and A
+// go from memory to the matrix cores' operands directly (both have K adjacent), the
+// loads of 128 K (64 in fp32) of a wave before the first is used.
 template <typename T, int NT, int TT>
 __device__ __forceinline__ void shrink(const LoraArgs &a, const int32_t *rows, int adapter, int count, int rank,
                                        int r0, float *lds) {
@@ -424,11 +432,11 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraArgs a, bool small) {
     x.run(a, parts, rows, adapter, count, rank, scale, c, c1);
 }
 
-// Column tiles of a wave
+// Column tiles of a wave (two instead of four at 33 to 64 ranks: 52 against 60 us, more waves fit)
 constexpr int wide_tiles(int steps) { return steps <= 1 ? 4 : (steps <= 4 ? 2 : 1); }
 
 struct Plan {
-    bool small, wide;                   // wide: four tiles of columns a wave, else one
+    bool small, wide;                   // wide: wide_tiles(steps) tiles of columns a wave, else one
     int64_t tiles;                      // at most
     int splits, nt, steps;
     int64_t kper, nper;
@@ -460,8 +468,9 @@ Plan plan_of(int64_t M, const mxs_lora &s) {
     p.kper = turn * (turns > want ? turns / want : 1);
     while (ceil_div(s.K, p.kper) > 128) p.kper += turn;
     p.splits = (int)ceil_div(s.K, p.kper);
-    // columns of Y a workgroup takes: 64 where that leaves the chip unfilled, else four
-    // tiles a wave, and several turns of them from 4096 workgroups on
+    // columns of Y a workgroup takes: 64 where 256 would leave the chip unfilled, else 512
+    // (prompts of 4096 rows: 79 us at 256, 74 at 512, 90 at 1024; 64 rows on 32 adapters: 67,
+    // 57, 55), and more from 4096 workgroups on
     p.wide = busy * ceil_div(s.N, (int64_t)256) >= 512;
     p.nper = p.wide ? 512 : 64;
     while (p.wide && p.nper < 2048 && busy * ceil_div(s.N, 2 * p.nper) >= 4096) p.nper *= 2;

@@ -188,6 +188,8 @@ __device__ __forceinline__ bool write_range(const SeqArgs &a, int64_t b, int &le
     return true;
 }
 
+// Latency bounds both kernels of a reservation: 2.3 + 8.1 us for two sequences over 64
+// pages, 3.4 + 9.3 for 96 over 16384, 64 of which copy half a page (70 KB).
 // Waves of the first workgroups count what a sequence needs and mark entries
 // whose page is shared by -2 - page (this decision stands while the second
 // kernel changes refs); the others build the bitmap, a wave a chunk.
@@ -374,7 +376,8 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
 // A workgroup a sequence. The slots of 256 kept tokens are found first, then tokens
 // are moved 1024 code words (with their scale bytes) at a time, in ascending
 // order: all are read before the first is written, and what a later turn reads no
-// earlier one has written, because path[i] >= i.
+// earlier one has written, because path[i] >= i. 96 sequences of up to 26 tokens take
+// 5.9 us (a thread a column, token after token: 15).
 __global__ __launch_bounds__(256) void k_kv4_compact(SeqArgs a, Planes pl, const int32_t *path, const int32_t *count,
                                                      int32_t *lens_out) {
     __shared__ int32_t from[256], to[256];

@@ -627,16 +627,17 @@ mxs_status mxs_kv4_fork(const mxs_kv4_cache *cache, int32_t *refs, int32_t *tabl
  * the new page is 1. A shared page that is replaced loses one reference, and its
  * tokens before lens[b] are copied first. (Where all holders of a page write to
  * it, each takes a copy and the page is free after the call.)
- * slots[cu[b] + i] receives the slot of token lens[b] + i, for mxs_kv4_append and
+ * slots[cu[b] + i] receives the slot of token lens[b] + i, for mxs_kv4_append, and
  * lens_out[b] = lens[b] + n, for mxs_attend_kv4_tree (lens_out may be lens).
- * A sequence whose table row is too short (lens[b] + n > ldt page_size, or lens[b]
- * < 0) is refused: its slots are -1, its table is left and lens_out[b] = lens[b].
- * So is, once the free pages run out, the first sequence that they do not serve
- * whole, and every later one that needs a page.
- * cu: [B + 1] int32 ascending from 0, cu[B] <= total; slots: [total] int64, those of no
- * sequence are left as they were. At most 2^24 pages, B <= 65535. ws: >=
- * mxs_kv4_reserve_workspace(pages, B) bytes, 16-byte aligned, contents scratch.
- * B = 0 is a no-op.
+ * A sequence whose table row is too short (lens[b] + n > ldt page_size), whose
+ * length would pass 2^31 - 1 or is negative is refused: its slots are -1, its
+ * table is left and lens_out[b] = lens[b]. So is, once the free pages run out, the
+ * first sequence that they do not serve whole, and every later one that needs a
+ * page.
+ * cu: [B + 1] int32 ascending from 0, cu[B] <= total; slots: [total] int64, those
+ * of no sequence are left as they were; total < 2^24. At most 2^24 pages, B <=
+ * 65535. ws: >= mxs_kv4_reserve_workspace(pages, B) bytes, 16-byte aligned,
+ * contents scratch. B = 0 is a no-op.
  * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE (negative sizes), MXS_ERR_UNSUPPORTED
  * (sizes, alignment), MXS_ERR_WORKSPACE, MXS_ERR_DEVICE.
  */
@@ -676,43 +677,48 @@ mxs_status mxs_kv4_release(const mxs_kv4_cache *cache, int32_t *refs, int32_t *t
 
 /*
  * Verification of drafted tokens against the target model, for a batch of B
- * sequences laid out as in mxs_attend_kv4_tree: rows cu[b] .. cu[b + 1] - 1 are the
- * n nodes of sequence b's tree, node 0 (the root) its last token, node i > 0 the
- * drafted token tokens[row] below node parents[row] < i (parents NULL: below i -
- * 1, a chain). Row r of logits holds the target's logits of the token after that
- * node. With T = temperature[b] (NULL: 1), l the row's logits and m their maximum,
+ * sequences laid out as in mxs_attend_kv4_tree: rows cu[b] .. cu[b + 1] - 1 are
+ * the n nodes of sequence b's tree, node 0 (the root) its last token, node i > 0
+ * the drafted token tokens[row] below node parents[row] < i (parents NULL: below
+ * i - 1, a chain). Row r of logits holds the target's logits of the token after
+ * that node. With T = temperature[b] (NULL: 1), l the row's logits and m their
+ * maximum,
  *     e(v) = exp((l(v) - m) / T),  Z = sum_v e(v)
- * (a NaN counts as -inf; where m is +inf, e is 1 there and 0 elsewhere).
- * The walk starts at the root. At node c with S = 0, R = Z, left = 1, its children
- * are tried in ascending order. draft given: row c of it is the distribution q
- * from which the children of node c were drawn (fp32, finite, not negative:
- * others count as 0); child x with number u = uniform[its row] is accepted iff
+ * (a NaN counts as -inf; where m is +inf, e is 1 there and 0 elsewhere). The
+ * walk starts at the root. At node c, with S = 0, R = Z and left = 1, its
+ * children are tried in ascending order. draft given: row c of it is the
+ * distribution q from which the children of node c were drawn (fp32; what is
+ * not finite or negative counts as 0); child x with the number u = uniform[its
+ * row] is accepted iff
  *     u q(x) R < max(e(x) - S q(x), 0) left;
  * a rejected one makes S += R / left, left -= q(x) unless `replacement` is set
- * (children drawn independently; otherwise each from what its elder siblings
- * left of q), and R = sum_v max(e(v) - S q(v), 0): the target's remaining
- * distribution. A child is rejected without effect where left <= 0. draft NULL:
- * children proposed without a distribution (q(x) = 1): accepted iff u R < e(x), a
- * rejected one takes e(x) out of the row (e(x) = 0, R less by it). The first accepted child becomes c. When
- * none is, the next token is the smallest v at which the cumulated remainder
- * exceeds uniform[cu[b]] R. So every token is distributed as the target alone would draw
- * it. T <= 0 or NaN is greedy: a child is accepted iff it is the lowest index of
- * the largest logit, which is the next token where none is.
+ * (children drawn independently; otherwise each from what its elder siblings left
+ * of q), and R = sum_v max(e(v) - S q(v), 0): what the target still has to give. A
+ * child is rejected without effect where left <= 0. draft NULL: children proposed
+ * without a distribution (q(x) = 1): accepted iff u R < e(x); a rejected one takes
+ * e(x) out of the row (e(x) = 0, R less by it). The first accepted child becomes
+ * c. When none is, the next token is the smallest v at which the cumulated
+ * remainder exceeds uniform[cu[b]] R. So every token is distributed as the target
+ * alone would draw it. T <= 0 or NaN is greedy: a child is accepted iff it is the
+ * lowest index of the largest logit, which is the next token where none is.
  * path[cu[b] + i] receives the i-th node kept (path[cu[b]] = 0, the root), -1
  * behind them, count[b] their number (1 + accepted; 0 where n = 0), next[b] the
  * next token; -1 where n = 0 or the row has no logit above -inf (then no child is
- * accepted either). Where rounding leaves nothing of the remainder, the next
- * token is drawn from e. A child with a token outside [0, V) is rejected, without effect. path and
- * count are what mxs_kv4_compact takes. Sums in fp64, in a fixed order.
- * logits: [total, V] of `dtype`, ldl elements between rows; draft [total, V] fp32
+ * accepted either). Where rounding leaves nothing of the remainder, the next token
+ * is drawn from e. A child with a token outside [0, V) is rejected without
+ * effect. path and count are what mxs_kv4_compact takes. Sums are in 64 bits, in
+ * an order fixed by the sizes, of weights within 1.1e-12 of e (those below
+ * 2^-1000 are 0).
+ * logits: [total, V] of `dtype`, ldl elements between rows; draft: [total, V] fp32
  * with ldd; tokens int64, parents int32, uniform fp64 (in [0, 1)): [total]; path:
- * [total] int32, rows of no sequence are left as they were; next: [B] int64. max_n: upper bound
- * of n known to the host, at most 1024 (longer trees are cut off: nodes past it are not
- * tried, their path is -1). V <= 2^20, total <= 2^22, B <= 65535. ws: >=
- * mxs_verify_tree_workspace bytes (0 for sizes that the call refuses), 16-byte
- * aligned, contents scratch; calls that may overlap need one each. B = 0 is a no-op.
- * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE, MXS_ERR_UNSUPPORTED, MXS_ERR_WORKSPACE,
- * MXS_ERR_DEVICE.
+ * [total] int32, rows of no sequence are left as they were; next: [B] int64.
+ * max_n: upper bound of n known to the host, at most 1024 (longer trees are cut
+ * off: nodes past it are not tried, their path is -1). V <= 2^20, total <= 2^22, B
+ * <= 65535. ws: >= mxs_verify_tree_workspace bytes (0 for sizes that the call
+ * refuses), 16-byte aligned, contents scratch; calls that may overlap need one
+ * each. B = 0 is a no-op.
+ * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE, MXS_ERR_UNSUPPORTED (sizes, alignment),
+ * MXS_ERR_WORKSPACE, MXS_ERR_DEVICE.
  */
 size_t mxs_verify_tree_workspace(int64_t B, int64_t total, int64_t max_n, int64_t V);
 mxs_status mxs_verify_tree(const void *logits, mxs_dtype dtype, int64_t ldl, int64_t V, const int64_t *tokens,
