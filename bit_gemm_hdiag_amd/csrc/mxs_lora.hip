@@ -13,8 +13,8 @@
 // Bound by memory: the adapters' bytes for few rows (64 rows on 32 adapters of rank
 // 64, 28672 x 8192: 16 + 51 us for 33 + 132 MB, half of the copy rate: each workgroup
 // waits for its rows, then V, then B; 34 us of the 51 are B alone), X and Y for prompts
-// (4096 rows of 8192 x 8192 at rank 16: 25 us for 67 MB of X, 69 for 268 MB of Y, 3.9
-// TB/s). 8 rows on 4 adapters take 3.8 + 6.1 us, mostly latency.
+// (4096 rows of 8192 x 8192 at rank 16: 24 us for 67 MB of X, 69 for 268 MB of Y, 3.9
+// TB/s). 8 rows on 4 adapters take 3.5 + 6.0 us, mostly latency.
 #include "mxs_device.h"
 #include "mxs_internal.h"
 
@@ -185,14 +185,14 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
 // loads of 128 K (64 in fp32) of a wave before the first is used.
 template <typename T, int NT, int TT>
 __device__ __forceinline__ void shrink(const LoraArgs &a, const int32_t *rows, int adapter, int count, int rank,
-                                       int r0, float *lds) {
+                                       int r0, int t0, float *lds) {
     constexpr int E = 16 / sizeof(T), STEP = 4 * E;         // elements of a lane and of a step
     constexpr int U = 4;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
     const T *x[TT], *w[NT];
 #pragma unroll
     for (int t = 0; t < TT; ++t)
-        x[t] = static_cast<const T *>(a.X) + (int64_t)rows[16 * t + col] * a.ldx + E * g;
+        x[t] = static_cast<const T *>(a.X) + (int64_t)rows[t0 + 16 * t + col] * a.ldx + E * g;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         int r = r0 + 16 * t + col;
@@ -230,39 +230,39 @@ __device__ __forceinline__ void shrink(const LoraArgs &a, const int32_t *rows, i
             for (int t = 0; t < TT; ++t) acc[i][t] = mma<T>(wv, load16(x[t] + k), acc[i][t]);
         }
     }
-    // [token][rank of this workgroup]: one wave's sums after the other
-    constexpr int W = 16 * NT + 4;
-    for (int v = 0; v < 4; ++v) {
-        if (wave == v) {
+    // [wave][token][rank of this workgroup], added in the order of the waves
+    constexpr int W = 16 * NT + 4, S = 16 * TT * W;
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    f32x4 *p = reinterpret_cast<f32x4 *>(lds + (16 * t + col) * W + 16 * i + 4 * g);
-                    *p = v == 0 ? acc[i][t] : *p + acc[i][t];
-                }
-        }
-        __syncthreads();
-    }
+        for (int t = 0; t < TT; ++t)
+            *reinterpret_cast<f32x4 *>(lds + wave * S + (16 * t + col) * W + 16 * i + 4 * g) = acc[i][t];
+    __syncthreads();
     float *out = a.V + (int64_t)blockIdx.y * a.M * a.Rp;
-    for (int e = threadIdx.x; e < count * 4 * NT; e += 256) {
+    const int there = count - t0 < 16 * TT ? count - t0 : 16 * TT;
+    for (int e = threadIdx.x; e < there * 4 * NT; e += 256) {
         const int t = e / (4 * NT), q = e - t * (4 * NT), r = r0 + 4 * q;
-        if (r < a.Rp)
-            *reinterpret_cast<f32x4 *>(out + (int64_t)rows[t] * a.Rp + r) = *reinterpret_cast<const f32x4 *>(lds + t * W + 4 * q);
+        if (r >= a.Rp) continue;
+        f32x4 v = *reinterpret_cast<const f32x4 *>(lds + t * W + 4 * q);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) v += *reinterpret_cast<const f32x4 *>(lds + k * S + t * W + 4 * q);
+        *reinterpret_cast<f32x4 *>(out + (int64_t)rows[t0 + t] * a.Rp + r) = v;
     }
 }
 
+// A workgroup takes 32 tokens of a tile (blockIdx.z: which, and which ranks): with 64
+// registers leave two waves a SIMD at ranks above 32, and 301 fp32 rows of 4096 take 8.8
+// instead of 7.2 us, prompts of 4096 rows 25.5 instead of 24.0
 template <typename T, int NT>
 __global__ __launch_bounds__(256) void k_lora_shrink(LoraArgs a, bool small) {
-    extern __shared__ __attribute__((aligned(16))) float lds[];
+    __shared__ __attribute__((aligned(16))) float lds[4 * 32 * (16 * NT + 4)];
     __shared__ int32_t rows[kTile];
     int adapter, count;
     if (!find_group(a, small, rows, adapter, count)) return;
-    const int rank = rank_of(a, adapter), r0 = blockIdx.z * 16 * NT;
-    if (r0 >= rank) return;
-    if (count <= 16) shrink<T, NT, 1>(a, rows, adapter, count, rank, r0, lds);
-    else if (count <= 32) shrink<T, NT, 2>(a, rows, adapter, count, rank, r0, lds);
-    else shrink<T, NT, 4>(a, rows, adapter, count, rank, r0, lds);
+    const int rank = rank_of(a, adapter), r0 = (blockIdx.z >> 1) * 16 * NT, t0 = 32 * (blockIdx.z & 1);
+    if (r0 >= rank || t0 >= count) return;
+    if (count - t0 <= 16) shrink<T, NT, 1>(a, rows, adapter, count, rank, r0, t0, lds);
+    else shrink<T, NT, 2>(a, rows, adapter, count, rank, r0, t0, lds);
 }
 
 // ------------------------------------------------------------ Y += scale B V
@@ -505,11 +505,12 @@ hipError_t go(LoraArgs a, const Plan &p, hipStream_t st) {
         hipLaunchKernelGGL(k_lora_group, dim3(1), dim3(1024), (size_t)a.n * 4, st, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    const dim3 gs((unsigned)p.tiles, (unsigned)p.splits, (unsigned)ceil_div(p.Rp, 16 * p.nt));
-    const size_t ls = (size_t)kTile * (16 * p.nt + 4) * 4;
-    if (p.nt == 1) hipLaunchKernelGGL((k_lora_shrink<T, 1>), gs, dim3(256), ls, st, a, p.small);
-    else if (p.nt == 2) hipLaunchKernelGGL((k_lora_shrink<T, 2>), gs, dim3(256), ls, st, a, p.small);
-    else hipLaunchKernelGGL((k_lora_shrink<T, 4>), gs, dim3(256), ls, st, a, p.small);
+    // tiles of at most 32 rows have no second half
+    const int halves = a.M > 32 ? 2 : 1;
+    const dim3 gs((unsigned)p.tiles, (unsigned)p.splits, (unsigned)(2 * ceil_div(p.Rp, 16 * p.nt) - 2 + halves));
+    if (p.nt == 1) hipLaunchKernelGGL((k_lora_shrink<T, 1>), gs, dim3(256), 0, st, a, p.small);
+    else if (p.nt == 2) hipLaunchKernelGGL((k_lora_shrink<T, 2>), gs, dim3(256), 0, st, a, p.small);
+    else hipLaunchKernelGGL((k_lora_shrink<T, 4>), gs, dim3(256), 0, st, a, p.small);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     switch (p.steps) {
         case 1: go_expand<T, 1>(a, p, st); break;
