@@ -88,7 +88,8 @@ class Case:
 SIZES = [(1, 32, 1, 1, 1), (1, 8192, 512, 16, 3), (2, 64, 3, 3, 2), (7, 96, 65, 8, 5), (16, 416, 64, 16, 4),
          (17, 1024, 63, 24, 1), (33, 160, 130, 27, 3), (63, 512, 200, 64, 40), (64, 2048, 1001, 128, 2),
          (65, 512, 256, 16, 7), (200, 96, 70, 100, 300), (300, 1056, 129, 33, 2), (1000, 256, 96, 40, 60),
-         (2050, 640, 300, 16, 5), (130, 32, 17, 5, 8192)]
+         (2050, 640, 300, 16, 5), (130, 32, 17, 5, 8192), (64, 64, 30000, 64, 20), (50, 96, 9001, 100, 30),
+         (700, 64, 17003, 24, 6), (300, 64, 30001, 8, 9), (33, 2080, 66, 48, 1)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

@@ -203,6 +203,17 @@ def test_reserve_takes_the_lowest_free_pages_across_chunks(mx):
     assert len(given) == 401 and (p.m_refs[given] == 1).all() and not np.isin(free[::7], given).any()
 
 
+def test_reserve_of_many_pages_at_once(mx):
+    """More pages than a workgroup notes in LDS, for one sequence and for the next, over several chunks."""
+    p = Pool(mx, 7000, 1, 1, 32, 4, 2500, 15)
+    p.write(p.reserve([257, 0, 1500, 3]))
+    p.release([100, -1, 700, 0])
+    p.fork([2], [1])
+    slots = p.reserve([2000, 256, 1300, 1])
+    p.same()
+    assert len(set(slots.tolist())) == len(slots) and (slots >= 0).all()
+
+
 def test_pool_that_runs_out(mx):
     """The first sequence that does not fit and later ones that need pages get none; one with room is served."""
     p = Pool(mx, 10, 4, 2, 64, 5, 8, 6)

@@ -161,6 +161,23 @@ def test_against_the_definition(mx, ns, V, kind, ld, draft, dtype):
     c.check(c.run(mx))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("ns,V,kind", [([3, 5, 1], 262145, "tree"), ([4, 3], 270001, "tree"), ([2], 1 << 20, "chain"),
+                                       ([8] * 300, 5003, "tree"), ([2] * 2100, 4097, "chain"),
+                                       ([64] + [1] * 200, 700, "tree"), ([64] + [1] * 4100, 600, "chain"),
+                                       ([40] + [2] * 1100, 9000, "tree")])
+def test_sizes_that_take_other_kernels(mx, ns, V, kind, draft, dtype):
+    """Vocabularies past 2^18, batches that fill the chip with a wave a chunk, one long tree among short ones."""
+    if draft and V * sum(ns) > 1 << 24:
+        ns = ns[:3] + ns[-100:]
+    temps = [0.5 + 0.2 * (b % 4) if b % 5 != 2 else 0.0 for b in range(len(ns))]
+    c = Case(ns, V, dtype, draft, V % 1000, kind, temps)
+    c.check(c.run(mx))
+    c.max_n = min(1024, max(ns) + 30)                             # a loose bound
+    c.check(c.run(mx))
+
+
 @pytest.mark.parametrize("draft", [True, False])
 def test_draws_follow_both_outcomes(mx, draft):
     """Many small trees: nodes accepted and rejected, siblings tried after a rejection."""
