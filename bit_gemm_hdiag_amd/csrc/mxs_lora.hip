@@ -290,6 +290,16 @@ __device__ __forceinline__ u32x4 load_b(const T *row, int r0, int rank) {
     return v;
 }
 
+// Eight bf16 numbers, the infinities among them 0
+__device__ __forceinline__ u32x4 without_infinities(u32x4 b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t u = b[j];
+        b[j] = ((u & 0x7FFFu) == 0x7F80u ? 0u : u & 0xFFFFu) | ((u & 0x7FFF0000u) == 0x7F800000u ? 0u : u & 0xFFFF0000u);
+    }
+    return b;
+}
+
 // A wave takes CT tiles of 16 columns at a time: their rows of B are loaded before
 // anything waits, then V's parts are read from LDS once for all of them, while
 // the next 16 tokens' part of Y is on its way.
@@ -344,6 +354,21 @@ struct Expand {
         w.load(a, c, adapter, rank);
         if (col < count) load_y<CT>(a.Y + (int64_t)rows[col] * a.ldy + c + 4 * g, a.N - c - 4 * g, later);
     }
+    // The sums of 16 tokens where one came out as NaN. An infinity of B meets a number as
+    // its first part only: the others may be 0, and their product with it NaN.
+    __device__ __forceinline__ void again(f32x4 acc[CT], const T *v0) const {
+        constexpr int P = Parts<T>::P, D = Parts<T>::D, W = STEPS * D + Parts<T>::E;
+#pragma unroll
+        for (int i = 0; i < CT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll 1
+            for (int q = 0; q < P; ++q) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(v0 + q * kTile * W + s * D);
+#pragma unroll
+                for (int i = 0; i < CT; ++i) acc[i] = mma<T>(q == 0 ? w.b[i][s] : without_infinities(w.b[i][s]), v, acc[i]);
+            }
+    }
     __device__ __forceinline__ void run(const LoraArgs &a, const T *parts, const int32_t *rows, int adapter, int count,
                                         int rank, float scale, int64_t c, int64_t c1) {
         constexpr int P = Parts<T>::P, D = Parts<T>::D, E = Parts<T>::E, W = STEPS * D + E;
@@ -367,6 +392,14 @@ struct Expand {
 #pragma unroll
                         for (int i = 0; i < CT; ++i) acc[i] = mma<T>(w.b[i][s], v, acc[i]);
                     }
+                if constexpr (P > 1) {
+                    bool nan = false;
+#pragma unroll
+                    for (int i = 0; i < CT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) nan |= acc[i][j] != acc[i][j];
+                    if (__ballot(nan)) again(acc, parts + (t + col) * W + E * g);
+                }
                 if (t + 16 >= count && c + 64 * CT < c1) load(a, rows, adapter, count, rank, c + 64 * CT);
                 if (t + col < count) {
 #pragma unroll

@@ -151,6 +151,27 @@ def test_infinite_products(mx, dtype):
     assert torch.equal(torch.nan_to_num(c.Y, nan=7.0), torch.nan_to_num(want, nan=7.0))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,R,n", [(3, 20, 1, 1), (5, 70, 3, 2), (40, 64, 24, 3), (90, 200, 40, 2), (70, 15000, 8, 9),
+                                     (33, 300, 100, 1), (70, 15000, 40, 9), (70, 15000, 128, 9)])
+def test_infinite_adapters(mx, M, N, R, n, dtype):
+    """Infinities in B: of V's sign where V is not 0, whatever bits V has, NaN where it is; other elements as ever."""
+    c = Case(mx, M, 64, N, R, n, dtype, M + R, True, ranks=False, scale=False)
+    at = torch.rand(c.B.shape, generator=torch.Generator().manual_seed(R))
+    c.B[(at < 0.15 / R).to(DEV)] = float("inf")
+    c.B[(at > 1 - 0.15 / R).to(DEV)] = -float("inf")
+    if M > 4:
+        c.X[3, 5], c.X[4, 6] = float("inf"), -float("inf")
+    want, x = c.Y.double().cpu().numpy(), c.X.double().cpu().numpy()
+    A, B = c.A.double().cpu().numpy(), c.B.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        for t, a in enumerate(c.ids.tolist()):
+            if 0 <= a < n:
+                want[t] += (B[a] * (A[a] * x[t]).sum(1)).sum(1)
+    assert np.isinf(want).any() and np.isfinite(want).any()
+    assert np.array_equal(c.run().double().cpu().numpy(), want, equal_nan=True)
+
+
 def test_values_of_v_near_the_largest(mx):
     """V up to the largest fp32 numbers: no part of it overflows."""
     c = Case(mx, 4, 32, 8, 2, 1, BF, 2, True, ranks=False, scale=False)
