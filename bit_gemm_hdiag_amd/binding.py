@@ -100,6 +100,7 @@ def _load():
         "mxs_kv4_reserve_workspace": (c_size_t, [c_int64, c_int64]),
         "mxs_kv4_reserve": (S, [P, P, P, c_int64, c_int64, P, P, c_int64, P, P, P, c_size_t, P]),
         "mxs_kv4_compact": (S, [P, P, c_int64, c_int64, P, P, P, P, c_int64, P, P]),
+        "mxs_kv4_compact_granted": (S, [P, P, c_int64, c_int64, P, P, P, P, P, c_int64, P, P]),
         "mxs_kv4_release": (S, [P, P, P, c_int64, c_int64, P, P, P, P]),
         "mxs_verify_tree_workspace": (c_size_t, [c_int64] * 4),
         "mxs_verify_tree": (S, [P, c_int32, c_int64, c_int64, P, P, P, c_int64, c_int64, c_int64, P, c_int64, c_int32,
@@ -127,7 +128,7 @@ EXPORTED = ("mxs_status_string", "mxs_last_error", "mxs_version", "mxs_budget_bl
             "mxs_mixed_gemm_prepared", "mxs_mixed_gemm_fused_prepared_workspace", "mxs_mixed_gemm_fused_prepared",
             "mxs_rope_frequencies", "mxs_rope", "mxs_kv4_append", "mxs_kv4_read", "mxs_attend_kv4_tree_workspace",
             "mxs_attend_kv4_tree", "mxs_kv4_copy", "mxs_kv4_fork", "mxs_kv4_reserve_workspace", "mxs_kv4_reserve",
-            "mxs_kv4_compact", "mxs_kv4_release", "mxs_verify_tree_workspace", "mxs_verify_tree",
+            "mxs_kv4_compact", "mxs_kv4_compact_granted", "mxs_kv4_release", "mxs_verify_tree_workspace", "mxs_verify_tree",
             "mxs_lora_add_workspace", "mxs_lora_add")
 
 
@@ -801,21 +802,39 @@ def mxs_kv4_reserve(cache: KV4Cache, refs: torch.Tensor, table: torch.Tensor, le
     return slots, lens_out
 
 
+def _compact(cache: KV4Cache, table, lens, cu, path, count, lens_out):
+    """(lens_out, arguments before and behind the slots) of a compaction."""
+    gpu, total = cache.gpu, path.numel()
+    pt, width, B = _table(cache, table)
+    if lens_out is None:
+        lens_out = torch.empty(B, dtype=torch.int32, device=cache.kc.device)
+    return lens_out, (cache._ref, pt, width, B, _vector(lens, "lens", torch.int32, B, gpu),
+                      _vector(cu, "cu", torch.int32, B + 1, gpu), _vector(path, "path", torch.int32, total, gpu),
+                      _vector(count, "count", torch.int32, B, gpu)), \
+        (total, _vector(lens_out, "lens_out", torch.int32, B, gpu))
+
+
 def mxs_kv4_compact(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor, path: torch.Tensor,
                     count: torch.Tensor, lens_out: torch.Tensor | None = None) -> torch.Tensor:
     """lens_out [B]: of the last cu[b + 1] - cu[b] tokens of every sequence, those
     numbered path[cu[b]] .. path[cu[b] + count[b] - 1] (ascending) are moved together
     behind the others, and the length ends there. path and count as
-    mxs_verify_tree returns them. lens_out may be lens."""
-    gpu = cache.gpu
-    pt, width, B = _table(cache, table)
-    total = path.numel()
-    if lens_out is None:
-        lens_out = torch.empty(B, dtype=torch.int32, device=cache.kc.device)
-    _call(gpu, _lib.mxs_kv4_compact, "mxs_kv4_compact", cache._ref, pt, width, B,
-          _vector(lens, "lens", torch.int32, B, gpu), _vector(cu, "cu", torch.int32, B + 1, gpu),
-          _vector(path, "path", torch.int32, total, gpu), _vector(count, "count", torch.int32, B, gpu), total,
-          _vector(lens_out, "lens_out", torch.int32, B, gpu))
+    mxs_verify_tree returns them. lens_out may be lens. For steps in which every
+    sequence was granted its room; otherwise mxs_kv4_compact_granted."""
+    lens_out, front, back = _compact(cache, table, lens, cu, path, count, lens_out)
+    _call(cache.gpu, _lib.mxs_kv4_compact, "mxs_kv4_compact", *front, *back)
+    return lens_out
+
+
+def mxs_kv4_compact_granted(cache: KV4Cache, table: torch.Tensor, lens: torch.Tensor, cu: torch.Tensor,
+                            path: torch.Tensor, count: torch.Tensor, slots: torch.Tensor,
+                            lens_out: torch.Tensor | None = None) -> torch.Tensor:
+    """As mxs_kv4_compact, with the slots [total] that mxs_kv4_reserve left for this
+    cu: a sequence that it refused (a first slot of -1) has none of its new tokens
+    in the cache and is left as it is, its length with it. total is path's."""
+    lens_out, front, back = _compact(cache, table, lens, cu, path, count, lens_out)
+    _call(cache.gpu, _lib.mxs_kv4_compact_granted, "mxs_kv4_compact_granted", *front,
+          _vector(slots, "slots", torch.int64, path.numel(), cache.gpu), *back)
     return lens_out
 
 

@@ -673,19 +673,32 @@ mxs_status mxs_kv4_reserve(const mxs_kv4_cache *cache, int32_t *refs, int32_t *t
                                                  stream), "kv4_reserve");
 }
 
+static mxs_status compact(const mxs_kv4_cache *cache, const int32_t *table, int64_t ldt, int64_t B,
+                          const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
+                          const int64_t *slots, int64_t total, int32_t *lens_out, hipStream_t stream, const char *name) {
+    const mxs_status r = check_table(cache, nullptr, false, table, ldt, B, lens, name);
+    if (r != MXS_OK) return r;
+    if (total < 0) return fail(MXS_ERR_SHAPE, "%s: total=%lld", name, (long long)total);
+    if (total > kMaxTokens) return fail(MXS_ERR_UNSUPPORTED, "%s: total=%lld", name, (long long)total);
+    if (B == 0) return ok();
+    if (!cu || !count || !lens_out || (total > 0 && !path)) return fail(MXS_ERR_ARG, "%s: NULL pointer", name);
+    if (!aligned(cu, 4) || !aligned(count, 4) || !aligned(path, 4) || !aligned(lens_out, 4) || !aligned(slots, 8))
+        return fail(MXS_ERR_UNSUPPORTED, "%s: misaligned pointer", name);
+    return device_status(mxs::launch_kv4_compact(*cache, table, ldt, B, lens, cu, path, count, slots, total, lens_out,
+                                                 stream), name);
+}
+
 mxs_status mxs_kv4_compact(const mxs_kv4_cache *cache, const int32_t *table, int64_t ldt, int64_t B,
                            const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
                            int64_t total, int32_t *lens_out, hipStream_t stream) {
-    const mxs_status r = check_table(cache, nullptr, false, table, ldt, B, lens, "kv4_compact");
-    if (r != MXS_OK) return r;
-    if (total < 0) return fail(MXS_ERR_SHAPE, "kv4_compact: total=%lld", (long long)total);
-    if (total > kMaxTokens) return fail(MXS_ERR_UNSUPPORTED, "kv4_compact: total=%lld", (long long)total);
-    if (B == 0) return ok();
-    if (!cu || !count || !lens_out || (total > 0 && !path)) return fail(MXS_ERR_ARG, "kv4_compact: NULL pointer");
-    if (!aligned(cu, 4) || !aligned(count, 4) || !aligned(path, 4) || !aligned(lens_out, 4))
-        return fail(MXS_ERR_UNSUPPORTED, "kv4_compact: misaligned pointer");
-    return device_status(mxs::launch_kv4_compact(*cache, table, ldt, B, lens, cu, path, count, total, lens_out,
-                                                 stream), "kv4_compact");
+    return compact(cache, table, ldt, B, lens, cu, path, count, nullptr, total, lens_out, stream, "kv4_compact");
+}
+
+mxs_status mxs_kv4_compact_granted(const mxs_kv4_cache *cache, const int32_t *table, int64_t ldt, int64_t B,
+                                   const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
+                                   const int64_t *slots, int64_t total, int32_t *lens_out, hipStream_t stream) {
+    if (B > 0 && total > 0 && !slots) return fail(MXS_ERR_ARG, "kv4_compact_granted: NULL pointer");
+    return compact(cache, table, ldt, B, lens, cu, path, count, slots, total, lens_out, stream, "kv4_compact_granted");
 }
 
 mxs_status mxs_kv4_release(const mxs_kv4_cache *cache, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,

@@ -98,7 +98,7 @@ hipError_t launch_kv4_reserve(const mxs_kv4_cache &c, int32_t *refs, int32_t *ta
                               int32_t *lens_out, void *ws, hipStream_t st);
 hipError_t launch_kv4_compact(const mxs_kv4_cache &c, const int32_t *table, int64_t ldt, int64_t B,
                               const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
-                              int64_t total, int32_t *lens_out, hipStream_t st);
+                              const int64_t *slots, int64_t total, int32_t *lens_out, hipStream_t st);
 hipError_t launch_kv4_release(const mxs_kv4_cache &c, int32_t *refs, int32_t *table, int64_t ldt, int64_t B,
                               const int32_t *lens, const int32_t *keep, int32_t *lens_out, hipStream_t st);
 

@@ -377,9 +377,10 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
 // are moved 1024 code words (with their scale bytes) at a time, in ascending
 // order: all are read before the first is written, and what a later turn reads no
 // earlier one has written, because path[i] >= i. 96 sequences of up to 26 tokens take
-// 5.9 us (a thread a column, token after token: 15).
+// 5.9 us (a thread a column, token after token: 15). A sequence whose first slot is -1
+// was refused its tokens: its last ones are not theirs, and may lie in shared pages.
 __global__ __launch_bounds__(256) void k_kv4_compact(SeqArgs a, Planes pl, const int32_t *path, const int32_t *count,
-                                                     int32_t *lens_out) {
+                                                     const int64_t *slots, int32_t *lens_out) {
     __shared__ int32_t from[256], to[256];
     const int64_t b = blockIdx.x;
     const int tid = threadIdx.x;
@@ -389,7 +390,7 @@ __global__ __launch_bounds__(256) void k_kv4_compact(SeqArgs a, Planes pl, const
     const int n = c1 > c0 ? c1 - c0 : 0;
     int kept = count[b];
     kept = kept < 0 ? 0 : (kept > n ? n : kept);
-    const bool moves = len >= n;
+    const bool moves = len >= n && !(slots && n > 0 && slots[c0] < 0);
     __syncthreads();                            // every thread has read lens before it may be written
     if (tid == 0) lens_out[b] = moves ? len - n + kept : len;
     if (!moves) return;
@@ -503,9 +504,9 @@ hipError_t launch_kv4_reserve(const mxs_kv4_cache &c, int32_t *refs, int32_t *ta
 
 hipError_t launch_kv4_compact(const mxs_kv4_cache &c, const int32_t *table, int64_t ldt, int64_t B,
                               const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
-                              int64_t total, int32_t *lens_out, hipStream_t st) {
+                              const int64_t *slots, int64_t total, int32_t *lens_out, hipStream_t st) {
     const SeqArgs a{nullptr, const_cast<int32_t *>(table), ldt, B, c.pages, total, lens, cu, c.page_size};
-    hipLaunchKernelGGL(k_kv4_compact, dim3((unsigned)B), dim3(256), 0, st, a, planes_of(c), path, count, lens_out);
+    hipLaunchKernelGGL(k_kv4_compact, dim3((unsigned)B), dim3(256), 0, st, a, planes_of(c), path, count, slots, lens_out);
     return hipGetLastError();
 }
 

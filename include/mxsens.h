@@ -633,7 +633,7 @@ mxs_status mxs_kv4_fork(const mxs_kv4_cache *cache, int32_t *refs, int32_t *tabl
  * length would pass 2^31 - 1 or is negative is refused: its slots are -1, its
  * table is left and lens_out[b] = lens[b]. So is, once the free pages run out, the
  * first sequence that they do not serve whole, and every later one that needs a
- * page.
+ * page. A step that goes on with the same cu ends in mxs_kv4_compact_granted.
  * cu: [B + 1] int32 ascending from 0, cu[B] <= total; slots: [total] int64, those
  * of no sequence are left as they were; total < 2^24. At most 2^24 pages, B <=
  * 65535. ws: >= mxs_kv4_reserve_workspace(pages, B) bytes, 16-byte aligned,
@@ -656,13 +656,30 @@ mxs_status mxs_kv4_reserve(const mxs_kv4_cache *cache, int32_t *refs, int32_t *t
  * tokens in no page are skipped; counts are taken between 0 and n. A sequence
  * with fewer than n cached tokens is left as it is, lens_out[b] = lens[b]. Tokens
  * are moved where they lie: the pages of the last n tokens are not shared (as
- * mxs_kv4_reserve leaves them). path: [total] int32, cu as above.
+ * mxs_kv4_reserve leaves them where it had room: every sequence with n > 0 has
+ * been granted them, or mxs_kv4_compact_granted is called). path: [total] int32,
+ * cu as above.
  * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE, MXS_ERR_UNSUPPORTED (B > 65535, ldt > 2^30,
  * alignment), MXS_ERR_DEVICE.
  */
 mxs_status mxs_kv4_compact(const mxs_kv4_cache *cache, const int32_t *table, int64_t ldt, int64_t B,
                            const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
                            int64_t total, int32_t *lens_out, hipStream_t stream);
+
+/*
+ * The same where mxs_kv4_reserve may have refused sequences: slots [total] are those
+ * that it left for this cu. A sequence with slots[cu[b]] < 0 has none of its n
+ * tokens in the cache; it is left as it is, lens_out[b] = lens[b] (mxs_kv4_compact
+ * would take the last n tokens that it did have for the drafted ones, and move
+ * them in pages that may be shared). The calls between only read for such a
+ * sequence: mxs_kv4_append skips its slots, and its rows of mxs_attend_kv4_tree's
+ * output, its path, count and next of mxs_verify_tree mean nothing. The same step
+ * can be repeated for it once pages are free.
+ * Errors: as mxs_kv4_compact.
+ */
+mxs_status mxs_kv4_compact_granted(const mxs_kv4_cache *cache, const int32_t *table, int64_t ldt, int64_t B,
+                                   const int32_t *lens, const int32_t *cu, const int32_t *path, const int32_t *count,
+                                   const int64_t *slots, int64_t total, int32_t *lens_out, hipStream_t stream);
 
 /*
  * Pages given back: every page of row b behind the first keep[b] tokens (entries

@@ -132,3 +132,41 @@ def test_binding_refuses_wrong_tensors(monkeypatch):
     for f in bad:
         with pytest.raises(ValueError):
             f()
+
+
+def test_compaction_with_the_slots_of_a_reservation(lib):
+    f = lib.mxs_kv4_compact_granted
+    f.argtypes, f.restype = [P, P, c_int64, c_int64, P, P, P, P, P, c_int64, P, P], c_int32
+
+    def call(c=None, table=A, ldt=10, B=4, lens=A, cu=A, path=A, count=A, slots=A, total=8, out=A):
+        return f(c or cache(), table, ldt, B, lens, cu, path, count, slots, total, out, None)
+    for bad, status in BAD_CACHES:
+        assert call(c=cache(**bad)) == status
+    assert call(B=0) == OK and call(B=0, slots=None, path=None) == OK
+    for k in ("table", "lens", "cu", "path", "count", "slots", "out"):
+        assert call(**{k: None}) == ARG, k
+        assert call(**{k: MIS4}) == UNSUPPORTED, k
+    assert call(slots=MIS8) == UNSUPPORTED
+    assert call(B=-1) == SHAPE and call(ldt=-1) == SHAPE and call(total=-1) == SHAPE
+    assert call(B=65536) == UNSUPPORTED and call(total=1 << 24) == UNSUPPORTED
+
+
+def test_binding_passes_the_slots_of_a_reservation(monkeypatch):
+    import torch
+    import bit_gemm_hdiag_amd as mx
+    from bit_gemm_hdiag_amd import binding
+    from test_binding_workspace import Device
+    calls = []
+    monkeypatch.setattr(binding, "_call", lambda gpu, fn, name, *args: calls.append((name, args)))
+    I32, I64 = torch.int32, torch.int64
+    c = mx.KV4Cache(*(Device((6, 16, 2, w), torch.uint8) for w in (32, 2, 32, 2)))
+    d = lambda n, t=I32: Device((n,), t)
+    args = c, Device((3, 5), I32), d(3), d(4), d(8), d(3)
+    mx.mxs_kv4_compact(*args, lens_out=d(3))
+    mx.mxs_kv4_compact_granted(*args, d(8, I64), lens_out=d(3))
+    assert [n for n, _ in calls] == ["mxs_kv4_compact", "mxs_kv4_compact_granted"]
+    assert [len(a) for _, a in calls] == [10, 11]
+    for slots in (d(7, I64), d(8)):
+        with pytest.raises(ValueError):
+            mx.mxs_kv4_compact_granted(*args, slots, lens_out=d(3))
+    assert len(calls) == 2

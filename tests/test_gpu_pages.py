@@ -402,3 +402,88 @@ def test_on_a_stream_of_the_callers(mx):
         p.release([-1, 0, 20, -1, -1, -1, 0, -1, -1])
     s.synchronize()
     p.same()
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_refused_sequences_keep_their_tokens(mx, graph):
+    """A step whose cu is never looked at on the host, over a pool that runs out: sequences that were refused, forks of
+    one another among them, keep table, length and tokens; the others are compacted; the step is repeated with room."""
+    p = Pool(mx, 12, 4, 2, 64, 6, 10, 21)
+    p.write(p.reserve([6, 14, 9, 0, 3, 0]))                       # 2 + 4 + 3 + 1 of 12 pages
+    p.fork([1], [3])
+    ns, paths = [2, 4, 4, 5, 1, 3], [[0, 1], [0, 2], [0, 2, 3], [0, 3, 4], [0], [0, 2]]
+    cu = np.concatenate([[0], np.cumsum(ns)])
+    path = np.full(cu[-1], -1)
+    for b, x in enumerate(paths):
+        path[cu[b]:cu[b] + len(x)] = x
+    cu, path, count = dev(cu), dev(path), dev([len(x) for x in paths])
+    total = int(path.numel())
+    g = torch.Generator(device=DEV).manual_seed(2)
+    k, v, q = (torch.randn((total, h, 64), generator=g, device=DEV) for h in (2, 2, 4))
+    logits = torch.randn((total, 50), generator=g, device=DEV)
+    tokens, u = torch.zeros(total, dtype=torch.int64, device=DEV), torch.rand(total, dtype=torch.float64, device=DEV)
+    ws = torch.empty(mx.mxs_kv4_reserve_workspace(12, 6), dtype=torch.uint8, device=DEV)
+    slots, grown = torch.empty(total, dtype=torch.int64, device=DEV), dev([0] * 6)
+
+    def step():
+        mx.mxs_kv4_reserve(p.cache, p.refs, p.table, p.lens, cu, slots=slots, lens_out=grown, ws=ws)
+        mx.mxs_kv4_append(p.cache, k, v, slots)
+        mx.mxs_kv4_compact_granted(p.cache, p.table, grown, cu, path, count, slots, lens_out=p.lens)
+        mx.mxs_kv4_release(p.cache, p.refs, p.table, p.lens, p.lens, lens_out=p.lens)
+
+    def tokens_of(b, n):
+        row = p.table[b].tolist()
+        at = [row[t // 4] * 4 + t % 4 for t in range(n)]
+        return [getattr(p.cache, x).flatten(0, 1)[at].clone() for x in PLANES]
+
+    def same(x, y):
+        return all(torch.equal(a, b) for a, b in zip(x, y))
+    lens = p.lens.tolist()
+    before = [tokens_of(b, n) for b, n in enumerate(lens)]
+    if graph:
+        torch.cuda.synchronize()
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            step()
+        once = captured.replay
+    else:
+        once = step
+    # 0 has room; 1 and 3 share a page that each would copy: 1 takes the last two, 2, 3 and 5 are refused; 4 has room
+    once()
+    torch.cuda.synchronize()
+    first = slots[cu[:-1].long()].tolist()
+    assert [x < 0 for x in first] == [False, False, True, True, False, True]
+    assert p.lens.tolist() == [8, 16, 9, 14, 4, 0]
+    for b, n in enumerate(lens):
+        assert same(tokens_of(b, n), before[b]), b
+    for b in (0, 1):                                              # the accepted ones, in their new places
+        a = torch.arange(len(paths[b]), device=DEV)
+        new = mx.mxs_kv4_read(p.cache, torch.tensor([int(p.table[b, (lens[b] + i) // 4]) * 4 + (lens[b] + i) % 4
+                                                     for i in a.tolist()], device=DEV), torch.float32)
+        other = mx.kv4_cache_alloc(2, 4, 2, 64)
+        rows = [int(cu[b]) + i for i in paths[b]]
+        mx.mxs_kv4_append(other, k[rows].contiguous(), v[rows].contiguous(), a)
+        want = mx.mxs_kv4_read(other, a, torch.float32)
+        assert torch.equal(new[0], want[0]) and torch.equal(new[1], want[1])
+    held = p.table[p.table >= 0]
+    assert torch.equal(torch.bincount(held, minlength=12).int(), p.refs)
+    # the calls that read change nothing for a refused sequence (the pool's bytes are any, NaN among them)
+    now = [getattr(p.cache, x).clone() for x in PLANES] + [p.table.clone(), p.lens.clone()]
+    out = mx.mxs_attend_kv4_tree(q, p.cache, p.table, grown, cu, 0.125, max_q=5)
+    mx.mxs_verify_tree(logits, tokens, cu, u)
+    assert out.shape == q.shape and same(now, [getattr(p.cache, x) for x in PLANES] + [p.table, p.lens])
+    # room again: the first two end
+    mx.mxs_kv4_release(p.cache, p.refs, p.table, p.lens, dev([0, 0, -1, -1, -1, -1]), lens_out=p.lens)
+    cu[:3] = 0                                                    # nothing more of theirs
+    p.lens[:2] = 0
+    shared = tokens_of(2, 9), tokens_of(3, 14)
+    path[:4] = torch.tensor([0, 2, 3, -1], device=DEV)
+    path[4:9] = torch.tensor([0, 3, 4, -1, -1], device=DEV)
+    path[9:13] = torch.tensor([0, 0, 2, -1], device=DEV)
+    cu[2:] = torch.tensor([0, 4, 9, 10, 13], device=DEV)
+    once()
+    torch.cuda.synchronize()
+    assert p.lens.tolist() == [0, 0, 12, 17, 5, 2]
+    assert same(tokens_of(2, 9), shared[0]) and same(tokens_of(3, 14), shared[1])
+    held = p.table[p.table >= 0]
+    assert torch.equal(torch.bincount(held, minlength=12).int(), p.refs)
