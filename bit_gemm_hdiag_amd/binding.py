@@ -958,7 +958,7 @@ def mxs_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, cu: torch.Tensor
             raise TypeError("draft must be fp32")
         pd, ldd = _matrix(draft, "draft", total, V, gpu)
     if max_n is None:
-        max_n = total
+        max_n = min(total, 1024)
     if path is None:
         path = torch.full((total,), -1, dtype=torch.int32, device=dev)
     if count is None:

@@ -82,3 +82,22 @@ def test_binding_refuses_wrong_tensors(monkeypatch):
                 dict(next_token=d(2, I32))):
         with pytest.raises((ValueError, TypeError)):
             mx.mxs_verify_tree(**{**ok, **bad})
+
+
+@pytest.mark.parametrize("total", [6, 1024, 1025, 9000])
+def test_default_bound_of_a_tree(monkeypatch, total):
+    """Without max_n a batch of any number of rows is taken; its trees hold at most 1024 nodes."""
+    import torch
+    import bit_gemm_hdiag_amd as mx
+    from bit_gemm_hdiag_amd import binding
+    from test_binding_workspace import Device
+    seen = []
+    monkeypatch.setattr(binding, "_call", lambda gpu, fn, name, *args: seen.append(args))
+    F64, I32, I64 = torch.float64, torch.int32, torch.int64
+    d = lambda n, t: Device((n,), t)
+    args = Device((total, 100), torch.bfloat16), d(total, I64), d(3, I32), d(total, F64)
+    outs = dict(path=d(total, I32), count=d(2, I32), next_token=d(2, I64), ws=d(1 << 16, torch.uint8))
+    mx.mxs_verify_tree(*args, **outs)
+    mx.mxs_verify_tree(*args, **outs, max_n=4)
+    assert [x[9] for x in seen] == [min(total, 1024), 4]
+    assert mx.mxs_verify_tree_workspace(2, total, seen[0][9], 100) > 0

@@ -341,6 +341,14 @@ def test_trees_longer_than_the_bound(mx):
         c.run(mx, max_n=1025)
 
 
+def test_batches_of_many_rows_without_a_bound(mx):
+    """max_n left out: more than 1024 rows in all, and a tree of more than 1024 nodes, cut off there."""
+    for ns in ([64] * 32, [3, 1100, 20]):
+        c = Case(ns, 60, BF, False, 3)
+        c.max_n = 1024
+        c.check(c.run(mx, max_n=None))
+
+
 def test_empty_batches(mx):
     c = Case([0, 0], 10, F32, True, 1)
     c.t_logits, c.t_draft = (torch.zeros(0, 10, device=DEV) for _ in range(2))
