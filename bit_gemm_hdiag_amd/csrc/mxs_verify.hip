@@ -96,7 +96,8 @@ struct Weight {
     // Where sums need none of the exceptions below: a finite maximum, T < inf, and
     // an fp32 number near m + lo. Weights below that one's, about 2^-1000, those of
     // NaN and -inf among them, count as that (the median of three is the smallest
-    // where one is NaN).
+    // where one is NaN): nothing beside the maximum's 1 in the sum of a row. Sums of a
+    // remainder, which may hold nothing else, leave them out.
     __device__ __forceinline__ bool plain() const {
         const double d = (double)low - m;
         return c > 0.0 && fabs(m) < INFINITY && d <= 0.9 * lo && d >= 1.02 * lo;
@@ -412,7 +413,7 @@ __global__ __launch_bounds__(256) void k_rest(Args a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const double x = r[j] - w.S * clean(q4[k / 4][j]);
-                    s += x > 0.0 ? x : 0.0;
+                    s += x > 0.0 && v[k + j] >= e.low ? x : 0.0;
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -625,7 +626,7 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const double x = r[k] - s0 * clean(q0[k]);
-                s += x > 0.0 ? x : 0.0;
+                s += x > 0.0 && (!plain || v0[k] >= e.low) ? x : 0.0;
             }
         }
         s = wave_sum(s);
@@ -642,7 +643,9 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
 }
 
 // The next token of every sequence: the chunk where the cumulated sum of what is
-// left crosses the random number, then the token in it.
+// left crosses the random number, then the token in it. What a chunk has left without
+// the tokens taken out of it is a difference, which rounding can leave above 0 where
+// they were all it had: a chunk in which nothing is found counts as 0 from then on.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_draw(Args a) {
     __shared__ double sums[kMaxChunks], wsum[16];
@@ -672,6 +675,7 @@ __global__ __launch_bounds__(1024) void k_draw(Args a) {
     // the sums of the remainder's chunks, or those of the row's less the tokens taken
     // out; the row's own where nothing is left of it
     bool rem = st.sums == kRemainder, whole = false;
+    uint64_t empty = 0;
 #pragma unroll 1
     for (;;) {
         if (wave == 0) {
@@ -687,6 +691,7 @@ __global__ __launch_bounds__(1024) void k_draw(Args a) {
                     }
                 }
             }
+            if (empty >> lane & 1) s = 0.0;
             const double upto = wave_scan(s), target = u * lane_of(upto, 63);
             // first one whose inclusive sum is past the target, else the last that holds anything
             const uint64_t found = __ballot(s > 0.0 && upto > target), any = __ballot(s > 0.0);
@@ -754,8 +759,13 @@ __global__ __launch_bounds__(1024) void k_draw(Args a) {
             if (tid == 0) a.next[b] = x;
             return;
         }
-        rem = false;                                  // nothing but rounding was left
-        whole = true;
+        if (w.at >= 0) {
+            empty |= 1ull << w.at;
+        } else {                                      // nothing but rounding was left of any chunk
+            rem = false;
+            whole = true;
+            empty = 0;
+        }
         __syncthreads();
     }
 }

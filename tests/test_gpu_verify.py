@@ -283,6 +283,51 @@ def test_ends_of_the_random_numbers(mx, draft):
     assert c.run(mx)[2].tolist() == [3999] * 3
 
 
+@pytest.mark.parametrize("kind", ["tree", "again", "none"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V,first", [(9000, 5000), (2600, 1500), (30011, 20500), (270001, 70000)])
+def test_remainders_behind_masked_tokens(mx, V, first, dtype, kind):
+    """The draw from a remainder whose first chunks hold masked tokens alone: 0 draws the first token that has any left."""
+    B = 40 if V < 20000 else 6
+    c = Case([5] * B, V, dtype, kind != "none", V, "again" if kind == "again" else "tree", sharp=1.0)
+    g = np.random.default_rng(1)
+    c.t_logits[:, :first] = -math.inf
+    c.parents = np.tile(np.array([-1, 0, 0, 0, 0], np.int32), B)
+    if c.draft is not None:
+        q = c.draft.copy()
+        q[:, :first] = 0
+        q[:, first:first + 3] *= 30                               # these are used up by a rejection
+        q = (q / q.sum(1, keepdims=True)).astype(np.float32)
+        c.draft = q
+        c.t_draft.copy_(torch.from_numpy(q))
+    c.tokens = g.choice(first + np.arange(40), c.total).astype(np.int64)
+    c.u[:] = 1 - 2.0 ** -53
+    c.u[::5] = 0.0
+    assert c.check(c.run(mx))[1] > 0
+
+
+@pytest.mark.parametrize("V", [3 * 4096, 40000, 300000])
+@pytest.mark.parametrize("kids", [2, 3, 5])
+def test_chunks_of_taken_tokens_alone(mx, V, kids):
+    """Without a draft's distribution: rejected tokens are all that the first chunk had. None of them is drawn."""
+    B = 64 if V < 100000 else 16
+    c = Case([kids + 1] * B, V, F32, False, kids, "tree", sharp=1.0)
+    g = np.random.default_rng(2)
+    c.parents = np.tile(np.array([-1] + [0] * kids, np.int32), B)
+    l = c.t_logits.view(B, kids + 1, V)
+    l[:, :, :16384 if V > 1 << 18 else 4096] = -math.inf
+    tok = np.zeros((B, kids + 1), np.int64)
+    for b in range(B):
+        at = g.choice(4096, kids, replace=False)
+        tok[b, 1:] = at
+        l[b, 0, torch.from_numpy(at).to(DEV)] = torch.from_numpy(g.standard_normal(kids)).float().to(DEV)
+    c.tokens = tok.reshape(-1)
+    for u in (0.0, 1e-17, 0.5):
+        c.u[:] = 1 - 2.0 ** -53
+        c.u[::kids + 1] = u
+        c.check(c.run(mx))
+
+
 def test_tokens_and_parents_that_do_not_belong(mx):
     for draft in (True, False):
         c = Case([10] * 8, 300, F32, draft, 12, "tree", None, sharp=1.0)
