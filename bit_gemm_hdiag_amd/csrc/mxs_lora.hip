@@ -489,18 +489,31 @@ Plan plan_of(int64_t M, const mxs_lora &s) {
     p.steps = (int)ceil_div(s.R, es == 2 ? 32 : 16);
     p.steps = p.steps <= 2 ? p.steps : (p.steps <= 4 ? 4 : 8);
     const int64_t ranks = ceil_div(p.Rp, 16 * p.nt);
-    // slices of K until the chip is filled, each a turn of the four waves or more, and
-    // V's partial sums below an eighth of X (or 2 MiB)
+    // slices of K until the chip is filled, as many as let V's partial sums stay below an
+    // eighth of X (or 2 MiB) wanted at most, each whole turns of the four waves: rounded
+    // down, so that there may be up to twice as many slices
     const int64_t turn = 1024 / es, turns = ceil_div(s.K, turn);
-    int64_t most = s.K * es / (32 * p.Rp);
-    const int64_t room = ((int64_t)1 << 19) / (M * p.Rp);
-    most = p.small ? 16 : (most > room ? most : room);
+    const int64_t eighth = s.K * es / (32 * p.Rp), room = ((int64_t)1 << 19) / (M * p.Rp);
+    const int64_t most = p.small ? 16 : (eighth > room ? eighth : room);
     int64_t want = ceil_div(1024, busy * ranks);
     want = want < most ? want : most;
     want = want < 1 ? 1 : (want > 64 ? 64 : want);
     p.kper = turn * (turns > want ? turns / want : 1);
     while (ceil_div(s.K, p.kper) > 128) p.kper += turn;
     p.splits = (int)ceil_div(s.K, p.kper);
+    // Rows of V that a workspace has room for: M times the slices, and no fewer than any
+    // smaller M takes, so that one for the largest batch serves all. The slices number less
+    // than 2 want; each of these bounds does not fall as M grows: a turn a slice (at most
+    // 128); twice what fills the chip (busy >= M / 64); twice `most`.
+    int64_t rows = M * (turns < 128 ? turns : 128);
+    auto bound = [&](int64_t r) { rows = rows < r ? rows : r; };
+    if (p.small) {
+        bound(32 * M);
+    } else {
+        const int64_t share = M * (eighth < 1 ? 1 : eighth), least = ((int64_t)1 << 19) / p.Rp;
+        bound(M + 2 * 1024 * kTile / ranks);
+        bound(2 * (share > least ? share : least));
+    }
     // columns of Y a workgroup takes: 64 where 256 would leave the chip unfilled, else 512
     // (prompts of 4096 rows: 79 us at 256, 74 at 512, 90 at 1024; 64 rows on 32 adapters: 67,
     // 57, 55), and more from 4096 workgroups on
@@ -514,7 +527,7 @@ Plan plan_of(int64_t M, const mxs_lora &s) {
         at += (bytes + 255) / 256 * 256;
         return o;
     };
-    p.V = take((size_t)p.splits * M * p.Rp * 4);
+    p.V = take((size_t)rows * p.Rp * 4);
     if (!p.small) {
         p.order = take((size_t)M * 4);
         p.list = take((size_t)p.tiles * sizeof(Tile));

@@ -776,8 +776,9 @@ typedef struct mxs_lora {
  * X: [M, ldx >= K] of set->dtype; ids: [M] int32; Y: [M, ldy >= N] fp32 (rows of
  * 16-byte alignment are faster, as are ranks of whole 16-byte vectors). K % 32
  * == 0, M <= 2^22. ws: >= mxs_lora_add_workspace bytes (0 for sizes that the
- * call refuses), 256-byte aligned, contents scratch; calls that may overlap need
- * one each. M = 0, N = 0 or n = 0 is a no-op.
+ * call refuses; never less for more rows, so that a workspace for the largest
+ * batch serves smaller ones), 256-byte aligned, contents scratch; calls that may
+ * overlap need one each. M = 0, N = 0 or n = 0 is a no-op.
  * Errors: MXS_ERR_ARG, MXS_ERR_SHAPE, MXS_ERR_UNSUPPORTED (sizes, alignment),
  * MXS_ERR_WORKSPACE, MXS_ERR_DEVICE.
  */

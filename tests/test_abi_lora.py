@@ -72,6 +72,19 @@ def test_workspace(lib):
     assert w(1 << 22, adapters(K=1 << 24, N=1 << 24, R=128, n=8192)) < 1 << 34
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("K,N,R,n", [(8192, 28672, 64, 48), (8192, 8192, 16, 16), (4096, 1001, 27, 9), (32, 100, 1, 1),
+                                     (14336, 4096, 128, 300), (1 << 20, 64, 8, 8192), (416, 64, 33, 2)])
+def test_workspace_for_the_largest_batch_serves_smaller_ones(lib, K, N, R, n, dtype):
+    s = adapters(K=K, N=N, R=R, n=n, dtype=dtype)
+    sizes = list(range(1, 9000)) + [x + d for k in range(14, 23) for x in (1 << k, 3 << k - 2) for d in (-1, 0, 1)]
+    last = 0
+    for M in sorted(x for x in sizes if x <= 1 << 22):
+        need = lib.mxs_lora_add_workspace(M, s)
+        assert need >= last, M
+        last = need
+
+
 def test_binding_refuses_wrong_tensors(monkeypatch):
     import torch
     import bit_gemm_hdiag_amd as mx

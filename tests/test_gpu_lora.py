@@ -199,6 +199,18 @@ def test_the_same_call_twice_gives_the_same_bits(mx, M):
         assert torch.equal(c.run(ws=ws), first)
 
 
+@pytest.mark.parametrize("K,N,R,n,most", [(8192, 256, 64, 48, 910), (8192, 256, 16, 16, 8128), (2048, 300, 40, 9, 400)])
+def test_one_workspace_for_all_batches(mx, K, N, R, n, most):
+    """A workspace of the size asked for the largest batch, with other bytes behind it, which stay."""
+    need = mx.mxs_lora_add_workspace(most, Case(mx, 1, K, N, R, n, BF, 1, True).set)
+    ws = torch.full((need + 4096,), 170, dtype=torch.uint8, device=DEV)
+    for M in (most, most - 1, most // 2 + 1, 65, 64, 63, 1):
+        c = Case(mx, M, K, N, R, n, BF, M, True)
+        ref, _ = c.reference()
+        assert np.array_equal(c.run(ws=ws[:need]).double().cpu().numpy(), ref), M
+        assert bool((ws[need:] == 170).all()), M
+
+
 def test_nothing_to_add(mx):
     for M in (8, 200):
         c = Case(mx, M, 64, 40, 8, 4, BF, 4, True, ranks=False)
