@@ -344,6 +344,20 @@ __device__ __forceinline__ void store_y(float *y, int64_t left, const f32x4 v[CT
     }
 }
 
+// One column tile of 16 tokens: B's infinities meet every part of V, or the first alone
+template <typename T, int STEPS, bool FIRST>
+__device__ __forceinline__ f32x4 tile_sum(Columns<T, STEPS, 1> b, const T *v0) {
+    constexpr int P = Parts<T>::P, D = Parts<T>::D, W = STEPS * D + Parts<T>::E;
+    f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+            acc = mma<T>(FIRST && q ? without_infinities(b.b[0][s]) : b.b[0][s],
+                         *reinterpret_cast<const u32x4 *>(v0 + q * kTile * W + s * D), acc);
+    return acc;
+}
+
 template <typename T, int STEPS, int CT>
 struct Expand {
     Columns<T, STEPS, CT> w;
@@ -354,25 +368,12 @@ struct Expand {
         w.load(a, c, adapter, rank);
         if (col < count) load_y<CT>(a.Y + (int64_t)rows[col] * a.ldy + c + 4 * g, a.N - c - 4 * g, later);
     }
-    // The sums of 16 tokens where one came out as NaN. An infinity of B meets a number as
-    // its first part only: the others may be 0, and their product with it NaN.
-    __device__ __forceinline__ void again(f32x4 acc[CT], const T *v0) const {
-        constexpr int P = Parts<T>::P, D = Parts<T>::D, W = STEPS * D + Parts<T>::E;
-#pragma unroll
-        for (int i = 0; i < CT; ++i) acc[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll 1
-            for (int q = 0; q < P; ++q) {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(v0 + q * kTile * W + s * D);
-#pragma unroll
-                for (int i = 0; i < CT; ++i) acc[i] = mma<T>(q == 0 ? w.b[i][s] : without_infinities(w.b[i][s]), v, acc[i]);
-            }
-    }
     __device__ __forceinline__ void run(const LoraArgs &a, const T *parts, const int32_t *rows, int adapter, int count,
                                         int rank, float scale, int64_t c, int64_t c1) {
         constexpr int P = Parts<T>::P, D = Parts<T>::D, E = Parts<T>::E, W = STEPS * D + E;
         const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+        const int64_t first = c;
+        bool left_out = false;
         for (; c < c1; c += 64 * CT) {
             const int64_t at = c + 4 * g, left = a.N - at;
             auto row = [&](int t) { return a.Y + (int64_t)rows[t + col] * a.ldy + at; };
@@ -392,27 +393,69 @@ struct Expand {
 #pragma unroll
                         for (int i = 0; i < CT; ++i) acc[i] = mma<T>(w.b[i][s], v, acc[i]);
                     }
-                if constexpr (P > 1) {
-                    bool nan = false;
-#pragma unroll
-                    for (int i = 0; i < CT; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) nan |= acc[i][j] != acc[i][j];
-                    if (__ballot(nan)) again(acc, parts + (t + col) * W + E * g);
-                }
                 if (t + 16 >= count && c + 64 * CT < c1) load(a, rows, adapter, count, rank, c + 64 * CT);
-                if (t + col < count) {
+                const bool nan = P > 1 && is_nan(acc);
+                left_out |= nan;
+                if (t + col < count && !nan) {
 #pragma unroll
                     for (int i = 0; i < CT; ++i) y[i] += scale * acc[i];
                     store_y<CT>(row(t), left, y);
                 }
             }
         }
+        if (P > 1 && __ballot(left_out)) rest(a, parts, rows, adapter, count, rank, scale, first, c1);
+    }
+    __device__ static __forceinline__ bool is_nan(const f32x4 acc[CT]) {
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+            nan |= __builtin_isunordered(acc[i][0], acc[i][1]) || __builtin_isunordered(acc[i][2], acc[i][3]);
+        return nan;
+    }
+    // What run() left out: lanes whose sums came out as NaN. An infinity of B meets a number
+    // as its first part only here: the others may be 0, and their product with it NaN.
+    __device__ static __forceinline__ void rest(const LoraArgs &a, const T *parts, const int32_t *rows, int adapter,
+                                                int count, int rank, float scale, int64_t c, int64_t c1) {
+        constexpr int W = STEPS * Parts<T>::D + Parts<T>::E;
+        const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+        Columns<T, STEPS, 1> b;
+#pragma unroll 1
+        for (; c < c1; c += 64 * CT) {
+#pragma unroll 1
+            for (int t = 0; t < count; t += 16) {
+                const T *v0 = parts + (t + col) * W + Parts<T>::E * g;
+                bool nan = false;
+#pragma unroll 1
+                for (int i = 0; i < CT; ++i) {
+                    b.load(a, c + 16 * i, adapter, rank);
+                    const f32x4 v = tile_sum<T, STEPS, false>(b, v0);
+                    nan |= __builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3]);
+                }
+                nan &= t + col < count;
+                if (!__ballot(nan)) continue;
+#pragma unroll 1
+                for (int i = 0; i < CT; ++i) {
+                    b.load(a, c + 16 * i, adapter, rank);
+                    const f32x4 v = tile_sum<T, STEPS, true>(b, v0);
+                    if (nan) {
+                        const int64_t at = c + 16 * i + 4 * g;
+                        float *row = a.Y + (int64_t)rows[t + col] * a.ldy + at;
+                        f32x4 u[1];
+                        load_y<1>(row, a.N - at, u);
+                        u[0] += scale * v;
+                        store_y<1>(row, a.N - at, u);
+                    }
+                }
+            }
+        }
     }
 };
 
+// Registers are kept to four waves a SIMD (three where LDS allows no more): unbounded, the
+// sums go to accumulation registers and the code for infinities costs a wave (64 rows on
+// 32 adapters 52 instead of 48 us, prompts of 4096 rows 76 instead of 68)
 template <typename T, int STEPS, int CT>
-__global__ __launch_bounds__(256) void k_lora_expand(LoraArgs a, bool small) {
+__global__ __launch_bounds__(256, STEPS <= 2 ? 4 : 3) void k_lora_expand(LoraArgs a, bool small) {
     constexpr int P = Parts<T>::P, D = Parts<T>::D, E = Parts<T>::E, Rd = STEPS * D, W = Rd + E;
     __shared__ __attribute__((aligned(16))) T parts[P * kTile * W];      // a row's place: 16 bytes of padding
     __shared__ int32_t rows[kTile];

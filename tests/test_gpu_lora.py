@@ -153,7 +153,7 @@ def test_infinite_products(mx, dtype):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("M,N,R,n", [(3, 20, 1, 1), (5, 70, 3, 2), (40, 64, 24, 3), (90, 200, 40, 2), (70, 15000, 8, 9),
-                                     (33, 300, 100, 1), (70, 15000, 40, 9), (70, 15000, 128, 9)])
+                                     (33, 300, 100, 1), (70, 15000, 40, 9), (70, 15000, 128, 9), (200, 15001, 12, 9)])
 def test_infinite_adapters(mx, M, N, R, n, dtype):
     """Infinities in B: of V's sign where V is not 0, whatever bits V has, NaN where it is; other elements as ever."""
     c = Case(mx, M, 64, N, R, n, dtype, M + R, True, ranks=False, scale=False)
