@@ -96,8 +96,8 @@ struct Weight {
     // Where sums need none of the exceptions below: a finite maximum, T < inf, and
     // an fp32 number near m + lo. Weights below that one's, about 2^-1000, those of
     // NaN and -inf among them, count as that (the median of three is the smallest
-    // where one is NaN): nothing beside the maximum's 1 in the sum of a row. Sums of a
-    // remainder, which may hold nothing else, leave them out.
+    // where one is NaN): nothing beside the maximum's 1 in the sum of a row, and below
+    // what a remainder counts (left_of).
     __device__ __forceinline__ bool plain() const {
         const double d = (double)low - m;
         return c > 0.0 && fabs(m) < INFINITY && d <= 0.9 * lo && d >= 1.02 * lo;
@@ -234,6 +234,8 @@ __device__ __forceinline__ int64_t sequence_of(const Args &a, int64_t row, int l
     return b;
 }
 
+// What is left of a weight: masked tokens, which sums may have as 2^-1000, have nothing
+__device__ __forceinline__ double left_of(double x) { return x > 0x1p-990 ? x : 0.0; }
 __device__ __forceinline__ double clean(float q) { return q > 0.f && q < INFINITY ? (double)q : 0.0; }
 
 // A chunk of a row, by a workgroup of 256 or (WAVE) by one wave: its maximum, and the
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(256) void k_rest(Args a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const double x = r[j] - w.S * clean(q4[k / 4][j]);
-                    s += x > 0.0 && v[k + j] >= e.low ? x : 0.0;
+                    s += left_of(x);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -421,7 +423,7 @@ __global__ __launch_bounds__(256) void k_rest(Args a) {
     } else {
 #pragma unroll 1
         for (int i = c * a.chunk + (int)threadIdx.x; i < (c + 1) * a.chunk && i < V; i += 256)
-            s += fmax(e(load1<T>(p + i)) - w.S * clean(q[i]), 0.0);
+            s += left_of(e(load1<T>(p + i)) - w.S * clean(q[i]));
     }
     s = wave_sum(s);
     if (lane == 0) ss[wave] = s;
@@ -626,7 +628,7 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const double x = r[k] - s0 * clean(q0[k]);
-                s += x > 0.0 && (!plain || v0[k] >= e.low) ? x : 0.0;
+                s += left_of(x);
             }
         }
         s = wave_sum(s);
@@ -720,7 +722,7 @@ __global__ __launch_bounds__(1024) void k_draw(Args a) {
                 if (rem) q = load4<float>(a.draft + (int64_t)st.cur * a.ldd + at, a.V - at, 0.f);
                 double r[4], part = 0.0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) r[k] = fmax(e(v[k]) - st.S * clean(q[k]), 0.0);
+                for (int k = 0; k < 4; ++k) r[k] = rem ? left_of(e(v[k]) - st.S * clean(q[k])) : e(v[k]);
                 for (int j = 0; j < st.gone && !whole; ++j) {
                     const int64_t k = a.gone[c0 + j] - at;
 #pragma unroll
