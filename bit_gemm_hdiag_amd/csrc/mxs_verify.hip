@@ -58,11 +58,13 @@ struct Piece {
     }
 };
 
-// exp((l - m) / T) for l <= m as 2^n p(f), n + f = (l - m) log2(e) / T, |f| <=
-// 1/2, with p the polynomial of degree 8 that interpolates 2^f at the Chebyshev
-// points: relative error below 1.1e-12, so of 2^17 tokens the draw of one in ten
-// million could move to a neighbour; p(0) = 1. n is taken from the low bits of
-// 1.5 2^52 + (l - m) log2(e) / T.
+// A row's weights are 2^(l c - k), c = log2(e) / T and k the whole number next to m c:
+// exp((l - m) / T) but for a factor that the row has in common. With N + f = l c, |f| <=
+// 1/2, that is 2^(N - k) p(f), p the polynomial of degree 10 that interpolates 2^f at
+// the Chebyshev points, 0 among them: with the roundings 3.4 2^-53 off. That of f adds 0.4
+// 2^-53, and c's own, as another T would, 1.2 2^-53 (m - l) / T. Sums against the maxima
+// of waves, chunks and rows differ by powers of two, which are exact. N - k is taken
+// from the low bits of l c + 1.5 2^52 - k. (Degree 8 would be 9600 2^-53 off.)
 struct Scale {
     double c, lo;                       // log2(e) / T; (l - m) below which a weight counts as 0 (2^-1000)
     __device__ __forceinline__ explicit Scale(float t) {
@@ -86,31 +88,47 @@ __device__ __forceinline__ double scaled(double p, double kn) {
     return __builtin_bit_cast(double, u);
 }
 constexpr double kMagic = 6755399441055744.0;
-constexpr double kP8 = 1.3255224884799127e-06, kP7 = 1.5310079402383103e-05, kP6 = 0.00015403455852419016,
-                 kP5 = 0.0013333450568000008, kP4 = 0.00961812915940262, kP3 = 0.05550410941205934,
-                 kP2 = 0.2402265069581299, kP1 = 0.6931471805459335;
+constexpr double kP10 = 7.072585949269223e-09, kP9 = 1.0208690299958306e-07, kP8 = 1.321544258792169e-06,
+                 kP7 = 1.5252657260200837e-05, kP6 = 0.0001540353044173605, kP5 = 0.0013333558230164974,
+                 kP4 = 0.009618129107606888, kP3 = 0.05550410866444772, kP2 = 0.24022650695910097,
+                 kP1 = 0.69314718055995;
 struct Weight {
-    double m, c, lo;
+    double m, c, lo, magic;             // magic: 1.5 2^52 - k
     float low;
-    __device__ __forceinline__ Weight(float mx, Scale t) : m((double)mx), c(t.c), lo(t.lo), low((float)((double)mx + t.lo)) {}
+    bool apart;                         // the weight is 1 at m and 0 elsewhere: m is infinite, or |m| c above 2^36,
+                                        // and any other fp32 number more than 2^-24 |m| away from m
+    __device__ __forceinline__ Weight(float mx, Scale t) : m((double)mx), c(t.c), lo(t.lo), low((float)((double)mx + t.lo)) {
+        const double k = exponent(mx);
+        apart = !(fabs(k) < 0x1p36);
+        magic = kMagic - k;
+    }
+    __device__ __forceinline__ double exponent(float mx) const { return rint((double)mx * c); }
+    // What a weight against the maximum mx counts against this one
+    __device__ __forceinline__ double of(float mx) const {
+        const double k = exponent(mx), n = k - (kMagic - magic);
+        if (apart || !(fabs(k) < 0x1p36)) return (double)mx == m ? 1.0 : 0.0;
+        return n < -1000.0 ? 0.0 : __longlong_as_double((int64_t)(1023 + (int)n) << 52);
+    }
     // Where sums need none of the exceptions below: a finite maximum, T < inf, and
     // an fp32 number near m + lo. Weights below that one's, about 2^-1000, those of
     // NaN and -inf among them, count as that (the median of three is the smallest
-    // where one is NaN): nothing beside the maximum's 1 in the sum of a row, and below
+    // where one is NaN): nothing beside the maximum's in the sum of a row, and below
     // what a remainder counts (left_of).
     __device__ __forceinline__ bool plain() const {
         const double d = (double)low - m;
-        return c > 0.0 && fabs(m) < INFINITY && d <= 0.9 * lo && d >= 1.02 * lo;
+        return !apart && c > 0.0 && d <= 0.9 * lo && d >= 1.02 * lo;
     }
     __device__ __forceinline__ void raw4(const float l[4], double w[4]) const {
         double kn[4], f[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const double d = (double)__builtin_amdgcn_fmed3f(l[k], low, INFINITY) - m;
-            kn[k] = fma(d, c, kMagic);
-            f[k] = fma(d, c, -(kn[k] - kMagic));
-            w[k] = fma(kP8, f[k], kP7);
+            const double x = (double)__builtin_amdgcn_fmed3f(l[k], low, INFINITY);
+            kn[k] = fma(x, c, magic);
+            f[k] = fma(x, c, magic - kn[k]);
+            w[k] = fma(kP10, f[k], kP9);
         }
+        horner4(w, f, kP8);
+        horner4(w, f, kP7);
         horner4(w, f, kP6);
         horner4(w, f, kP5);
         horner4(w, f, kP4);
@@ -120,9 +138,11 @@ struct Weight {
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = scaled(fma(w[k], f[k], 1.0), kn[k]);
     }
-    __device__ __forceinline__ double power(double d) const {
-        const double kn = fma(d, c, kMagic), f = fma(d, c, -(kn - kMagic));
-        double p = fma(kP8, f, kP7);
+    __device__ __forceinline__ double power(double l) const {
+        const double kn = fma(l, c, magic), f = fma(l, c, magic - kn);
+        double p = fma(kP10, f, kP9);
+        p = fma(p, f, kP8);
+        p = fma(p, f, kP7);
         p = fma(p, f, kP6);
         p = fma(p, f, kP5);
         p = fma(p, f, kP4);
@@ -131,11 +151,12 @@ struct Weight {
         p = fma(p, f, kP1);
         return scaled(fma(p, f, 1.0), kn);
     }
-    // Weights below 2^-1000 are 0. m = +inf leaves 1 where l is +inf too, m = -inf
-    // nothing; NaN is 0, and -inf at any T (at T = inf all other weights are 1)
+    // Weights below 2^-1000 are 0, and those of NaN and of -inf at any T (at T = inf all
+    // others are 1)
     __device__ __forceinline__ double operator()(float l) const {
-        const double d = (double)l - m;
-        return !(l > -INFINITY) ? 0.0 : ((double)l == m || c == 0.0 ? (m < INFINITY || (double)l == m ? 1.0 : 0.0) : (m == INFINITY || d < lo ? 0.0 : power(d)));
+        if (!(l > -INFINITY)) return 0.0;
+        if (apart) return (double)l == m ? 1.0 : 0.0;
+        return (double)l - m < lo ? 0.0 : power((double)l);
     }
 };
 
@@ -334,7 +355,7 @@ __device__ __forceinline__ void chunk_stats(const Args &a, int64_t row, int c, f
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
             if (greedy) r = ms[i] == mm && ss[i] < r ? ss[i] : r;
-            else r += ss[i] * all(ms[i]);
+            else r += ss[i] * all.of(ms[i]);
         }
         a.mx[row * a.C + c] = mm;
         a.sum[row * a.C + c] = r;
@@ -518,7 +539,7 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
             best = wave_min(mc == m ? (int)zc : best);
             z = m == -INFINITY ? 0.0 : 1.0;
         } else {
-            z = wave_sum(zc * Weight(m, sc)(mc));
+            z = wave_sum(zc * Weight(m, sc).of(mc));
         }
         if (lane == 0) {
             node_m[i] = m;
@@ -686,7 +707,7 @@ __global__ __launch_bounds__(1024) void k_draw(Args a) {
                 if (rem) {
                     s = a.rest[b * a.C + lane];
                 } else {
-                    s = zc * e(mc);
+                    s = zc * e.of(mc);
                     for (int k = 0; k < st.gone && !whole; ++k) {
                         const int x = a.gone[c0 + k];
                         if (x / a.chunk == lane) s = fmax(s - e(load1<T>(row + x)), 0.0);

@@ -724,8 +724,9 @@ mxs_status mxs_kv4_release(const mxs_kv4_cache *cache, int32_t *refs, int32_t *t
  * accepted either). Where rounding leaves nothing of the remainder, the next token
  * is drawn from e. A child with a token outside [0, V) is rejected without
  * effect. path and count are what mxs_kv4_compact takes. Sums are in 64 bits, in
- * an order fixed by the sizes, of weights within 1.1e-12 of e (those below
- * 2^-1000 are 0, and what a draft leaves of one and is below 2^-990).
+ * an order fixed by the sizes, of weights within (4 + 1.2 (m - l) / T) 2^-53 of e,
+ * relative to it and to a factor that the row has in common (those below 2^-1000
+ * are 0, and what a draft leaves of one and is below 2^-990).
  * logits: [total, V] of `dtype`, ldl elements between rows; draft: [total, V] fp32
  * with ldd; tokens int64, parents int32, uniform fp64 (in [0, 1)): [total]; path:
  * [total] int32, rows of no sequence are left as they were; next: [B] int64.

@@ -328,6 +328,65 @@ def test_chunks_of_taken_tokens_alone(mx, V, kids):
         c.check(c.run(mx))
 
 
+def border(e, at, side):
+    """The random number just on one side of where the draw passes from token at - 1 to `at`, from extended precision.
+
+    The kernel's two sums that decide are off, relative to theirs, by no more than (in units of 2^-53, with (m - l) / T
+    <= 2): 7 each for the weights, and the roundings of 7 sums and products and of the number: 22. It lies 32 off."""
+    cum = np.cumsum(e, axis=1)
+    return (cum[:, at - 1] / cum[:, -1] * (1 + side * np.longdouble(2.0) ** -48)).astype(np.float64)
+
+
+@pytest.mark.parametrize("T", [1.0, 0.37])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,V,places", [(4000, 2, (0, 1)), (300, 3 * 4096, (0, 4096, 5120, 5127)),
+                                        (40, 300000, (7, 16384, 17500, 17501)), (900, 2000, (0, 1023, 1024, 1999))])
+def test_borders_of_the_draw(mx, B, V, places, dtype, T):
+    """Random numbers next to a border: the weights have the bits that 64-bit sums need, in one wave, over the waves of
+    a chunk and over chunks."""
+    g = np.random.default_rng(V + B)
+    few = torch.zeros(B, len(places), dtype=dtype)
+    few[:, 1:] = torch.from_numpy(-2 * float(np.float32(T)) * np.sort(g.random((B, len(places) - 1)), axis=1)).to(dtype)
+    l = torch.full((B, V), -math.inf, dtype=dtype, device=DEV)
+    l[:, torch.tensor(places, device=DEV)] = few.to(DEV)
+    e = np.exp(few.double().numpy().astype(np.longdouble) / np.longdouble(np.float32(T)))
+    d = lambda x, t: torch.from_numpy(np.ascontiguousarray(x)).to(t).to(DEV)
+    for at in range(1, len(places)):
+        for side in (-1, 1):
+            nxt = mx.mxs_verify_tree(l, torch.zeros(B, dtype=torch.int64, device=DEV), d(np.arange(B + 1), torch.int32),
+                                     d(border(e, at, side), torch.float64), max_n=1,
+                                     temperature=torch.full((B,), T, device=DEV))[2]
+            want = places[at - 1 if side < 0 else at]
+            assert bool((nxt == want).all()), (at, side, int((nxt != want).sum()))
+
+
+@pytest.mark.parametrize("offset", [-300.0, 1024.0, 70000.0])
+def test_borders_of_the_draw_far_from_zero(mx, offset):
+    """As test_borders_of_the_draw, logits (fp32, of which the weights are taken) far from 0."""
+    g = np.random.default_rng(7)
+    B = 2000
+    l = torch.full((B, 2), offset, dtype=F32)
+    l[:, 1] -= torch.from_numpy(2 * g.random(B)).float()
+    d = lambda x, t: torch.from_numpy(np.ascontiguousarray(x)).to(t).to(DEV)
+    e = np.exp((l.double() - offset).numpy().astype(np.longdouble))
+    for side in (-1, 1):
+        nxt = mx.mxs_verify_tree(l.to(DEV), torch.zeros(B, dtype=torch.int64, device=DEV), d(np.arange(B + 1), torch.int32),
+                                 d(border(e, 1, side), torch.float64), max_n=1)[2]
+        assert bool((nxt == (0 if side < 0 else 1)).all()), (side, int((nxt != (0 if side < 0 else 1)).sum()))
+
+
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("scale,offset", [(1.0, 900.0), (1.0, -30000.0), (1e-6, 1e-4), (1e25, 1e26), (1e-40, 0.0)])
+def test_logits_and_temperatures_of_any_size(mx, scale, offset, draft):
+    """Temperatures at which logits are some 1e3 to 1e12 of them away from 0, next to each other or far apart."""
+    for V in (300, 6000):
+        temps = [scale * t for t in (1.0, 0.3, 1e-2, 1e-4, 1e-7, 3e-9, 1e-9, 1e-12)]
+        c = Case([5] * 8, V, F32, draft, 5, "tree", temps, sharp=2.0)
+        l = (c.t_logits.double() * scale + offset).float()
+        c.t_logits.copy_(l)
+        c.check(c.run(mx))
+
+
 def test_tokens_and_parents_that_do_not_belong(mx):
     for draft in (True, False):
         c = Case([10] * 8, 300, F32, draft, 12, "tree", None, sharp=1.0)
