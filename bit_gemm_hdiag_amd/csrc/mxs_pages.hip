@@ -122,10 +122,11 @@ __global__ __launch_bounds__(256) void k_kv4_fork(int32_t *refs, int32_t *table,
 }
 
 // ------------------------------------------------------------------- reserve
-// Workspace: a bitmap of the free pages, their number in each chunk, the pages
-// that each sequence needs (-1: its row is too short), and the pages granted.
+// Workspace: bitmaps of the free and of the shared pages, the number of free ones in
+// each chunk, the pages that each sequence needs (-1: its row is too short), and the
+// pages granted.
 struct Reserve {
-    uint16_t *map;
+    uint16_t *map, *shared;
     int32_t *counts, *need, *grant;
     int chunks;
 };
@@ -138,10 +139,11 @@ size_t reserve_layout(int64_t pages, int64_t B, void *ws, Reserve *r) {
         at += (bytes + 15) / 16 * 16;
         return o;
     };
-    const size_t map = take(chunks * 64 * 2), counts = take(chunks * 4), need = take(B * 4), grant = take(pages * 4);
+    const size_t map = take(chunks * 64 * 2), shared = take(chunks * 64 * 2), counts = take(chunks * 4), need = take(B * 4), grant = take(pages * 4);
     if (r) {
         uint8_t *w = static_cast<uint8_t *>(ws);
         r->map = reinterpret_cast<uint16_t *>(w + map);
+        r->shared = reinterpret_cast<uint16_t *>(w + shared);
         r->counts = reinterpret_cast<int32_t *>(w + counts);
         r->need = reinterpret_cast<int32_t *>(w + need);
         r->grant = reinterpret_cast<int32_t *>(w + grant);
@@ -190,9 +192,9 @@ __device__ __forceinline__ bool write_range(const SeqArgs &a, int64_t b, int &le
 
 // Latency bounds both kernels of a reservation: 2.3 + 8.1 us for two sequences over 64
 // pages, 3.4 + 9.3 for 96 over 16384, 64 of which copy half a page (70 KB).
-// Waves of the first workgroups count what a sequence needs and mark entries
-// whose page is shared by -2 - page (this decision stands while the second
-// kernel changes refs); the others build the bitmap, a wave a chunk.
+// Waves of the first workgroups count what a sequence needs; the others build the
+// bitmaps, a wave a chunk. Which pages were shared is read from there while the second
+// kernel changes refs, so no entry is written before its page is granted.
 __global__ __launch_bounds__(256) void k_kv4_need(SeqArgs a, Reserve r, int seq_groups) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if ((int)blockIdx.x < seq_groups) {
@@ -205,14 +207,11 @@ __global__ __launch_bounds__(256) void k_kv4_need(SeqArgs a, Reserve r, int seq_
             return;
         }
         int need = 0;
-        int32_t *row = a.table + b * a.ldt;
+        const int32_t *row = a.table + b * a.ldt;
         for (int64_t j = lane; j < nj; j += 64) {
             const int32_t p = row[j0 + j];
             const bool held = p >= 0 && p < a.pages;
-            const bool shared = held && a.refs[p] > 1;
-            if (shared) row[j0 + j] = -2 - p;
-            else if (!held) row[j0 + j] = -1;
-            need += !held || shared;
+            need += !held || a.refs[p] > 1;
         }
         need = wave_sum(need);
         if (lane == 0) r.need[b] = need;
@@ -222,19 +221,26 @@ __global__ __launch_bounds__(256) void k_kv4_need(SeqArgs a, Reserve r, int seq_
     if (chunk >= r.chunks) return;
     // 16 pages a lane, all loaded at once
     const int64_t p0 = (int64_t)chunk * kChunkPages + 16 * lane;
-    uint32_t mine = 0;
+    uint32_t mine = 0, many = 0;
     if (p0 + 16 <= a.pages) {
         int4 v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) __builtin_memcpy(&v[k], a.refs + p0 + 4 * k, 16);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k) {
             mine |= ((v[k].x == 0) | (v[k].y == 0) << 1 | (v[k].z == 0) << 2 | (v[k].w == 0) << 3) << 4 * k;
+            many |= ((v[k].x > 1) | (v[k].y > 1) << 1 | (v[k].z > 1) << 2 | (v[k].w > 1) << 3) << 4 * k;
+        }
     } else {
 #pragma unroll 1
-        for (int k = 0; k < 16 && p0 + k < a.pages; ++k) mine |= (uint32_t)(a.refs[p0 + k] == 0) << k;
+        for (int k = 0; k < 16 && p0 + k < a.pages; ++k) {
+            const int32_t v = a.refs[p0 + k];
+            mine |= (uint32_t)(v == 0) << k;
+            many |= (uint32_t)(v > 1) << k;
+        }
     }
     r.map[(int64_t)chunk * 64 + lane] = (uint16_t)mine;
+    r.shared[(int64_t)chunk * 64 + lane] = (uint16_t)many;
     const int c = wave_sum(__popc(mine));
     if (lane == 0) r.counts[chunk] = c;
 }
@@ -281,7 +287,17 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
     int64_t wanted = 0;                         // 64 bits: no lens and cu make it wrap
     int avail = 0, mine = 0, upto = 0;
     const int per = (r.chunks + 255) / 256;
+    // entries of the first turn and whether they take a page, loaded before anything waits
+    auto entry = [&](int64_t j, bool &takes) {
+        const int32_t p = j < nj ? row[j0 + j] : 0;
+        const bool held = p >= 0 && p < a.pages;
+        takes = j < nj && (!held || (r.shared[p >> 4] >> (p & 15) & 1));
+        return held ? p : -1;
+    };
+    bool takes = false;
+    int32_t page = -1;
     if (need > 0) {
+        page = entry(tid, takes);
         // pages that earlier sequences need, and all that are free, a run of chunks a thread
         for (int64_t i = tid; i < b; i += 256) wanted += r.need[i] > 0 ? r.need[i] : 0;
         for (int i = tid * per; i < (tid + 1) * per && i < r.chunks; ++i) mine += r.counts[i];
@@ -297,8 +313,6 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
         for (int w = 0; w < wave; ++w) upto += sums[0][w];
     }
     if (need < 0 || (need > 0 && wanted + need > avail)) {
-        for (int64_t j = tid; j < nj; j += 256)
-            if (row[j0 + j] < -1) row[j0 + j] = -2 - row[j0 + j];
         for (int i = tid; i < n; i += 256) slots[c0 + i] = -1;
         if (tid == 0) lens_out[b] = len;
         return;
@@ -335,21 +349,21 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
         int at = 0;
         for (int64_t t0 = 0; t0 < nj; t0 += 256) {
             const int64_t j = t0 + tid;
-            const int32_t v = j < nj ? row[j0 + j] : 0;
-            const uint64_t takes = __ballot(v < 0);
-            if (lane == 0) sums[1][wave] = __popcll(takes);
+            if (t0 > 0) page = entry(j, takes);
+            const uint64_t who = __ballot(takes);
+            if (lane == 0) sums[1][wave] = __popcll(who);
             __syncthreads();
-            int rank = at + __popcll(takes & ((1ull << lane) - 1));
+            int rank = at + __popcll(who & ((1ull << lane) - 1));
             for (int w = 0; w < wave; ++w) rank += sums[1][w];
             at += sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
-            if (v < 0) {
+            if (takes) {
                 const int32_t p = grant[rank];
                 row[j0 + j] = p;
                 a.refs[p] = 1;
-                if (v < -1) {
-                    atomicSub(a.refs + (-2 - v), 1);
+                if (page >= 0) {
+                    atomicSub(a.refs + page, 1);
                     if (j == 0) {
-                        old_last = -2 - v;
+                        old_last = page;
                         new_last = p;
                     }
                 }

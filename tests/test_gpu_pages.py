@@ -404,6 +404,36 @@ def test_on_a_stream_of_the_callers(mx):
     p.same()
 
 
+def test_refused_sequences_keep_their_entries(mx):
+    """Entries that name no page (any negative number, any past the pool) take pages where there is room; the table of a
+    refused sequence is left as it was, shared pages and such entries among it."""
+    p = Pool(mx, 7, 4, 1, 32, 5, 8, 1)
+    p.write(p.reserve([9, 3, 0, 4, 0]))                           # 3 + 1 + 1 of 7 pages
+    p.fork([0], [4])
+    big = 2 ** 31 - 1
+    odd = {(0, 3): -7, (0, 4): 7, (0, 5): 1 << 30, (1, 1): -2 ** 31, (1, 2): -2 ** 31 + 5, (1, 3): big, (2, 0): -3,
+           (2, 1): 99, (3, 1): -2, (3, 2): -9}
+    for at, v in odd.items():
+        p.table[at] = v
+    before, refs = p.table.clone(), p.refs.clone()
+    ns = [16, 3, 0, 6, 5]                                         # wants 2 + 2 (shared), 1, 0, 2, 2 (shared, another)
+    slots, lens = mx.mxs_kv4_reserve(p.cache, p.refs, p.table, p.lens, dev(np.concatenate([[0], np.cumsum(ns)])), total=30)
+    assert lens.tolist() == [9, 3, 0, 4, 9] and bool((slots == -1).all())
+    assert torch.equal(p.table, before) and torch.equal(p.refs, refs)
+    ns = [0, 2, 8, 0, 0]
+    slots, lens = mx.mxs_kv4_reserve(p.cache, p.refs, p.table, p.lens, dev(np.concatenate([[0], np.cumsum(ns)])), total=10)
+    assert lens.tolist() == [9, 5, 0, 4, 9]                       # one of the two free pages, then two of one
+    assert slots[:2].tolist() == [int(p.table[1, 0]) * 4 + 3, int(p.table[1, 1]) * 4] and bool((slots[2:] == -1).all())
+    assert int(p.table[1, 1]) == 5 and torch.equal(p.table[[0, 2, 3, 4]], before[[0, 2, 3, 4]])
+    assert p.table[1, 2:].tolist() == before[1, 2:].tolist()
+    mx.mxs_kv4_release(p.cache, p.refs, p.table, lens, dev([0, -1, -1, -1, 0]), lens_out=lens)
+    slots, lens = mx.mxs_kv4_reserve(p.cache, p.refs, p.table, lens, dev([0, 0, 0, 8, 13, 13]), total=13)
+    assert lens.tolist() == [0, 5, 8, 9, 0] and bool((slots >= 0).all()) and len(set(slots.tolist())) == 13
+    assert bool((p.table[2, :2] >= 0).all()) and bool((p.table[2, :2] < 7).all()) and p.table[3, 2] in range(7)
+    held = p.table[(p.table >= 0) & (p.table < 7)]
+    assert torch.equal(torch.bincount(held, minlength=7).int(), p.refs)
+
+
 @pytest.mark.parametrize("graph", [False, True])
 def test_refused_sequences_keep_their_tokens(mx, graph):
     """A step whose cu is never looked at on the host, over a pool that runs out: sequences that were refused, forks of
