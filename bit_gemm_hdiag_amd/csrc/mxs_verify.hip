@@ -595,6 +595,9 @@ __global__ __launch_bounds__(1024) void k_walk(Args a) {
                     ok = u * R < r;
                     if (!ok && r > 0.0) {
                         if (lane == 0) gone[ngone] = i;
+                        // all lanes read it for the next child
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                        __builtin_amdgcn_wave_barrier();
                         ++ngone;
                         R = R > r ? R - r : 0.0;
                     }

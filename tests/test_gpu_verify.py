@@ -523,3 +523,17 @@ def test_on_a_stream_of_the_callers(mx):
         got = c.run(mx)
     s.synchronize()
     c.check(got)
+
+
+@pytest.mark.parametrize("kids", [2, 63, 64, 200])
+def test_the_same_token_proposed_again(mx, kids):
+    """Without a draft's distribution: a child whose token an elder sibling had is rejected, wherever it stands among
+    them, and takes nothing out of the row again."""
+    V, B = 400, 40
+    c = Case([kids + 1] * B, V, F32, False, kids, "tree", sharp=1.0)
+    g = np.random.default_rng(kids)
+    c.parents = np.tile(np.array([-1] + [0] * kids, np.int32), B)
+    c.tokens = g.integers(0, max(2, kids // 2), c.total).astype(np.int64)
+    for u in (None, 1 - 2.0 ** -53):
+        c.u = g.random(c.total) if u is None else np.where(np.arange(c.total) % (kids + 1), u, g.random(c.total))
+        c.check(c.run(mx))
