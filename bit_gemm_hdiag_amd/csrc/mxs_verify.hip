@@ -74,10 +74,11 @@ struct Scale {
     }
 };
 // p <- p f + c for four numbers, c a constant in scalar registers (the compiler
-// would copy it into the result's registers first, an instruction more each time)
+// would copy it into the result's registers first, an instruction more each time). Each
+// result is written before the last f is read, so it shares no register with one.
 __device__ __forceinline__ void horner4(double p[4], const double f[4], double c) {
     asm("v_fma_f64 %0, %0, %4, %8\n\tv_fma_f64 %1, %1, %5, %8\n\tv_fma_f64 %2, %2, %6, %8\n\tv_fma_f64 %3, %3, %7, %8"
-        : "+v"(p[0]), "+v"(p[1]), "+v"(p[2]), "+v"(p[3])
+        : "+&v"(p[0]), "+&v"(p[1]), "+&v"(p[2]), "+&v"(p[3])
         : "v"(f[0]), "v"(f[1]), "v"(f[2]), "v"(f[3]), "s"(c));
 }
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
