@@ -489,7 +489,8 @@ __global__ __launch_bounds__(256, STEPS <= 2 ? 4 : 3) void k_lora_expand(LoraArg
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
-                // cut, not rounded: no part overflows, and three of 8 bits hold all 24
+                // cut, not rounded: no part overflows, and three of 8 bits hold all 24 (those
+                // above 2^-133, the smallest bf16 number)
                 uint32_t h[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {

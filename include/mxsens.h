@@ -770,8 +770,8 @@ typedef struct mxs_lora {
  * fp32 output of the mxs_mixed_gemm calls over the same tokens; X is the layer's
  * input in its own channel order (no permutation) and does not overlap Y. Exact
  * products of the inputs with fp32 sums; A X is kept in fp32 (it enters the bf16
- * matrix cores as exact three-part sums) and the result is scaled and added in
- * fp32. Every sum has an order fixed by the sizes: the result is deterministic,
+ * matrix cores as exact three-part sums, but for bits below 2^-133, which are cut)
+ * and the result is scaled and added in fp32. Every sum has an order fixed by the sizes: the result is deterministic,
  * and what the other rows hold does not change a row (their number moves the
  * split of K, and with it the rounding).
  * X: [M, ldx >= K] of set->dtype; ids: [M] int32; Y: [M, ldy >= N] fp32 (rows of

@@ -188,6 +188,47 @@ def test_values_of_v_near_the_largest(mx):
     assert torch.equal(c.Y, big.float()[:, None].expand(4, 8))
 
 
+def test_every_bit_of_v_near_the_largest(mx):
+    """V of more bits than bf16 has, above the largest bf16 number: a first part that is rounded would be infinite."""
+    c = Case(mx, 4, 32, 8, 2, 1, BF, 2, True, ranks=False, scale=False)
+    top = torch.tensor([0x7F7F], dtype=torch.int16).view(BF).item()
+    x = torch.tensor([[top, 0.75 * 2.0 ** 120], [-top, -0.75 * 2.0 ** 120], [1.0, 2.0 ** -20], [-3.0, 2.0 ** -16]])
+    want = x.double().sum(1).float()
+    assert torch.equal(want.double(), x.double().sum(1)) and torch.isfinite(want).all()
+    assert torch.isinf(want[:2].to(BF)).all()
+    c.A.zero_()
+    c.A[0, 0, :2] = 1.0
+    c.X.zero_()
+    c.X[:, :2] = x.to(BF).to(DEV)
+    assert torch.equal(c.X[:, :2].float().cpu(), x)
+    c.B.zero_()
+    c.B[0, :, 0] = 1.0
+    c.ids.zero_()
+    c.Y.zero_()
+    assert torch.equal(c.run().cpu(), want[:, None].expand(4, 8))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_small_values_of_v(mx, dtype):
+    """bf16: bits of V below 2^-133, the smallest number of a part, are cut; above them it is whole, X, A and B below
+    2^-126 among them. fp32: whole down to 2^-149."""
+    c = Case(mx, 8, 32, 4, 2, 1, dtype, 2, True, ranks=False, scale=False)
+    for t in (c.A, c.X, c.B, c.Y, c.ids):
+        t.zero_()
+    c.A[0, 0, :3] = torch.tensor([2.0 ** -60, 1.0, 2.0 ** 60], device=DEV).to(dtype)
+    c.X[0, 0], c.X[1, 0], c.X[2, 0], c.X[3, 1] = 2.0 ** -66, 1.5 * 2.0 ** -60, 2.0 ** -73, 2.0 ** -130
+    c.X[4, 2] = 2.0 ** -130
+    c.X[5, 0], c.X[5, 1] = 2.0 ** -50, 2.0 ** -133
+    c.X[6, 0], c.X[6, 1] = 2.0 ** -74, 2.0 ** -133                # V = 1.5 * 2^-133
+    c.X[7, 0] = -2.0 ** -85
+    c.B[0, 0, 0], c.B[0, 1, 0], c.B[0, 2, 0] = 2.0 ** 100, 1.0, -2.0 ** 90
+    v = (c.A[0, 0].double() * c.X.double()).sum(1).cpu()
+    got, want = c.run().double().cpu(), v[:, None] * c.B[0, :, 0].double().cpu()
+    cut = 2.0 ** -133 if dtype is BF else 0.0
+    assert torch.equal(got[:6, [0, 2]], want[:6, [0, 2]])
+    assert bool(((got - want).abs() <= cut * c.B[0, :, 0].double().abs().cpu()).all())
+
+
 @pytest.mark.parametrize("M", [50, 900])
 def test_the_same_call_twice_gives_the_same_bits(mx, M):
     c = Case(mx, M, 2048, 300, 40, 9, BF, 3, False)
