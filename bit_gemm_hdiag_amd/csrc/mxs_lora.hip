@@ -11,10 +11,10 @@
 // its tokens and are not stored, and where a token sits does not change its value.
 //
 // Bound by memory: the adapters' bytes for few rows (64 rows on 32 adapters of rank
-// 64, 28672 x 8192: 16 + 51 us for 33 + 132 MB, half of the copy rate: each workgroup
-// waits for its rows, then V, then B; 34 us of the 51 are B alone), X and Y for prompts
-// (4096 rows of 8192 x 8192 at rank 16: 24 us for 67 MB of X, 69 for 268 MB of Y, 3.9
-// TB/s). 8 rows on 4 adapters take 3.5 + 6.0 us, mostly latency.
+// 64, 28672 x 8192: 16 + 48 us for 33 + 132 MB, half of the copy rate: each workgroup
+// waits for its rows, then V, then B; B alone takes 34 us), X and Y for prompts (4096 rows
+// of 8192 x 8192 at rank 16: 24 us for 67 MB of X, 68 for 268 MB of Y, 3.9 TB/s). 8 rows
+// on 4 adapters take 3.6 + 5.6 us, mostly latency.
 #include "mxs_device.h"
 #include "mxs_internal.h"
 

@@ -190,8 +190,10 @@ __device__ __forceinline__ bool write_range(const SeqArgs &a, int64_t b, int &le
     return true;
 }
 
-// Latency bounds both kernels of a reservation: 2.3 + 8.1 us for two sequences over 64
-// pages, 3.4 + 9.3 for 96 over 16384, 64 of which copy half a page (70 KB).
+// Latency bounds both kernels of a reservation: 2.4 + 8.3 us for two sequences over 64
+// pages, 3.3 + 9.3 for 96 over 16384, 64 of which copy half a page (70 KB). A prompt's
+// slots are written by its workgroup alone, one a thread and turn: 9.3 us for eight of
+// 4096 tokens, 119 for one of 131072.
 // Waves of the first workgroups count what a sequence needs; the others build the
 // bitmaps, a wave a chunk. Which pages were shared is read from there while the second
 // kernel changes refs, so no entry is written before its page is granted.
@@ -391,7 +393,7 @@ __global__ __launch_bounds__(256) void k_kv4_take(SeqArgs a, Reserve r, Planes p
 // are moved 1024 code words (with their scale bytes) at a time, in ascending
 // order: all are read before the first is written, and what a later turn reads no
 // earlier one has written, because path[i] >= i. 96 sequences of up to 26 tokens take
-// 5.9 us (a thread a column, token after token: 15). A sequence whose first slot is -1
+// 6.0 us (a thread a column, token after token: 15). A sequence whose first slot is -1
 // was refused its tokens: its last ones are not theirs, and may lie in shared pages.
 __global__ __launch_bounds__(256) void k_kv4_compact(SeqArgs a, Planes pl, const int32_t *path, const int32_t *count,
                                                      const int64_t *slots, int32_t *lens_out) {
